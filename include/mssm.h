@@ -13,7 +13,11 @@
  *    (mssm_ssd_trapezoidal_fwd; decode: mssm_ssd_trapezoidal_state_update),
  *    with a complex-valued state as well (mssm_mamba3_siso_update), and with
  *    several inputs and outputs per channel, Mamba-3 MIMO
- *    (mssm_ssd_mimo_fwd; decode: mssm_ssd_mimo_state_update).
+ *    (mssm_ssd_mimo_fwd; decode: mssm_ssd_mimo_state_update);
+ *  - what stands on either side of the scans in a language model (embedding,
+ *    blocks with a norm in front and a residual stream, norm, tied head; "Mamba-2 y state-space
+ *    models", 4.3), for training and serving: mssm_embedding_fwd and _bwd,
+ *    mssm_norm_fwd and _bwd, mssm_linear_cross_entropy_fwd and _bwd.
  *
  *  1. mssm_selective_scan_fwd -- the Mamba-1 selective scan.  Defined by the
  *     linear state recurrence h_t = A h_{t-1} + B x_t with readout y_t = C h_t
@@ -471,6 +475,135 @@ int mssm_selective_scan_plan(const mssm_scan_desc* desc, int32_t* split_seq, int
 int mssm_ssd_plan(const mssm_ssd_desc* desc, int32_t* route);
 /* The same for mssm_ssd_mimo_fwd with this rank. */
 int mssm_ssd_mimo_plan(const mssm_ssd_desc* desc, int32_t rank, int32_t* route);
+
+/* Embedding lookup and the gradient of its table (the first and, with a tied
+ * head, the last matrix of the language model of "Mamba-2 y state-space
+ * models", 4.3):
+ *     out[t,:]  = scale * weight[ids[t],:]
+ *     dweight[v,:] (+)= scale * sum over the t with ids[t] = v of dout[t,:]
+ *   ids          : [tokens] int32 or int64 (id_bytes 4 or 8).  An id outside
+ *                  [0, vocab) names no row (padding, say -1): its row of out
+ *                  is zero and it adds to no gradient.
+ *   weight       : [vocab, dim] (io_dtype);  out, dout : [tokens, dim] (io_dtype)
+ *   dweight      : [vocab, dim] in grad_dtype, io_dtype or MSSM_F32.  Every
+ *                  row is written: overwritten (rows without a token with
+ *                  zeros), or, with accumulate != 0, added to (the sum is
+ *                  taken in fp32 and rounded once), as for a head tied to the
+ *                  embedding or gradients gathered over several batches.
+ * The gradient is summed in fp32 over the tokens sorted by id, in token order:
+ * the same result on every run.  tokens may be 0, up to 2^26 - 1; vocab up to
+ * 2^30; dim up to 2^20 (MSSM_ERR_UNSUPPORTED above); scale finite.  workspace
+ * (the gradient only): at least mssm_embedding_bwd_workspace_size(desc) bytes,
+ * 256-byte aligned.  Element-aligned pointers.  Other rules as
+ * mssm_selective_scan_fwd. */
+typedef struct {
+    int64_t tokens, vocab, dim;
+    float scale;
+    int32_t io_dtype;   /* mssm_dtype */
+    int32_t id_bytes;   /* 4 or 8 */
+    uint32_t flags;     /* reserved, must be 0 */
+} mssm_embedding_desc;
+
+int mssm_embedding_fwd(const mssm_embedding_desc* desc, const void* ids, const void* weight, void* out, void* stream);
+int mssm_embedding_bwd(const mssm_embedding_desc* desc, const void* ids, const void* dout, void* dweight,
+                       int32_t grad_dtype, int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+size_t mssm_embedding_bwd_workspace_size(const mssm_embedding_desc* desc);
+
+/* Layer norm and RMS norm over the last axis, with the residual add that
+ * precedes them in the blocks, and their gradients:
+ *     h   = x + residual              (or x; kept rounded to res_dtype in residual_out)
+ *     out = (h - mu) * rstd * weight + bias
+ *     mu  = mean(h) (MSSM_LAYER_NORM) or 0 (MSSM_RMS_NORM),  rstd = (mean((h - mu)^2) + eps)^(-1/2)
+ *   x, out             : [rows, dim] (io_dtype)
+ *   residual           : [rows, dim] (res_dtype), nullable
+ *   residual_out       : [rows, dim] (res_dtype); required with residual,
+ *                        nullable without.  What is normalised is h as kept
+ *                        here (x itself when it is NULL).
+ *   weight, bias       : [dim] fp32; bias nullable (NULL for the RMS norm)
+ *   mean, rstd         : [rows] fp32, nullable; for the gradients (mean: layer norm only)
+ * mssm_norm_bwd, with xh = (h - mu) rstd and g = dout * weight:
+ *     dh = rstd * (g - xh mean(g xh) - [layer norm] mean(g)) + dresidual
+ *     dweight = sum over rows of dout xh,   dbias = sum over rows of dout
+ *   h                  : [rows, dim] (res_dtype): residual_out of the forward,
+ *                        or x (then res_dtype is x's type)
+ *   mean, rstd         : as the forward wrote them
+ *   dout               : [rows, dim] (io_dtype)
+ *   dresidual          : [rows, dim] (res_dtype), nullable: gradient of residual_out
+ *   dx                 : [rows, dim] (io_dtype);  dresidual_in : [rows, dim]
+ *                        (res_dtype): dh in either type; one may be NULL
+ *   dweight, dbias     : [dim] fp32, overwritten; dbias nullable (NULL for the RMS norm)
+ * io_dtype MSSM_BF16 takes either res_dtype, MSSM_F32 takes MSSM_F32.  eps is
+ * positive.  rows may be 0 (the backward pass then writes zero dweight and
+ * dbias), up to 2^26 - 1 of at most 256 columns, 2^22 - 1 of more; dim up to
+ * 2^20.  Statistics and sums are fp32, in a fixed order: the same result on
+ * every run.  workspace (the gradients only): at least
+ * mssm_norm_bwd_workspace_size(desc) bytes, 256-byte aligned.  Element-aligned
+ * pointers.  Other rules as mssm_selective_scan_fwd. */
+#define MSSM_LAYER_NORM 0
+#define MSSM_RMS_NORM 1
+typedef struct {
+    int64_t rows, dim;
+    float eps;
+    int32_t kind;       /* MSSM_LAYER_NORM or MSSM_RMS_NORM */
+    int32_t io_dtype;   /* mssm_dtype */
+    int32_t res_dtype;  /* mssm_dtype */
+    uint32_t flags;     /* reserved, must be 0 */
+} mssm_norm_desc;
+
+int mssm_norm_fwd(const mssm_norm_desc* desc, const void* x, const void* residual, const float* weight,
+                  const float* bias, void* out, void* residual_out, float* mean, float* rstd, void* stream);
+int mssm_norm_bwd(const mssm_norm_desc* desc, const void* h, const float* weight, const float* mean,
+                  const float* rstd, const void* dout, const void* dresidual, void* dx, void* dresidual_in,
+                  float* dweight, float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+size_t mssm_norm_bwd_workspace_size(const mssm_norm_desc* desc);
+
+/* Softmax cross entropy of a linear head, from the hidden states and the
+ * head's weight (tied to the embedding or not), without keeping the logits:
+ *     l[t,v] = sum_d x[t,d] * weight[v,d]
+ *     lse[t] = log(sum_v exp(l[t,v])),   loss[t] = lse[t] - l[t, targets[t]]
+ *   x       : [tokens, dim] (io_dtype);  weight : [vocab, dim] (io_dtype)
+ *   targets : [tokens] int32 or int64 (id_bytes 4 or 8).  A token whose target
+ *             is ignore_id or outside [0, vocab) is left out: its loss and lse
+ *             are 0, its dx is 0, its x (whatever it holds) enters no sum and
+ *             its dloss and dlse are not read; the work done is that of the
+ *             tokens left.
+ *   loss, lse : [tokens] fp32
+ * mssm_linear_cross_entropy_bwd: the gradients of sum(loss * dloss) + sum(lse * dlse),
+ *     G[t,v] = exp(l[t,v] - lse[t]) * (dloss[t] + dlse[t]) - [v = targets[t]] * dloss[t]
+ *     dx = G weight,   dweight (+)= G^T x
+ *   lse     : as the forward wrote it;  dloss : [tokens] fp32 (a mean over the
+ *             counted tokens: 1 / their number);  dlse : [tokens] fp32,
+ *             nullable (= 0; a penalty on lse enters here)
+ *   dx      : [tokens, dim] (io_dtype);  dweight : [vocab, dim] in grad_dtype,
+ *             io_dtype or MSSM_F32, overwritten, or added to with accumulate != 0
+ *             (in fp32, rounded once); one of dx and dweight may be NULL
+ * Products are summed in fp32.  With MSSM_BF16 G is rounded to bf16, whatever
+ * grad_dtype; with MSSM_F32 every product carries 24 bits.  All sums are taken
+ * in a fixed order: the same result on every run.
+ * tokens may be 0, up to 2^26 - 1; vocab up to 2^30; dim up to 2^20.  bf16
+ * weight of a dim that is a multiple of 64 must be 16-byte aligned (it is read
+ * in place; any other weight is laid out piece by piece in the workspace
+ * first), other pointers element-aligned.  workspace: at least the bytes the
+ * size queries ask, 256-byte aligned; it holds the counted tokens' x, and
+ * pieces of at most about 512 MiB (256 vocabulary rows at least) of partial
+ * sums, of G and of the laid-out weight.  Other rules as mssm_selective_scan_fwd. */
+typedef struct {
+    int64_t tokens, vocab, dim;
+    int64_t ignore_id;
+    int32_t io_dtype;   /* mssm_dtype */
+    int32_t id_bytes;   /* 4 or 8 */
+    uint32_t flags;     /* reserved, must be 0 */
+} mssm_cross_entropy_desc;
+
+int mssm_linear_cross_entropy_fwd(const mssm_cross_entropy_desc* desc, const void* x, const void* weight,
+                                  const void* targets, float* loss, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+size_t mssm_linear_cross_entropy_fwd_workspace_size(const mssm_cross_entropy_desc* desc);
+int mssm_linear_cross_entropy_bwd(const mssm_cross_entropy_desc* desc, const void* x, const void* weight,
+                                  const void* targets, const float* lse, const float* dloss, const float* dlse,
+                                  void* dx, void* dweight, int32_t grad_dtype, int32_t accumulate, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+size_t mssm_linear_cross_entropy_bwd_workspace_size(const mssm_cross_entropy_desc* desc);
 
 /* Static text for a status code (never NULL). */
 const char* mssm_status_string(int status);

@@ -37,6 +37,28 @@ class SSDDesc(ctypes.Structure):
                 ("chunk", ctypes.c_int64), ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
+class EmbeddingDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("io_dtype", ctypes.c_int32), ("id_bytes", ctypes.c_int32),
+                ("flags", ctypes.c_uint32)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("kind", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32)]
+
+
+class CrossEntropyDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("ignore_id", ctypes.c_int64), ("io_dtype", ctypes.c_int32), ("id_bytes", ctypes.c_int32),
+                ("flags", ctypes.c_uint32)]
+
+
+MSSM_LAYER_NORM = 0
+MSSM_RMS_NORM = 1
+
+
 # every exported symbol and its ctypes signature (checked against include/mssm.h by the tests)
 _P, _SZ, _I = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
 SIGNATURES = {
@@ -64,6 +86,18 @@ SIGNATURES = {
     "mssm_selective_scan_fwd_ckpt_workspace_size": (_SZ, [ctypes.POINTER(ScanDesc)]),
     "mssm_selective_scan_checkpoint_size": (_SZ, [ctypes.POINTER(ScanDesc)]),
     "mssm_selective_scan_bwd_workspace_size": (_SZ, [ctypes.POINTER(ScanDesc)]),
+    "mssm_embedding_fwd": (_I, [ctypes.POINTER(EmbeddingDesc)] + [_P] * 4),
+    "mssm_embedding_bwd": (_I, [ctypes.POINTER(EmbeddingDesc)] + [_P] * 3 +
+                           [ctypes.c_int32, ctypes.c_int32, _P, _SZ, _P]),
+    "mssm_embedding_bwd_workspace_size": (_SZ, [ctypes.POINTER(EmbeddingDesc)]),
+    "mssm_norm_fwd": (_I, [ctypes.POINTER(NormDesc)] + [_P] * 9),
+    "mssm_norm_bwd": (_I, [ctypes.POINTER(NormDesc)] + [_P] * 11 + [_SZ, _P]),
+    "mssm_norm_bwd_workspace_size": (_SZ, [ctypes.POINTER(NormDesc)]),
+    "mssm_linear_cross_entropy_fwd": (_I, [ctypes.POINTER(CrossEntropyDesc)] + [_P] * 6 + [_SZ, _P]),
+    "mssm_linear_cross_entropy_fwd_workspace_size": (_SZ, [ctypes.POINTER(CrossEntropyDesc)]),
+    "mssm_linear_cross_entropy_bwd": (_I, [ctypes.POINTER(CrossEntropyDesc)] + [_P] * 8 +
+                                      [ctypes.c_int32, ctypes.c_int32, _P, _SZ, _P]),
+    "mssm_linear_cross_entropy_bwd_workspace_size": (_SZ, [ctypes.POINTER(CrossEntropyDesc)]),
     "mssm_status_string": (ctypes.c_char_p, [_I]),
     "mssm_last_error_detail": (ctypes.c_char_p, []),
     "mssm_abi_version": (_I, []),
@@ -751,3 +785,321 @@ def _ssd_update_call(fn, state, x_prev, B_prev, x, delta, lam, A, B, C, D, z, ou
     if st != MSSM_OK:
         raise MssmError(st, fn)
     return out
+
+
+# --------------------------------------------------------------------------
+# Around the scan: embedding, norm, loss
+# --------------------------------------------------------------------------
+def _id_bytes(name, ids) -> int:
+    torch = _torch()
+    if ids.dtype == torch.int64:
+        return 8
+    if ids.dtype == torch.int32:
+        return 4
+    raise TypeError(f"{name} must be int32 or int64, got {ids.dtype}")
+
+
+def _grad_code(name, t, io_dtype) -> int:
+    torch = _torch()
+    if t.dtype == torch.float32:
+        return MSSM_F32
+    if t.dtype == io_dtype:
+        return _io_code(io_dtype)
+    raise TypeError(f"{name} must be {io_dtype} or torch.float32, got {t.dtype}")
+
+
+def _empty(stream, shape, dtype):
+    """A new tensor on the current GPU, in the memory pool of the stream that the call runs on: memory of the
+    current stream's pool could still be in use there, or be handed out again while the call runs."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device="cuda")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device="cuda")
+
+
+def _workspace(need, workspace, stream):
+    """(pointer, bytes, tensor to keep) of a call's workspace, allocated when none is given."""
+    torch = _torch()
+    if need == 0:
+        return None, 0, None
+    if workspace is None:
+        workspace = _empty(stream, need, torch.uint8)
+    elif workspace.get_device() != torch.cuda.current_device():
+        raise ValueError("workspace must be on the current GPU")
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def embedding_bwd_workspace_size(tokens, vocab, dim, io_dtype=MSSM_BF16) -> int:
+    d = EmbeddingDesc(tokens, vocab, dim, 1.0, io_dtype, 8, 0)
+    return lib.mssm_embedding_bwd_workspace_size(ctypes.byref(d))
+
+
+def embedding_fwd(ids, weight, scale: float = 1.0, out=None, stream=None):
+    """scale * weight[ids] (mssm_embedding_fwd).
+
+    ids: int32 or int64 of any shape; weight: [vocab, dim] float32 or bfloat16.  An id outside
+    [0, vocab) gives a row of zeros.  Returns out [*ids.shape, dim] in weight's type."""
+    torch = _torch()
+    if weight.dim() != 2:
+        raise ValueError("weight must be [vocab, dim]")
+    vocab, dim = weight.shape
+    io, nb = _io_code(weight.dtype), _id_bytes("ids", ids)
+    cur = torch.cuda.current_device()
+    _check_gpu("ids", ids, ids.dtype, ids.shape, cur)
+    _check_gpu("weight", weight, weight.dtype, (vocab, dim), cur)
+    shape = tuple(ids.shape) + (dim,)
+    if out is None:
+        out = _empty(stream, shape, weight.dtype)
+    _check_gpu("out", out, weight.dtype, shape, cur)
+    d = EmbeddingDesc(ids.numel(), vocab, dim, scale, io, nb, 0)
+    st = lib.mssm_embedding_fwd(ctypes.byref(d), _ptr(ids), _ptr(weight), _ptr(out), _stream_handle(stream))
+    if st != MSSM_OK:
+        raise MssmError(st, "mssm_embedding_fwd")
+    return out
+
+
+def embedding_bwd(ids, dout, vocab: int, scale: float = 1.0, dweight=None, accumulate: bool = False, workspace=None,
+                  stream=None):
+    """Gradient of embedding_fwd's weight (mssm_embedding_bwd): row v is scale * the sum of dout over the
+    tokens with id v, in the same order on every run.
+
+    ids: int32 or int64; dout: [*ids.shape, dim].  dweight: [vocab, dim] in dout's type or float32 (allocated
+    in dout's type when None), overwritten, or added to when accumulate.  Returns dweight."""
+    torch = _torch()
+    if dout.dim() != ids.dim() + 1:
+        raise ValueError("dout must be [*ids.shape, dim]")
+    dim = dout.shape[-1]
+    io, nb = _io_code(dout.dtype), _id_bytes("ids", ids)
+    cur = torch.cuda.current_device()
+    _check_gpu("ids", ids, ids.dtype, ids.shape, cur)
+    _check_gpu("dout", dout, dout.dtype, tuple(ids.shape) + (dim,), cur)
+    if dweight is None:
+        if accumulate:
+            raise ValueError("accumulate adds to dweight, which must be given")
+        dweight = _empty(stream, (vocab, dim), dout.dtype)
+    gd = _grad_code("dweight", dweight, dout.dtype)
+    _check_gpu("dweight", dweight, dweight.dtype, (vocab, dim), cur)
+    d = EmbeddingDesc(ids.numel(), vocab, dim, scale, io, nb, 0)
+    ws, ws_bytes, _keep = _workspace(lib.mssm_embedding_bwd_workspace_size(ctypes.byref(d)), workspace, stream)
+    st = lib.mssm_embedding_bwd(ctypes.byref(d), _ptr(ids), _ptr(dout), _ptr(dweight), gd, int(accumulate), ws,
+                                ws_bytes, _stream_handle(stream))
+    if st != MSSM_OK:
+        raise MssmError(st, "mssm_embedding_bwd")
+    return dweight
+
+
+def norm_bwd_workspace_size(rows, dim) -> int:
+    d = NormDesc(rows, dim, 1e-5, MSSM_LAYER_NORM, MSSM_F32, MSSM_F32, 0)
+    return lib.mssm_norm_bwd_workspace_size(ctypes.byref(d))
+
+
+def layer_norm_fwd(x, weight, bias=None, residual=None, eps: float = 1e-5, return_residual: bool = False,
+                   residual_dtype=None, return_stats: bool = False, out=None, residual_out=None, stream=None):
+    """Layer norm over the last axis of h = x + residual (mssm_norm_fwd).
+
+    x: [..., dim] float32 or bfloat16; weight, bias: [dim] float32; residual: x's shape, x's type or float32.
+    h is kept in residual_out (residual's type, else residual_dtype, else x's), and what is normalised is h as kept.
+    Returns out, and after it residual_out with return_residual and (mean, rstd), float32 of x's leading
+    shape, with return_stats: the gradients take them.  Without a residual h is x itself, unless
+    return_residual."""
+    return _norm_fwd(MSSM_LAYER_NORM, x, weight, bias, residual, eps, return_residual, residual_dtype, return_stats,
+                     out, residual_out, stream)
+
+
+def rms_norm_fwd(x, weight, residual=None, eps: float = 1e-5, return_residual: bool = False, residual_dtype=None,
+                 return_stats: bool = False, out=None, residual_out=None, stream=None):
+    """RMS norm over the last axis of h = x + residual (mssm_norm_fwd): as layer_norm_fwd without the mean and
+    the bias.  Returns out, then residual_out with return_residual, then rstd with return_stats."""
+    return _norm_fwd(MSSM_RMS_NORM, x, weight, None, residual, eps, return_residual, residual_dtype, return_stats,
+                     out, residual_out, stream)
+
+
+def _norm_fwd(kind, x, weight, bias, residual, eps, return_residual, residual_dtype, return_stats, out, residual_out,
+              stream):
+    torch = _torch()
+    if x.dim() < 1:
+        raise ValueError("x must be [..., dim]")
+    shape, dim = tuple(x.shape), x.shape[-1]
+    rows = x.numel() // dim if dim else 0
+    io = _io_code(x.dtype)
+    cur = torch.cuda.current_device()
+    rdt = residual.dtype if residual is not None else (residual_out.dtype if residual_out is not None else
+                                                       (residual_dtype or x.dtype))
+    if residual_dtype is not None and residual_dtype != rdt:
+        raise TypeError(f"residual_dtype is {residual_dtype}, but the residual is {rdt}")
+    res = _grad_code("residual", residual, x.dtype) if residual is not None else _res_code(rdt, x.dtype)
+    _check_gpu("x", x, x.dtype, shape, cur)
+    _check_gpu("residual", residual, rdt, shape, cur)
+    _check_gpu("weight", weight, torch.float32, (dim,), cur)
+    _check_gpu("bias", bias, torch.float32, (dim,), cur)
+    if out is None:
+        out = _empty(stream, shape, x.dtype)
+    _check_gpu("out", out, x.dtype, shape, cur)
+    if residual_out is None and (return_residual or residual is not None):
+        residual_out = _empty(stream, shape, rdt)
+    _check_gpu("residual_out", residual_out, rdt, shape, cur)
+    mean = rstd = None
+    if return_stats:
+        rstd = _empty(stream, shape[:-1], torch.float32)
+        if kind == MSSM_LAYER_NORM:
+            mean = _empty(stream, shape[:-1], torch.float32)
+    d = NormDesc(rows, dim, eps, kind, io, res, 0)
+    st = lib.mssm_norm_fwd(ctypes.byref(d), _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(out),
+                           _ptr(residual_out), _ptr(mean), _ptr(rstd), _stream_handle(stream))
+    if st != MSSM_OK:
+        raise MssmError(st, "mssm_norm_fwd")
+    got = (out,) + ((residual_out,) if return_residual else ())
+    if return_stats:
+        got += (mean, rstd) if kind == MSSM_LAYER_NORM else (rstd,)
+    return got if len(got) > 1 else out
+
+
+def _res_code(rdt, io_dtype) -> int:
+    if rdt != io_dtype and rdt != _torch().float32:
+        raise TypeError(f"the residual must be {io_dtype} or torch.float32, got {rdt}")
+    return _io_code(rdt)
+
+
+def layer_norm_bwd(h, weight, mean, rstd, dout, dresidual=None, want_dresidual: bool = False, want_dbias: bool = True,
+                   dx=None, workspace=None, stream=None):
+    """Gradients of layer_norm_fwd (mssm_norm_bwd).
+
+    h: what was normalised, residual_out of the forward (or x when there was none); mean, rstd: its
+    statistics; dout: gradient of out; dresidual: gradient of residual_out (h's type) or None.
+    Returns a dict: dx (dout's type; the gradient of x and, when the types agree, of the residual), dresidual
+    (the same in h's type, when want_dresidual), dweight and dbias (float32)."""
+    return _norm_bwd(MSSM_LAYER_NORM, h, weight, mean, rstd, dout, dresidual, want_dresidual, want_dbias, dx,
+                     workspace, stream)
+
+
+def rms_norm_bwd(h, weight, rstd, dout, dresidual=None, want_dresidual: bool = False, dx=None, workspace=None,
+                 stream=None):
+    """Gradients of rms_norm_fwd (mssm_norm_bwd): as layer_norm_bwd without mean and dbias."""
+    return _norm_bwd(MSSM_RMS_NORM, h, weight, None, rstd, dout, dresidual, want_dresidual, False, dx, workspace,
+                     stream)
+
+
+def _norm_bwd(kind, h, weight, mean, rstd, dout, dresidual, want_dresidual, want_dbias, dx, workspace, stream):
+    torch = _torch()
+    if h.dim() < 1:
+        raise ValueError("h must be [..., dim]")
+    shape, dim = tuple(h.shape), h.shape[-1]
+    rows = h.numel() // dim if dim else 0
+    io = _io_code(dout.dtype)
+    res = _res_code(h.dtype, dout.dtype)
+    cur = torch.cuda.current_device()
+    _check_gpu("h", h, h.dtype, shape, cur)
+    _check_gpu("dout", dout, dout.dtype, shape, cur)
+    _check_gpu("dresidual", dresidual, h.dtype, shape, cur)
+    _check_gpu("weight", weight, torch.float32, (dim,), cur)
+    if kind == MSSM_LAYER_NORM and mean is None:
+        raise ValueError("mean is required")
+    _check_gpu("mean", mean, torch.float32, shape[:-1], cur)
+    _check_gpu("rstd", rstd, torch.float32, shape[:-1], cur)
+    if dx is None:
+        dx = _empty(stream, shape, dout.dtype)
+    _check_gpu("dx", dx, dout.dtype, shape, cur)
+    dres = _empty(stream, shape, h.dtype) if want_dresidual else None
+    dweight = _empty(stream, (dim,), torch.float32)
+    dbias = _empty(stream, (dim,), torch.float32) if want_dbias else None
+    d = NormDesc(rows, dim, 1.0, kind, io, res, 0)
+    ws, ws_bytes, _keep = _workspace(lib.mssm_norm_bwd_workspace_size(ctypes.byref(d)), workspace, stream)
+    st = lib.mssm_norm_bwd(ctypes.byref(d), _ptr(h), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dout),
+                           _ptr(dresidual), _ptr(dx), _ptr(dres), _ptr(dweight), _ptr(dbias), ws, ws_bytes,
+                           _stream_handle(stream))
+    if st != MSSM_OK:
+        raise MssmError(st, "mssm_norm_bwd")
+    return {"dx": dx, "dresidual": dres, "dweight": dweight, "dbias": dbias}
+
+
+def linear_cross_entropy_fwd_workspace_size(tokens, vocab, dim, io_dtype=MSSM_BF16) -> int:
+    d = CrossEntropyDesc(tokens, vocab, dim, -100, io_dtype, 8, 0)
+    return lib.mssm_linear_cross_entropy_fwd_workspace_size(ctypes.byref(d))
+
+
+def linear_cross_entropy_bwd_workspace_size(tokens, vocab, dim, io_dtype=MSSM_BF16) -> int:
+    d = CrossEntropyDesc(tokens, vocab, dim, -100, io_dtype, 8, 0)
+    return lib.mssm_linear_cross_entropy_bwd_workspace_size(ctypes.byref(d))
+
+
+def _xent_args(x, weight, targets, ignore_id, cur):
+    if x.dim() < 1 or weight.dim() != 2 or x.shape[-1] != weight.shape[1]:
+        raise ValueError("x must be [..., dim] and weight [vocab, dim]")
+    vocab, dim = weight.shape
+    io, nb = _io_code(x.dtype), _id_bytes("targets", targets)
+    _check_gpu("x", x, x.dtype, tuple(x.shape), cur)
+    _check_gpu("weight", weight, x.dtype, (vocab, dim), cur)
+    _check_gpu("targets", targets, targets.dtype, tuple(x.shape[:-1]), cur)
+    return CrossEntropyDesc(targets.numel(), vocab, dim, ignore_id, io, nb, 0)
+
+
+def linear_cross_entropy_fwd(x, weight, targets, ignore_id: int = -100, loss=None, lse=None, workspace=None,
+                             stream=None):
+    """Cross entropy of softmax(x @ weight.T) against targets, token by token, without keeping the logits
+    (mssm_linear_cross_entropy_fwd).
+
+    x: [..., dim] and weight: [vocab, dim], float32 or bfloat16 alike; targets: int32 or int64 of x's leading
+    shape.  A token whose target is ignore_id or outside [0, vocab) is left out: loss and lse 0.
+    Returns (loss, lse), float32 of targets' shape; lse is log sum exp of the token's logits."""
+    torch = _torch()
+    cur = torch.cuda.current_device()
+    d = _xent_args(x, weight, targets, ignore_id, cur)
+    shape = tuple(targets.shape)
+    loss = _empty(stream, shape, torch.float32) if loss is None else loss
+    lse = _empty(stream, shape, torch.float32) if lse is None else lse
+    _check_gpu("loss", loss, torch.float32, shape, cur)
+    _check_gpu("lse", lse, torch.float32, shape, cur)
+    ws, ws_bytes, _keep = _workspace(lib.mssm_linear_cross_entropy_fwd_workspace_size(ctypes.byref(d)), workspace,
+                                     stream)
+    st = lib.mssm_linear_cross_entropy_fwd(ctypes.byref(d), _ptr(x), _ptr(weight), _ptr(targets), _ptr(loss),
+                                           _ptr(lse), ws, ws_bytes, _stream_handle(stream))
+    if st != MSSM_OK:
+        raise MssmError(st, "mssm_linear_cross_entropy_fwd")
+    return loss, lse
+
+
+def linear_cross_entropy_bwd(x, weight, targets, lse, dloss, dlse=None, ignore_id: int = -100, want_dx: bool = True,
+                             want_dweight: bool = True, dx=None, dweight=None, accumulate: bool = False,
+                             workspace=None, stream=None):
+    """Gradients of sum(loss * dloss) + sum(lse * dlse) with respect to x and weight
+    (mssm_linear_cross_entropy_bwd).
+
+    lse: as linear_cross_entropy_fwd returned it; dloss, dlse: float32 of targets' shape (dlse None: zero).
+    dweight: [vocab, dim] in x's type or float32 (allocated in x's type when None), overwritten, or added to
+    when accumulate (a head tied to the embedding, several batches).  Returns a dict of dx and dweight (None
+    for one that is not wanted)."""
+    torch = _torch()
+    cur = torch.cuda.current_device()
+    d = _xent_args(x, weight, targets, ignore_id, cur)
+    shape = tuple(targets.shape)
+    _check_gpu("lse", lse, torch.float32, shape, cur)
+    _check_gpu("dloss", dloss, torch.float32, shape, cur)
+    _check_gpu("dlse", dlse, torch.float32, shape, cur)
+    if not want_dx and not want_dweight:
+        raise ValueError("nothing to compute: want_dx and want_dweight are both False")
+    if want_dx:
+        dx = _empty(stream, tuple(x.shape), x.dtype) if dx is None else dx
+        _check_gpu("dx", dx, x.dtype, tuple(x.shape), cur)
+    else:
+        dx = None
+    gd = d.io_dtype
+    if want_dweight:
+        if dweight is None:
+            if accumulate:
+                raise ValueError("accumulate adds to dweight, which must be given")
+            dweight = _empty(stream, tuple(weight.shape), weight.dtype)
+        gd = _grad_code("dweight", dweight, x.dtype)
+        _check_gpu("dweight", dweight, dweight.dtype, tuple(weight.shape), cur)
+    else:
+        dweight = None
+    ws, ws_bytes, _keep = _workspace(lib.mssm_linear_cross_entropy_bwd_workspace_size(ctypes.byref(d)), workspace,
+                                     stream)
+    st = lib.mssm_linear_cross_entropy_bwd(ctypes.byref(d), _ptr(x), _ptr(weight), _ptr(targets), _ptr(lse),
+                                           _ptr(dloss), _ptr(dlse), _ptr(dx), _ptr(dweight), gd, int(accumulate), ws,
+                                           ws_bytes, _stream_handle(stream))
+    if st != MSSM_OK:
+        raise MssmError(st, "mssm_linear_cross_entropy_bwd")
+    return {"dx": dx, "dweight": dweight}

@@ -6,10 +6,11 @@
 #include <cstring>
 #include <limits>
 
+#include "checks.h"
 #include "internal.h"
 
-namespace {
-
+namespace mssm {
+// text of the calling thread's last launch failure
 thread_local char g_err[256] = "";
 
 void set_err(hipError_t e) {
@@ -17,30 +18,14 @@ void set_err(hipError_t e) {
   std::strncpy(g_err, s ? s : "unknown HIP error", sizeof(g_err) - 1);
   g_err[sizeof(g_err) - 1] = '\0';
 }
+}  // namespace mssm
+
+using namespace mssm::checks;
+using mssm::set_err;
+
+namespace {
 
 constexpr int64_t kSimds = 256 * 4;   // MI355X: 256 CUs x 4 SIMDs
-
-bool mul_ok(int64_t a, int64_t b, int64_t* r) {
-  if (a < 0 || b < 0) return false;
-  if (a != 0 && b > std::numeric_limits<int64_t>::max() / a) return false;
-  *r = a * b;
-  return true;
-}
-
-bool aligned(const void* p, size_t a) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Range {
-  uintptr_t lo, hi;
-};
-Range rng(const void* p, int64_t bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return {a, a + static_cast<uintptr_t>(bytes)};
-}
-bool overlap(const void* p, int64_t pb, const void* q, int64_t qb) {
-  if (p == nullptr || q == nullptr || pb <= 0 || qb <= 0) return false;
-  const Range a = rng(p, pb), b = rng(q, qb);
-  return a.lo < b.hi && b.lo < a.hi;
-}
 
 // --------------------------------------------------------------------------
 // Mamba-1 planning
@@ -162,7 +147,7 @@ const char* mssm_status_string(int status) {
   }
 }
 
-const char* mssm_last_error_detail(void) { return g_err; }
+const char* mssm_last_error_detail(void) { return mssm::g_err; }
 
 int mssm_selective_scan_plan(const mssm_scan_desc* desc, int32_t* split_seq, int32_t* split_state) {
   const int v = validate_scan_desc(desc);

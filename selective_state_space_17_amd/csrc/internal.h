@@ -161,4 +161,81 @@ size_t scan_bwd_workspace_bytes(int64_t batch, int64_t L, int64_t dim, int64_t N
 int64_t scan_bwd_grid_blocks(int64_t batch, int64_t dim, int64_t N);
 hipError_t scan_bwd_launch(const ScanBwdArgs& a, hipStream_t stream);
 
+// ---------------------------------------------------------------------------
+// Around the scan: embedding, norm, loss
+// ---------------------------------------------------------------------------
+struct EmbedArgs {
+  const void* ids;
+  int id_bytes;          // 4 or 8
+  float scale;
+  int64_t tokens, vocab, dim;
+  int io;                // 0 fp32, 1 bf16
+  const void* weight;    // lookup
+  void* out;
+  const void* dout;      // gradient
+  void* dweight;
+  int grad_io;           // dweight in the io type; else fp32
+  int accumulate;
+  void* workspace;
+};
+
+hipError_t embed_fwd_launch(const EmbedArgs& a, hipStream_t stream);
+// workspace: the tokens sorted by id (two buffers of pairs), digit counts, sums of runs that cross slices
+size_t embed_bwd_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim);
+hipError_t embed_bwd_launch(const EmbedArgs& a, hipStream_t stream);
+
+struct NormArgs {
+  int64_t rows, dim;
+  float eps;
+  int layer;             // 1 layer norm, 0 RMS norm
+  int io, res_io;        // 0 fp32, 1 bf16: x, out, dout, dx; residual stream (backward: h, dresidual)
+  const void* x;
+  const void* residual;  // nullable
+  const float* weight;
+  const float* bias;     // nullable
+  void* out;
+  void* residual_out;    // nullable
+  float* mean;           // forward: nullable output; backward: input (layer norm)
+  float* rstd;           // forward: nullable output; backward: input
+  const void* h;
+  const void* dout;
+  const void* dresidual;   // nullable
+  void* dx;                // nullable
+  void* dresidual_in;      // nullable
+  float* dweight;
+  float* dbias;            // nullable
+  void* workspace;
+};
+
+hipError_t norm_fwd_launch(const NormArgs& a, hipStream_t stream);
+// workspace: partial sums of dweight and dbias
+size_t norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
+hipError_t norm_bwd_launch(const NormArgs& a, hipStream_t stream);
+
+struct XentArgs {
+  int64_t tokens, vocab, dim;
+  int64_t ignore;
+  int io;                // 0 fp32, 1 bf16
+  int id_bytes;          // 4 or 8
+  const void* x;
+  const void* weight;
+  const void* targets;
+  float* loss;           // forward
+  float* lse;
+  const float* lse_in;   // gradients
+  const float* dloss;
+  const float* dlse;     // nullable
+  void* dx;              // nullable
+  void* dweight;         // nullable
+  int grad_io;           // dweight in the io type; else fp32
+  int accumulate;
+  void* workspace;
+};
+
+// workspace: the counted tokens' x as the products read it, the forward's partial sums or a piece of the
+// logits' gradient, and, where the weight cannot be read in place, a piece of it laid out
+size_t xent_workspace_bytes(const XentArgs& a, bool grad);
+hipError_t xent_fwd_launch(const XentArgs& a, hipStream_t stream);
+hipError_t xent_bwd_launch(const XentArgs& a, hipStream_t stream);
+
 }  // namespace mssm

@@ -1,0 +1,202 @@
+"""Layer norm and RMS norm with the residual add, forward and backward, against the plain 64-bit forms."""
+import pytest
+import torch
+
+import model_ops as R
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def M():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import selective_state_space_17_amd as m
+    return m
+
+
+# (rows, dim, io, residual type or None)
+CASES = [
+    (1, 1, F32, None),
+    (1, 2, BF16, F32),
+    (3, 7, BF16, BF16),
+    (5, 64, F32, F32),
+    (4, 66, BF16, None),
+    (130, 250, BF16, F32),
+    (9, 257, F32, None),
+    (66, 512, BF16, BF16),
+    (2100, 72, BF16, None),
+    (7, 1000, BF16, F32),
+    (3000, 1024, BF16, F32),
+    (5, 1023, F32, F32),
+    (1500, 1032, F32, None),
+    (11, 2560, BF16, F32),
+    (1100, 2050, BF16, BF16),
+    (4, 5120, BF16, F32),
+    (3, 9000, F32, F32),
+    (2, 16384, BF16, F32),
+    (3, 16392, BF16, BF16),
+    (2, 5001, F32, None),
+    (70, 20001, BF16, F32),
+]
+
+
+def make(rows, dim, io, res, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn(rows, dim, generator=g) * 0.8 + 0.3).to(io)
+    r = None if res is None else (torch.randn(rows, dim, generator=g) * 2).to(res)
+    w = 1 + 0.2 * torch.randn(dim, generator=g)
+    b = 0.1 * torch.randn(dim, generator=g)
+    dout = torch.randn(rows, dim, generator=g).to(io)
+    dr = None if res is None else torch.randn(rows, dim, generator=g).to(res)
+    return x, r, w, b, dout, dr
+
+
+def cu(t):
+    return None if t is None else t.cuda()
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"r{c[0]}_d{c[1]}_{str(c[2])[6:]}_{str(c[3])[6:]}")
+def test_norm(M, case, kind):
+    rows, dim, io, res = case
+    layer = kind == "layer"
+    say("norm", kind, case)
+    x, r, w, b, dout, dr = make(rows, dim, io, res, 31 * rows + dim)
+    args = (cu(x), cu(w)) + ((cu(b),) if layer else ())
+    got = (M.layer_norm_fwd if layer else M.rms_norm_fwd)(*args, residual=cu(r), return_residual=r is not None,
+                                                          return_stats=True)
+    got = list(got)
+    want = R.norm_fwd(x, r, w, b if layer else None, 1e-5, layer, res)
+    R.check(got[0], want["out"], "out")
+    if res is not None:
+        R.check(got[1], want["residual"], "residual")
+    rstd = got[-1].cpu()
+    R.check(rstd, want["rstd"], "rstd")
+    if layer:
+        R.check(got[-2], want["mean"], "mean")
+    mean = got[-2].cpu() if layer else None
+    h = x if res is None else got[1].cpu()
+    stats = (cu(mean), cu(rstd)) if layer else (cu(rstd),)
+    bwd = M.layer_norm_bwd if layer else M.rms_norm_bwd
+    grads = bwd(cu(h), cu(w), *stats, cu(dout), dresidual=cu(dr), want_dresidual=res is not None)
+    ref = R.norm_bwd(h, w, mean, rstd, dout, dr, layer)
+    R.check(grads["dx"], ref["dx"], "dx")
+    if res is not None:
+        R.check(grads["dresidual"], ref["dresidual"], "dresidual")
+    R.check(grads["dweight"], ref["dweight"], "dweight")
+    if layer:
+        R.check(grads["dbias"], ref["dbias"], "dbias")
+    again = bwd(cu(h), cu(w), *stats, cu(dout), dresidual=cu(dr), want_dresidual=res is not None)
+    for k, t in grads.items():
+        assert t is None or torch.equal(t, again[k]), f"{k} differs between two calls"
+
+
+def test_gradient_against_differences(M):
+    """The layer norm's gradient with the residual add, against central differences of the 64-bit forward."""
+    torch.manual_seed(7)
+    x, r, w, b = (torch.randn(3, 10, dtype=torch.float64) for _ in range(4))
+    w, b = w[0], b[0]
+    dout, dr = torch.randn(3, 10, dtype=torch.float64), torch.randn(3, 10, dtype=torch.float64)
+    x, r, w, b, dout, dr = (t.float().double() for t in (x, r, w, b, dout, dr))
+
+    def loss(x, r, w, b):
+        h = x + r
+        c = h - h.mean(1, keepdim=True)
+        y = c / (c.pow(2).mean(1, keepdim=True) + 1e-5).sqrt() * w + b
+        return float((y * dout).sum() + (h * dr).sum())
+
+    f = lambda t: t.float().cuda()  # noqa: E731
+    out, h, mean, rstd = M.layer_norm_fwd(f(x), f(w), f(b), residual=f(r), return_residual=True, return_stats=True)
+    g = M.layer_norm_bwd(h, f(w), mean, rstd, f(dout), dresidual=f(dr))
+    for name, t, got in (("dx", x, g["dx"]), ("dx", r, g["dx"]), ("dweight", w, g["dweight"]), ("dbias", b, g["dbias"])):
+        d = torch.zeros_like(t)
+        for i in range(t.numel()):
+            e = torch.zeros_like(t).reshape(-1)
+            e[i] = 1e-5
+            e = e.reshape(t.shape)
+            a = [x, r, w, b]
+            k = [j for j, v in enumerate(a) if v is t][0]
+            hi, lo = list(a), list(a)
+            hi[k], lo[k] = t + e, t - e
+            d.view(-1)[i] = (loss(*hi) - loss(*lo)) / 2e-5
+        # differences: h^2 / 6 of a third derivative of order 1e2, and 1e-16 x 1e2 / h; fp32: some 1e2 u
+        assert (got.cpu().double() - d).abs().max() < 2e-5 * (1 + d.abs().max()), name
+
+
+def test_first_block_without_a_residual(M):
+    """return_residual without a residual starts the stream: a copy of x in the stream's type."""
+    x, _, w, _, _, _ = make(10, 96, BF16, None, 4)
+    out, stream = M.rms_norm_fwd(cu(x), cu(w), return_residual=True, residual_dtype=F32)
+    assert stream.dtype == F32 and torch.equal(stream.cpu(), x.float())
+    assert torch.equal(out, M.rms_norm_fwd(cu(x), cu(w)))
+
+
+def test_constant_and_huge_rows(M):
+    """A row of equal values has variance 0: out is the bias; large values do not overflow the layer norm's centring."""
+    x = torch.stack([torch.full((64,), 3.0), torch.full((64,), -1e18), torch.zeros(64)])
+    w, b = torch.randn(64), torch.randn(64)
+    out = M.layer_norm_fwd(x.cuda(), w.cuda(), b.cuda()).cpu()
+    assert torch.equal(out, b.expand(3, 64))
+    assert torch.equal(M.rms_norm_fwd(torch.zeros(2, 64).cuda(), w.cuda()).cpu(), torch.zeros(2, 64))
+
+
+def test_a_row_of_nan_stays_alone(M):
+    x = torch.randn(6, 300)
+    clean = M.layer_norm_fwd(x.cuda(), torch.ones(300).cuda()).cpu()
+    x[2, 5] = float("nan")
+    x[4, 0] = float("inf")
+    out = M.layer_norm_fwd(x.cuda(), torch.ones(300).cuda()).cpu()
+    keep = [0, 1, 3, 5]
+    assert torch.equal(out[keep], clean[keep]) and out[2].isnan().all() and out[4].isnan().any()
+
+
+def test_no_rows_and_no_bias_gradient(M):
+    w = torch.randn(40).cuda()
+    assert M.layer_norm_fwd(torch.zeros(0, 40).cuda(), w).shape == (0, 40)
+    e = torch.zeros(0, 40).cuda()
+    g = M.layer_norm_bwd(e, w, torch.zeros(0).cuda(), torch.zeros(0).cuda(), e)
+    assert torch.equal(g["dweight"].cpu(), torch.zeros(40)) and torch.equal(g["dbias"].cpu(), torch.zeros(40))
+    x, _, _, _, dout, _ = make(6, 40, F32, None, 5)
+    _, mean, rstd = M.layer_norm_fwd(cu(x), w, return_stats=True)
+    a = M.layer_norm_bwd(cu(x), w, mean, rstd, cu(dout))
+    b = M.layer_norm_bwd(cu(x), w, mean, rstd, cu(dout), want_dbias=False)
+    assert b["dbias"] is None and torch.equal(a["dx"], b["dx"]) and torch.equal(a["dweight"], b["dweight"])
+
+
+def test_leading_shape_and_unaligned_views(M):
+    x, _, w, b, _, _ = make(24, 48, BF16, None, 6)
+    ref = M.layer_norm_fwd(cu(x), cu(w), cu(b))
+    buf = torch.zeros(24 * 48 + 1, dtype=BF16).cuda()
+    v = buf[1:].view(2, 3, 4, 48)
+    v.copy_(x.reshape(2, 3, 4, 48))
+    out, mean, rstd = M.layer_norm_fwd(v, cu(w), cu(b), return_stats=True)
+    assert mean.shape == (2, 3, 4) and rstd.shape == (2, 3, 4)
+    assert (out.reshape(24, 48).float() - ref.float()).abs().max() <= 2.0 ** -7 * ref.float().abs().max()
+
+
+def test_refusals(M):
+    x, r, w, b, dout, dr = (cu(t) for t in make(4, 64, BF16, F32, 8))
+    with pytest.raises(TypeError):
+        M.layer_norm_fwd(x.half(), w)
+    with pytest.raises(TypeError):
+        M.layer_norm_fwd(x, w.bfloat16())
+    with pytest.raises(TypeError):
+        M.layer_norm_fwd(x.float(), w, residual=r.bfloat16())
+    with pytest.raises(ValueError, match="contiguous"):
+        M.rms_norm_fwd(x[:, ::2], w[:32])
+    with pytest.raises(ValueError, match="shape"):
+        M.rms_norm_fwd(x, w[:63])
+    with pytest.raises(ValueError, match="GPU tensor"):
+        M.rms_norm_fwd(x, w.cpu())
+    for eps in (0.0, -1.0, float("nan"), float("inf")):
+        with pytest.raises(M.MssmError):
+            M.rms_norm_fwd(x, w, eps=eps)
+    with pytest.raises(ValueError, match="mean"):
+        M.layer_norm_bwd(x, w, None, torch.ones(4).cuda(), dout)
+    with pytest.raises(TypeError):
+        M.rms_norm_bwd(x.half(), w, torch.ones(4).cuda(), dout)
+    with pytest.raises(M.MssmError):
+        M.rms_norm_fwd(x, w, out=x)
