@@ -35,10 +35,11 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kBK = 64;                 // k per step
-constexpr int kRow = kBK * 2;           // bytes of an LDS row
+constexpr int kBK = 64;                 // k per step: two matrix instructions'
+constexpr int kRow = kBK * 2;           // bytes of a row of a step
 constexpr int kPlane = 64 * kRow;       // LDS tiles are planes of 64 rows x 128 bytes
 constexpr int kTokTile = 256;           // compacted tokens are padded to this
+constexpr int kSkew = 34;               // rows between panels: 4352 bytes, see Operand
 constexpr int kTerms = 3;               // bf16 terms of an fp32 value
 constexpr int kPairs = 6;               // term products kept
 __device__ __constant__ const int kPairA[kPairs] = {2, 0, 1, 1, 0, 0};
@@ -62,39 +63,49 @@ __device__ __forceinline__ void split3(float v, uint16_t (&t)[kTerms]) {
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));   // low half of a flat LDS address
 }
-// lane l's 16 bytes go from global memory to LDS offset lds + 16 l (lds is wave-uniform)
-__device__ __forceinline__ void dma16(const void* g, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
-               :: "v"(g), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory", "m0");
+// lane l's 16 bytes at base + off go to LDS offset lds + 16 l (base and lds are wave-uniform).  Written as asm
+// so that the compiler does not wait for these loads before the LDS reads of the other buffer; they are
+// waited for by count.  No output register: nothing can be overwritten while a load is in flight.
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory", "m0");
 }
 
 // ------------------------------------------------------------------------------------------------ product
+// An operand as the products read it, in bytes.  K-contiguous: `row` from one output row to the next, `step`
+// per 64 k.  K-strided: `row` from one k to the next, `plane` per 64 output columns, `step` per 64 k.  What
+// this library lays out itself (x, G, and the weight where it must) is kept in panels of 64 columns, [panel]
+// [row][64]: 64 k of a tile's rows, or 64 rows of a panel, are then one contiguous stretch either way it is read.
+// Panels stand kSkew rows further apart than they are long, off the powers of two at which every workgroup
+// would be at the same memory channels at the same time.
+struct Operand {
+  const unsigned char* p;
+  int64_t row, step, plane;
+  int64_t term;            // between the bf16 terms of a split operand
+  int rows, planes;        // what may be read: rows, and (K-strided) panels of 64 columns
+};
+
 struct ProductParams {
-  const uint16_t* A;
-  const uint16_t* B;
-  int64_t lda, ldb;        // elements between rows
-  int64_t pa, pb;          // elements between an operand's bf16 terms (split operands)
-  int M, N;                // rows of the output on either side (columns past them are not stored)
-  int rows_a, cols_a;      // what may be read of A: rows, and (K-strided) columns
-  int rows_b, cols_b;
+  Operand A, B;
+  int M, N;                // rows of the output on either side (what lies past them is not stored)
   int K;                   // multiple of 64; with k_is_tokens: the compacted count, rounded up, instead
-  int tiles_m, tiles_n;
+  int slices;              // workgroups that share a tile's k (kGradX, kGradW), each with sums of its own
   int k_is_tokens, n_is_tokens;
   const int* count;        // compacted tokens
   // epilogues
-  int v0, vocab;           // first vocabulary row of this piece
+  int v0;                  // first vocabulary row of this piece
   const int* tgt;          // compacted targets
-  float2* part;            // [2 * tiles_m][tok_cap]: maximum, sum of exponentials
+  float2* part;            // [tile_m][wave row][tok_cap]: maximum, sum of exponentials
   int64_t tok_cap;
   float* tlogit;           // target's logit
   const float* lse;        // compacted
   const float* gl;         // dloss + dlse
   const float* g;          // dloss
-  uint16_t* dl;            // [tok][piece], one or three terms
-  int64_t ldl, pdl;
-  float* dxacc;            // [tok_cap][ldx], sums over pieces
-  int64_t ldx;
-  int first, last;         // piece
+  uint16_t* dl;            // panels [vocabulary / 64][token][64], one or three terms
+  int64_t pdl;             // elements between them
+  float* sums;             // [slices][n][lds]: sums over k slices and pieces, or null: straight to out
+  int64_t lds, slice_elems;
+  int first;               // of the pieces that share sums
   const int* rows;         // compacted -> token
   void* out;               // dx or dW
   int64_t dim;
@@ -103,237 +114,347 @@ struct ProductParams {
 
 enum { kLogits = 0, kGradLogits = 1, kGradX = 2, kGradW = 3 };
 
+template <typename T> __device__ __forceinline__ T lds_at(uint32_t addr) {
+  return *(__attribute__((address_space(3))) const T*)static_cast<uintptr_t>(addr);
+}
+// the scheduler keeps what stands before this before it
+__device__ __forceinline__ void fence_schedule() { __builtin_amdgcn_sched_barrier(0); }
+
+// One workgroup stays on a CU (two of the small tile) and takes tile after tile.  The loads run two steps of
+// 64 k ahead of the matrix cores and cross tile borders: a tile's first steps are on their way while the
+// tile before it is finished and stored.
 template <int BM, int BN, int WM, int WN, bool ATR, bool BTR, bool SPLIT, int EPI>
 __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) {
-  constexpr int kWavesN = WM * WN;
+  constexpr int kW = WM * WN;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;      // 16 x 16 tiles of a wave
-  constexpr int LA = BM / 8 / kWavesN, LB = BN / 8 / kWavesN;   // 1 KB loads of a wave per step
-  static_assert(LA * 8 * kWavesN == BM && LB * 8 * kWavesN == BN, "loads split evenly over the waves");
-  __shared__ __attribute__((aligned(16))) unsigned char as[2][BM * kRow];
-  __shared__ __attribute__((aligned(16))) unsigned char bs[2][BN * kRow];
+  constexpr int LA = BM / 8 / kW, LB = BN / 8 / kW;        // 1 KB loads of a wave per step
+  constexpr int LR = (LA + LB + TM - 1) / TM;              // loads between two rows of multiplications
+  constexpr int RR = (TM + TN + TM - 2) / (TM - 1);        // fragments read there
+  static_assert(LA * 8 * kW == BM && LB * 8 * kW == BN, "loads split evenly over the waves");
+  static_assert(TM % 4 == 0 && TN % 4 == 0, "a wave's share of a tile is whole panels");
+  constexpr int kA = BM * kRow, kB = BN * kRow;            // bytes of a buffer
+  __shared__ __attribute__((aligned(128))) unsigned char as[2][kA];
+  __shared__ __attribute__((aligned(128))) unsigned char bs[2][kB];
 
   const int lane = threadIdx.x % kLanes;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
   const int wm = w / WN, wn = w % WN;
   const int count = *p.count;
 
-  // workgroup -> tile.  Workgroups b, b + 8, ... share an XCD and its L2: each XCD takes a contiguous range
-  // of an order that walks bands of 8 n-tiles, m outer, so that what runs on it at one time is a block of
-  // few m-tiles by 8 n-tiles.
-  const int total = p.tiles_m * p.tiles_n;
+  // Jobs: tiles x slices of k.  Workgroups b, b + 8, ... share an XCD and its L2: each XCD takes a contiguous
+  // range of an order that walks bands of 8 n-tiles, m outer, so that what runs on it at one time is a block
+  // of few m-tiles by 8 n-tiles.
+  const int tiles_m = (p.M + BM - 1) / BM;
+  const int tiles_n = ((p.n_is_tokens ? count : p.N) + BN - 1) / BN;
+  const int tiles = tiles_m * tiles_n, total = tiles * p.slices;
   const int per = (total + 7) / 8;
-  const int tile = (blockIdx.x % 8) * per + blockIdx.x / 8;
-  if (tile >= total || blockIdx.x / 8 >= per) return;
-  const int band = tile / (p.tiles_m * 8);
-  const int left = p.tiles_n - band * 8, wide = left < 8 ? left : 8;
-  const int in_band = tile - band * p.tiles_m * 8;
-  const int m0 = in_band / wide * BM, n0 = (band * 8 + in_band % wide) * BN;
-  if (p.n_is_tokens && n0 >= count) return;
-  const int steps1 = (p.k_is_tokens ? (count + kBK - 1) / kBK * kBK : p.K) / kBK;
-  const int steps = SPLIT ? steps1 * kPairs : steps1;
+  const int stride = gridDim.x / 8;
+  const int job_end = (blockIdx.x % 8 + 1) * per < total ? (blockIdx.x % 8 + 1) * per : total;
+  const int steps1 = ((p.k_is_tokens ? count : p.K) + kBK - 1) / kBK;   // of one pair of terms
+  const int all = SPLIT ? steps1 * kPairs : steps1;
+  struct Job {
+    int m0, n0, slice, begin, steps;
+  };
+  auto job_at = [&](int job) {
+    Job j;
+    j.slice = job / tiles;
+    const int tile = job - j.slice * tiles;
+    const int band = tile / (tiles_m * 8);
+    const int left = tiles_n - band * 8, wide = left < 8 ? left : 8;
+    const int in_band = tile - band * tiles_m * 8;
+    j.m0 = in_band / wide * BM;
+    j.n0 = (band * 8 + in_band % wide) * BN;
+    j.begin = static_cast<int>(static_cast<int64_t>(all) * j.slice / p.slices);
+    j.steps = static_cast<int>(static_cast<int64_t>(all) * (j.slice + 1) / p.slices) - j.begin;
+    return j;
+  };
 
-  // this lane's part of the loads: row lane / 8 of an 8-row group, 16-byte chunk lane % 8 as stored; the
-  // chunk it holds is xor-ed with the row, so that both kinds of reads below are free of bank conflicts
+  // ---- loads.  A load is 8 rows x 128 bytes (K-strided: of a plane of 64 columns), a lane's part row
+  // lane / 8 and the 16-byte chunk lane % 8 as stored.  The chunk it holds is xor-ed with a key of the row that
+  // keeps the reads below free of bank conflicts: K-contiguous, where 16 lanes read one chunk of 16 rows, the
+  // row's low three bits; K-strided, where 32 lanes read a pair of chunks of rows r .. r + 3 and r + 8 .. r + 11,
+  // its bits 1 and 3 (above the bit within the pair).  Rows past the matrix are its last row again, panels its
+  // last panel.
   const int lrow = lane / 8;
-  auto src = [&](const uint16_t* base, int64_t ld, bool tr, int group, int o0, int rows, int cols) {
-    if (!tr) {     // rows of the tile are output rows, 64 k each
-      const int r = group * 8 + lrow;
-      const int c = (lane % 8) ^ (r & 7);
-      const int row = o0 + r < rows ? o0 + r : rows - 1;
-      return base + static_cast<int64_t>(row) * ld + c * 8;
-    }
-    const int r = group % 8 * 8 + lrow;               // k within the step
-    const int c = (lane % 8) ^ (r & 7);
-    const int col = o0 + group / 8 * 64 + c * 8;
-    return base + static_cast<int64_t>(r) * ld + (col < cols ? col : 0);
-  };
-  const uint16_t* ga[LA];
-  const uint16_t* gb[LB];
+  int ljob = (blockIdx.x % 8) * per + blockIdx.x / 8;   // job, step and pair of terms of the next loads
+  int lleft = 0, lk = 0, lseg = 0;
+  const unsigned char *la = nullptr, *lb = nullptr;
+  uint32_t oa[LA], ob[LB];
+  auto offsets = [&](const Operand& o, bool tr, int o0, auto& off) {
 #pragma unroll
-  for (int i = 0; i < LA; ++i) ga[i] = src(p.A, p.lda, ATR, i * kWavesN + w, m0, p.rows_a, p.cols_a);
-#pragma unroll
-  for (int i = 0; i < LB; ++i) gb[i] = src(p.B, p.ldb, BTR, i * kWavesN + w, n0, p.rows_b, p.cols_b);
-  const uint32_t as_a = lds_addr(&as[0][0]), bs_a = lds_addr(&bs[0][0]);
-
-  auto issue = [&](int step, int buf) {
-    int seg = 0, k = step;
-    if constexpr (SPLIT) {
-      seg = step / steps1;
-      k = step - seg * steps1;
-    }
-    const int64_t oa = (SPLIT ? kPairA[seg] * p.pa : 0) + static_cast<int64_t>(k) * kBK * (ATR ? p.lda : 1);
-    const int64_t ob = (SPLIT ? kPairB[seg] * p.pb : 0) + static_cast<int64_t>(k) * kBK * (BTR ? p.ldb : 1);
-#pragma unroll
-    for (int i = 0; i < LA; ++i) {
-      const uint16_t* a = ga[i] + oa;
-      if constexpr (ATR) {   // k rows past the matrix (the last step of a piece): its last row again
-        const int r = k * kBK + (i * kWavesN + w) % 8 * 8 + lrow;
-        if (r >= p.rows_a) a -= static_cast<int64_t>(r - (p.rows_a - 1)) * p.lda;
+    for (int i = 0; i < static_cast<int>(sizeof(off) / sizeof(off[0])); ++i) {
+      const int r = (i * kW + w) * 8 + lrow;
+      if (!tr) {
+        off[i] = static_cast<uint32_t>((o0 + r < o.rows ? r : o.rows - 1 - o0) * o.row) + ((lane % 8) ^ lrow) * 16;
+      } else {
+        off[i] = static_cast<uint32_t>(r % 64 * o.row) + ((lane % 8) ^ ((r & 2) | (r & 8) / 2)) * 16;
       }
-      dma16(a, as_a + buf * BM * kRow + (i * kWavesN + w) * 1024);
     }
-#pragma unroll
-    for (int i = 0; i < LB; ++i) dma16(gb[i] + ob, bs_a + buf * BN * kRow + (i * kWavesN + w) * 1024);
+  };
+  Job lj{};
+  auto start_load = [&]() {   // the next job with steps, if there is one; else the last loads are repeated
+    while (ljob < job_end) {
+      const Job j = job_at(ljob);
+      if (j.steps > 0) {
+        lj = j;
+        lleft = j.steps;
+        lseg = SPLIT ? j.begin / steps1 : 0;
+        lk = j.begin - lseg * steps1;
+        offsets(p.A, ATR, j.m0, oa);
+        offsets(p.B, BTR, j.n0, ob);
+        la = p.A.p + (ATR ? 0 : j.m0 * p.A.row);
+        lb = p.B.p + (BTR ? 0 : j.n0 * p.B.row);
+        return;
+      }
+      ljob += stride;
+    }
+  };
+  const uint32_t as_a = lds_addr(&as[0][0]), bs_a = lds_addr(&bs[0][0]);
+  // load i of a step into buffer `buf`
+  auto load_a = [&](int i, int buf) {
+    const unsigned char* a = la + lk * p.A.step + (SPLIT ? kPairA[lseg] * p.A.term : 0);
+    uint32_t o = oa[i];
+    if constexpr (ATR) {
+      const int plane = lj.m0 / 64 + i * kW / 8;
+      a += (plane < p.A.planes ? plane : p.A.planes - 1) * p.A.plane;
+      if ((lk + 1) * kBK > p.A.rows) {   // k rows past the matrix: its last row again
+        const int over = lk * kBK + (i * kW + w) % 8 * 8 + lrow - (p.A.rows - 1);
+        if (over > 0) o -= static_cast<uint32_t>(over * p.A.row);
+      }
+    }
+    dma16(a, o, as_a + buf * kA + (i * kW + w) * 1024);
+  };
+  auto load_b = [&](int i, int buf) {
+    const unsigned char* b = lb + lk * p.B.step + (SPLIT ? kPairB[lseg] * p.B.term : 0);
+    if constexpr (BTR) {
+      const int plane = lj.n0 / 64 + i * kW / 8;
+      b += (plane < p.B.planes ? plane : p.B.planes - 1) * p.B.plane;
+    }
+    dma16(b, ob[i], bs_a + buf * kB + (i * kW + w) * 1024);
+  };
+  auto load_one = [&](int i, int buf) {
+    if (i < LA) load_a(i < LA ? i : 0, buf);
+    else load_b(i - LA < LB ? i - LA : 0, buf);
+  };
+  auto loaded = [&]() {   // after a step's last load
+    if (lleft > 1) {
+      --lleft;
+      if (++lk == steps1) {
+        lk = 0;
+        ++lseg;
+      }
+    } else if (ljob < job_end) {
+      ljob += stride;
+      start_load();
+    }
   };
 
-  auto frag = [&](const unsigned char* base, bool tr, int t16, int ks) -> bf16x8 {
-    if (!tr) {
-      const int r = t16 * 16 + lane % 16;
-      const int c = ks * 4 + lane / 16;
-      return *reinterpret_cast<const bf16x8*>(base + r * kRow + ((c ^ (r & 7)) << 4));
-    }
-    // in each 16-lane group, lane j receives element j of the four 16-element rows its lanes point at
-    const int j = lane % 16;
-    const int col = t16 * 16 + j % 4 * 4;
-    const unsigned char* plane = base + col / 64 * kPlane;
+  // ---- fragments.  K-strided: in each 16-lane group, lane j receives element j of the four 16-element rows
+  // that its lanes point at.
+  uint32_t fa_at[2], fb_at[2];   // by k half
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = lane % 16;
+    const uint32_t kc = r * kRow + (((h * 4 + lane / 16) ^ (r & 7)) << 4);
+    const int j = lane % 16, tr = lane / 16 * 8 + j / 4;
+    const uint32_t ks = (h * 32 + tr) * kRow + (((j % 4 / 2) ^ ((tr & 2) | (tr & 8) / 2)) << 4) + j % 2 * 8;
+    fa_at[h] = as_a + (ATR ? ks + wm * (TM / 4) * kPlane : kc + wm * TM * 16 * kRow);
+    fb_at[h] = bs_a + (BTR ? ks + wn * (TN / 4) * kPlane : kc + wn * TN * 16 * kRow);
+  }
+  auto frag = [&](uint32_t at, bool tr, int t) -> bf16x8 {
+    if (!tr) return lds_at<bf16x8>(at + t * 16 * kRow);
     u32x4_t f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int r = ks * 32 + lane / 16 * 8 + h * 4 + j / 4;
-      const unsigned char* at = plane + r * kRow + (((col % 64 / 8) ^ (r & 7)) << 4) + col % 8 * 2;
+      const uint32_t addr = (at ^ (t % 4 * 32)) + t / 4 * kPlane + h * 4 * kRow;
       const u32x2_t v = __builtin_bit_cast(
-          u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(const_cast<unsigned char*>(at))));
+          u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)static_cast<uintptr_t>(addr)));
       f[2 * h] = v[0];
       f[2 * h + 1] = v[1];
     }
     return __builtin_bit_cast(bf16x8, f);
   };
-
   f32x4_t acc[TM][TN];
+  bf16x8 fa[2][TM], fb[2][TN];
+  auto read_one = [&](int q, uint32_t at_a, uint32_t at_b, int set) {
+    if (q < TN) fb[set][q < TN ? q : 0] = frag(at_b, BTR, q < TN ? q : 0);
+    else fa[set][q - TN < TM ? q - TN : 0] = frag(at_a, ATR, q - TN < TM ? q - TN : 0);
+  };
+  auto multiply_row = [&](int i, int set) {
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < TN; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[set][i], fb[set][j], acc[i][j], 0, 0, 0);
+  };
 
-  if (steps > 0) issue(0, 0);
-  for (int s = 0; s < steps; ++s) {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  // ---- Two LDS buffers, two sets of fragments.  A step's second half is read while its first half is
+  // multiplied; between the halves every wave has read all of the step's buffer, so one barrier there frees it
+  // for the loads two steps ahead and publishes the next step's, whose first half is then read while the
+  // second half is multiplied.  Reads and loads are spread between the multiplications: all waves at once
+  // would queue for the LDS with the matrix cores idle.
+  start_load();
+  if (lleft > 0) {   // (no steps at all where no token counts: the tiles are then stored as zeros)
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+      for (int q = 0; q < LA + LB; ++q) load_one(q, b);
+      loaded();
+    }
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LA + LB) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (s + 1 < steps) issue(s + 1, (s + 1) & 1);
-    const unsigned char* a = as[s & 1];
-    const unsigned char* b = bs[s & 1];
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      bf16x8 fa[TM], fb[TN];
-#pragma unroll
-      for (int i = 0; i < TM; ++i) fa[i] = frag(a, ATR, wm * TM + i, ks);
-#pragma unroll
-      for (int j = 0; j < TN; ++j) fb[j] = frag(b, BTR, wn * TN + j, ks);
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-    }
   }
-
-  // accumulator e of tile (i, j): row m = m0 + (wm TM + i) 16 + 4 (lane / 16) + e, column n = n0 + (wn TN + j) 16 + lane % 16
-  const int mrow = m0 + wm * TM * 16 + lane / 16 * 4;
-  const int ncol = n0 + wn * TN * 16 + lane % 16;
-  if constexpr (EPI == kLogits) {
+  int buf = 0;
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int n = ncol + j * 16;
-      const int y = p.tgt[n] - p.v0;   // padded tokens have target -1
-      float mx = -__builtin_inff();
+  for (int q = 0; q < TM + TN; ++q) read_one(q, fa_at[0], fb_at[0], 0);
+  for (int job = (blockIdx.x % 8) * per + blockIdx.x / 8; job < job_end; job += stride) {
+    const Job cur = job_at(job);
+    const int m0 = cur.m0, n0 = cur.n0, slice = cur.slice;
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int m = mrow + i * 16 + e;
-          if (m < p.M) mx = __builtin_fmaxf(mx, acc[i][j][e]);
-          if (m == y && n < count) p.tlogit[n] = acc[i][j][e];
-        }
-      mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16, 64));
-      mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32, 64));
-      const float ref = mx == -__builtin_inff() ? 0.f : mx;
-      float s = 0.f;
+      for (int j = 0; j < TN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < cur.steps; ++s, buf ^= 1) {
+      fence_schedule();
+      {
+        const uint32_t at_a = fa_at[1] + buf * kA, at_b = fb_at[1] + buf * kB;
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
+        for (int i = 0; i < TM; ++i) {
+          multiply_row(i, 0);
+          fence_schedule();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int m = mrow + i * 16 + e;
-          if (m < p.M) s += __builtin_amdgcn_exp2f((acc[i][j][e] - ref) * kLog2e);
-        }
-      s += __shfl_xor(s, 16, 64);
-      s += __shfl_xor(s, 32, 64);
-      if (lane < 16) p.part[(static_cast<int64_t>(m0 / BM) * WM + wm) * p.tok_cap + n] = float2{mx, s};
-    }
-  } else if constexpr (EPI == kGradLogits) {
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int n = ncol + j * 16;
-      const bool on = n < count;
-      const int y = p.tgt[n] - p.v0;
-      const float lse = p.lse[n], gl = p.gl[n], g = p.g[n];
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        float d[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int m = mrow + i * 16 + e;
-          const float v = __builtin_amdgcn_exp2f((acc[i][j][e] - lse) * kLog2e) * gl - (m == y ? g : 0.f);
-          d[e] = on && m < p.M ? v : 0.f;
-        }
-        uint16_t* const to = p.dl + n * p.ldl + mrow + i * 16;
-        if constexpr (SPLIT) {
-          uint16_t t[4][kTerms];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) split3(d[e], t[e]);
-#pragma unroll
-          for (int k = 0; k < kTerms; ++k)
-            *reinterpret_cast<u32x2_t*>(to + k * p.pdl) =
-                u32x2_t{t[0][k] | static_cast<uint32_t>(t[1][k]) << 16, t[2][k] | static_cast<uint32_t>(t[3][k]) << 16};
-        } else {
-          *reinterpret_cast<u32x2_t*>(to) = u32x2_t{pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3])};
+          for (int q = i * RR; q < (i + 1) * RR && q < TM + TN; ++q) read_one(q, at_a, at_b, 1);
+          fence_schedule();
         }
       }
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      fence_schedule();
+      {
+        const uint32_t at_a = fa_at[0] + (buf ^ 1) * kA, at_b = fb_at[0] + (buf ^ 1) * kB;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          multiply_row(i, 1);
+          fence_schedule();
+#pragma unroll
+          for (int q = i * LR; q < (i + 1) * LR && q < LA + LB; ++q) load_one(q, buf);
+#pragma unroll
+          for (int q = i * RR; q < (i + 1) * RR && q < TM + TN; ++q) read_one(q, at_a, at_b, 0);
+          fence_schedule();
+        }
+      }
+      loaded();
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int n = ncol + j * 16;
-      if (EPI == kGradX ? n >= count : n >= p.N) continue;
-      const int64_t row = EPI == kGradX ? static_cast<int64_t>(p.rows[n]) : n;
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const int m = mrow + i * 16;
-        if (m >= p.M) continue;
-        float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-        if constexpr (EPI == kGradX) {
-          if (!p.first) {
-            float o[4];
-            load_row<4>(p.dxacc + n * p.ldx + m, o);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += o[e];
+
+    // accumulator e of tile (i, j): row m = m0 + (wm TM + i) 16 + 4 (lane / 16) + e, column n = n0 + (wn TN + j) 16 + lane % 16
+    const int mrow = m0 + wm * TM * 16 + lane / 16 * 4;
+    const int ncol = n0 + wn * TN * 16 + lane % 16;
+    if constexpr (EPI == kLogits) {
+  #pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int n = ncol + j * 16;
+        const int y = p.tgt[n] - p.v0;   // padded tokens have target -1
+        float mx = -__builtin_inff();
+  #pragma unroll
+        for (int i = 0; i < TM; ++i)
+  #pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int m = mrow + i * 16 + e;
+            if (m < p.M) mx = __builtin_fmaxf(mx, acc[i][j][e]);
+            if (m == y && n < count) p.tlogit[n] = acc[i][j][e];
           }
-          if (!p.last) {
-            store_row<4>(p.dxacc + n * p.ldx + m, v);
-            continue;
+        mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16, 64));
+        mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32, 64));
+        const float ref = mx == -__builtin_inff() ? 0.f : mx;
+        float s = 0.f;
+  #pragma unroll
+        for (int i = 0; i < TM; ++i)
+  #pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int m = mrow + i * 16 + e;
+            if (m < p.M) s += __builtin_amdgcn_exp2f((acc[i][j][e] - ref) * kLog2e);
+          }
+        s += __shfl_xor(s, 16, 64);
+        s += __shfl_xor(s, 32, 64);
+        if (lane < 16) p.part[(static_cast<int64_t>(m0 / BM) * WM + wm) * p.tok_cap + n] = float2{mx, s};
+      }
+    } else if constexpr (EPI == kGradLogits) {
+  #pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int n = ncol + j * 16;
+        const bool on = n < count;
+        const int y = p.tgt[n] - p.v0;
+        const float lse = p.lse[n], gl = p.gl[n], g = p.g[n];
+  #pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          float d[4];
+  #pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int m = mrow + i * 16 + e;
+            const float v = __builtin_amdgcn_exp2f((acc[i][j][e] - lse) * kLog2e) * gl - (m == y ? g : 0.f);
+            d[e] = on && m < p.M ? v : 0.f;
+          }
+          uint16_t* const to = p.dl + ((mrow + i * 16) / 64 * (p.tok_cap + kSkew) + n) * 64 + (mrow + i * 16) % 64;
+          if constexpr (SPLIT) {
+            uint16_t t[4][kTerms];
+  #pragma unroll
+            for (int e = 0; e < 4; ++e) split3(d[e], t[e]);
+  #pragma unroll
+            for (int k = 0; k < kTerms; ++k)
+              *reinterpret_cast<u32x2_t*>(to + k * p.pdl) =
+                  u32x2_t{t[0][k] | static_cast<uint32_t>(t[1][k]) << 16, t[2][k] | static_cast<uint32_t>(t[3][k]) << 16};
+          } else {
+            *reinterpret_cast<u32x2_t*>(to) = u32x2_t{pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3])};
           }
         }
-        const int64_t at = row * p.dim + m;
-        auto put = [&](auto* to) {
-          using T = std::remove_reference_t<decltype(*to)>;
-          if (p.vec) {   // dim and the pointer allow four elements at once; m is a multiple of 4
-            if (EPI == kGradW && p.accumulate) {
+      }
+    } else {
+  #pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int n = ncol + j * 16;
+        if (EPI == kGradX ? n >= count : n >= p.N) continue;
+        const int64_t row = EPI == kGradX ? static_cast<int64_t>(p.rows[n]) : n;
+  #pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          const int m = mrow + i * 16;
+          if (m >= p.M) continue;
+          float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+          if (p.sums != nullptr) {
+            float* const to = p.sums + slice * p.slice_elems + n * p.lds + m;
+            if (!p.first) {
               float o[4];
               load_row<4>(to, o);
-#pragma unroll
+  #pragma unroll
               for (int e = 0; e < 4; ++e) v[e] += o[e];
             }
             store_row<4>(to, v);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (m + e < p.M) to[e] = narrow<T>(EPI == kGradW && p.accumulate ? v[e] + widen(to[e]) : v[e]);
+            continue;
           }
-        };
-        if (SPLIT || p.out_f32) put(static_cast<float*>(p.out) + at);
-        else put(static_cast<uint16_t*>(p.out) + at);
+          const int64_t at = row * p.dim + m;
+          auto put = [&](auto* to) {
+            using T = std::remove_reference_t<decltype(*to)>;
+            if (p.vec) {   // dim and the pointer allow four elements at once; m is a multiple of 4
+              if (EPI == kGradW && p.accumulate) {
+                float o[4];
+                load_row<4>(to, o);
+  #pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] += o[e];
+              }
+              store_row<4>(to, v);
+            } else {
+  #pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (m + e < p.M) to[e] = narrow<T>(EPI == kGradW && p.accumulate ? v[e] + widen(to[e]) : v[e]);
+            }
+          };
+          if (SPLIT || p.out_f32) put(static_cast<float*>(p.out) + at);
+          else put(static_cast<uint16_t*>(p.out) + at);
+        }
       }
     }
   }
+  // the last loads may still be on their way into this workgroup's LDS
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 // -------------------------------------------------------------------------------------- around the products
@@ -342,11 +463,13 @@ struct PrepParams {
   int id_bytes;
   int64_t ignore, vocab, tokens, dim, dpad, tok_cap;
   const void* x;
-  uint16_t* xc;            // [terms][tok_cap][dpad]
+  int vec;                 // x is read 16 bytes at a time
+  uint16_t* xc;            // panels [term][dpad / 64][tok_cap][64]
+  int* tally;              // counted tokens of each group of kGroup, or null: counted again where needed
   int* count;
   int* rows;
   int* tgt;
-  int per;                 // tokens of a workgroup
+  int per;                 // tokens of a workgroup (64 at most)
   int work_blocks;         // workgroups with tokens; the ones after them pad
   // forward
   float* loss;
@@ -362,8 +485,70 @@ struct PrepParams {
 };
 
 constexpr int kPadBlocks = 16;
+constexpr int kGroup = 4096;
 
-// Which tokens count, in order, and their x as the products read it: rows padded to a multiple of 64 with
+__device__ __forceinline__ bool token_counts(const PrepParams& p, int64_t t) {
+  const int64_t y = id_at(p.targets, p.id_bytes, t);
+  return y >= 0 && y < p.vocab && y != p.ignore;
+}
+
+// the sum of every thread's n over the workgroup of 256
+__device__ __forceinline__ int block_count(int n, int* red) {
+#pragma unroll
+  for (int step = 1; step < kLanes; step *= 2) n += __shfl_xor(n, step, kLanes);
+  if (threadIdx.x % kLanes == 0) red[threadIdx.x / kLanes] = n;
+  __syncthreads();
+  return red[0] + red[1] + red[2] + red[3];
+}
+
+__global__ __launch_bounds__(256) void tally_kernel(PrepParams p) {
+  __shared__ int red[4];
+  const int64_t lo = static_cast<int64_t>(blockIdx.x) * kGroup;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kGroup / 256; ++i) {
+    const int64_t t = lo + i * 256 + threadIdx.x;
+    n += t < p.tokens && token_counts(p, t);
+  }
+  n = block_count(n, red);
+  if (threadIdx.x == 0) p.tally[blockIdx.x] = n;
+}
+
+// 8 elements of a row, laid out: bf16 as it is, fp32 as three terms; past the row's end zeros
+template <typename T>
+__device__ __forceinline__ void lay_out(const T* row, int64_t col, int64_t dim, bool vec, uint16_t* to, int64_t term) {
+  if constexpr (sizeof(T) == 2) {
+    u32x4_t v = {0, 0, 0, 0};
+    if (vec && col + 8 <= dim) {
+      v = *reinterpret_cast<const u32x4_t*>(row + col);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (col + e < dim) v[e / 2] |= static_cast<uint32_t>(row[col + e]) << (e % 2 * 16);
+    }
+    *reinterpret_cast<u32x4_t*>(to) = v;
+  } else {
+    float f[8];
+    if (vec && col + 8 <= dim) {
+      load_row<8>(row + col, f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = col + e < dim ? row[col + e] : 0.f;
+    }
+    uint16_t t[8][kTerms];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) split3(f[e], t[e]);
+#pragma unroll
+    for (int k = 0; k < kTerms; ++k) {
+      u32x4_t v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = t[2 * e][k] | static_cast<uint32_t>(t[2 * e + 1][k]) << 16;
+      *reinterpret_cast<u32x4_t*>(to + k * term) = v;
+    }
+  }
+}
+
+// Which tokens count, in order, and their x as the products read it: in panels of 64 columns, padded with
 // zeros, fp32 as three bf16 terms; after the last one, zero rows up to the end of its tile of 256.
 template <typename T>
 __global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
@@ -371,33 +556,22 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
   const int wave = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
   const bool pad = static_cast<int>(blockIdx.x) >= p.work_blocks;
   const int64_t lo = pad ? p.tokens : static_cast<int64_t>(blockIdx.x) * p.per;
-  auto counts = [&](int64_t t) {
-    const int64_t y = id_at(p.targets, p.id_bytes, t);
-    return y >= 0 && y < p.vocab && y != p.ignore;
-  };
   int before = 0;
-  for (int64_t t = threadIdx.x; t < lo; t += 256) before += counts(t);
-#pragma unroll
-  for (int step = 1; step < kLanes; step *= 2) before += __shfl_xor(before, step, kLanes);
-  if (lane == 0) red[wave] = before;
-  __syncthreads();
-  before = red[0] + red[1] + red[2] + red[3];
+  int64_t from = 0;
+  if (p.tally != nullptr) {
+    const int groups = static_cast<int>(lo / kGroup);
+    for (int g = threadIdx.x; g < groups; g += 256) before += p.tally[g];
+    from = static_cast<int64_t>(groups) * kGroup;
+  }
+#pragma unroll 4
+  for (int64_t t = from + threadIdx.x; t < lo; t += 256) before += token_counts(p, t);
+  before = block_count(before, red);
 
-  constexpr int kT = sizeof(T) == 4 ? kTerms : 1;
-  const int64_t plane = p.tok_cap * p.dpad;
+  const int64_t term = (p.tok_cap + kSkew) * p.dpad;
   auto put = [&](int64_t i, int64_t t, bool real) {
-    uint16_t* to = p.xc + i * p.dpad;
-    const T* from = static_cast<const T*>(p.x) + t * p.dim;
-    for (int c = lane; c < p.dpad; c += kLanes) {
-      if constexpr (kT == 1) {
-        to[c] = real && c < p.dim ? from[c] : 0;
-      } else {
-        uint16_t s[kTerms] = {0, 0, 0};
-        if (real && c < p.dim) split3(from[c], s);
-#pragma unroll
-        for (int k = 0; k < kTerms; ++k) to[k * plane + c] = s[k];
-      }
-    }
+    const T* row = static_cast<const T*>(p.x) + t * p.dim;
+    for (int64_t c = lane * 8; c < p.dpad; c += kLanes * 8)
+      lay_out<T>(row, c, real ? p.dim : 0, p.vec != 0, p.xc + (c / 64 * (p.tok_cap + kSkew) + i) * 64 + c % 64, term);
   };
   if (pad) {
     if (blockIdx.x == static_cast<unsigned>(p.work_blocks) && threadIdx.x == 0) *p.count = before;
@@ -413,8 +587,8 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
     return;
   }
   const int64_t hi = lo + p.per < p.tokens ? lo + p.per : p.tokens;
-  // per <= 64: lane l of every wave looks at token lo + l
-  const bool mine = lo + lane < hi && counts(lo + lane);
+  // lane l of every wave looks at token lo + l
+  const bool mine = lo + lane < hi && token_counts(p, lo + lane);
   const uint64_t mask = __ballot(mine);
   for (int64_t t = lo + wave; t < hi; t += 4) {
     const int l = static_cast<int>(t - lo);
@@ -439,23 +613,15 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
   }
 }
 
-// rows of the weight as the products read them (width not a multiple of 64, or fp32)
+// rows of the weight as the products read them (width not a multiple of 64, or fp32), in panels
+// [term][dpad / 64][rows][64]: 32 rows a workgroup
 template <typename T>
-__global__ __launch_bounds__(256) void weight_kernel(const T* w, uint16_t* to, int64_t rows, int64_t dim, int64_t dpad) {
-  constexpr int kT = sizeof(T) == 4 ? kTerms : 1;
-  const int wave = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + wave;
+__global__ __launch_bounds__(256) void weight_kernel(const T* w, uint16_t* to, int64_t rows, int64_t dim, int64_t dpad,
+                                                     int vec) {
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x / 8;
   if (r >= rows) return;
-  for (int64_t c = lane; c < dpad; c += kLanes) {
-    if constexpr (kT == 1) {
-      to[r * dpad + c] = c < dim ? w[r * dim + c] : 0;
-    } else {
-      uint16_t s[kTerms] = {0, 0, 0};
-      if (c < dim) split3(w[r * dim + c], s);
-#pragma unroll
-      for (int k = 0; k < kTerms; ++k) to[(k * rows + r) * dpad + c] = s[k];
-    }
-  }
+  for (int64_t c = threadIdx.x % 8 * 8; c < dpad; c += 64)
+    lay_out<T>(w + r * dim, c, dim, vec != 0, to + (c / 64 * (rows + kSkew) + r) * 64 + c % 64, (rows + kSkew) * dpad);
 }
 
 // Joins the tiles' (maximum, sum) of a piece with those of the pieces before it; after the last piece, the
@@ -502,16 +668,91 @@ __global__ __launch_bounds__(256) void join_kernel(JoinParams p) {
   p.loss[p.rows[n]] = lse - p.tlogit[n];
 }
 
+// The slices' sums, added in order, to where they belong: dx (token rows) or dW (added to what is there on
+// request).  A wave takes a row of the output.
+struct SumParams {
+  const float* sums;
+  int slices;
+  int64_t slice_elems, lds;
+  int n;                   // rows of the sums; with count: the compacted tokens instead
+  const int* count;
+  const int* rows;         // compacted -> token (dx), or null
+  void* out;
+  int64_t dim;
+  int accumulate, vec;
+};
+
+template <typename T>
+__global__ __launch_bounds__(256) void sum_kernel(SumParams p) {
+  const int wave = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+  const int n = blockIdx.x * 4 + wave;
+  if (n >= (p.count != nullptr ? *p.count : p.n)) return;
+  T* const out = static_cast<T*>(p.out) + (p.rows != nullptr ? p.rows[n] : n) * p.dim;
+  for (int64_t m = lane * 4; m < p.dim; m += kLanes * 4) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < p.slices; ++k) {
+      float o[4];
+      load_row<4>(p.sums + k * p.slice_elems + n * p.lds + m, o);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += o[e];
+    }
+    if (p.vec) {
+      if (p.accumulate) {
+        float o[4];
+        load_row<4>(out + m, o);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += o[e];
+      }
+      store_row<4>(out + m, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (m + e < p.dim) out[m + e] = narrow<T>(p.accumulate ? v[e] + widen(out[m + e]) : v[e]);
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------------------------- host side
 constexpr size_t up256(size_t b) { return (b + 255) / 256 * 256; }
-constexpr int64_t kPieceBytes = int64_t{512} << 20;   // of G, or of the weight as the products read it
+constexpr int64_t kPieceBytes = (int64_t{1} << 30) + (int64_t{1} << 27);   // of G, or of the weight as the products read it
+constexpr int kCUs = 256;
+
+// How a product is cut: 256 x 256 tiles, one to a CU, or 128 x 128, two to a CU; and the slices of its k.
+struct Cut {
+  bool big;
+  int slices;
+};
+
+// Time in units of one 128 x 128 tile on a CU of its own.
+Cut cut(int64_t m, int64_t n, int64_t steps, bool sliced) {
+  const int64_t big = ((m + 255) / 256) * ((n + 255) / 256), small = ((m + 127) / 128) * ((n + 127) / 128);
+  Cut best{false, 1};
+  double least = 0;
+  for (int b = 0; b < 2; ++b) {
+    const int64_t tiles = b ? big : small, slots = b ? kCUs : 2 * kCUs;
+    // enough slices to fill the chip, of eight steps at least
+    int64_t s = sliced ? slots / tiles : 1;
+    if (s > steps / 8) s = steps / 8;
+    if (s > 16) s = 16;
+    if (s < 1) s = 1;
+    const int64_t rounds = (tiles * s + slots - 1) / slots;
+    const double time = static_cast<double>(rounds) * (b ? 4.0 : 2.0 * 1.25) / static_cast<double>(s);
+    if (b == 0 || time < least) {
+      least = time;
+      best = {b == 1, static_cast<int>(s)};
+    }
+  }
+  return best;
+}
 
 struct XentPlan {
   bool copy_w;             // the weight needs a laid-out copy
   int terms;
   int64_t dpad, tok_cap, piece;    // piece: vocabulary rows, a multiple of 256
   int pieces;
-  size_t off_count, off_rows, off_tgt, off_a, off_b, off_c, off_xc, off_part, off_w, off_dl, off_dx, bytes;
+  Cut logits, gx, gw;
+  bool sum_x, sum_w;       // sums in the workspace, joined afterwards
+  size_t off_count, off_rows, off_tgt, off_a, off_b, off_c, off_xc, off_tally, off_part, off_w, off_dl, off_sx, off_sw, bytes;
 };
 
 XentPlan xent_plan(const XentArgs& a, bool grad) {
@@ -529,6 +770,15 @@ XentPlan xent_plan(const XentArgs& a, bool grad) {
   if (n.piece < 256) n.piece = 256;
   if (n.piece > vpad) n.piece = vpad;
   n.pieces = static_cast<int>((a.vocab + n.piece - 1) / n.piece);
+  n.piece = ((a.vocab + n.pieces - 1) / n.pieces + 255) / 256 * 256;   // pieces of equal size
+  n.pieces = static_cast<int>((a.vocab + n.piece - 1) / n.piece);
+  const int64_t per_step = a.io ? kBK : kBK / kPairs;   // k per step
+  const int64_t tok = a.tokens > 0 ? a.tokens : 1;
+  n.logits = cut(n.piece < a.vocab ? n.piece : a.vocab, tok, n.dpad / per_step, false);
+  n.gx = cut(a.dim, tok, n.piece / per_step, true);
+  n.gw = cut(a.dim, n.piece < a.vocab ? n.piece : a.vocab, tok / per_step, true);
+  n.sum_x = n.gx.slices > 1 || n.pieces > 1;
+  n.sum_w = n.gw.slices > 1;
   size_t at = 0;
   auto take = [&](size_t b) { const size_t o = at; at += up256(b); return o; };
   const size_t tc = static_cast<size_t>(n.tok_cap);
@@ -538,29 +788,40 @@ XentPlan xent_plan(const XentArgs& a, bool grad) {
   n.off_a = take(tc * 4);
   n.off_b = take(tc * (grad ? 4 : 8));
   n.off_c = take(tc * 4);
-  n.off_xc = take(tc * n.dpad * 2 * n.terms);
-  n.off_w = take(n.copy_w ? size_t(n.piece) * n.dpad * 2 * n.terms : 0);
+  n.off_xc = take((tc + kSkew) * n.dpad * 2 * n.terms);
+  n.off_tally = take((tc + kGroup - 1) / kGroup * 4);
+  n.off_w = take(n.copy_w ? size_t(n.piece + kSkew) * n.dpad * 2 * n.terms : 0);
   n.off_part = take(grad ? 0 : size_t(n.piece) / 64 * tc * 8);
-  n.off_dl = take(grad ? tc * n.piece * 2 * n.terms : 0);
-  n.off_dx = take(grad && n.pieces > 1 ? tc * n.dpad * 4 : 0);
+  n.off_dl = take(grad ? (tc + kSkew) * n.piece * 2 * n.terms : 0);
+  n.off_sx = take(grad && n.sum_x ? tc * n.dpad * 4 * n.gx.slices : 0);
+  n.off_sw = take(grad && n.sum_w ? size_t(n.piece) * n.dpad * 4 * n.gw.slices : 0);
   n.bytes = at;
   return n;
 }
 
 template <int BM, int BN, int WM, int WN, bool ATR, bool BTR, bool SPLIT, int EPI>
-hipError_t product(ProductParams p, hipStream_t stream) {
-  p.tiles_m = (p.M + BM - 1) / BM;
-  p.tiles_n = (p.N + BN - 1) / BN;
-  const int total = p.tiles_m * p.tiles_n;
+hipError_t product(const ProductParams& p, int per_cu, hipStream_t stream) {
+  const int64_t total = int64_t{(p.M + BM - 1) / BM} * ((p.N + BN - 1) / BN) * p.slices;
   if (total == 0) return hipSuccess;
+  const int64_t want = (total + 7) / 8 * 8, most = int64_t{kCUs} * per_cu;
   product_kernel<BM, BN, WM, WN, ATR, BTR, SPLIT, EPI>
-      <<<dim3(static_cast<unsigned>((total + 7) / 8 * 8)), WM * WN * 64, 0, stream>>>(p);
+      <<<dim3(static_cast<unsigned>(want < most ? want : most)), WM * WN * 64, 0, stream>>>(p);
   return hipGetLastError();
 }
 
+constexpr int kPartBig = 128, kPartSmall = 64;   // vocabulary rows of a partial sum: a wave's share of a tile
+
 template <bool ATR, bool BTR, bool SPLIT, int EPI>
-hipError_t product_any(const ProductParams& p, hipStream_t stream) {
-  return product<128, 128, 2, 2, ATR, BTR, SPLIT, EPI>(p, stream);
+hipError_t product_any(const Cut& c, ProductParams p, hipStream_t stream) {
+  p.slices = c.slices;
+  return c.big ? product<256, 256, 2, 4, ATR, BTR, SPLIT, EPI>(p, 1, stream)
+               : product<128, 128, 2, 2, ATR, BTR, SPLIT, EPI>(p, 2, stream);
+}
+
+template <typename T> hipError_t sum_slices(const SumParams& p, int64_t rows, hipStream_t stream) {
+  if (rows == 0) return hipSuccess;
+  sum_kernel<T><<<dim3(static_cast<unsigned>((rows + 3) / 4)), 256, 0, stream>>>(p);
+  return hipGetLastError();
 }
 
 template <typename T> hipError_t prep(const XentArgs& a, const XentPlan& n, unsigned char* ws, bool grad, hipStream_t stream) {
@@ -583,25 +844,50 @@ template <typename T> hipError_t prep(const XentArgs& a, const XentPlan& n, unsi
   } else {
     p.loss = a.loss; p.lse_out = a.lse;
   }
+  p.vec = a.dim % (16 / sizeof(T)) == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
+  // a few thousand tokens are counted again by every workgroup; more are counted group by group first
+  if (a.tokens > 2 * kGroup) {
+    p.tally = reinterpret_cast<int*>(ws + n.off_tally);
+    tally_kernel<<<dim3(static_cast<unsigned>((a.tokens + kGroup - 1) / kGroup)), 256, 0, stream>>>(p);
+  }
   prep_kernel<T><<<dim3(static_cast<unsigned>(p.work_blocks + kPadBlocks)), 256, 0, stream>>>(p);
   return hipGetLastError();
 }
 
-// the piece's rows of the weight as an operand
+// a matrix in panels of 64 columns, [panel][rows][64], one or three of them
+Operand panels(const void* p, int64_t rows, int64_t cols, bool k_strided) {
+  Operand o{};
+  o.p = static_cast<const unsigned char*>(p);
+  o.row = kRow;
+  o.plane = (rows + kSkew) * kRow;
+  o.step = k_strided ? kBK * int64_t{kRow} : o.plane;
+  o.term = o.plane * (cols / 64);
+  o.rows = static_cast<int>(rows);
+  o.planes = static_cast<int>(cols / 64);
+  return o;
+}
+
+// the piece's rows of the weight, laid out first where they cannot be read in place
 template <typename T>
-hipError_t weight_operand(const XentArgs& a, const XentPlan& n, unsigned char* ws, int64_t v0, int64_t rows,
-                          ProductParams* p, hipStream_t stream) {
-  p->A = static_cast<const uint16_t*>(a.weight) + v0 * a.dim;
-  p->lda = n.dpad;
-  p->pa = rows * n.dpad;
-  p->rows_a = static_cast<int>(rows);
-  p->cols_a = static_cast<int>(n.dpad);
+hipError_t lay_out_weight(const XentArgs& a, const XentPlan& n, unsigned char* ws, int64_t v0, int64_t rows,
+                          hipStream_t stream) {
   if (!n.copy_w) return hipSuccess;
-  uint16_t* to = reinterpret_cast<uint16_t*>(ws + n.off_w);
-  weight_kernel<T><<<dim3(static_cast<unsigned>((rows + 3) / 4)), 256, 0, stream>>>(
-      static_cast<const T*>(a.weight) + v0 * a.dim, to, rows, a.dim, n.dpad);
-  p->A = to;
+  const int vec = a.dim % (16 / sizeof(T)) == 0 && reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
+  weight_kernel<T><<<dim3(static_cast<unsigned>((rows + 31) / 32)), 256, 0, stream>>>(
+      static_cast<const T*>(a.weight) + v0 * a.dim, reinterpret_cast<uint16_t*>(ws + n.off_w), rows, a.dim, n.dpad, vec);
   return hipGetLastError();
+}
+
+Operand weight_operand(const XentArgs& a, const XentPlan& n, unsigned char* ws, int64_t v0, int64_t rows, bool k_strided) {
+  if (n.copy_w) return panels(ws + n.off_w, rows, n.dpad, k_strided);
+  Operand o{};
+  o.p = static_cast<const unsigned char*>(a.weight) + v0 * a.dim * 2;
+  o.row = a.dim * 2;
+  o.step = k_strided ? kBK * a.dim * 2 : kRow;
+  o.plane = kRow;
+  o.rows = static_cast<int>(rows);
+  o.planes = static_cast<int>(a.dim / 64);
+  return o;
 }
 
 template <typename T> hipError_t xent_fwd_t(const XentArgs& a, hipStream_t stream) {
@@ -612,11 +898,10 @@ template <typename T> hipError_t xent_fwd_t(const XentArgs& a, hipStream_t strea
   for (int k = 0; k < n.pieces && e == hipSuccess; ++k) {
     const int64_t v0 = k * n.piece, rows = v0 + n.piece < a.vocab ? n.piece : a.vocab - v0;
     ProductParams p{};
-    e = weight_operand<T>(a, n, ws, v0, rows, &p, stream);
+    e = lay_out_weight<T>(a, n, ws, v0, rows, stream);
     if (e != hipSuccess) return e;
-    p.B = reinterpret_cast<uint16_t*>(ws + n.off_xc);
-    p.ldb = n.dpad; p.pb = n.tok_cap * n.dpad;
-    p.rows_b = static_cast<int>(n.tok_cap); p.cols_b = static_cast<int>(n.dpad);
+    p.A = weight_operand(a, n, ws, v0, rows, false);
+    p.B = panels(ws + n.off_xc, n.tok_cap, n.dpad, false);
     p.M = static_cast<int>(rows); p.N = static_cast<int>(n.tok_cap); p.K = static_cast<int>(n.dpad);
     p.n_is_tokens = 1;
     p.count = reinterpret_cast<int*>(ws + n.off_count);
@@ -625,10 +910,10 @@ template <typename T> hipError_t xent_fwd_t(const XentArgs& a, hipStream_t strea
     p.part = reinterpret_cast<float2*>(ws + n.off_part);
     p.tok_cap = n.tok_cap;
     p.tlogit = reinterpret_cast<float*>(ws + n.off_a);
-    e = product_any<false, false, kSplit, kLogits>(p, stream);
+    e = product_any<false, false, kSplit, kLogits>(n.logits, p, stream);
     if (e != hipSuccess) return e;
     JoinParams j{};
-    j.part = p.part; j.tiles = static_cast<int>((rows + 127) / 128 * 2); j.first = k == 0; j.last = k + 1 == n.pieces;
+    j.part = p.part; j.tiles = static_cast<int>(n.logits.big ? (rows + 255) / 256 * (256 / kPartBig) : (rows + 127) / 128 * (128 / kPartSmall)); j.first = k == 0; j.last = k + 1 == n.pieces;
     j.tok_cap = n.tok_cap; j.count = p.count; j.rows = reinterpret_cast<int*>(ws + n.off_rows);
     j.run = reinterpret_cast<float2*>(ws + n.off_b); j.tlogit = p.tlogit; j.loss = a.loss; j.lse = a.lse;
     join_kernel<<<dim3(static_cast<unsigned>((a.tokens + 15) / 16)), 256, 0, stream>>>(j);
@@ -646,15 +931,13 @@ template <typename T> hipError_t xent_bwd_t(const XentArgs& a, hipStream_t strea
     const int64_t v0 = k * n.piece, rows = v0 + n.piece < a.vocab ? n.piece : a.vocab - v0;
     const int64_t rpad = (rows + 255) / 256 * 256;
     ProductParams p{};
-    e = weight_operand<T>(a, n, ws, v0, rows, &p, stream);
+    e = lay_out_weight<T>(a, n, ws, v0, rows, stream);
     if (e != hipSuccess) return e;
-    const ProductParams w = p;
-    uint16_t* const xc = reinterpret_cast<uint16_t*>(ws + n.off_xc);
     uint16_t* const dl = reinterpret_cast<uint16_t*>(ws + n.off_dl);
     p.count = reinterpret_cast<int*>(ws + n.off_count);
-    // G of the piece, [token][rpad]
-    p.B = xc; p.ldb = n.dpad; p.pb = n.tok_cap * n.dpad;
-    p.rows_b = static_cast<int>(n.tok_cap); p.cols_b = static_cast<int>(n.dpad);
+    // G of the piece
+    p.A = weight_operand(a, n, ws, v0, rows, false);
+    p.B = panels(ws + n.off_xc, n.tok_cap, n.dpad, false);
     p.M = static_cast<int>(rows); p.N = static_cast<int>(n.tok_cap); p.K = static_cast<int>(n.dpad);
     p.n_is_tokens = 1;
     p.tgt = reinterpret_cast<int*>(ws + n.off_tgt);
@@ -662,39 +945,57 @@ template <typename T> hipError_t xent_bwd_t(const XentArgs& a, hipStream_t strea
     p.lse = reinterpret_cast<float*>(ws + n.off_a);
     p.gl = reinterpret_cast<float*>(ws + n.off_b);
     p.g = reinterpret_cast<float*>(ws + n.off_c);
-    p.dl = dl; p.ldl = rpad; p.pdl = n.tok_cap * rpad;
+    p.dl = dl; p.pdl = (n.tok_cap + kSkew) * rpad;
     p.tok_cap = n.tok_cap;
-    e = product_any<false, false, kSplit, kGradLogits>(p, stream);
+    e = product_any<false, false, kSplit, kGradLogits>(n.logits, p, stream);
     if (e != hipSuccess) return e;
     if (a.dx != nullptr) {     // dx += G W: m = width, n = token, k = vocabulary
-      ProductParams q = w;
+      ProductParams q{};
       q.count = p.count;
-      q.B = dl; q.ldb = rpad; q.pb = p.pdl;
-      q.rows_b = static_cast<int>(n.tok_cap); q.cols_b = static_cast<int>(rpad);
+      q.A = weight_operand(a, n, ws, v0, rows, true);
+      q.B = panels(dl, n.tok_cap, rpad, false);
       q.M = static_cast<int>(a.dim); q.N = static_cast<int>(n.tok_cap); q.K = static_cast<int>((rows + 63) / 64 * 64);
       q.n_is_tokens = 1;
-      q.dxacc = reinterpret_cast<float*>(ws + n.off_dx); q.ldx = n.dpad;
-      q.first = k == 0; q.last = k + 1 == n.pieces;
+      q.first = k == 0;
       q.rows = reinterpret_cast<int*>(ws + n.off_rows);
       q.out = a.dx; q.dim = a.dim; q.out_f32 = kSplit;
       q.vec = a.dim % 4 == 0 && reinterpret_cast<uintptr_t>(a.dx) % (4 * sizeof(T)) == 0;
-      e = product_any<true, false, kSplit, kGradX>(q, stream);
+      if (n.sum_x) {
+        q.sums = reinterpret_cast<float*>(ws + n.off_sx);
+        q.lds = n.dpad; q.slice_elems = n.tok_cap * n.dpad;
+      }
+      e = product_any<true, false, kSplit, kGradX>(n.gx, q, stream);
+      if (e == hipSuccess && n.sum_x && k + 1 == n.pieces) {
+        SumParams t{};
+        t.sums = q.sums; t.slices = n.gx.slices; t.slice_elems = q.slice_elems; t.lds = q.lds; t.count = q.count;
+        t.rows = q.rows; t.out = a.dx; t.dim = a.dim; t.vec = q.vec;
+        e = sum_slices<T>(t, a.tokens, stream);
+      }
       if (e != hipSuccess) return e;
     }
     if (a.dweight != nullptr) {   // dW of the piece = G^T x: m = width, n = vocabulary row, k = token
       ProductParams q{};
       const size_t gs = a.grad_io ? sizeof(T) : 4;
       q.count = p.count;
-      q.A = xc; q.lda = n.dpad; q.pa = n.tok_cap * n.dpad;
-      q.rows_a = static_cast<int>(n.tok_cap); q.cols_a = static_cast<int>(n.dpad);
-      q.B = dl; q.ldb = rpad; q.pb = p.pdl;
-      q.rows_b = static_cast<int>(n.tok_cap); q.cols_b = static_cast<int>(rpad);
+      q.A = panels(ws + n.off_xc, n.tok_cap, n.dpad, true);
+      q.B = panels(dl, n.tok_cap, rpad, true);
       q.M = static_cast<int>(a.dim); q.N = static_cast<int>(rows);
       q.k_is_tokens = 1;
       q.out = static_cast<unsigned char*>(a.dweight) + v0 * a.dim * gs;
       q.dim = a.dim; q.out_f32 = gs == 4; q.accumulate = a.accumulate;
       q.vec = a.dim % 4 == 0 && reinterpret_cast<uintptr_t>(a.dweight) % (4 * gs) == 0;
-      e = product_any<true, true, kSplit, kGradW>(q, stream);
+      q.first = 1;
+      if (n.sum_w) {
+        q.sums = reinterpret_cast<float*>(ws + n.off_sw);
+        q.lds = n.dpad; q.slice_elems = n.piece * n.dpad;
+      }
+      e = product_any<true, true, kSplit, kGradW>(n.gw, q, stream);
+      if (e == hipSuccess && n.sum_w) {
+        SumParams t{};
+        t.sums = q.sums; t.slices = n.gw.slices; t.slice_elems = q.slice_elems; t.lds = q.lds;
+        t.n = static_cast<int>(rows); t.out = q.out; t.dim = a.dim; t.accumulate = q.accumulate; t.vec = q.vec;
+        e = q.out_f32 ? sum_slices<float>(t, rows, stream) : sum_slices<uint16_t>(t, rows, stream);
+      }
     }
   }
   return e;
