@@ -584,9 +584,10 @@ size_t mssm_norm_bwd_workspace_size(const mssm_norm_desc* desc);
  * weight of a dim that is a multiple of 64 must be 16-byte aligned (it is read
  * in place; any other weight is laid out piece by piece in the workspace
  * first), other pointers element-aligned.  workspace: at least the bytes the
- * size queries ask, 256-byte aligned; it holds the counted tokens' x, and
- * pieces of at most about 512 MiB (256 vocabulary rows at least) of partial
- * sums, of G and of the laid-out weight.  Other rules as mssm_selective_scan_fwd. */
+ * size queries ask, 256-byte aligned; it holds the counted tokens' x, a piece
+ * of at most about 896 MiB (but 256 vocabulary rows at least) of G or partial
+ * sums and laid-out weight, up to 128 MiB of sums over parts of k, and where
+ * the vocabulary takes several pieces dx in fp32.  Other rules as mssm_selective_scan_fwd. */
 typedef struct {
     int64_t tokens, vocab, dim;
     int64_t ignore_id;

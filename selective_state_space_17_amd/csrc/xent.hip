@@ -89,9 +89,9 @@ struct ProductParams {
   Operand A, B;
   int M, N;                // rows of the output on either side (what lies past them is not stored)
   int K;                   // multiple of 64; with k_is_tokens: the compacted count, rounded up, instead
-  int slices;              // workgroups that share a tile's k (kGradX, kGradW), each with sums of its own
   int k_is_tokens, n_is_tokens;
-  const int* count;        // compacted tokens
+  const int* plan;         // [0]: compacted tokens
+  int slices_at;           // where in plan the slices of the tiles of the last round stand; 0: not sliced
   // epilogues
   int v0;                  // first vocabulary row of this piece
   const int* tgt;          // compacted targets
@@ -103,9 +103,10 @@ struct ProductParams {
   const float* g;          // dloss
   uint16_t* dl;            // panels [vocabulary / 64][token][64], one or three terms
   int64_t pdl;             // elements between them
-  float* sums;             // [slices][n][lds]: sums over k slices and pieces, or null: straight to out
-  int64_t lds, slice_elems;
-  int first;               // of the pieces that share sums
+  float* sums;             // [job][BN][BM]: a slice's sums
+  float* over;             // [n][ld_over]: sums over pieces, or null
+  int64_t ld_over;
+  int first, last;         // of the pieces
   const int* rows;         // compacted -> token
   void* out;               // dx or dW
   int64_t dim;
@@ -113,6 +114,42 @@ struct ProductParams {
 };
 
 enum { kLogits = 0, kGradLogits = 1, kGradX = 2, kGradW = 3 };
+
+// Four neighbouring elements (m .. m + 3, of row n of the other side) of a product's output, to where they belong.
+template <bool SPLIT, int EPI>
+__device__ __forceinline__ void put_four(const ProductParams& p, int64_t row, int n, int m, float (&v)[4]) {
+  if (EPI == kGradX && p.over != nullptr) {
+    float* const to = p.over + n * p.ld_over + m;
+    if (!p.first) {
+      float o[4];
+      load_row<4>(to, o);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += o[e];
+    }
+    if (!p.last) {
+      store_row<4>(to, v);
+      return;
+    }
+  }
+  auto put = [&](auto* to) {
+    using T = std::remove_reference_t<decltype(*to)>;
+    if (p.vec) {   // dim and the pointer allow four elements at once; m is a multiple of 4
+      if (EPI == kGradW && p.accumulate) {
+        float o[4];
+        load_row<4>(to, o);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += o[e];
+      }
+      store_row<4>(to, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (m + e < p.M) to[e] = narrow<T>(EPI == kGradW && p.accumulate ? v[e] + widen(to[e]) : v[e]);
+    }
+  };
+  if (SPLIT || p.out_f32) put(static_cast<float*>(p.out) + row * p.dim + m);
+  else put(static_cast<uint16_t*>(p.out) + row * p.dim + m);
+}
 
 template <typename T> __device__ __forceinline__ T lds_at(uint32_t addr) {
   return *(__attribute__((address_space(3))) const T*)static_cast<uintptr_t>(addr);
@@ -139,33 +176,48 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
   const int lane = threadIdx.x % kLanes;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
   const int wm = w / WN, wn = w % WN;
-  const int count = *p.count;
+  const int count = p.plan[0];
 
-  // Jobs: tiles x slices of k.  Workgroups b, b + 8, ... share an XCD and its L2: each XCD takes a contiguous
-  // range of an order that walks bands of 8 n-tiles, m outer, so that what runs on it at one time is a block
-  // of few m-tiles by 8 n-tiles.
+  // Jobs.  Whole tiles as long as every workgroup gets one; the tiles of the last, partial round are cut along
+  // k where that fills the chip, each slice with sums of its own that are added afterwards.  Workgroups b,
+  // b + 8, ... share an XCD and its L2: each XCD takes a contiguous range of an order that walks bands of 8
+  // n-tiles, m outer, so that what runs on it at one time is a block of few m-tiles by 8 n-tiles.
   const int tiles_m = (p.M + BM - 1) / BM;
   const int tiles_n = ((p.n_is_tokens ? count : p.N) + BN - 1) / BN;
-  const int tiles = tiles_m * tiles_n, total = tiles * p.slices;
-  const int per = (total + 7) / 8;
-  const int stride = gridDim.x / 8;
-  const int job_end = (blockIdx.x % 8 + 1) * per < total ? (blockIdx.x % 8 + 1) * per : total;
+  const int tiles = tiles_m * tiles_n;
+  const int whole = p.slices_at != 0 ? tiles / static_cast<int>(gridDim.x) * static_cast<int>(gridDim.x) : 0;
+  const int slices = p.slices_at != 0 ? p.plan[p.slices_at] : 1;
+  const int rest = tiles - whole, cut = rest * slices;
+  const int xcd = blockIdx.x % 8, stride = gridDim.x / 8;
+  const int whole8 = whole / 8, cut8 = (cut + 7) / 8;      // of an XCD
+  const int mine = cut - xcd * cut8 < cut8 ? cut - xcd * cut8 : cut8;
+  const int job_first = blockIdx.x / 8, job_end = whole8 + (mine > 0 ? mine : 0);
   const int steps1 = ((p.k_is_tokens ? count : p.K) + kBK - 1) / kBK;   // of one pair of terms
   const int all = SPLIT ? steps1 * kPairs : steps1;
   struct Job {
-    int m0, n0, slice, begin, steps;
+    int m0, n0, sum, begin, steps;   // sum: which sums, or -1
   };
-  auto job_at = [&](int job) {
+  auto job_at = [&](int i) {
     Job j;
-    j.slice = job / tiles;
-    const int tile = job - j.slice * tiles;
+    int tile;
+    if (i < whole8) {
+      tile = xcd * whole8 + i;
+      j.sum = -1;
+      j.begin = 0;
+      j.steps = all;
+    } else {
+      const int c = xcd * cut8 + i - whole8;
+      const int slice = c / rest;
+      tile = whole + c - slice * rest;
+      j.sum = slices > 1 ? c : -1;
+      j.begin = static_cast<int>(static_cast<int64_t>(all) * slice / slices);
+      j.steps = static_cast<int>(static_cast<int64_t>(all) * (slice + 1) / slices) - j.begin;
+    }
     const int band = tile / (tiles_m * 8);
     const int left = tiles_n - band * 8, wide = left < 8 ? left : 8;
     const int in_band = tile - band * tiles_m * 8;
     j.m0 = in_band / wide * BM;
     j.n0 = (band * 8 + in_band % wide) * BN;
-    j.begin = static_cast<int>(static_cast<int64_t>(all) * j.slice / p.slices);
-    j.steps = static_cast<int>(static_cast<int64_t>(all) * (j.slice + 1) / p.slices) - j.begin;
     return j;
   };
 
@@ -176,7 +228,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
   // its bits 1 and 3 (above the bit within the pair).  Rows past the matrix are its last row again, panels its
   // last panel.
   const int lrow = lane / 8;
-  int ljob = (blockIdx.x % 8) * per + blockIdx.x / 8;   // job, step and pair of terms of the next loads
+  int ljob = job_first;   // job, step and pair of terms of the next loads
   int lleft = 0, lk = 0, lseg = 0;
   const unsigned char *la = nullptr, *lb = nullptr;
   uint32_t oa[LA], ob[LB];
@@ -306,9 +358,9 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
   int buf = 0;
 #pragma unroll
   for (int q = 0; q < TM + TN; ++q) read_one(q, fa_at[0], fb_at[0], 0);
-  for (int job = (blockIdx.x % 8) * per + blockIdx.x / 8; job < job_end; job += stride) {
+  for (int job = job_first; job < job_end; job += stride) {
     const Job cur = job_at(job);
-    const int m0 = cur.m0, n0 = cur.n0, slice = cur.slice;
+    const int m0 = cur.m0, n0 = cur.n0;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -347,59 +399,66 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
     }
 
     // accumulator e of tile (i, j): row m = m0 + (wm TM + i) 16 + 4 (lane / 16) + e, column n = n0 + (wn TN + j) 16 + lane % 16
-    const int mrow = m0 + wm * TM * 16 + lane / 16 * 4;
+    const int wave_m = m0 + wm * TM * 16;
+    const int mrow = wave_m + lane / 16 * 4;
     const int ncol = n0 + wn * TN * 16 + lane % 16;
+    auto each = [&](int j, auto&& f) {   // accumulator = f(accumulator, row)
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = f(acc[i][j][e], mrow + i * 16 + e);
+    };
     if constexpr (EPI == kLogits) {
-  #pragma unroll
+#pragma unroll
       for (int j = 0; j < TN; ++j) {
         const int n = ncol + j * 16;
+        if (m0 + BM > p.M) each(j, [&](float a, int m) { return m < p.M ? a : -__builtin_inff(); });
         const int y = p.tgt[n] - p.v0;   // padded tokens have target -1
+        if (__ballot(y >= wave_m && y < wave_m + TM * 16) != 0)
+          each(j, [&](float a, int m) {
+            if (m == y) p.tlogit[n] = a;
+            return a;
+          });
         float mx = -__builtin_inff();
-  #pragma unroll
-        for (int i = 0; i < TM; ++i)
-  #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int m = mrow + i * 16 + e;
-            if (m < p.M) mx = __builtin_fmaxf(mx, acc[i][j][e]);
-            if (m == y && n < count) p.tlogit[n] = acc[i][j][e];
-          }
+        each(j, [&](float a, int) {
+          mx = __builtin_fmaxf(mx, a);
+          return a;
+        });
         mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16, 64));
         mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32, 64));
-        const float ref = mx == -__builtin_inff() ? 0.f : mx;
+        // exp(a - mx) = 2^(a log2e - c) 2^(c - mx log2e): one multiply-add an element, and the rounding of
+        // c = mx log2e taken out of the sum once
+        const float ref = mx == -__builtin_inff() ? 0.f : mx, c = ref * kLog2e;
         float s = 0.f;
-  #pragma unroll
-        for (int i = 0; i < TM; ++i)
-  #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int m = mrow + i * 16 + e;
-            if (m < p.M) s += __builtin_amdgcn_exp2f((acc[i][j][e] - ref) * kLog2e);
-          }
+        each(j, [&](float a, int) {
+          s += __builtin_amdgcn_exp2f(__builtin_fmaf(a, kLog2e, -c));
+          return a;
+        });
         s += __shfl_xor(s, 16, 64);
         s += __shfl_xor(s, 32, 64);
+        s *= __builtin_amdgcn_exp2f(__builtin_fmaf(-ref, kLog2e, c));
         if (lane < 16) p.part[(static_cast<int64_t>(m0 / BM) * WM + wm) * p.tok_cap + n] = float2{mx, s};
       }
     } else if constexpr (EPI == kGradLogits) {
-  #pragma unroll
+#pragma unroll
       for (int j = 0; j < TN; ++j) {
         const int n = ncol + j * 16;
-        const bool on = n < count;
+        const float lse = p.lse[n], g = p.g[n], c = lse * kLog2e;
+        const float gl = p.gl[n] * __builtin_amdgcn_exp2f(__builtin_fmaf(-lse, kLog2e, c));   // as in the forward pass
+        each(j, [&](float a, int) { return __builtin_amdgcn_exp2f(__builtin_fmaf(a, kLog2e, -c)) * gl; });
         const int y = p.tgt[n] - p.v0;
-        const float lse = p.lse[n], gl = p.gl[n], g = p.g[n];
-  #pragma unroll
+        if (__ballot(y >= wave_m && y < wave_m + TM * 16) != 0) each(j, [&](float a, int m) { return a - (m == y ? g : 0.f); });
+        if (m0 + BM > p.M || n0 + BN > count) each(j, [&](float a, int m) { return n < count && m < p.M ? a : 0.f; });
+#pragma unroll
         for (int i = 0; i < TM; ++i) {
-          float d[4];
-  #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int m = mrow + i * 16 + e;
-            const float v = __builtin_amdgcn_exp2f((acc[i][j][e] - lse) * kLog2e) * gl - (m == y ? g : 0.f);
-            d[e] = on && m < p.M ? v : 0.f;
-          }
-          uint16_t* const to = p.dl + ((mrow + i * 16) / 64 * (p.tok_cap + kSkew) + n) * 64 + (mrow + i * 16) % 64;
+          const f32x4_t d = acc[i][j];
+          const int m = mrow + i * 16;
+          uint16_t* const to = p.dl + (m / 64 * (p.tok_cap + kSkew) + n) * 64 + m % 64;
           if constexpr (SPLIT) {
             uint16_t t[4][kTerms];
-  #pragma unroll
+#pragma unroll
             for (int e = 0; e < 4; ++e) split3(d[e], t[e]);
-  #pragma unroll
+#pragma unroll
             for (int k = 0; k < kTerms; ++k)
               *reinterpret_cast<u32x2_t*>(to + k * p.pdl) =
                   u32x2_t{t[0][k] | static_cast<uint32_t>(t[1][k]) << 16, t[2][k] | static_cast<uint32_t>(t[3][k]) << 16};
@@ -409,52 +468,77 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
         }
       }
     } else {
-  #pragma unroll
+#pragma unroll
       for (int j = 0; j < TN; ++j) {
         const int n = ncol + j * 16;
+        if (cur.sum >= 0) {
+          float* const to = p.sums + (static_cast<int64_t>(cur.sum) * BN + n - n0) * BM + mrow - m0;
+#pragma unroll
+          for (int i = 0; i < TM; ++i) *reinterpret_cast<f32x4_t*>(to + i * 16) = acc[i][j];
+          continue;
+        }
         if (EPI == kGradX ? n >= count : n >= p.N) continue;
         const int64_t row = EPI == kGradX ? static_cast<int64_t>(p.rows[n]) : n;
-  #pragma unroll
+#pragma unroll
         for (int i = 0; i < TM; ++i) {
-          const int m = mrow + i * 16;
-          if (m >= p.M) continue;
           float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-          if (p.sums != nullptr) {
-            float* const to = p.sums + slice * p.slice_elems + n * p.lds + m;
-            if (!p.first) {
-              float o[4];
-              load_row<4>(to, o);
-  #pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] += o[e];
-            }
-            store_row<4>(to, v);
-            continue;
-          }
-          const int64_t at = row * p.dim + m;
-          auto put = [&](auto* to) {
-            using T = std::remove_reference_t<decltype(*to)>;
-            if (p.vec) {   // dim and the pointer allow four elements at once; m is a multiple of 4
-              if (EPI == kGradW && p.accumulate) {
-                float o[4];
-                load_row<4>(to, o);
-  #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] += o[e];
-              }
-              store_row<4>(to, v);
-            } else {
-  #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (m + e < p.M) to[e] = narrow<T>(EPI == kGradW && p.accumulate ? v[e] + widen(to[e]) : v[e]);
-            }
-          };
-          if (SPLIT || p.out_f32) put(static_cast<float*>(p.out) + at);
-          else put(static_cast<uint16_t*>(p.out) + at);
+          if (mrow + i * 16 < p.M) put_four<SPLIT, EPI>(p, row, n, mrow + i * 16, v);
         }
       }
     }
   }
   // the last loads may still be on their way into this workgroup's LDS
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// Adds the slices of the tiles of the last round, in order: workgroup (tile, share of its n).
+constexpr int kShares = 8;
+template <int BM, int BN, bool SPLIT, int EPI>
+__global__ __launch_bounds__(256) void sum_kernel(ProductParams p, int slots) {
+  const int count = p.plan[0], slices = p.plan[p.slices_at];
+  if (slices == 1) return;
+  const int tiles_m = (p.M + BM - 1) / BM;
+  const int tiles_n = ((p.n_is_tokens ? count : p.N) + BN - 1) / BN;
+  const int tiles = tiles_m * tiles_n, rest = tiles % slots;
+  const int t = blockIdx.x / kShares;
+  if (t >= rest) return;
+  const int tile = tiles - rest + t;
+  const int band = tile / (tiles_m * 8);
+  const int left = tiles_n - band * 8, wide = left < 8 ? left : 8;
+  const int in_band = tile - band * tiles_m * 8;
+  const int m = in_band / wide * BM + threadIdx.x % (BM / 4) * 4, n0 = (band * 8 + in_band % wide) * BN;
+  if (m >= p.M) return;
+  constexpr int kRows = BN / kShares, kAtOnce = 256 / (BM / 4);
+  const int first = blockIdx.x % kShares * kRows + threadIdx.x / (BM / 4);
+  for (int i = 0; i < kRows; i += kAtOnce) {
+    const int n = n0 + first + i;
+    if (n >= (EPI == kGradX ? count : p.N)) return;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = 0; s < slices; ++s) {
+      float o[4];
+      load_row<4>(p.sums + ((static_cast<int64_t>(s) * rest + t) * BN + first + i) * BM + threadIdx.x % (BM / 4) * 4, o);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += o[e];
+    }
+    put_four<SPLIT, EPI>(p, EPI == kGradX ? static_cast<int64_t>(p.rows[n]) : n, n, m, v);
+  }
+}
+
+// How many slices the tiles of the last round are cut into: the least time, in steps of a workgroup.  A slice
+// costs some four steps more (its start, its sums' way out) and the addition some eight.  At most two rounds
+// of slices, which bounds the sums' memory.
+__device__ int pick_slices(int tiles, int steps, int slots) {
+  const int rest = tiles % slots;
+  int best = 1, least = steps;
+  for (int s = 2; rest > 0 && rest * s <= 2 * slots && steps / s >= 4; ++s) {
+    const int time = (rest * s + slots - 1) / slots * ((steps + s - 1) / s + 4) + 8;
+    if (time < least) {
+      least = time;
+      best = s;
+    }
+  }
+  return best;
 }
 
 // -------------------------------------------------------------------------------------- around the products
@@ -466,7 +550,8 @@ struct PrepParams {
   int vec;                 // x is read 16 bytes at a time
   uint16_t* xc;            // panels [term][dpad / 64][tok_cap][64]
   int* tally;              // counted tokens of each group of kGroup, or null: counted again where needed
-  int* count;
+  int* plan;               // written: the count, and the slices of dx, of dW, of the last piece's dW
+  int pairs, steps_x, tile_x, tile_w, tiles_mx, tiles_w, tiles_w_last;
   int* rows;
   int* tgt;
   int per;                 // tokens of a workgroup (64 at most)
@@ -483,6 +568,10 @@ struct PrepParams {
   float* c_g;
   void* dx;                // nullable: rows of tokens left out are zeroed
 };
+
+constexpr int kCUs = 256;
+constexpr int kBig = 256, kSmall = 128;   // tiles: one workgroup to a CU, or two
+__host__ __device__ constexpr int slots_of(int tile) { return tile == kBig ? kCUs : 2 * kCUs; }
 
 constexpr int kPadBlocks = 16;
 constexpr int kGroup = 4096;
@@ -574,7 +663,15 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
       lay_out<T>(row, c, real ? p.dim : 0, p.vec != 0, p.xc + (c / 64 * (p.tok_cap + kSkew) + i) * 64 + c % 64, term);
   };
   if (pad) {
-    if (blockIdx.x == static_cast<unsigned>(p.work_blocks) && threadIdx.x == 0) *p.count = before;
+    if (blockIdx.x == static_cast<unsigned>(p.work_blocks) && threadIdx.x < 4) {
+      const int steps_w = (before + kBK - 1) / kBK * p.pairs;
+      const int tiles_x = p.tiles_mx * ((before + p.tile_x - 1) / p.tile_x);
+      p.plan[threadIdx.x] = threadIdx.x == 0   ? before
+                            : p.c_lse == nullptr ? 1
+                            : threadIdx.x == 1 ? pick_slices(tiles_x, p.steps_x, slots_of(p.tile_x))
+                            : threadIdx.x == 2 ? pick_slices(p.tiles_w, steps_w, slots_of(p.tile_w))
+                                               : pick_slices(p.tiles_w_last, steps_w, slots_of(p.tile_w));
+    }
     const int64_t end = (before + kTokTile - 1) / kTokTile * int64_t{kTokTile};
     for (int64_t i = before + (blockIdx.x - p.work_blocks) * 4 + wave; i < end; i += kPadBlocks * 4) {
       put(i, 0, false);
@@ -624,13 +721,12 @@ __global__ __launch_bounds__(256) void weight_kernel(const T* w, uint16_t* to, i
     lay_out<T>(w + r * dim, c, dim, vec != 0, to + (c / 64 * (rows + kSkew) + r) * 64 + c % 64, (rows + kSkew) * dpad);
 }
 
-// Joins the tiles' (maximum, sum) of a piece with those of the pieces before it; after the last piece, the
-// loss.  16 tokens x 16 shares of the tiles a workgroup.
+// Joins the tiles' (maximum, sum) of a piece with those of the pieces before it; after the last piece, the loss.
 struct JoinParams {
   const float2* part;
   int tiles, first, last;
   int64_t tok_cap;
-  const int* count;
+  const int* plan;
   const int* rows;
   float2* run;
   const float* tlogit;
@@ -645,19 +741,28 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
   return {m, a.y * __builtin_amdgcn_exp2f((a.x - ref) * kLog2e) + b.y * __builtin_amdgcn_exp2f((b.x - ref) * kLog2e)};
 }
 
+// TL tokens x 256 / TL shares of the tiles a workgroup: many tokens side by side, or many shares of a few.
+template <int TL>
 __global__ __launch_bounds__(256) void join_kernel(JoinParams p) {
-  __shared__ float2 red[16][17];
-  const int tl = threadIdx.x % 16, share = threadIdx.x / 16;
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * 16 + tl;
-  const int count = *p.count;
-  if (static_cast<int64_t>(blockIdx.x) * 16 >= count) return;
+  constexpr int kShareN = 256 / TL;
+  __shared__ float2 red[kShareN][TL + 1];
+  const int tl = threadIdx.x % TL, share = threadIdx.x / TL;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * TL + tl;
+  const int count = *p.plan;
+  if (static_cast<int64_t>(blockIdx.x) * TL >= count) return;
   float2 r = {-__builtin_inff(), 0.f};
-  if (n < count)
-    for (int k = share; k < p.tiles; k += 16) r = join(r, p.part[k * p.tok_cap + n]);
+  if (n < count) {
+#pragma unroll 4
+    for (int k = share; k < p.tiles; k += kShareN) r = join(r, p.part[k * p.tok_cap + n]);
+  }
   red[share][tl] = r;
   __syncthreads();
+  for (int step = kShareN / 2; step > 0; step /= 2) {
+    if (share < step) red[share][tl] = join(red[share][tl], red[share + step][tl]);
+    __syncthreads();
+  }
   if (share != 0 || n >= count) return;
-  for (int k = 1; k < 16; ++k) r = join(r, red[k][tl]);
+  r = red[0][tl];
   if (!p.first) r = join(p.run[n], r);
   if (!p.last) {
     p.run[n] = r;
@@ -668,81 +773,28 @@ __global__ __launch_bounds__(256) void join_kernel(JoinParams p) {
   p.loss[p.rows[n]] = lse - p.tlogit[n];
 }
 
-// The slices' sums, added in order, to where they belong: dx (token rows) or dW (added to what is there on
-// request).  A wave takes a row of the output.
-struct SumParams {
-  const float* sums;
-  int slices;
-  int64_t slice_elems, lds;
-  int n;                   // rows of the sums; with count: the compacted tokens instead
-  const int* count;
-  const int* rows;         // compacted -> token (dx), or null
-  void* out;
-  int64_t dim;
-  int accumulate, vec;
-};
-
-template <typename T>
-__global__ __launch_bounds__(256) void sum_kernel(SumParams p) {
-  const int wave = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
-  const int n = blockIdx.x * 4 + wave;
-  if (n >= (p.count != nullptr ? *p.count : p.n)) return;
-  T* const out = static_cast<T*>(p.out) + (p.rows != nullptr ? p.rows[n] : n) * p.dim;
-  for (int64_t m = lane * 4; m < p.dim; m += kLanes * 4) {
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < p.slices; ++k) {
-      float o[4];
-      load_row<4>(p.sums + k * p.slice_elems + n * p.lds + m, o);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += o[e];
-    }
-    if (p.vec) {
-      if (p.accumulate) {
-        float o[4];
-        load_row<4>(out + m, o);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += o[e];
-      }
-      store_row<4>(out + m, v);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (m + e < p.dim) out[m + e] = narrow<T>(p.accumulate ? v[e] + widen(out[m + e]) : v[e]);
-    }
-  }
-}
-
 // ---------------------------------------------------------------------------------------------- host side
 constexpr size_t up256(size_t b) { return (b + 255) / 256 * 256; }
-constexpr int64_t kPieceBytes = (int64_t{1} << 30) + (int64_t{1} << 27);   // of G, or of the weight as the products read it
-constexpr int kCUs = 256;
+constexpr int64_t kPieceBytes = int64_t{896} << 20;   // of a piece's G (or partial sums) and laid-out weight
 
-// How a product is cut: 256 x 256 tiles, one to a CU, or 128 x 128, two to a CU; and the slices of its k.
-struct Cut {
-  bool big;
-  int slices;
-};
+int64_t tiles_of(int64_t m, int64_t n, int tile) { return (m + tile - 1) / tile * ((n + tile - 1) / tile); }
 
-// Time in units of one 128 x 128 tile on a CU of its own.
-Cut cut(int64_t m, int64_t n, int64_t steps, bool sliced) {
-  const int64_t big = ((m + 255) / 256) * ((n + 255) / 256), small = ((m + 127) / 128) * ((n + 127) / 128);
-  Cut best{false, 1};
-  double least = 0;
-  for (int b = 0; b < 2; ++b) {
-    const int64_t tiles = b ? big : small, slots = b ? kCUs : 2 * kCUs;
-    // enough slices to fill the chip, of eight steps at least
-    int64_t s = sliced ? slots / tiles : 1;
-    if (s > steps / 8) s = steps / 8;
-    if (s > 16) s = 16;
-    if (s < 1) s = 1;
-    const int64_t rounds = (tiles * s + slots - 1) / slots;
-    const double time = static_cast<double>(rounds) * (b ? 4.0 : 2.0 * 1.25) / static_cast<double>(s);
-    if (b == 0 || time < least) {
-      least = time;
-      best = {b == 1, static_cast<int>(s)};
-    }
-  }
-  return best;
+// The tile of a product whose last round is sliced: the large one unless it is more than a quarter empty (the
+// small one takes 1.25 times as long for the same work: twice the loads and LDS reads a multiplication).
+int tile_sliced(int64_t m, int64_t n) { return 4 * tiles_of(m, n, kBig) <= 1.25 * tiles_of(m, n, kSmall) ? kBig : kSmall; }
+
+// The tile of a product that is not: the one that takes fewer rounds, in units of a large tile's.
+int tile_whole(int64_t m, int64_t n) {
+  const int64_t big = (tiles_of(m, n, kBig) + kCUs - 1) / kCUs, small = (tiles_of(m, n, kSmall) + 2 * kCUs - 1) / (2 * kCUs);
+  return static_cast<double>(big) <= 0.5 * 1.25 * static_cast<double>(small) ? kBig : kSmall;
+}
+
+// Most that the slices' sums of a product may take (see pick_slices): two rounds of slices of four steps or more.
+int64_t sums_bytes(int64_t tiles, int64_t steps, int tile) {
+  const int64_t most = 2 * int64_t{slots_of(tile)};
+  if (steps < 8) return 0;
+  const int64_t jobs = tiles < slots_of(tile) && tiles * (steps / 4) < most ? tiles * (steps / 4) : most;
+  return jobs * tile * tile * 4;
 }
 
 struct XentPlan {
@@ -750,9 +802,8 @@ struct XentPlan {
   int terms;
   int64_t dpad, tok_cap, piece;    // piece: vocabulary rows, a multiple of 256
   int pieces;
-  Cut logits, gx, gw;
-  bool sum_x, sum_w;       // sums in the workspace, joined afterwards
-  size_t off_count, off_rows, off_tgt, off_a, off_b, off_c, off_xc, off_tally, off_part, off_w, off_dl, off_sx, off_sw, bytes;
+  int logits, gx, gw;      // tiles
+  size_t off_plan, off_rows, off_tgt, off_a, off_b, off_c, off_xc, off_tally, off_part, off_w, off_dl, off_over, off_sums, bytes;
 };
 
 XentPlan xent_plan(const XentArgs& a, bool grad) {
@@ -765,24 +816,21 @@ XentPlan xent_plan(const XentArgs& a, bool grad) {
   int64_t row = 1;   // bytes a vocabulary row of a piece costs
   if (grad) row += n.tok_cap * 2 * n.terms;
   else row += n.tok_cap / 8;   // a partial of 8 bytes per 64 rows
-  if (n.copy_w && n.dpad * 2 * n.terms > row) row = n.dpad * 2 * n.terms;
+  if (n.copy_w) row += n.dpad * 2 * n.terms;
   n.piece = kPieceBytes / row / 256 * 256;
   if (n.piece < 256) n.piece = 256;
   if (n.piece > vpad) n.piece = vpad;
   n.pieces = static_cast<int>((a.vocab + n.piece - 1) / n.piece);
   n.piece = ((a.vocab + n.pieces - 1) / n.pieces + 255) / 256 * 256;   // pieces of equal size
   n.pieces = static_cast<int>((a.vocab + n.piece - 1) / n.piece);
-  const int64_t per_step = a.io ? kBK : kBK / kPairs;   // k per step
-  const int64_t tok = a.tokens > 0 ? a.tokens : 1;
-  n.logits = cut(n.piece < a.vocab ? n.piece : a.vocab, tok, n.dpad / per_step, false);
-  n.gx = cut(a.dim, tok, n.piece / per_step, true);
-  n.gw = cut(a.dim, n.piece < a.vocab ? n.piece : a.vocab, tok / per_step, true);
-  n.sum_x = n.gx.slices > 1 || n.pieces > 1;
-  n.sum_w = n.gw.slices > 1;
+  const int64_t tok = a.tokens > 0 ? a.tokens : 1, rows = n.piece < a.vocab ? n.piece : a.vocab;
+  n.logits = tile_whole(rows, tok);
+  n.gx = tile_sliced(a.dim, tok);
+  n.gw = tile_sliced(a.dim, rows);
   size_t at = 0;
   auto take = [&](size_t b) { const size_t o = at; at += up256(b); return o; };
   const size_t tc = static_cast<size_t>(n.tok_cap);
-  n.off_count = take(4);
+  n.off_plan = take(16);
   n.off_rows = take(tc * 4);
   n.off_tgt = take(tc * 4);
   n.off_a = take(tc * 4);
@@ -793,35 +841,34 @@ XentPlan xent_plan(const XentArgs& a, bool grad) {
   n.off_w = take(n.copy_w ? size_t(n.piece + kSkew) * n.dpad * 2 * n.terms : 0);
   n.off_part = take(grad ? 0 : size_t(n.piece) / 64 * tc * 8);
   n.off_dl = take(grad ? (tc + kSkew) * n.piece * 2 * n.terms : 0);
-  n.off_sx = take(grad && n.sum_x ? tc * n.dpad * 4 * n.gx.slices : 0);
-  n.off_sw = take(grad && n.sum_w ? size_t(n.piece) * n.dpad * 4 * n.gw.slices : 0);
+  n.off_over = take(grad && n.pieces > 1 ? tc * n.dpad * 4 : 0);
+  const int64_t pairs = a.io ? 1 : kPairs;
+  const int64_t sx = sums_bytes(tiles_of(a.dim, tok, n.gx), (rows + kBK - 1) / kBK * pairs, n.gx);
+  const int64_t sw = sums_bytes(tiles_of(a.dim, rows, n.gw), (tok + kBK - 1) / kBK * pairs, n.gw);
+  n.off_sums = take(grad ? static_cast<size_t>(sx > sw ? sx : sw) : 0);   // dx and dW in turn
   n.bytes = at;
   return n;
 }
 
-template <int BM, int BN, int WM, int WN, bool ATR, bool BTR, bool SPLIT, int EPI>
-hipError_t product(const ProductParams& p, int per_cu, hipStream_t stream) {
-  const int64_t total = int64_t{(p.M + BM - 1) / BM} * ((p.N + BN - 1) / BN) * p.slices;
-  if (total == 0) return hipSuccess;
-  const int64_t want = (total + 7) / 8 * 8, most = int64_t{kCUs} * per_cu;
-  product_kernel<BM, BN, WM, WN, ATR, BTR, SPLIT, EPI>
-      <<<dim3(static_cast<unsigned>(want < most ? want : most)), WM * WN * 64, 0, stream>>>(p);
+template <int BM, int WM, int WN, bool ATR, bool BTR, bool SPLIT, int EPI>
+hipError_t product(const ProductParams& p, hipStream_t stream) {
+  constexpr int kSlots = slots_of(BM);
+  const int64_t tiles = tiles_of(p.M, p.N, BM);
+  if (tiles == 0) return hipSuccess;
+  const int64_t want = p.slices_at != 0 ? kSlots : (tiles + 7) / 8 * 8;
+  product_kernel<BM, BM, WM, WN, ATR, BTR, SPLIT, EPI>
+      <<<dim3(static_cast<unsigned>(want < kSlots ? want : kSlots)), WM * WN * 64, 0, stream>>>(p);
+  if constexpr (EPI == kGradX || EPI == kGradW) {
+    const int64_t sliced = tiles < kSlots ? tiles : kSlots;
+    sum_kernel<BM, BM, SPLIT, EPI><<<dim3(static_cast<unsigned>(sliced * kShares)), 256, 0, stream>>>(p, kSlots);
+  }
   return hipGetLastError();
 }
-
-constexpr int kPartBig = 128, kPartSmall = 64;   // vocabulary rows of a partial sum: a wave's share of a tile
 
 template <bool ATR, bool BTR, bool SPLIT, int EPI>
-hipError_t product_any(const Cut& c, ProductParams p, hipStream_t stream) {
-  p.slices = c.slices;
-  return c.big ? product<256, 256, 2, 4, ATR, BTR, SPLIT, EPI>(p, 1, stream)
-               : product<128, 128, 2, 2, ATR, BTR, SPLIT, EPI>(p, 2, stream);
-}
-
-template <typename T> hipError_t sum_slices(const SumParams& p, int64_t rows, hipStream_t stream) {
-  if (rows == 0) return hipSuccess;
-  sum_kernel<T><<<dim3(static_cast<unsigned>((rows + 3) / 4)), 256, 0, stream>>>(p);
-  return hipGetLastError();
+hipError_t product_any(int tile, const ProductParams& p, hipStream_t stream) {
+  return tile == kBig ? product<kBig, 2, 4, ATR, BTR, SPLIT, EPI>(p, stream)
+                      : product<kSmall, 2, 2, ATR, BTR, SPLIT, EPI>(p, stream);
 }
 
 template <typename T> hipError_t prep(const XentArgs& a, const XentPlan& n, unsigned char* ws, bool grad, hipStream_t stream) {
@@ -829,7 +876,7 @@ template <typename T> hipError_t prep(const XentArgs& a, const XentPlan& n, unsi
   p.targets = a.targets; p.id_bytes = a.id_bytes; p.ignore = a.ignore; p.vocab = a.vocab; p.tokens = a.tokens;
   p.dim = a.dim; p.dpad = n.dpad; p.tok_cap = n.tok_cap; p.x = a.x;
   p.xc = reinterpret_cast<uint16_t*>(ws + n.off_xc);
-  p.count = reinterpret_cast<int*>(ws + n.off_count);
+  p.plan = reinterpret_cast<int*>(ws + n.off_plan);
   p.rows = reinterpret_cast<int*>(ws + n.off_rows);
   p.tgt = reinterpret_cast<int*>(ws + n.off_tgt);
   // about a thousand workgroups, of at most 64 tokens
@@ -837,6 +884,13 @@ template <typename T> hipError_t prep(const XentArgs& a, const XentPlan& n, unsi
   p.per = static_cast<int>(per < 1 ? 1 : per > 64 ? 64 : per);
   p.work_blocks = static_cast<int>((a.tokens + p.per - 1) / p.per);
   if (grad) {
+    const int64_t rows = n.piece < a.vocab ? n.piece : a.vocab, last = a.vocab - (n.pieces - 1) * n.piece;
+    p.pairs = a.io ? 1 : kPairs;
+    p.steps_x = static_cast<int>((rows + kBK - 1) / kBK) * p.pairs;
+    p.tile_x = n.gx; p.tile_w = n.gw;
+    p.tiles_mx = static_cast<int>((a.dim + n.gx - 1) / n.gx);
+    p.tiles_w = static_cast<int>(tiles_of(a.dim, rows, n.gw));
+    p.tiles_w_last = static_cast<int>(tiles_of(a.dim, last, n.gw));
     p.lse = a.lse_in; p.dloss = a.dloss; p.dlse = a.dlse; p.dx = a.dx;
     p.c_lse = reinterpret_cast<float*>(ws + n.off_a);
     p.c_gl = reinterpret_cast<float*>(ws + n.off_b);
@@ -904,7 +958,7 @@ template <typename T> hipError_t xent_fwd_t(const XentArgs& a, hipStream_t strea
     p.B = panels(ws + n.off_xc, n.tok_cap, n.dpad, false);
     p.M = static_cast<int>(rows); p.N = static_cast<int>(n.tok_cap); p.K = static_cast<int>(n.dpad);
     p.n_is_tokens = 1;
-    p.count = reinterpret_cast<int*>(ws + n.off_count);
+    p.plan = reinterpret_cast<int*>(ws + n.off_plan);
     p.tgt = reinterpret_cast<int*>(ws + n.off_tgt);
     p.v0 = static_cast<int>(v0);
     p.part = reinterpret_cast<float2*>(ws + n.off_part);
@@ -913,10 +967,11 @@ template <typename T> hipError_t xent_fwd_t(const XentArgs& a, hipStream_t strea
     e = product_any<false, false, kSplit, kLogits>(n.logits, p, stream);
     if (e != hipSuccess) return e;
     JoinParams j{};
-    j.part = p.part; j.tiles = static_cast<int>(n.logits.big ? (rows + 255) / 256 * (256 / kPartBig) : (rows + 127) / 128 * (128 / kPartSmall)); j.first = k == 0; j.last = k + 1 == n.pieces;
-    j.tok_cap = n.tok_cap; j.count = p.count; j.rows = reinterpret_cast<int*>(ws + n.off_rows);
+    j.part = p.part; j.tiles = static_cast<int>((rows + n.logits - 1) / n.logits * 2); j.first = k == 0; j.last = k + 1 == n.pieces;
+    j.tok_cap = n.tok_cap; j.plan = p.plan; j.rows = reinterpret_cast<int*>(ws + n.off_rows);
     j.run = reinterpret_cast<float2*>(ws + n.off_b); j.tlogit = p.tlogit; j.loss = a.loss; j.lse = a.lse;
-    join_kernel<<<dim3(static_cast<unsigned>((a.tokens + 15) / 16)), 256, 0, stream>>>(j);
+    if (a.tokens <= 512) join_kernel<2><<<dim3(static_cast<unsigned>((a.tokens + 1) / 2)), 256, 0, stream>>>(j);
+    else join_kernel<16><<<dim3(static_cast<unsigned>((a.tokens + 15) / 16)), 256, 0, stream>>>(j);
     e = hipGetLastError();
   }
   return e;
@@ -934,7 +989,7 @@ template <typename T> hipError_t xent_bwd_t(const XentArgs& a, hipStream_t strea
     e = lay_out_weight<T>(a, n, ws, v0, rows, stream);
     if (e != hipSuccess) return e;
     uint16_t* const dl = reinterpret_cast<uint16_t*>(ws + n.off_dl);
-    p.count = reinterpret_cast<int*>(ws + n.off_count);
+    p.plan = reinterpret_cast<int*>(ws + n.off_plan);
     // G of the piece
     p.A = weight_operand(a, n, ws, v0, rows, false);
     p.B = panels(ws + n.off_xc, n.tok_cap, n.dpad, false);
@@ -951,32 +1006,28 @@ template <typename T> hipError_t xent_bwd_t(const XentArgs& a, hipStream_t strea
     if (e != hipSuccess) return e;
     if (a.dx != nullptr) {     // dx += G W: m = width, n = token, k = vocabulary
       ProductParams q{};
-      q.count = p.count;
+      q.plan = p.plan;
       q.A = weight_operand(a, n, ws, v0, rows, true);
       q.B = panels(dl, n.tok_cap, rpad, false);
       q.M = static_cast<int>(a.dim); q.N = static_cast<int>(n.tok_cap); q.K = static_cast<int>((rows + 63) / 64 * 64);
       q.n_is_tokens = 1;
-      q.first = k == 0;
+      q.slices_at = 1;
+      q.first = k == 0; q.last = k + 1 == n.pieces;
       q.rows = reinterpret_cast<int*>(ws + n.off_rows);
       q.out = a.dx; q.dim = a.dim; q.out_f32 = kSplit;
       q.vec = a.dim % 4 == 0 && reinterpret_cast<uintptr_t>(a.dx) % (4 * sizeof(T)) == 0;
-      if (n.sum_x) {
-        q.sums = reinterpret_cast<float*>(ws + n.off_sx);
-        q.lds = n.dpad; q.slice_elems = n.tok_cap * n.dpad;
+      q.sums = reinterpret_cast<float*>(ws + n.off_sums);
+      if (n.pieces > 1) {
+        q.over = reinterpret_cast<float*>(ws + n.off_over);
+        q.ld_over = n.dpad;
       }
       e = product_any<true, false, kSplit, kGradX>(n.gx, q, stream);
-      if (e == hipSuccess && n.sum_x && k + 1 == n.pieces) {
-        SumParams t{};
-        t.sums = q.sums; t.slices = n.gx.slices; t.slice_elems = q.slice_elems; t.lds = q.lds; t.count = q.count;
-        t.rows = q.rows; t.out = a.dx; t.dim = a.dim; t.vec = q.vec;
-        e = sum_slices<T>(t, a.tokens, stream);
-      }
       if (e != hipSuccess) return e;
     }
     if (a.dweight != nullptr) {   // dW of the piece = G^T x: m = width, n = vocabulary row, k = token
       ProductParams q{};
       const size_t gs = a.grad_io ? sizeof(T) : 4;
-      q.count = p.count;
+      q.plan = p.plan;
       q.A = panels(ws + n.off_xc, n.tok_cap, n.dpad, true);
       q.B = panels(dl, n.tok_cap, rpad, true);
       q.M = static_cast<int>(a.dim); q.N = static_cast<int>(rows);
@@ -984,18 +1035,9 @@ template <typename T> hipError_t xent_bwd_t(const XentArgs& a, hipStream_t strea
       q.out = static_cast<unsigned char*>(a.dweight) + v0 * a.dim * gs;
       q.dim = a.dim; q.out_f32 = gs == 4; q.accumulate = a.accumulate;
       q.vec = a.dim % 4 == 0 && reinterpret_cast<uintptr_t>(a.dweight) % (4 * gs) == 0;
-      q.first = 1;
-      if (n.sum_w) {
-        q.sums = reinterpret_cast<float*>(ws + n.off_sw);
-        q.lds = n.dpad; q.slice_elems = n.piece * n.dpad;
-      }
+      q.slices_at = k + 1 == n.pieces ? 3 : 2;
+      q.sums = reinterpret_cast<float*>(ws + n.off_sums);
       e = product_any<true, true, kSplit, kGradW>(n.gw, q, stream);
-      if (e == hipSuccess && n.sum_w) {
-        SumParams t{};
-        t.sums = q.sums; t.slices = n.gw.slices; t.slice_elems = q.slice_elems; t.lds = q.lds;
-        t.n = static_cast<int>(rows); t.out = q.out; t.dim = a.dim; t.accumulate = q.accumulate; t.vec = q.vec;
-        e = q.out_f32 ? sum_slices<float>(t, rows, stream) : sum_slices<uint16_t>(t, rows, stream);
-      }
     }
   }
   return e;
