@@ -8,9 +8,10 @@
 // few ids very often, so a row of dW may be the sum of one token or of a tenth of the batch.  The tokens
 // are therefore sorted by id (a stable radix sort: equal ids keep their token order, so the sums are taken
 // in a fixed order and the result is the same on every run), and the sorted list is cut into slices of
-// equal length: a wave sums the runs of equal ids inside its slice, writes the rows of runs that lie wholly
-// inside, and leaves the sums of runs that cross a border in the workspace, where a second kernel adds
-// them slice by slice.  No atomics on data, no slice longer than another.
+// sixteen: a wave loads its slice's rows at once, sums the runs of equal ids, writes the rows of runs that lie
+// wholly inside, and leaves the sums of runs that cross a border in the workspace, where a second kernel adds
+// them in order.  No atomics on data, no slice longer than another.  The rows of ids that do not occur are
+// zeroed beforehand, by workgroups that run beside the sort.
 #include "device_util.h"
 #include "internal.h"
 
@@ -58,9 +59,141 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(EmbedParams p) {
   }
 }
 
-// ---------------------------------------------------------------------------------------- sort by id
+// ---------------------------------------------------------------------------------------- rows without a token
+template <typename G>
+__device__ __forceinline__ void zero_rows(G* p, int64_t n, int64_t block, int64_t blocks, int threads) {
+  constexpr int V = 16 / sizeof(G);
+  const float z[V] = {};
+  const int64_t step = blocks * threads * V;
+  const bool vec = reinterpret_cast<uintptr_t>(p) % 16 == 0;
+  for (int64_t i = (block * threads + threadIdx.x) * V; i < n; i += step) {
+    if (vec && i + V <= n) {
+      store_row<V>(p + i, z);
+    } else {
+      for (int64_t j = i; j < n && j < i + V; ++j) p[j] = 0;
+    }
+  }
+}
+
+template <typename G>
+__global__ __launch_bounds__(kThreads) void embed_zero_kernel(G* p, int64_t n) {
+  zero_rows<G>(p, n, blockIdx.x, gridDim.x, kThreads);
+}
+
+__device__ __forceinline__ uint32_t sort_key(const void* ids, int id_bytes, int64_t vocab, int64_t i) {
+  const int64_t id = id_at(ids, id_bytes, i);
+  return static_cast<uint32_t>(id < 0 || id > vocab ? vocab : id);
+}
+
+// ------------------------------------------------------------------------------- sort of up to 16384 by id
+// One workgroup sorts the whole list in LDS, while the others zero dW: a word holds key << 14 | token, four bits
+// of the key a pass, a thread keeps E consecutive words, so the order of equal digits is the input's.
+// 16384 tokens: four passes (50280 ids) hide behind the zeros of a table of 50280 x 768; by the passes over
+// memory below they took 45 us, and the zeros 13 us before them.
+constexpr int kLdsThreads = 1024, kTokenBits = 14, kLdsMost = 1 << kTokenBits, kDigitBits = 4, kDigits = 1 << kDigitBits;
+constexpr int kLdsWaves = kLdsThreads / kLanes;
+
+struct LdsSortParams {
+  const void* ids;
+  int id_bytes;
+  int64_t vocab;
+  int n, passes;
+  uint32_t* keys;
+  uint32_t* toks;
+  int64_t total;     // elements of dW to zero; 0: none
+};
+
+// inclusive prefix sum over the wave's lanes (16-bit halves side by side work too, if they do not overflow)
+__device__ __forceinline__ uint32_t wave_prefix(uint32_t v) {
+  const int lane = threadIdx.x % kLanes;
+#pragma unroll
+  for (int step = 1; step < kLanes; step *= 2) {
+    const uint32_t o = __shfl_up(v, step, kLanes);
+    v += lane >= step ? o : 0u;
+  }
+  return v;
+}
+
+template <typename G, int E>
+__global__ __launch_bounds__(kLdsThreads) void sort_lds_kernel(LdsSortParams p, G* dweight) {
+  __shared__ __attribute__((aligned(16))) uint32_t words[kLdsThreads * E];
+  __shared__ __attribute__((aligned(16))) uint16_t at[kLdsThreads][kDigits];   // where a thread's next word of each digit goes
+  __shared__ uint32_t sums[kDigits * kLdsWaves];
+  if (blockIdx.x > 0) {
+    zero_rows<G>(dweight, p.total, blockIdx.x - 1, gridDim.x - 1, kLdsThreads);
+    return;
+  }
+  const int tid = threadIdx.x, wave = tid / kLanes, lane = tid % kLanes;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int i = e * kLdsThreads + tid;   // (what lies past the end sorts last)
+    words[i] = i < p.n ? sort_key(p.ids, p.id_bytes, p.vocab, i) << kTokenBits | static_cast<uint32_t>(i) : ~0u;
+  }
+  __syncthreads();
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = kTokenBits + pass * kDigitBits;
+    uint32_t v[E];
+    int rank[E];
+    uint64_t cnt[2] = {0, 0};   // eight digits each, a byte a digit: at most E = 16
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      v[e] = words[tid * E + e];
+      const int d = v[e] >> shift & (kDigits - 1);
+      const uint64_t c = d < 8 ? cnt[0] : cnt[1];
+      rank[e] = static_cast<int>(c >> (d % 8 * 8) & 0xff);
+      const uint64_t one = uint64_t{1} << (d % 8 * 8);
+      cnt[0] += d < 8 ? one : 0;
+      cnt[1] += d < 8 ? 0 : one;
+    }
+    // prefix over the wave's threads, two digits to a word
+    uint32_t own[kDigits / 2], pre[kDigits / 2];
+#pragma unroll
+    for (int d = 0; d < kDigits / 2; ++d) {
+      const uint64_t c = cnt[d / 4] >> (d % 4 * 16);
+      own[d] = static_cast<uint32_t>(c & 0xff) | static_cast<uint32_t>(c >> 8 & 0xff) << 16;
+      pre[d] = wave_prefix(own[d]);
+      if (lane == kLanes - 1) {
+        sums[(2 * d) * kLdsWaves + wave] = pre[d] & 0xffff;
+        sums[(2 * d + 1) * kLdsWaves + wave] = pre[d] >> 16;
+      }
+    }
+    __syncthreads();
+    if (wave == 0) {   // prefix over (digit, wave), four to a lane
+      uint32_t q[4], s = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        q[k] = s;
+        s += sums[lane * 4 + k];
+      }
+      const uint32_t before = wave_prefix(s) - s;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sums[lane * 4 + k] = before + q[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int d = 0; d < kDigits / 2; ++d) {
+      const uint32_t ex = pre[d] - own[d];
+      at[tid][2 * d] = static_cast<uint16_t>(sums[(2 * d) * kLdsWaves + wave] + (ex & 0xffff));
+      at[tid][2 * d + 1] = static_cast<uint16_t>(sums[(2 * d + 1) * kLdsWaves + wave] + (ex >> 16));
+    }
+    // (each thread reads back its own line of `at`; all words are in registers since the first barrier)
+#pragma unroll
+    for (int e = 0; e < E; ++e) words[at[tid][v[e] >> shift & (kDigits - 1)] + rank[e]] = v[e];
+    __syncthreads();
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int i = e * kLdsThreads + tid;
+    if (i < p.n) {
+      p.keys[i] = words[i] >> kTokenBits;
+      p.toks[i] = words[i] & (kLdsMost - 1);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------- sort of any number by id
 // Least-significant-digit radix sort of (id, token) pairs, ids outside [0, vocab) sorted last as `vocab`.
-constexpr int kTile = 2048;                    // pairs per workgroup
+constexpr int kTile = 1024;                    // pairs per workgroup
 constexpr int kPerWave = kTile / kWaves;       // a wave's pairs are consecutive, so its order is the input's
 constexpr int kMaxDigits = 512;
 
@@ -77,9 +210,7 @@ struct SortParams {
 };
 
 __device__ __forceinline__ uint32_t key_at(const SortParams& p, int i) {
-  if (p.ids == nullptr) return p.keys[i];
-  const int64_t id = id_at(p.ids, p.id_bytes, i);
-  return static_cast<uint32_t>(id < 0 || id > p.vocab ? p.vocab : id);
+  return p.ids == nullptr ? p.keys[i] : sort_key(p.ids, p.id_bytes, p.vocab, i);
 }
 
 __global__ __launch_bounds__(kThreads) void sort_hist_kernel(SortParams p) {
@@ -172,6 +303,8 @@ __global__ __launch_bounds__(kThreads) void sort_scatter_kernel(SortParams p) {
 }
 
 // ------------------------------------------------------------------------------------------- gradient
+constexpr int kSlice = 16;
+
 struct EmbedGradParams {
   const uint32_t* keys;    // sorted
   const uint32_t* toks;
@@ -180,7 +313,7 @@ struct EmbedGradParams {
   float* part;             // [slices][2][dim]: the slice's first run if it began earlier; its last if it goes on
   float scale;
   int64_t dim;
-  int n, slice, slices;
+  int n, slices;
   uint32_t vocab;
   int accumulate;
 };
@@ -199,7 +332,7 @@ __device__ __forceinline__ void write_grad(G* row, const float (&acc)[V], float 
   store_row<V>(row, v);
 }
 
-// One wave: one slice of the sorted list x one chunk of 64 V columns.
+// One wave: one slice of the sorted list x one chunk of 64 V columns.  Lane i holds the slice's i-th key and token.
 template <typename T, typename G, int V>
 __global__ __launch_bounds__(kThreads) void embed_grad_kernel(EmbedGradParams p) {
   const int wave = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
@@ -207,29 +340,36 @@ __global__ __launch_bounds__(kThreads) void embed_grad_kernel(EmbedGradParams p)
   if (s >= p.slices) return;
   const int64_t col = (static_cast<int64_t>(blockIdx.y) * kLanes + lane) * V;
   const bool on = col < p.dim;
-  const int lo = static_cast<int>(s) * p.slice;
-  const int hi = lo + p.slice < p.n ? lo + p.slice : p.n;
-  const T* dout = static_cast<const T*>(p.dout);
+  const int lo = static_cast<int>(s) * kSlice;
+  // lanes 0 .. 15: the slice; 16: what follows it; 17: what stands before it (~0: nothing)
+  const int at = lane <= kSlice ? lo + lane : lo - 1;
+  const uint32_t key = lane <= kSlice + 1 && at >= 0 && at < p.n ? p.keys[at] : ~0u;
+  const uint32_t tok = lane < kSlice && at < p.n ? p.toks[at] : 0u;
+  const T* dout = static_cast<const T*>(p.dout) + (on ? col : 0);
+  float v[kSlice][V];
+#pragma unroll
+  for (int i = 0; i < kSlice; ++i) {
+    // (a token that is not to be counted is not read: its row may hold anything)
+    if (static_cast<uint32_t>(__builtin_amdgcn_readlane(key, i)) < p.vocab)
+      load_row<V>(dout + static_cast<int64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(tok, i))) * p.dim, v[i]);
+  }
   float acc[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  bool head = lo > 0 && p.keys[lo - 1] == p.keys[lo];
-  for (int i = lo; i < hi; ++i) {
-    const uint32_t key = p.keys[i];
-    if (key >= p.vocab) break;   // ids outside the table come last
-    if (on) {
-      float v[V];
-      load_row<V>(dout + static_cast<int64_t>(p.toks[i]) * p.dim + col, v);
+  for (int j = 0; j < V; ++j) acc[j] = 0.f;
+  bool head = __builtin_amdgcn_readlane(key, kSlice + 1) == __builtin_amdgcn_readlane(key, 0);
 #pragma unroll
-      for (int j = 0; j < V; ++j) acc[j] += v[j];
-    }
-    const bool last = i + 1 == p.n || p.keys[i + 1] != key;
-    if (last || i + 1 == hi) {
+  for (int i = 0; i < kSlice; ++i) {
+    const uint32_t k = __builtin_amdgcn_readlane(key, i);
+    if (k >= p.vocab) break;   // ids outside the table come last
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[j] += v[i][j];
+    const bool last = static_cast<uint32_t>(__builtin_amdgcn_readlane(key, i + 1)) != k;
+    if (last || i + 1 == kSlice) {
       if (on) {
         if (head || !last) {
           store_row<V>(p.part + (s * 2 + (head ? 0 : 1)) * p.dim + col, acc);
         } else {
-          write_grad<G, V>(static_cast<G*>(p.dweight) + key * p.dim + col, acc, p.scale, p.accumulate != 0);
+          write_grad<G, V>(static_cast<G*>(p.dweight) + k * p.dim + col, acc, p.scale, p.accumulate != 0);
         }
       }
       head = false;
@@ -239,43 +379,51 @@ __global__ __launch_bounds__(kThreads) void embed_grad_kernel(EmbedGradParams p)
   }
 }
 
-// Runs that cross slices: the wave of the slice where such a run begins adds its parts in order.
+// Runs that cross slices: the workgroup of the slice where such a run begins adds its parts, each wave a
+// quarter of them in order, the quarters in order.
 template <typename G, int V>
 __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedGradParams p) {
+  __shared__ float red[kWaves][kLanes * V];
   const int wave = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
-  const int64_t s = static_cast<int64_t>(blockIdx.x) * kWaves + wave;
+  const int64_t s = blockIdx.x;
   if (s + 1 >= p.slices) return;
-  const int lo = static_cast<int>(s) * p.slice, next = lo + p.slice;
+  const int lo = static_cast<int>(s) * kSlice, next = lo + kSlice;
   const uint32_t key = p.keys[next - 1];
   if (key >= p.vocab || p.keys[next] != key) return;        // nothing goes on past this slice
   if (lo > 0 && p.keys[lo - 1] == key) return;              // the run began in an earlier slice
+  // the last slice the run reaches into: its first key is still the run's
+  int64_t have = s + 1, not_in = p.slices;
+  while (not_in - have > 1) {
+    const int64_t mid = (have + not_in) / 2;
+    if (p.keys[mid * kSlice] == key) have = mid;
+    else not_in = mid;
+  }
+  const int parts = static_cast<int>(have - s) + 1;          // the first from the second half of its line
   const int64_t col = (static_cast<int64_t>(blockIdx.y) * kLanes + lane) * V;
-  if (col >= p.dim) return;
+  const bool on = col < p.dim;
+  const int quarter = (parts + kWaves - 1) / kWaves;
+  const int end = (wave + 1) * quarter < parts ? (wave + 1) * quarter : parts;
   float acc[V];
-  load_row<V>(p.part + (s * 2 + 1) * p.dim + col, acc);
-  for (int64_t j = s + 1; j < p.slices && p.keys[j * p.slice] == key; ++j) {
-    float v[V];
-    load_row<V>(p.part + j * 2 * p.dim + col, v);
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] += v[i];
+  for (int j = 0; j < V; ++j) acc[j] = 0.f;
+  if (on) {
+#pragma unroll 8
+    for (int k = wave * quarter; k < end; ++k) {
+      float v[V];
+      load_row<V>(p.part + ((s + k) * 2 + (k == 0 ? 1 : 0)) * p.dim + col, v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc[j] += v[j];
+    }
   }
+#pragma unroll
+  for (int j = 0; j < V; ++j) red[wave][j * kLanes + lane] = acc[j];
+  __syncthreads();
+  if (wave != 0 || !on) return;
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w)
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[j] += red[w][j * kLanes + lane];
   write_grad<G, V>(static_cast<G*>(p.dweight) + key * p.dim + col, acc, p.scale, p.accumulate != 0);
-}
-
-// rows without a token
-template <typename G>
-__global__ __launch_bounds__(kThreads) void embed_zero_kernel(G* p, int64_t n) {
-  constexpr int V = 16 / sizeof(G);
-  const float z[V] = {};
-  int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * V;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads * V;
-  if (reinterpret_cast<uintptr_t>(p) % 16 == 0) {
-    for (; i + V <= n; i += step) store_row<V>(p + i, z);
-    for (int64_t j = i; j < n && j < i + V; ++j) p[j] = 0;
-  } else {
-    for (; i < n; i += step)
-      for (int64_t j = i; j < n && j < i + V; ++j) p[j] = 0;
-  }
 }
 
 int sort_passes(int64_t vocab, int* bits) {
@@ -285,9 +433,6 @@ int sort_passes(int64_t vocab, int* bits) {
   *bits = (need + passes - 1) / passes;
   return passes;
 }
-
-// a slice long enough that the crossing runs' parts stay few, short enough that the slices fill the chip
-int slice_len(int64_t tokens) { return tokens >= (1 << 17) ? 64 : tokens >= (1 << 15) ? 32 : 16; }
 
 constexpr size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
@@ -326,43 +471,62 @@ template <typename T, typename G> hipError_t embed_bwd_t(const EmbedArgs& a, hip
   uint32_t* hist = reinterpret_cast<uint32_t*>(ws + 4 * up256(size_t(n) * 4));
   float* part = reinterpret_cast<float*>(ws + 4 * up256(size_t(n) * 4) + up256((size_t(1) << bits) * tiles * 4));
 
-  if (!a.accumulate) {
-    const int64_t total = a.vocab * a.dim;
-    const int64_t want = (total + kThreads * 8 - 1) / (kThreads * 8);
-    embed_zero_kernel<G><<<dim3(static_cast<unsigned>(want < 8192 ? want : 8192)), kThreads, 0, stream>>>(
-        static_cast<G*>(a.dweight), total);
+  const int64_t total = a.accumulate ? 0 : a.vocab * a.dim;
+  EmbedGradParams g{};
+  if (n > 0 && n <= kLdsMost && a.vocab < (int64_t{1} << (32 - kTokenBits)) - 1) {
+    LdsSortParams sp{a.ids, a.id_bytes, a.vocab, n, 1, buf[0], buf[1], total};
+    while ((int64_t{1} << (kDigitBits * sp.passes)) <= a.vocab) ++sp.passes;   // the keys are 0 .. vocab
+    const int64_t want = (total + kLdsThreads * 32 - 1) / (kLdsThreads * 32);
+    const dim3 grid(1 + static_cast<unsigned>(want < 2048 ? want : 2048));
+    G* const dw = static_cast<G*>(a.dweight);
+    if (n <= kLdsThreads) sort_lds_kernel<G, 1><<<grid, kLdsThreads, 0, stream>>>(sp, dw);
+    else if (n <= 4 * kLdsThreads) sort_lds_kernel<G, 4><<<grid, kLdsThreads, 0, stream>>>(sp, dw);
+    else sort_lds_kernel<G, 16><<<grid, kLdsThreads, 0, stream>>>(sp, dw);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    g.keys = buf[0];
+    g.toks = buf[1];
+  } else {
+    if (total > 0) {
+      const int64_t want = (total + kThreads * 32 - 1) / (kThreads * 32);
+      embed_zero_kernel<G><<<dim3(static_cast<unsigned>(want < 8192 ? want : 8192)), kThreads, 0, stream>>>(
+          static_cast<G*>(a.dweight), total);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    if (n == 0) return hipSuccess;
+    SortParams sp{};
+    sp.n = n; sp.tiles = tiles; sp.bits = bits; sp.vocab = a.vocab; sp.hist = hist; sp.id_bytes = a.id_bytes;
+    for (int k = 0; k < passes; ++k) {
+      sp.ids = k == 0 ? a.ids : nullptr;
+      sp.keys = buf[(k & 1) ? 0 : 2];
+      sp.toks = buf[(k & 1) ? 1 : 3];
+      sp.out_keys = buf[(k & 1) ? 2 : 0];
+      sp.out_toks = buf[(k & 1) ? 3 : 1];
+      sp.shift = k * bits;
+      sort_hist_kernel<<<dim3(tiles), kThreads, 0, stream>>>(sp);
+      sort_scan_kernel<<<dim3(1), kScanThreads, 0, stream>>>(hist, (int64_t{1} << bits) * tiles);
+      sort_scatter_kernel<<<dim3(tiles), kThreads, 0, stream>>>(sp);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    g.keys = sp.out_keys;
+    g.toks = sp.out_toks;
   }
-  if (n == 0) return hipSuccess;
-  SortParams sp{};
-  sp.n = n; sp.tiles = tiles; sp.bits = bits; sp.vocab = a.vocab; sp.hist = hist; sp.id_bytes = a.id_bytes;
-  for (int k = 0; k < passes; ++k) {
-    sp.ids = k == 0 ? a.ids : nullptr;
-    sp.keys = buf[(k & 1) ? 0 : 2];
-    sp.toks = buf[(k & 1) ? 1 : 3];
-    sp.out_keys = buf[(k & 1) ? 2 : 0];
-    sp.out_toks = buf[(k & 1) ? 3 : 1];
-    sp.shift = k * bits;
-    sort_hist_kernel<<<dim3(tiles), kThreads, 0, stream>>>(sp);
-    sort_scan_kernel<<<dim3(1), kScanThreads, 0, stream>>>(hist, (int64_t{1} << bits) * tiles);
-    sort_scatter_kernel<<<dim3(tiles), kThreads, 0, stream>>>(sp);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  EmbedGradParams p{};
-  p.keys = sp.out_keys; p.toks = sp.out_toks; p.dout = a.dout; p.dweight = a.dweight; p.part = part;
-  p.scale = a.scale; p.dim = a.dim; p.n = n; p.slice = slice_len(n); p.slices = (n + p.slice - 1) / p.slice;
+  EmbedGradParams p = g;
+  p.dout = a.dout; p.dweight = a.dweight; p.part = part;
+  p.scale = a.scale; p.dim = a.dim; p.n = n; p.slices = (n + kSlice - 1) / kSlice;
   p.vocab = static_cast<uint32_t>(a.vocab); p.accumulate = a.accumulate;
   const void* ptrs[] = {a.dout, a.dweight, part};
   const int es[] = {sizeof(T), sizeof(G), 4};
   const int v = vector_width(a.dim, ptrs, es, 3, 16 / sizeof(T));
   return launch_width(v, [&](auto V) {
     constexpr int kV = decltype(V)::value > static_cast<int>(16 / sizeof(T)) ? 1 : decltype(V)::value;
-    const dim3 grid(static_cast<unsigned>((p.slices + kWaves - 1) / kWaves),
-                    static_cast<unsigned>((a.dim + kLanes * kV - 1) / (kLanes * kV)));
-    embed_grad_kernel<T, G, kV><<<grid, kThreads, 0, stream>>>(p);
-    embed_join_kernel<G, kV><<<grid, kThreads, 0, stream>>>(p);
+    const unsigned chunks = static_cast<unsigned>((a.dim + kLanes * kV - 1) / (kLanes * kV));
+    embed_grad_kernel<T, G, kV><<<dim3(static_cast<unsigned>((p.slices + kWaves - 1) / kWaves), chunks), kThreads, 0,
+                                  stream>>>(p);
+    if (p.slices > 1)
+      embed_join_kernel<G, kV><<<dim3(static_cast<unsigned>(p.slices - 1), chunks), kThreads, 0, stream>>>(p);
   });
 }
 
@@ -373,7 +537,7 @@ size_t embed_bwd_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim) {
   int bits = 0;
   sort_passes(vocab, &bits);
   const size_t n = static_cast<size_t>(tokens), tiles = (n + kTile - 1) / kTile;
-  const size_t slice = static_cast<size_t>(slice_len(tokens)), slices = (n + slice - 1) / slice;
+  const size_t slices = (n + kSlice - 1) / kSlice;
   return 4 * up256(n * 4) + up256((size_t{1} << bits) * tiles * 4) + up256(slices * 2 * dim * 4);
 }
 

@@ -208,7 +208,35 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormParams 
       }
     }
   }
-  float* const out = p.part + group * 2 * p.dim;
+  if constexpr (WAVE) {
+    // the workgroup's waves add up first, in order
+    __shared__ float sums[3][C * kLanes * V];
+    const int wave = threadIdx.x / kLanes;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (half == 1 && !p.layer) break;
+      float(&mine)[C][V] = half == 0 ? dw : db;
+      __syncthreads();
+      if (wave > 0) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int i = 0; i < V; ++i) sums[wave - 1][(c * V + i) * kLanes + tid] = mine[c][i];
+      }
+      __syncthreads();
+      if (wave == 0) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const int at = (c * V + i) * kLanes + tid;
+            mine[c][i] = ((mine[c][i] + sums[0][at]) + sums[1][at]) + sums[2][at];
+          }
+      }
+    }
+    if (wave > 0) return;
+  }
+  float* const out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.dim;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int col = (c * tr + tid) * V;
@@ -296,19 +324,26 @@ __global__ __launch_bounds__(kColThreads) void norm_cols_wide_kernel(NormParams 
   if (p.layer) p.part[(blockIdx.y * 2 + 1) * static_cast<int64_t>(p.dim) + c] = db;
 }
 
-// dw, db = sum over the groups, in a fixed order: a workgroup owns 64 columns, its waves every fourth group
-__global__ __launch_bounds__(256) void norm_sum_kernel(const float* part, int64_t groups, int dim, float* dw, float* db) {
-  __shared__ float red[4][kLanes];
+// dw, db = sum over the groups, in a fixed order: a workgroup of 1024 owns 64 columns, wave w every 16th group
+// from w on, eight loads in flight.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(kSumWaves * kLanes) void norm_sum_kernel(const float* part, int64_t groups, int dim,
+                                                                      float* dw, float* db) {
+  __shared__ float red[kSumWaves][kLanes];
   const int wave = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
   const int c = blockIdx.x * kLanes + lane;
-  float* const to = blockIdx.y == 0 ? dw : db;
-  if (to == nullptr) return;   // uniform over the workgroup
   float s = 0.f;
-  if (c < dim)
-    for (int64_t g = wave; g < groups; g += 4) s += part[(g * 2 + blockIdx.y) * dim + c];
+  if (c < dim) {
+#pragma unroll 8
+    for (int64_t g = wave; g < groups; g += kSumWaves) s += part[(g * 2 + blockIdx.y) * dim + c];
+  }
   red[wave][lane] = s;
   __syncthreads();
-  if (wave == 0 && c < dim) to[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+  if (wave == 0 && c < dim) {
+#pragma unroll
+    for (int w = 1; w < kSumWaves; ++w) s += red[w][lane];
+    (blockIdx.y == 0 ? dw : db)[c] = s;
+  }
 }
 
 // ---------------------------------------------------------------------------------------------- plan
@@ -338,11 +373,9 @@ NormPlan norm_plan(int64_t dim, int v) {
   return n;
 }
 
-// partial sums of dw (and db) the backward pass leaves
-int64_t norm_groups(int64_t rows, int64_t dim) {
-  const int64_t most = dim <= 1024 ? 2048 : 1024;   // waves of small rows, workgroups of larger ones
-  return rows < most ? (rows + 3) / 4 * 4 : most;
-}
+// workgroups of the backward pass, each of which leaves a partial sum of dw (and db): four to a CU, fewer for
+// few rows
+int64_t norm_groups(int64_t rows) { return rows < 1024 ? rows : 1024; }
 
 template <typename K> hipError_t norm_dispatch(const NormPlan& n, K&& k) {
 #define MSSM_NORM_CASE(v, c)                                                                      \
@@ -398,7 +431,7 @@ template <typename T, typename R> hipError_t norm_bwd_t(const NormArgs& a, hipSt
   const void* ptrs[] = {a.h, a.dout, a.dresidual, a.weight, a.dx, a.dresidual_in, a.workspace};
   const int es[] = {sizeof(R), sizeof(T), sizeof(R), 4, sizeof(T), sizeof(R), 4};
   const NormPlan n = norm_plan(a.dim, norm_width(a.dim, ptrs, es, 7));
-  int64_t groups = norm_groups(a.rows, a.dim);
+  int64_t groups = norm_groups(n.wave ? (a.rows + 3) / 4 : a.rows);
   hipError_t e = hipSuccess;
   if (a.rows == 0) {
     groups = 0;   // the sums over no rows are written as zeros
@@ -409,22 +442,21 @@ template <typename T, typename R> hipError_t norm_bwd_t(const NormArgs& a, hipSt
                                        static_cast<unsigned>(groups)), kColThreads, 0, stream>>>(p);
     e = hipGetLastError();
   } else {
-    const int64_t blocks = n.wave ? groups / 4 : groups;
     e = norm_dispatch(n, [&](auto V, auto C, auto W) {
       norm_bwd_kernel<T, R, decltype(V)::value, decltype(C)::value, decltype(W)::value>
-          <<<dim3(static_cast<unsigned>(blocks)), n.threads, 0, stream>>>(p);
+          <<<dim3(static_cast<unsigned>(groups)), n.threads, 0, stream>>>(p);
     });
   }
   if (e != hipSuccess) return e;
-  norm_sum_kernel<<<dim3(static_cast<unsigned>((a.dim + kLanes - 1) / kLanes), a.dbias != nullptr ? 2 : 1), 256, 0,
-                    stream>>>(p.part, groups, p.dim, a.dweight, a.dbias);
+  norm_sum_kernel<<<dim3(static_cast<unsigned>((a.dim + kLanes - 1) / kLanes), a.dbias != nullptr ? 2 : 1),
+                    kSumWaves * kLanes, 0, stream>>>(p.part, groups, p.dim, a.dweight, a.dbias);
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t dim) {
-  return static_cast<size_t>(norm_groups(rows, dim)) * 2 * static_cast<size_t>(dim) * 4;
+  return static_cast<size_t>(norm_groups(rows)) * 2 * static_cast<size_t>(dim) * 4;
 }
 
 hipError_t norm_fwd_launch(const NormArgs& a, hipStream_t stream) {
