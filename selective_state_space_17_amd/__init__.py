@@ -790,30 +790,51 @@ def _ssd_update_call(fn, state, x_prev, B_prev, x, delta, lam, A, B, C, D, z, ou
 # --------------------------------------------------------------------------
 # Around the scan: embedding, norm, loss
 # --------------------------------------------------------------------------
+# (a decode step's call is dominated by what happens here on the host: one dictionary lookup instead of
+# comparisons, no check twice, memory shaped after a tensor at hand where there is one)
+_CODES = {}
+
+
+def _codes(io_dtype) -> int:
+    code = _CODES.get(io_dtype)
+    if code is None:
+        code = _CODES[io_dtype] = _io_code(io_dtype)
+    return code
+
+
 def _id_bytes(name, ids) -> int:
     torch = _torch()
-    if ids.dtype == torch.int64:
+    if ids.dtype is torch.int64:
         return 8
-    if ids.dtype == torch.int32:
+    if ids.dtype is torch.int32:
         return 4
     raise TypeError(f"{name} must be int32 or int64, got {ids.dtype}")
 
 
 def _grad_code(name, t, io_dtype) -> int:
-    torch = _torch()
-    if t.dtype == torch.float32:
-        return MSSM_F32
-    if t.dtype == io_dtype:
-        return _io_code(io_dtype)
-    raise TypeError(f"{name} must be {io_dtype} or torch.float32, got {t.dtype}")
+    if t.dtype != io_dtype and t.dtype != _torch().float32:
+        raise TypeError(f"{name} must be {io_dtype} or torch.float32, got {t.dtype}")
+    return _codes(t.dtype)
 
 
-def _empty(stream, shape, dtype):
-    """A new tensor on the current GPU, in the memory pool of the stream that the call runs on: memory of the
-    current stream's pool could still be in use there, or be handed out again while the call runs."""
+def _check_place(name, t, cur):
+    """_check_gpu for a tensor whose own type and shape define the problem."""
+    if t.get_device() != cur or not t.is_contiguous():
+        _check_gpu(name, t, t.dtype, t.shape, cur)
+
+
+def _stream_on(stream, cur) -> int:
+    """_stream_handle with the current device known."""
+    return _torch()._C._cuda_getCurrentRawStream(cur) if stream is None else _stream_handle(stream)
+
+
+def _empty(stream, shape, dtype, like=None):
+    """A new tensor on the current GPU (like: one of this shape and type), in the memory pool of the stream that
+    the call runs on: memory of the current stream's pool could still be in use there, or be handed out again
+    while the call runs."""
     torch = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device="cuda")
+        return torch.empty_like(like) if like is not None else torch.empty(shape, dtype=dtype, device="cuda")
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device="cuda")
 
@@ -846,16 +867,18 @@ def embedding_fwd(ids, weight, scale: float = 1.0, out=None, stream=None):
     if weight.dim() != 2:
         raise ValueError("weight must be [vocab, dim]")
     vocab, dim = weight.shape
-    io, nb = _io_code(weight.dtype), _id_bytes("ids", ids)
+    io, nb = _codes(weight.dtype), _id_bytes("ids", ids)
     cur = torch.cuda.current_device()
-    _check_gpu("ids", ids, ids.dtype, ids.shape, cur)
-    _check_gpu("weight", weight, weight.dtype, (vocab, dim), cur)
-    shape = tuple(ids.shape) + (dim,)
+    _check_place("ids", ids, cur)
+    _check_place("weight", weight, cur)
+    shape = (*ids.shape, dim)
     if out is None:
         out = _empty(stream, shape, weight.dtype)
-    _check_gpu("out", out, weight.dtype, shape, cur)
+    else:
+        _check_gpu("out", out, weight.dtype, shape, cur)
     d = EmbeddingDesc(ids.numel(), vocab, dim, scale, io, nb, 0)
-    st = lib.mssm_embedding_fwd(ctypes.byref(d), _ptr(ids), _ptr(weight), _ptr(out), _stream_handle(stream))
+    st = lib.mssm_embedding_fwd(ctypes.byref(d), ids.data_ptr(), weight.data_ptr(), out.data_ptr(),
+                                _stream_on(stream, cur))
     if st != MSSM_OK:
         raise MssmError(st, "mssm_embedding_fwd")
     return out
@@ -872,10 +895,10 @@ def embedding_bwd(ids, dout, vocab: int, scale: float = 1.0, dweight=None, accum
     if dout.dim() != ids.dim() + 1:
         raise ValueError("dout must be [*ids.shape, dim]")
     dim = dout.shape[-1]
-    io, nb = _io_code(dout.dtype), _id_bytes("ids", ids)
+    io, nb = _codes(dout.dtype), _id_bytes("ids", ids)
     cur = torch.cuda.current_device()
-    _check_gpu("ids", ids, ids.dtype, ids.shape, cur)
-    _check_gpu("dout", dout, dout.dtype, tuple(ids.shape) + (dim,), cur)
+    _check_place("ids", ids, cur)
+    _check_gpu("dout", dout, dout.dtype, (*ids.shape, dim), cur)
     if dweight is None:
         if accumulate:
             raise ValueError("accumulate adds to dweight, which must be given")
@@ -885,7 +908,7 @@ def embedding_bwd(ids, dout, vocab: int, scale: float = 1.0, dweight=None, accum
     d = EmbeddingDesc(ids.numel(), vocab, dim, scale, io, nb, 0)
     ws, ws_bytes, _keep = _workspace(lib.mssm_embedding_bwd_workspace_size(ctypes.byref(d)), workspace, stream)
     st = lib.mssm_embedding_bwd(ctypes.byref(d), _ptr(ids), _ptr(dout), _ptr(dweight), gd, int(accumulate), ws,
-                                ws_bytes, _stream_handle(stream))
+                                ws_bytes, _stream_on(stream, cur))
     if st != MSSM_OK:
         raise MssmError(st, "mssm_embedding_bwd")
     return dweight
@@ -922,45 +945,51 @@ def _norm_fwd(kind, x, weight, bias, residual, eps, return_residual, residual_dt
     torch = _torch()
     if x.dim() < 1:
         raise ValueError("x must be [..., dim]")
-    shape, dim = tuple(x.shape), x.shape[-1]
+    shape, dim, xt = x.shape, x.shape[-1], x.dtype
     rows = x.numel() // dim if dim else 0
-    io = _io_code(x.dtype)
+    io = _codes(xt)
     cur = torch.cuda.current_device()
+    _check_place("x", x, cur)
+    _check_gpu("weight", weight, torch.float32, (dim,), cur)
+    if bias is not None:
+        _check_gpu("bias", bias, torch.float32, (dim,), cur)
     rdt = residual.dtype if residual is not None else (residual_out.dtype if residual_out is not None else
-                                                       (residual_dtype or x.dtype))
+                                                       (residual_dtype or xt))
     if residual_dtype is not None and residual_dtype != rdt:
         raise TypeError(f"residual_dtype is {residual_dtype}, but the residual is {rdt}")
-    res = _grad_code("residual", residual, x.dtype) if residual is not None else _res_code(rdt, x.dtype)
-    _check_gpu("x", x, x.dtype, shape, cur)
-    _check_gpu("residual", residual, rdt, shape, cur)
-    _check_gpu("weight", weight, torch.float32, (dim,), cur)
-    _check_gpu("bias", bias, torch.float32, (dim,), cur)
+    res = _res_code(rdt, xt)
+    if residual is not None:
+        _check_gpu("residual", residual, rdt, shape, cur)
     if out is None:
-        out = _empty(stream, shape, x.dtype)
-    _check_gpu("out", out, x.dtype, shape, cur)
-    if residual_out is None and (return_residual or residual is not None):
+        out = _empty(stream, shape, xt, x)
+    else:
+        _check_gpu("out", out, xt, shape, cur)
+    if residual_out is not None:
+        _check_gpu("residual_out", residual_out, rdt, shape, cur)
+    elif residual is not None:
+        residual_out = _empty(stream, shape, rdt, residual)
+    elif return_residual:
         residual_out = _empty(stream, shape, rdt)
-    _check_gpu("residual_out", residual_out, rdt, shape, cur)
     mean = rstd = None
     if return_stats:
         rstd = _empty(stream, shape[:-1], torch.float32)
         if kind == MSSM_LAYER_NORM:
-            mean = _empty(stream, shape[:-1], torch.float32)
+            mean = _empty(stream, shape[:-1], torch.float32, rstd)
     d = NormDesc(rows, dim, eps, kind, io, res, 0)
-    st = lib.mssm_norm_fwd(ctypes.byref(d), _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(out),
-                           _ptr(residual_out), _ptr(mean), _ptr(rstd), _stream_handle(stream))
+    st = lib.mssm_norm_fwd(ctypes.byref(d), x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias),
+                           out.data_ptr(), _ptr(residual_out), _ptr(mean), _ptr(rstd), _stream_on(stream, cur))
     if st != MSSM_OK:
         raise MssmError(st, "mssm_norm_fwd")
-    got = (out,) + ((residual_out,) if return_residual else ())
     if return_stats:
-        got += (mean, rstd) if kind == MSSM_LAYER_NORM else (rstd,)
-    return got if len(got) > 1 else out
+        stats = (mean, rstd) if kind == MSSM_LAYER_NORM else (rstd,)
+        return (out, residual_out, *stats) if return_residual else (out, *stats)
+    return (out, residual_out) if return_residual else out
 
 
 def _res_code(rdt, io_dtype) -> int:
     if rdt != io_dtype and rdt != _torch().float32:
         raise TypeError(f"the residual must be {io_dtype} or torch.float32, got {rdt}")
-    return _io_code(rdt)
+    return _codes(rdt)
 
 
 def layer_norm_bwd(h, weight, mean, rstd, dout, dresidual=None, want_dresidual: bool = False, want_dbias: bool = True,
@@ -986,12 +1015,12 @@ def _norm_bwd(kind, h, weight, mean, rstd, dout, dresidual, want_dresidual, want
     torch = _torch()
     if h.dim() < 1:
         raise ValueError("h must be [..., dim]")
-    shape, dim = tuple(h.shape), h.shape[-1]
+    shape, dim = h.shape, h.shape[-1]
     rows = h.numel() // dim if dim else 0
-    io = _io_code(dout.dtype)
+    io = _codes(dout.dtype)
     res = _res_code(h.dtype, dout.dtype)
     cur = torch.cuda.current_device()
-    _check_gpu("h", h, h.dtype, shape, cur)
+    _check_place("h", h, cur)
     _check_gpu("dout", dout, dout.dtype, shape, cur)
     _check_gpu("dresidual", dresidual, h.dtype, shape, cur)
     _check_gpu("weight", weight, torch.float32, (dim,), cur)
@@ -1000,16 +1029,17 @@ def _norm_bwd(kind, h, weight, mean, rstd, dout, dresidual, want_dresidual, want
     _check_gpu("mean", mean, torch.float32, shape[:-1], cur)
     _check_gpu("rstd", rstd, torch.float32, shape[:-1], cur)
     if dx is None:
-        dx = _empty(stream, shape, dout.dtype)
-    _check_gpu("dx", dx, dout.dtype, shape, cur)
-    dres = _empty(stream, shape, h.dtype) if want_dresidual else None
+        dx = _empty(stream, shape, dout.dtype, dout)
+    else:
+        _check_gpu("dx", dx, dout.dtype, shape, cur)
+    dres = _empty(stream, shape, h.dtype, h) if want_dresidual else None
     dweight = _empty(stream, (dim,), torch.float32)
     dbias = _empty(stream, (dim,), torch.float32) if want_dbias else None
     d = NormDesc(rows, dim, 1.0, kind, io, res, 0)
     ws, ws_bytes, _keep = _workspace(lib.mssm_norm_bwd_workspace_size(ctypes.byref(d)), workspace, stream)
     st = lib.mssm_norm_bwd(ctypes.byref(d), _ptr(h), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dout),
                            _ptr(dresidual), _ptr(dx), _ptr(dres), _ptr(dweight), _ptr(dbias), ws, ws_bytes,
-                           _stream_handle(stream))
+                           _stream_on(stream, cur))
     if st != MSSM_OK:
         raise MssmError(st, "mssm_norm_bwd")
     return {"dx": dx, "dresidual": dres, "dweight": dweight, "dbias": dbias}
@@ -1029,10 +1059,10 @@ def _xent_args(x, weight, targets, ignore_id, cur):
     if x.dim() < 1 or weight.dim() != 2 or x.shape[-1] != weight.shape[1]:
         raise ValueError("x must be [..., dim] and weight [vocab, dim]")
     vocab, dim = weight.shape
-    io, nb = _io_code(x.dtype), _id_bytes("targets", targets)
-    _check_gpu("x", x, x.dtype, tuple(x.shape), cur)
+    io, nb = _codes(x.dtype), _id_bytes("targets", targets)
+    _check_place("x", x, cur)
     _check_gpu("weight", weight, x.dtype, (vocab, dim), cur)
-    _check_gpu("targets", targets, targets.dtype, tuple(x.shape[:-1]), cur)
+    _check_gpu("targets", targets, targets.dtype, x.shape[:-1], cur)
     return CrossEntropyDesc(targets.numel(), vocab, dim, ignore_id, io, nb, 0)
 
 
@@ -1055,7 +1085,7 @@ def linear_cross_entropy_fwd(x, weight, targets, ignore_id: int = -100, loss=Non
     ws, ws_bytes, _keep = _workspace(lib.mssm_linear_cross_entropy_fwd_workspace_size(ctypes.byref(d)), workspace,
                                      stream)
     st = lib.mssm_linear_cross_entropy_fwd(ctypes.byref(d), _ptr(x), _ptr(weight), _ptr(targets), _ptr(loss),
-                                           _ptr(lse), ws, ws_bytes, _stream_handle(stream))
+                                           _ptr(lse), ws, ws_bytes, _stream_on(stream, cur))
     if st != MSSM_OK:
         raise MssmError(st, "mssm_linear_cross_entropy_fwd")
     return loss, lse
@@ -1099,7 +1129,7 @@ def linear_cross_entropy_bwd(x, weight, targets, lse, dloss, dlse=None, ignore_i
                                      stream)
     st = lib.mssm_linear_cross_entropy_bwd(ctypes.byref(d), _ptr(x), _ptr(weight), _ptr(targets), _ptr(lse),
                                            _ptr(dloss), _ptr(dlse), _ptr(dx), _ptr(dweight), gd, int(accumulate), ws,
-                                           ws_bytes, _stream_handle(stream))
+                                           ws_bytes, _stream_on(stream, cur))
     if st != MSSM_OK:
         raise MssmError(st, "mssm_linear_cross_entropy_bwd")
     return {"dx": dx, "dweight": dweight}

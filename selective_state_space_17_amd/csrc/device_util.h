@@ -29,19 +29,18 @@ template <> __device__ __forceinline__ uint16_t narrow<uint16_t>(float v) {
 // v as it reads back after being stored as T
 template <typename T> __device__ __forceinline__ float rounded(float v) { return widen(narrow<T>(v)); }
 
-// V consecutive elements (V = 1, 2, 4 or 8; p aligned to min(16, V * sizeof(T)) bytes)
+// The same vectors at any element's address: gfx950 takes wide global accesses at any alignment, so rows of an
+// odd length are read as widely as others.
+typedef f32x4_t f32x4_u __attribute__((aligned(4)));
+typedef u32x4_t u32x4_u __attribute__((aligned(2)));
+typedef u32x2_t u32x2_u __attribute__((aligned(2)));
+
+// V = 4 or 8 consecutive elements at p, any alignment
 template <int V> __device__ __forceinline__ void load_row(const float* p, float (&v)[V]) {
-  if constexpr (V >= 4) {
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
-      const f32x4_t t = *reinterpret_cast<const f32x4_t*>(p + 4 * i);
-      v[4 * i] = t[0]; v[4 * i + 1] = t[1]; v[4 * i + 2] = t[2]; v[4 * i + 3] = t[3];
-    }
-  } else if constexpr (V == 2) {
-    const f32x2_t t = *reinterpret_cast<const f32x2_t*>(p);
-    v[0] = t[0]; v[1] = t[1];
-  } else {
-    v[0] = *p;
+  for (int i = 0; i < V / 4; ++i) {
+    const f32x4_t t = *reinterpret_cast<const f32x4_u*>(p + 4 * i);
+    v[4 * i] = t[0]; v[4 * i + 1] = t[1]; v[4 * i + 2] = t[2]; v[4 * i + 3] = t[3];
   }
 }
 __device__ __forceinline__ void split_bf16(uint32_t w, float& a, float& b) {
@@ -50,40 +49,44 @@ __device__ __forceinline__ void split_bf16(uint32_t w, float& a, float& b) {
 }
 template <int V> __device__ __forceinline__ void load_row(const uint16_t* p, float (&v)[V]) {
   if constexpr (V == 8) {
-    const u32x4_t t = *reinterpret_cast<const u32x4_t*>(p);
+    const u32x4_t t = *reinterpret_cast<const u32x4_u*>(p);
 #pragma unroll
     for (int i = 0; i < 4; ++i) split_bf16(t[i], v[2 * i], v[2 * i + 1]);
-  } else if constexpr (V == 4) {
-    const u32x2_t t = *reinterpret_cast<const u32x2_t*>(p);
+  } else {
+    const u32x2_t t = *reinterpret_cast<const u32x2_u*>(p);
     split_bf16(t[0], v[0], v[1]);
     split_bf16(t[1], v[2], v[3]);
-  } else if constexpr (V == 2) {
-    split_bf16(*reinterpret_cast<const uint32_t*>(p), v[0], v[1]);
-  } else {
-    v[0] = widen(*p);
   }
 }
 template <int V> __device__ __forceinline__ void store_row(float* p, const float (&v)[V]) {
-  if constexpr (V >= 4) {
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i)
-      *reinterpret_cast<f32x4_t*>(p + 4 * i) = f32x4_t{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-  } else if constexpr (V == 2) {
-    *reinterpret_cast<f32x2_t*>(p) = f32x2_t{v[0], v[1]};
-  } else {
-    *p = v[0];
-  }
+  for (int i = 0; i < V / 4; ++i)
+    *reinterpret_cast<f32x4_u*>(p + 4 * i) = f32x4_t{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
 }
 template <int V> __device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[V]) {
   if constexpr (V == 8) {
-    *reinterpret_cast<u32x4_t*>(p) = u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+    *reinterpret_cast<u32x4_u*>(p) = u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
                                              pack_bf16(v[6], v[7])};
-  } else if constexpr (V == 4) {
-    *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-  } else if constexpr (V == 2) {
-    *reinterpret_cast<uint32_t*>(p) = pack_bf16(v[0], v[1]);
   } else {
-    *p = narrow<uint16_t>(v[0]);
+    *reinterpret_cast<u32x2_u*>(p) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+  }
+}
+// the first n of V elements (n <= 0: none, and n >= V: all); what is not there reads as zero
+template <int V, typename T> __device__ __forceinline__ void load_row(const T* p, float (&v)[V], int64_t n) {
+  if (n >= V) {
+    load_row<V>(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = i < n ? widen(p[i]) : 0.f;
+  }
+}
+template <int V, typename T> __device__ __forceinline__ void store_row(T* p, const float (&v)[V], int64_t n) {
+  if (n >= V) {
+    store_row<V>(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) p[i] = narrow<T>(v[i]);
   }
 }
 
@@ -104,20 +107,6 @@ __device__ __forceinline__ float wave_sum(float v) {
 // ids and targets are int32 or int64
 __device__ __forceinline__ int64_t id_at(const void* ids, int id_bytes, int64_t i) {
   return id_bytes == 8 ? static_cast<const int64_t*>(ids)[i] : static_cast<const int32_t*>(ids)[i];
-}
-
-// largest element count of 8, 4, 2, 1 that divides dim and that every pointer's alignment allows, for
-// elements of at most `es` bytes (16-byte accesses at most need 16-byte alignment)
-inline int vector_width(int64_t dim, const void* const* ptrs, const int* elem_bytes, int n, int most) {
-  for (int v = most; v > 1; v /= 2) {
-    bool ok = dim % v == 0;
-    for (int i = 0; ok && i < n; ++i) {
-      const uintptr_t need = static_cast<uintptr_t>(v * elem_bytes[i] < 16 ? v * elem_bytes[i] : 16);
-      ok = ptrs[i] == nullptr || reinterpret_cast<uintptr_t>(ptrs[i]) % need == 0;
-    }
-    if (ok) return v;
-  }
-  return 1;
 }
 
 }  // namespace mssm

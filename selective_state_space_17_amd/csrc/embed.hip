@@ -44,18 +44,14 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(EmbedParams p) {
   const T* src = static_cast<const T*>(p.weight) + (in ? id : 0) * p.dim;
   T* dst = static_cast<T*>(p.out) + t * p.dim;
   const float s = in ? p.scale : 0.f;
-  const int chunks = static_cast<int>(p.dim / V);
+  const int chunks = static_cast<int>((p.dim + V - 1) / V);
   for (int c = (wave % WPR) * kLanes + lane; c < chunks; c += WPR * kLanes) {
+    const int64_t col = static_cast<int64_t>(c) * V;
     float v[V];
-    if (in) {
-      load_row<V>(src + static_cast<int64_t>(c) * V, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = 0.f;
-    }
+    load_row<V>(src + col, v, in ? p.dim - col : 0);
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] *= s;
-    store_row<V>(dst + static_cast<int64_t>(c) * V, v);
+    store_row<V>(dst + col, v, p.dim - col);
   }
 }
 
@@ -65,14 +61,7 @@ __device__ __forceinline__ void zero_rows(G* p, int64_t n, int64_t block, int64_
   constexpr int V = 16 / sizeof(G);
   const float z[V] = {};
   const int64_t step = blocks * threads * V;
-  const bool vec = reinterpret_cast<uintptr_t>(p) % 16 == 0;
-  for (int64_t i = (block * threads + threadIdx.x) * V; i < n; i += step) {
-    if (vec && i + V <= n) {
-      store_row<V>(p + i, z);
-    } else {
-      for (int64_t j = i; j < n && j < i + V; ++j) p[j] = 0;
-    }
-  }
+  for (int64_t i = (block * threads + threadIdx.x) * V; i < n; i += step) store_row<V>(p + i, z, n - i);
 }
 
 template <typename G>
@@ -86,12 +75,14 @@ __device__ __forceinline__ uint32_t sort_key(const void* ids, int id_bytes, int6
 }
 
 // ------------------------------------------------------------------------------- sort of up to 16384 by id
-// One workgroup sorts the whole list in LDS, while the others zero dW: a word holds key << 14 | token, four bits
-// of the key a pass, a thread keeps E consecutive words, so the order of equal digits is the input's.
-// 16384 tokens: four passes (50280 ids) hide behind the zeros of a table of 50280 x 768; by the passes over
-// memory below they took 45 us, and the zeros 13 us before them.
+// One workgroup sorts the whole list in LDS, while the others zero dW.  A word holds key << 14 | token; four bits
+// of the key a pass.  A thread holds E consecutive words and counts them into counters of its own (LDS adds that
+// return what was there: a word's rank among the thread's equal digits); wave d turns digit d's counters into
+// positions.  A thread's words, and the counters of the threads a lane scans, stand 17 words apart: no bank
+// conflicts either way.
 constexpr int kLdsThreads = 1024, kTokenBits = 14, kLdsMost = 1 << kTokenBits, kDigitBits = 4, kDigits = 1 << kDigitBits;
-constexpr int kLdsWaves = kLdsThreads / kLanes;
+constexpr int kLdsWaves = kLdsThreads / kLanes, kLine = kLdsThreads / kLanes;   // counters of a digit that a lane scans
+static_assert(kDigits == kLdsWaves, "one wave to a digit");
 
 struct LdsSortParams {
   const void* ids;
@@ -103,7 +94,7 @@ struct LdsSortParams {
   int64_t total;     // elements of dW to zero; 0: none
 };
 
-// inclusive prefix sum over the wave's lanes (16-bit halves side by side work too, if they do not overflow)
+// sum over the lanes up to and including this one
 __device__ __forceinline__ uint32_t wave_prefix(uint32_t v) {
   const int lane = threadIdx.x % kLanes;
 #pragma unroll
@@ -116,77 +107,69 @@ __device__ __forceinline__ uint32_t wave_prefix(uint32_t v) {
 
 template <typename G, int E>
 __global__ __launch_bounds__(kLdsThreads) void sort_lds_kernel(LdsSortParams p, G* dweight) {
-  __shared__ __attribute__((aligned(16))) uint32_t words[kLdsThreads * E];
-  __shared__ __attribute__((aligned(16))) uint16_t at[kLdsThreads][kDigits];   // where a thread's next word of each digit goes
-  __shared__ uint32_t sums[kDigits * kLdsWaves];
+  constexpr int kPad = E > 1 ? E + 1 : 1;   // words of a thread, and what separates them from the next's
+  __shared__ uint32_t words[kLdsThreads * kPad];
+  __shared__ uint32_t cnt[kDigits][kLdsThreads / kLine * (kLine + 1)];
+  __shared__ uint32_t totals[kDigits];
   if (blockIdx.x > 0) {
     zero_rows<G>(dweight, p.total, blockIdx.x - 1, gridDim.x - 1, kLdsThreads);
     return;
   }
   const int tid = threadIdx.x, wave = tid / kLanes, lane = tid % kLanes;
+  auto word_at = [](uint32_t i) -> uint32_t { return E > 1 ? i + i / E : i; };
+  const int mine = tid + tid / kLine;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int i = e * kLdsThreads + tid;   // (what lies past the end sorts last)
-    words[i] = i < p.n ? sort_key(p.ids, p.id_bytes, p.vocab, i) << kTokenBits | static_cast<uint32_t>(i) : ~0u;
+    words[word_at(i)] = i < p.n ? sort_key(p.ids, p.id_bytes, p.vocab, i) << kTokenBits | static_cast<uint32_t>(i) : ~0u;
   }
-  __syncthreads();
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = kTokenBits + pass * kDigitBits;
-    uint32_t v[E];
-    int rank[E];
-    uint64_t cnt[2] = {0, 0};   // eight digits each, a byte a digit: at most E = 16
+#pragma unroll
+    for (int d = 0; d < kDigits; ++d) cnt[d][mine] = 0;
+    __syncthreads();
+    uint32_t v[E], rank[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = words[tid * kPad + e];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      rank[e] = __hip_atomic_fetch_add(&cnt[v[e] >> shift & (kDigits - 1)][mine], 1u, __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_WORKGROUP);
+    __syncthreads();
+    {
+      uint32_t c[kLine], s = 0;
+#pragma unroll
+      for (int k = 0; k < kLine; ++k) {
+        c[k] = s;
+        s += cnt[wave][lane * (kLine + 1) + k];
+      }
+      const uint32_t upto = wave_prefix(s);
+#pragma unroll
+      for (int k = 0; k < kLine; ++k) cnt[wave][lane * (kLine + 1) + k] = upto - s + c[k];
+      if (lane == kLanes - 1) totals[wave] = upto;
+    }
+    __syncthreads();
+    if (wave == 0 && lane < kDigits) {
+      uint32_t before = 0;
+      for (int d = 0; d < lane; ++d) before += totals[d];
+      __builtin_amdgcn_wave_barrier();
+      totals[lane] = before;
+    }
+    __syncthreads();
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      v[e] = words[tid * E + e];
-      const int d = v[e] >> shift & (kDigits - 1);
-      const uint64_t c = d < 8 ? cnt[0] : cnt[1];
-      rank[e] = static_cast<int>(c >> (d % 8 * 8) & 0xff);
-      const uint64_t one = uint64_t{1} << (d % 8 * 8);
-      cnt[0] += d < 8 ? one : 0;
-      cnt[1] += d < 8 ? 0 : one;
+      const uint32_t d = v[e] >> shift & (kDigits - 1);
+      words[word_at(totals[d] + cnt[d][mine] + rank[e])] = v[e];   // (all words are in registers)
     }
-    // prefix over the wave's threads, two digits to a word
-    uint32_t own[kDigits / 2], pre[kDigits / 2];
-#pragma unroll
-    for (int d = 0; d < kDigits / 2; ++d) {
-      const uint64_t c = cnt[d / 4] >> (d % 4 * 16);
-      own[d] = static_cast<uint32_t>(c & 0xff) | static_cast<uint32_t>(c >> 8 & 0xff) << 16;
-      pre[d] = wave_prefix(own[d]);
-      if (lane == kLanes - 1) {
-        sums[(2 * d) * kLdsWaves + wave] = pre[d] & 0xffff;
-        sums[(2 * d + 1) * kLdsWaves + wave] = pre[d] >> 16;
-      }
-    }
-    __syncthreads();
-    if (wave == 0) {   // prefix over (digit, wave), four to a lane
-      uint32_t q[4], s = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        q[k] = s;
-        s += sums[lane * 4 + k];
-      }
-      const uint32_t before = wave_prefix(s) - s;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) sums[lane * 4 + k] = before + q[k];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int d = 0; d < kDigits / 2; ++d) {
-      const uint32_t ex = pre[d] - own[d];
-      at[tid][2 * d] = static_cast<uint16_t>(sums[(2 * d) * kLdsWaves + wave] + (ex & 0xffff));
-      at[tid][2 * d + 1] = static_cast<uint16_t>(sums[(2 * d + 1) * kLdsWaves + wave] + (ex >> 16));
-    }
-    // (each thread reads back its own line of `at`; all words are in registers since the first barrier)
-#pragma unroll
-    for (int e = 0; e < E; ++e) words[at[tid][v[e] >> shift & (kDigits - 1)] + rank[e]] = v[e];
     __syncthreads();
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int i = e * kLdsThreads + tid;
     if (i < p.n) {
-      p.keys[i] = words[i] >> kTokenBits;
-      p.toks[i] = words[i] & (kLdsMost - 1);
+      const uint32_t v = words[word_at(i)];
+      p.keys[i] = v >> kTokenBits;
+      p.toks[i] = v & (kLdsMost - 1);
     }
   }
 }
@@ -319,17 +302,17 @@ struct EmbedGradParams {
 };
 
 template <typename G, int V>
-__device__ __forceinline__ void write_grad(G* row, const float (&acc)[V], float scale, bool accumulate) {
+__device__ __forceinline__ void write_grad(G* row, const float (&acc)[V], float scale, bool accumulate, int64_t n) {
   float v[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = acc[i] * scale;
   if (accumulate) {
     float old[V];
-    load_row<V>(row, old);
+    load_row<V>(row, old, n);
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] += old[i];
   }
-  store_row<V>(row, v);
+  store_row<V>(row, v, n);
 }
 
 // One wave: one slice of the sorted list x one chunk of 64 V columns.  Lane i holds the slice's i-th key and token.
@@ -339,7 +322,8 @@ __global__ __launch_bounds__(kThreads) void embed_grad_kernel(EmbedGradParams p)
   const int64_t s = static_cast<int64_t>(blockIdx.x) * kWaves + wave;
   if (s >= p.slices) return;
   const int64_t col = (static_cast<int64_t>(blockIdx.y) * kLanes + lane) * V;
-  const bool on = col < p.dim;
+  const int64_t left = p.dim - col;
+  const bool on = left > 0;
   const int lo = static_cast<int>(s) * kSlice;
   // lanes 0 .. 15: the slice; 16: what follows it; 17: what stands before it (~0: nothing)
   const int at = lane <= kSlice ? lo + lane : lo - 1;
@@ -351,7 +335,7 @@ __global__ __launch_bounds__(kThreads) void embed_grad_kernel(EmbedGradParams p)
   for (int i = 0; i < kSlice; ++i) {
     // (a token that is not to be counted is not read: its row may hold anything)
     if (static_cast<uint32_t>(__builtin_amdgcn_readlane(key, i)) < p.vocab)
-      load_row<V>(dout + static_cast<int64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(tok, i))) * p.dim, v[i]);
+      load_row<V>(dout + static_cast<int64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(tok, i))) * p.dim, v[i], left);
   }
   float acc[V];
 #pragma unroll
@@ -367,9 +351,9 @@ __global__ __launch_bounds__(kThreads) void embed_grad_kernel(EmbedGradParams p)
     if (last || i + 1 == kSlice) {
       if (on) {
         if (head || !last) {
-          store_row<V>(p.part + (s * 2 + (head ? 0 : 1)) * p.dim + col, acc);
+          store_row<V>(p.part + (s * 2 + (head ? 0 : 1)) * p.dim + col, acc, left);
         } else {
-          write_grad<G, V>(static_cast<G*>(p.dweight) + k * p.dim + col, acc, p.scale, p.accumulate != 0);
+          write_grad<G, V>(static_cast<G*>(p.dweight) + k * p.dim + col, acc, p.scale, p.accumulate != 0, left);
         }
       }
       head = false;
@@ -400,7 +384,8 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedGradParams p)
   }
   const int parts = static_cast<int>(have - s) + 1;          // the first from the second half of its line
   const int64_t col = (static_cast<int64_t>(blockIdx.y) * kLanes + lane) * V;
-  const bool on = col < p.dim;
+  const int64_t left = p.dim - col;
+  const bool on = left > 0;
   const int quarter = (parts + kWaves - 1) / kWaves;
   const int end = (wave + 1) * quarter < parts ? (wave + 1) * quarter : parts;
   float acc[V];
@@ -410,7 +395,7 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedGradParams p)
 #pragma unroll 8
     for (int k = wave * quarter; k < end; ++k) {
       float v[V];
-      load_row<V>(p.part + ((s + k) * 2 + (k == 0 ? 1 : 0)) * p.dim + col, v);
+      load_row<V>(p.part + ((s + k) * 2 + (k == 0 ? 1 : 0)) * p.dim + col, v, left);
 #pragma unroll
       for (int j = 0; j < V; ++j) acc[j] += v[j];
     }
@@ -423,7 +408,7 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedGradParams p)
   for (int w = 1; w < kWaves; ++w)
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] += red[w][j * kLanes + lane];
-  write_grad<G, V>(static_cast<G*>(p.dweight) + key * p.dim + col, acc, p.scale, p.accumulate != 0);
+  write_grad<G, V>(static_cast<G*>(p.dweight) + key * p.dim + col, acc, p.scale, p.accumulate != 0, left);
 }
 
 int sort_passes(int64_t vocab, int* bits) {
@@ -436,28 +421,14 @@ int sort_passes(int64_t vocab, int* bits) {
 
 constexpr size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
-template <typename F> hipError_t launch_width(int v, F&& f) {
-  switch (v) {
-    case 8: f(std::integral_constant<int, 8>{}); break;
-    case 4: f(std::integral_constant<int, 4>{}); break;
-    case 2: f(std::integral_constant<int, 2>{}); break;
-    default: f(std::integral_constant<int, 1>{}); break;
-  }
-  return hipGetLastError();
-}
-
 template <typename T> hipError_t embed_fwd_t(const EmbedArgs& a, hipStream_t stream) {
   EmbedParams p{a.ids, a.id_bytes, a.scale, a.tokens, a.vocab, a.dim, a.weight, a.out};
-  const void* ptrs[] = {a.weight, a.out};
-  const int es[] = {sizeof(T), sizeof(T)};
-  const int v = vector_width(a.dim, ptrs, es, 2, 16 / sizeof(T));
-  return launch_width(v, [&](auto V) {
-    constexpr int kV = decltype(V)::value > static_cast<int>(16 / sizeof(T)) ? 1 : decltype(V)::value;
-    if (a.tokens < 4096)
-      embed_kernel<T, kV, kWaves><<<dim3(static_cast<unsigned>(a.tokens)), kThreads, 0, stream>>>(p);
-    else
-      embed_kernel<T, kV, 1><<<dim3(static_cast<unsigned>((a.tokens + kWaves - 1) / kWaves)), kThreads, 0, stream>>>(p);
-  });
+  constexpr int kV = 16 / sizeof(T);
+  if (a.tokens < 4096)
+    embed_kernel<T, kV, kWaves><<<dim3(static_cast<unsigned>(a.tokens)), kThreads, 0, stream>>>(p);
+  else
+    embed_kernel<T, kV, 1><<<dim3(static_cast<unsigned>((a.tokens + kWaves - 1) / kWaves)), kThreads, 0, stream>>>(p);
+  return hipGetLastError();
 }
 
 template <typename T, typename G> hipError_t embed_bwd_t(const EmbedArgs& a, hipStream_t stream) {
@@ -481,6 +452,7 @@ template <typename T, typename G> hipError_t embed_bwd_t(const EmbedArgs& a, hip
     G* const dw = static_cast<G*>(a.dweight);
     if (n <= kLdsThreads) sort_lds_kernel<G, 1><<<grid, kLdsThreads, 0, stream>>>(sp, dw);
     else if (n <= 4 * kLdsThreads) sort_lds_kernel<G, 4><<<grid, kLdsThreads, 0, stream>>>(sp, dw);
+    else if (n <= 8 * kLdsThreads) sort_lds_kernel<G, 8><<<grid, kLdsThreads, 0, stream>>>(sp, dw);
     else sort_lds_kernel<G, 16><<<grid, kLdsThreads, 0, stream>>>(sp, dw);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -517,17 +489,13 @@ template <typename T, typename G> hipError_t embed_bwd_t(const EmbedArgs& a, hip
   p.dout = a.dout; p.dweight = a.dweight; p.part = part;
   p.scale = a.scale; p.dim = a.dim; p.n = n; p.slices = (n + kSlice - 1) / kSlice;
   p.vocab = static_cast<uint32_t>(a.vocab); p.accumulate = a.accumulate;
-  const void* ptrs[] = {a.dout, a.dweight, part};
-  const int es[] = {sizeof(T), sizeof(G), 4};
-  const int v = vector_width(a.dim, ptrs, es, 3, 16 / sizeof(T));
-  return launch_width(v, [&](auto V) {
-    constexpr int kV = decltype(V)::value > static_cast<int>(16 / sizeof(T)) ? 1 : decltype(V)::value;
-    const unsigned chunks = static_cast<unsigned>((a.dim + kLanes * kV - 1) / (kLanes * kV));
-    embed_grad_kernel<T, G, kV><<<dim3(static_cast<unsigned>((p.slices + kWaves - 1) / kWaves), chunks), kThreads, 0,
-                                  stream>>>(p);
-    if (p.slices > 1)
-      embed_join_kernel<G, kV><<<dim3(static_cast<unsigned>(p.slices - 1), chunks), kThreads, 0, stream>>>(p);
-  });
+  constexpr int kV = 16 / sizeof(T);
+  const unsigned chunks = static_cast<unsigned>((a.dim + kLanes * kV - 1) / (kLanes * kV));
+  embed_grad_kernel<T, G, kV><<<dim3(static_cast<unsigned>((p.slices + kWaves - 1) / kWaves), chunks), kThreads, 0,
+                                stream>>>(p);
+  if (p.slices > 1)
+    embed_join_kernel<G, kV><<<dim3(static_cast<unsigned>(p.slices - 1), chunks), kThreads, 0, stream>>>(p);
+  return hipGetLastError();
 }
 
 }  // namespace

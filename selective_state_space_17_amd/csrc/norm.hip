@@ -8,11 +8,12 @@
 //   dw   = sum_rows dout xh,   db = sum_rows dout
 //
 // Bound by memory: a row is read once and kept in registers between its statistics and its output, so every
-// tensor crosses HBM once.  A row belongs to one wave (up to 1024 columns) or one workgroup (up to 16
-// thousand); each thread owns the same columns of every row it visits.  In the backward pass the workgroups
+// tensor crosses HBM once.  A row belongs to one wave (up to 1024 columns) or one workgroup (up to 16384); each thread owns the same columns of every row it visits.  In the backward pass the workgroups
 // walk over rows and keep their columns' dw and db in registers, write them once as partial sums, and a
 // second kernel adds the partial sums in a fixed order: no atomics, the same result on every run.
 // Statistics, sums and gradients are fp32 whatever the types.
+#include <type_traits>
+
 #include "device_util.h"
 #include "internal.h"
 
@@ -81,18 +82,17 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_fwd_kernel(NormParams 
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int col = (c * tr + tid) * V;
-#pragma unroll
-    for (int i = 0; i < V; ++i) h[c][i] = 0.f;
-    if (col < p.dim) {
-      load_row<V>(static_cast<const T*>(p.x) + base + col, h[c]);
+    const int left = p.dim - col;
+    load_row<V>(static_cast<const T*>(p.x) + base + col, h[c], left);
+    if (left > 0) {
       if (p.residual != nullptr) {
         float r[V];
-        load_row<V>(static_cast<const R*>(p.residual) + base + col, r);
+        load_row<V>(static_cast<const R*>(p.residual) + base + col, r, left);
 #pragma unroll
         for (int i = 0; i < V; ++i) h[c][i] += r[i];
       }
       if (p.residual_out != nullptr) {
-        store_row<V>(static_cast<R*>(p.residual_out) + base + col, h[c]);
+        store_row<V>(static_cast<R*>(p.residual_out) + base + col, h[c], left);
 #pragma unroll
         for (int i = 0; i < V; ++i) h[c][i] = rounded<R>(h[c][i]);
       }
@@ -106,19 +106,19 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_fwd_kernel(NormParams 
     float s = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const bool on = (c * tr + tid) * V < p.dim;
+      const int left = p.dim - (c * tr + tid) * V;
 #pragma unroll
-      for (int i = 0; i < V; ++i) s += on ? h[c][i] - first : 0.f;
+      for (int i = 0; i < V; ++i) s += i < left ? h[c][i] - first : 0.f;
     }
     mu = first + row_sum<WAVE>(s, red, 0) * inv;
   }
   float q = 0.f;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const bool on = (c * tr + tid) * V < p.dim;
+    const int left = p.dim - (c * tr + tid) * V;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float d = on ? h[c][i] - mu : 0.f;
+      const float d = i < left ? h[c][i] - mu : 0.f;
       q = __builtin_fmaf(d, d, q);
     }
   }
@@ -130,18 +130,19 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_fwd_kernel(NormParams 
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int col = (c * tr + tid) * V;
-    if (col < p.dim) {
+    const int left = p.dim - col;
+    if (left > 0) {
       float w[V], y[V];
-      load_row<V>(p.weight + col, w);
+      load_row<V>(p.weight + col, w, left);
 #pragma unroll
       for (int i = 0; i < V; ++i) y[i] = (h[c][i] - mu) * rs * w[i];
       if (p.bias != nullptr) {
         float b[V];
-        load_row<V>(p.bias + col, b);
+        load_row<V>(p.bias + col, b, left);
 #pragma unroll
         for (int i = 0; i < V; ++i) y[i] += b[i];
       }
-      store_row<V>(static_cast<T*>(p.out) + base + col, y);
+      store_row<V>(static_cast<T*>(p.out) + base + col, y, left);
     }
   }
 }
@@ -160,8 +161,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormParams 
   for (int c = 0; c < C; ++c) {
     const int col = (c * tr + tid) * V;
 #pragma unroll
-    for (int i = 0; i < V; ++i) dw[c][i] = db[c][i] = w[c][i] = 0.f;
-    if (col < p.dim) load_row<V>(p.weight + col, w[c]);
+    for (int i = 0; i < V; ++i) dw[c][i] = db[c][i] = 0.f;
+    load_row<V>(p.weight + col, w[c], p.dim - col);
   }
   int turn = 0;
   for (int64_t row = group; row < p.rows; row += groups, turn ^= 2) {
@@ -172,11 +173,10 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormParams 
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int col = (c * tr + tid) * V;
-#pragma unroll
-      for (int i = 0; i < V; ++i) xh[c][i] = g[c][i] = 0.f;
-      if (col < p.dim) {
-        load_row<V>(static_cast<const R*>(p.h) + base + col, xh[c]);
-        load_row<V>(static_cast<const T*>(p.dout) + base + col, g[c]);
+      const int left = p.dim - col;
+      load_row<V>(static_cast<const R*>(p.h) + base + col, xh[c], left);
+      load_row<V>(static_cast<const T*>(p.dout) + base + col, g[c], left);   // zeros past the row's end
+      if (left > 0) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           xh[c][i] = (xh[c][i] - mu) * rs;
@@ -193,18 +193,19 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormParams 
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int col = (c * tr + tid) * V;
-      if (col < p.dim) {
+      const int left = p.dim - col;
+      if (left > 0) {
         float d[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) d[i] = rs * (g[c][i] - xh[c][i] * s1 - s2);
         if (p.dresidual != nullptr) {
           float r[V];
-          load_row<V>(static_cast<const R*>(p.dresidual) + base + col, r);
+          load_row<V>(static_cast<const R*>(p.dresidual) + base + col, r, left);
 #pragma unroll
           for (int i = 0; i < V; ++i) d[i] += r[i];
         }
-        if (p.dx != nullptr) store_row<V>(static_cast<T*>(p.dx) + base + col, d);
-        if (p.dresidual_in != nullptr) store_row<V>(static_cast<R*>(p.dresidual_in) + base + col, d);
+        if (p.dx != nullptr) store_row<V>(static_cast<T*>(p.dx) + base + col, d, left);
+        if (p.dresidual_in != nullptr) store_row<V>(static_cast<R*>(p.dresidual_in) + base + col, d, left);
       }
     }
   }
@@ -240,10 +241,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormParams 
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int col = (c * tr + tid) * V;
-    if (col < p.dim) {
-      store_row<V>(out + col, dw[c]);
-      if (p.layer) store_row<V>(out + p.dim + col, db[c]);
-    }
+    store_row<V>(out + col, dw[c], p.dim - col);
+    if (p.layer) store_row<V>(out + p.dim + col, db[c], p.dim - col);
   }
 }
 
@@ -347,29 +346,26 @@ __global__ __launch_bounds__(kSumWaves * kLanes) void norm_sum_kernel(const floa
 }
 
 // ---------------------------------------------------------------------------------------------- plan
-// V elements per access, C accesses per thread and row, whether a row is one wave, threads per workgroup
+// C accesses of kVec elements per thread and row, whether a row is one wave, threads per workgroup
+constexpr int kVec = 8, kMostC = 2;
 struct NormPlan {
-  int V = 0, C = 0, threads = 0;
+  int C = 0, threads = 0;
   bool wave = false, wide = false;
 };
 
-NormPlan norm_plan(int64_t dim, int v) {
+NormPlan norm_plan(int64_t dim) {
   NormPlan n;
-  n.V = v;
-  const int64_t chunks = dim / v;
-  const int most = v == 8 ? 2 : 4;
-  if (chunks <= kLanes * most) {
+  const int64_t chunks = (dim + kVec - 1) / kVec;
+  if (chunks <= kLanes * kMostC) {
     n.wave = true;
     n.threads = 256;
     n.C = static_cast<int>((chunks + kLanes - 1) / kLanes);
   } else {
-    n.C = 1;
-    while (n.C < most && chunks > int64_t{n.C} * 256) n.C *= 2;
+    n.C = chunks > 256 ? 2 : 1;
     const int64_t t = ((chunks + n.C - 1) / n.C + kLanes - 1) / kLanes * kLanes;
     n.wide = t > kMaxWaves * kLanes;
     n.threads = static_cast<int>(t);
   }
-  if (n.C == 3) n.C = 4;
   return n;
 }
 
@@ -378,20 +374,15 @@ NormPlan norm_plan(int64_t dim, int v) {
 int64_t norm_groups(int64_t rows) { return rows < 1024 ? rows : 1024; }
 
 template <typename K> hipError_t norm_dispatch(const NormPlan& n, K&& k) {
-#define MSSM_NORM_CASE(v, c)                                                                      \
-  if (n.V == v && n.C == c) {                                                                     \
-    if (n.wave) k(std::integral_constant<int, v>{}, std::integral_constant<int, c>{}, std::true_type{});  \
-    else k(std::integral_constant<int, v>{}, std::integral_constant<int, c>{}, std::false_type{});        \
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
+  if (n.wave) {
+    if (n.C == 1) k(One{}, std::true_type{});
+    else k(Two{}, std::true_type{});
+  } else {
+    if (n.C == 1) k(One{}, std::false_type{});
+    else k(Two{}, std::false_type{});
   }
-  MSSM_NORM_CASE(8, 1)
-  MSSM_NORM_CASE(8, 2)
-  MSSM_NORM_CASE(2, 1)
-  MSSM_NORM_CASE(2, 2)
-  MSSM_NORM_CASE(2, 4)
-  MSSM_NORM_CASE(1, 1)
-  MSSM_NORM_CASE(1, 2)
-  MSSM_NORM_CASE(1, 4)
-#undef MSSM_NORM_CASE
   return hipGetLastError();
 }
 
@@ -405,32 +396,23 @@ NormParams params(const NormArgs& a) {
   return p;
 }
 
-int norm_width(int64_t dim, const void* const* ptrs, const int* es, int n) {
-  const int v = vector_width(dim, ptrs, es, n, 8);
-  return v == 4 ? 2 : v;
-}
-
 template <typename T, typename R> hipError_t norm_fwd_t(const NormArgs& a, hipStream_t stream) {
   const NormParams p = params(a);
-  const void* ptrs[] = {a.x, a.residual, a.weight, a.bias, a.out, a.residual_out};
-  const int es[] = {sizeof(T), sizeof(R), 4, 4, sizeof(T), sizeof(R)};
-  const NormPlan n = norm_plan(a.dim, norm_width(a.dim, ptrs, es, 6));
+  const NormPlan n = norm_plan(a.dim);
   if (n.wide) {
     norm_fwd_wide_kernel<T, R><<<dim3(static_cast<unsigned>(a.rows)), kWideThreads, 0, stream>>>(p);
     return hipGetLastError();
   }
   const int64_t blocks = n.wave ? (a.rows + 3) / 4 : a.rows;
-  return norm_dispatch(n, [&](auto V, auto C, auto W) {
-    norm_fwd_kernel<T, R, decltype(V)::value, decltype(C)::value, decltype(W)::value>
+  return norm_dispatch(n, [&](auto C, auto W) {
+    norm_fwd_kernel<T, R, kVec, decltype(C)::value, decltype(W)::value>
         <<<dim3(static_cast<unsigned>(blocks)), n.threads, 0, stream>>>(p);
   });
 }
 
 template <typename T, typename R> hipError_t norm_bwd_t(const NormArgs& a, hipStream_t stream) {
   const NormParams p = params(a);
-  const void* ptrs[] = {a.h, a.dout, a.dresidual, a.weight, a.dx, a.dresidual_in, a.workspace};
-  const int es[] = {sizeof(R), sizeof(T), sizeof(R), 4, sizeof(T), sizeof(R), 4};
-  const NormPlan n = norm_plan(a.dim, norm_width(a.dim, ptrs, es, 7));
+  const NormPlan n = norm_plan(a.dim);
   int64_t groups = norm_groups(n.wave ? (a.rows + 3) / 4 : a.rows);
   hipError_t e = hipSuccess;
   if (a.rows == 0) {
@@ -442,8 +424,8 @@ template <typename T, typename R> hipError_t norm_bwd_t(const NormArgs& a, hipSt
                                        static_cast<unsigned>(groups)), kColThreads, 0, stream>>>(p);
     e = hipGetLastError();
   } else {
-    e = norm_dispatch(n, [&](auto V, auto C, auto W) {
-      norm_bwd_kernel<T, R, decltype(V)::value, decltype(C)::value, decltype(W)::value>
+    e = norm_dispatch(n, [&](auto C, auto W) {
+      norm_bwd_kernel<T, R, kVec, decltype(C)::value, decltype(W)::value>
           <<<dim3(static_cast<unsigned>(groups)), n.threads, 0, stream>>>(p);
     });
   }

@@ -110,7 +110,7 @@ struct ProductParams {
   const int* rows;         // compacted -> token
   void* out;               // dx or dW
   int64_t dim;
-  int out_f32, accumulate, vec;
+  int out_f32, accumulate;
 };
 
 enum { kLogits = 0, kGradLogits = 1, kGradX = 2, kGradW = 3 };
@@ -132,20 +132,13 @@ __device__ __forceinline__ void put_four(const ProductParams& p, int64_t row, in
     }
   }
   auto put = [&](auto* to) {
-    using T = std::remove_reference_t<decltype(*to)>;
-    if (p.vec) {   // dim and the pointer allow four elements at once; m is a multiple of 4
-      if (EPI == kGradW && p.accumulate) {
-        float o[4];
-        load_row<4>(to, o);
+    if (EPI == kGradW && p.accumulate) {
+      float o[4];
+      load_row<4>(to, o, p.M - m);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += o[e];
-      }
-      store_row<4>(to, v);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (m + e < p.M) to[e] = narrow<T>(EPI == kGradW && p.accumulate ? v[e] + widen(to[e]) : v[e]);
+      for (int e = 0; e < 4; ++e) v[e] += o[e];
     }
+    store_row<4>(to, v, p.M - m);
   };
   if (SPLIT || p.out_f32) put(static_cast<float*>(p.out) + row * p.dim + m);
   else put(static_cast<uint16_t*>(p.out) + row * p.dim + m);
@@ -547,7 +540,6 @@ struct PrepParams {
   int id_bytes;
   int64_t ignore, vocab, tokens, dim, dpad, tok_cap;
   const void* x;
-  int vec;                 // x is read 16 bytes at a time
   uint16_t* xc;            // panels [term][dpad / 64][tok_cap][64]
   int* tally;              // counted tokens of each group of kGroup, or null: counted again where needed
   int* plan;               // written: the count, and the slices of dx, of dW, of the last piece's dW
@@ -605,11 +597,11 @@ __global__ __launch_bounds__(256) void tally_kernel(PrepParams p) {
 
 // 8 elements of a row, laid out: bf16 as it is, fp32 as three terms; past the row's end zeros
 template <typename T>
-__device__ __forceinline__ void lay_out(const T* row, int64_t col, int64_t dim, bool vec, uint16_t* to, int64_t term) {
+__device__ __forceinline__ void lay_out(const T* row, int64_t col, int64_t dim, uint16_t* to, int64_t term) {
   if constexpr (sizeof(T) == 2) {
     u32x4_t v = {0, 0, 0, 0};
-    if (vec && col + 8 <= dim) {
-      v = *reinterpret_cast<const u32x4_t*>(row + col);
+    if (col + 8 <= dim) {
+      v = *reinterpret_cast<const u32x4_u*>(row + col);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -618,12 +610,7 @@ __device__ __forceinline__ void lay_out(const T* row, int64_t col, int64_t dim, 
     *reinterpret_cast<u32x4_t*>(to) = v;
   } else {
     float f[8];
-    if (vec && col + 8 <= dim) {
-      load_row<8>(row + col, f);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = col + e < dim ? row[col + e] : 0.f;
-    }
+    load_row<8>(row + col, f, dim - col);
     uint16_t t[8][kTerms];
 #pragma unroll
     for (int e = 0; e < 8; ++e) split3(f[e], t[e]);
@@ -660,7 +647,7 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
   auto put = [&](int64_t i, int64_t t, bool real) {
     const T* row = static_cast<const T*>(p.x) + t * p.dim;
     for (int64_t c = lane * 8; c < p.dpad; c += kLanes * 8)
-      lay_out<T>(row, c, real ? p.dim : 0, p.vec != 0, p.xc + (c / 64 * (p.tok_cap + kSkew) + i) * 64 + c % 64, term);
+      lay_out<T>(row, c, real ? p.dim : 0, p.xc + (c / 64 * (p.tok_cap + kSkew) + i) * 64 + c % 64, term);
   };
   if (pad) {
     if (blockIdx.x == static_cast<unsigned>(p.work_blocks) && threadIdx.x < 4) {
@@ -713,12 +700,11 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
 // rows of the weight as the products read them (width not a multiple of 64, or fp32), in panels
 // [term][dpad / 64][rows][64]: 32 rows a workgroup
 template <typename T>
-__global__ __launch_bounds__(256) void weight_kernel(const T* w, uint16_t* to, int64_t rows, int64_t dim, int64_t dpad,
-                                                     int vec) {
+__global__ __launch_bounds__(256) void weight_kernel(const T* w, uint16_t* to, int64_t rows, int64_t dim, int64_t dpad) {
   const int64_t r = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x / 8;
   if (r >= rows) return;
   for (int64_t c = threadIdx.x % 8 * 8; c < dpad; c += 64)
-    lay_out<T>(w + r * dim, c, dim, vec != 0, to + (c / 64 * (rows + kSkew) + r) * 64 + c % 64, (rows + kSkew) * dpad);
+    lay_out<T>(w + r * dim, c, dim, to + (c / 64 * (rows + kSkew) + r) * 64 + c % 64, (rows + kSkew) * dpad);
 }
 
 // Joins the tiles' (maximum, sum) of a piece with those of the pieces before it; after the last piece, the loss.
@@ -898,7 +884,6 @@ template <typename T> hipError_t prep(const XentArgs& a, const XentPlan& n, unsi
   } else {
     p.loss = a.loss; p.lse_out = a.lse;
   }
-  p.vec = a.dim % (16 / sizeof(T)) == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
   // a few thousand tokens are counted again by every workgroup; more are counted group by group first
   if (a.tokens > 2 * kGroup) {
     p.tally = reinterpret_cast<int*>(ws + n.off_tally);
@@ -926,9 +911,8 @@ template <typename T>
 hipError_t lay_out_weight(const XentArgs& a, const XentPlan& n, unsigned char* ws, int64_t v0, int64_t rows,
                           hipStream_t stream) {
   if (!n.copy_w) return hipSuccess;
-  const int vec = a.dim % (16 / sizeof(T)) == 0 && reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
   weight_kernel<T><<<dim3(static_cast<unsigned>((rows + 31) / 32)), 256, 0, stream>>>(
-      static_cast<const T*>(a.weight) + v0 * a.dim, reinterpret_cast<uint16_t*>(ws + n.off_w), rows, a.dim, n.dpad, vec);
+      static_cast<const T*>(a.weight) + v0 * a.dim, reinterpret_cast<uint16_t*>(ws + n.off_w), rows, a.dim, n.dpad);
   return hipGetLastError();
 }
 
@@ -1015,7 +999,6 @@ template <typename T> hipError_t xent_bwd_t(const XentArgs& a, hipStream_t strea
       q.first = k == 0; q.last = k + 1 == n.pieces;
       q.rows = reinterpret_cast<int*>(ws + n.off_rows);
       q.out = a.dx; q.dim = a.dim; q.out_f32 = kSplit;
-      q.vec = a.dim % 4 == 0 && reinterpret_cast<uintptr_t>(a.dx) % (4 * sizeof(T)) == 0;
       q.sums = reinterpret_cast<float*>(ws + n.off_sums);
       if (n.pieces > 1) {
         q.over = reinterpret_cast<float*>(ws + n.off_over);
@@ -1034,7 +1017,6 @@ template <typename T> hipError_t xent_bwd_t(const XentArgs& a, hipStream_t strea
       q.k_is_tokens = 1;
       q.out = static_cast<unsigned char*>(a.dweight) + v0 * a.dim * gs;
       q.dim = a.dim; q.out_f32 = gs == 4; q.accumulate = a.accumulate;
-      q.vec = a.dim % 4 == 0 && reinterpret_cast<uintptr_t>(a.dweight) % (4 * gs) == 0;
       q.slices_at = k + 1 == n.pieces ? 3 : 2;
       q.sums = reinterpret_cast<float*>(ws + n.off_sums);
       e = product_any<true, true, kSplit, kGradW>(n.gw, q, stream);
