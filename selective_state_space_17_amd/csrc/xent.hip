@@ -115,6 +115,20 @@ struct ProductParams {
 
 enum { kLogits = 0, kGradLogits = 1, kGradX = 2, kGradW = 3 };
 
+// Rows 4 q .. 4 q + 3 of two neighbouring row tiles (as bf16; q: the lane's sixteen) to rows 8 q .. 8 q + 7 of the
+// 32 rows that they form: tile and q's high bit change places, then that and q's low bit.
+__device__ __forceinline__ u32x4_t two_tiles(u32x2_t a, u32x2_t b) {
+  u32x4_t v;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto s = __builtin_amdgcn_permlane32_swap(a[i], b[i], false, false);
+    const auto t = __builtin_amdgcn_permlane16_swap(s[0], s[1], false, false);
+    v[i] = t[0];
+    v[2 + i] = t[1];
+  }
+  return v;
+}
+
 // Four neighbouring elements (m .. m + 3, of row n of the other side) of a product's output, to where they belong.
 template <bool SPLIT, int EPI>
 __device__ __forceinline__ void put_four(const ProductParams& p, int64_t row, int n, int m, float (&v)[4]) {
@@ -173,8 +187,9 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
 
   // Jobs.  Whole tiles as long as every workgroup gets one; the tiles of the last, partial round are cut along
   // k where that fills the chip, each slice with sums of its own that are added afterwards.  Workgroups b,
-  // b + 8, ... share an XCD and its L2: each XCD takes a contiguous range of an order that walks bands of 8
-  // n-tiles, m outer, so that what runs on it at one time is a block of few m-tiles by 8 n-tiles.
+  // b + 8, ... share an XCD and its L2: each XCD takes a contiguous range of an order that walks bands of 4
+  // n-tiles, m outer, so that what runs on it at one time is a block of 8 m-tiles by 4 n-tiles (bands of 16: 2 %
+  // slower, of 8: 1 %).
   const int tiles_m = (p.M + BM - 1) / BM;
   const int tiles_n = ((p.n_is_tokens ? count : p.N) + BN - 1) / BN;
   const int tiles = tiles_m * tiles_n;
@@ -206,11 +221,11 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
       j.begin = static_cast<int>(static_cast<int64_t>(all) * slice / slices);
       j.steps = static_cast<int>(static_cast<int64_t>(all) * (slice + 1) / slices) - j.begin;
     }
-    const int band = tile / (tiles_m * 8);
-    const int left = tiles_n - band * 8, wide = left < 8 ? left : 8;
-    const int in_band = tile - band * tiles_m * 8;
+    const int band = tile / (tiles_m * 4);
+    const int left = tiles_n - band * 4, wide = left < 4 ? left : 4;
+    const int in_band = tile - band * tiles_m * 4;
     j.m0 = in_band / wide * BM;
-    j.n0 = (band * 8 + in_band % wide) * BN;
+    j.n0 = (band * 4 + in_band % wide) * BN;
     return j;
   };
 
@@ -442,21 +457,31 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
         const int y = p.tgt[n] - p.v0;
         if (__ballot(y >= wave_m && y < wave_m + TM * 16) != 0) each(j, [&](float a, int m) { return a - (m == y ? g : 0.f); });
         if (m0 + BM > p.M || n0 + BN > count) each(j, [&](float a, int m) { return n < count && m < p.M ? a : 0.f; });
+        // two row tiles together: a lane gets 8 neighbouring elements, the four lanes of a token 64 bytes
+        uint16_t* const to = p.dl + (wave_m / 64 * (p.tok_cap + kSkew) + n) * 64 + lane / 16 * 8;
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          const f32x4_t d = acc[i][j];
-          const int m = mrow + i * 16;
-          uint16_t* const to = p.dl + (m / 64 * (p.tok_cap + kSkew) + n) * 64 + m % 64;
+        for (int i = 0; i < TM; i += 2) {
+          uint16_t* const at = to + (i / 4 * (p.tok_cap + kSkew)) * 64 + i % 4 * 16;
           if constexpr (SPLIT) {
-            uint16_t t[4][kTerms];
+            uint16_t t[2][4][kTerms];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) split3(d[e], t[e]);
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int k = 0; k < kTerms; ++k)
-              *reinterpret_cast<u32x2_t*>(to + k * p.pdl) =
-                  u32x2_t{t[0][k] | static_cast<uint32_t>(t[1][k]) << 16, t[2][k] | static_cast<uint32_t>(t[3][k]) << 16};
+              for (int e = 0; e < 4; ++e) split3(acc[i + h][j][e], t[h][e]);
+#pragma unroll
+            for (int k = 0; k < kTerms; ++k) {
+              u32x2_t d[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                d[h] = u32x2_t{t[h][0][k] | static_cast<uint32_t>(t[h][1][k]) << 16,
+                               t[h][2][k] | static_cast<uint32_t>(t[h][3][k]) << 16};
+              *reinterpret_cast<u32x4_t*>(at + k * p.pdl) = two_tiles(d[0], d[1]);
+            }
           } else {
-            *reinterpret_cast<u32x2_t*>(to) = u32x2_t{pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3])};
+            const f32x4_t x = acc[i][j], y = acc[i + 1][j];
+            *reinterpret_cast<u32x4_t*>(at) =
+                two_tiles(u32x2_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])},
+                          u32x2_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])});
           }
         }
       }
@@ -496,10 +521,10 @@ __global__ __launch_bounds__(256) void sum_kernel(ProductParams p, int slots) {
   const int t = blockIdx.x / kShares;
   if (t >= rest) return;
   const int tile = tiles - rest + t;
-  const int band = tile / (tiles_m * 8);
-  const int left = tiles_n - band * 8, wide = left < 8 ? left : 8;
-  const int in_band = tile - band * tiles_m * 8;
-  const int m = in_band / wide * BM + threadIdx.x % (BM / 4) * 4, n0 = (band * 8 + in_band % wide) * BN;
+  const int band = tile / (tiles_m * 4);
+  const int left = tiles_n - band * 4, wide = left < 4 ? left : 4;
+  const int in_band = tile - band * tiles_m * 4;
+  const int m = in_band / wide * BM + threadIdx.x % (BM / 4) * 4, n0 = (band * 4 + in_band % wide) * BN;
   if (m >= p.M) return;
   constexpr int kRows = BN / kShares, kAtOnce = 256 / (BM / 4);
   const int first = blockIdx.x % kShares * kRows + threadIdx.x / (BM / 4);
