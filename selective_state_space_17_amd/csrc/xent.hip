@@ -17,11 +17,14 @@
 // transposing LDS reads.  Tiles go from global memory straight into LDS.
 //
 // bf16 inputs enter the matrix cores as they are; products are summed in fp32.  G is rounded to bf16 (the
-// gradients' own type) once.  fp32 inputs are split into three bf16 terms, v = hi + mid + lo with 24
-// significant bits in all, and a product is the six term products that matter,
-//   hi hi + hi mid + mid hi + hi lo + lo hi + mid mid
-// (what is left out is below 2^-24 of the product), summed in fp32 smallest first: six bf16 products at the
-// matrix cores' bf16 rate beat one product at their fp32 rate, a sixteenth of it.
+// gradients' own type) once; for up to 256 tokens, where few roundings average out and the weight's bytes are what
+// the time goes into, it is kept in two bf16 terms.
+// fp32 inputs are split into two fp16 terms, v s = hi + lo to within 2^-24 of v s, and a product is the three term
+// products hi lo + lo hi + hi hi (what is left out is below 2^-24 of the product), summed in fp32, smallest first.
+// s is a power of two for each matrix that brings its largest finite magnitude to [2^14, 2^15): fp16's range then
+// reaches 2^-40 below that, where a value's own 24 bits end.  Three fp16 products take a fifth of the time of one
+// product at the matrix cores' fp32 rate, a sixteenth of fp16's; with three bf16 terms and six products the fp32
+// step of 1001 x 1000 x 32003 took 1.47 ms.
 #include <type_traits>
 
 #include "device_util.h"
@@ -31,6 +34,7 @@ namespace mssm {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 
@@ -40,24 +44,21 @@ constexpr int kRow = kBK * 2;           // bytes of a row of a step
 constexpr int kPlane = 64 * kRow;       // LDS tiles are planes of 64 rows x 128 bytes
 constexpr int kTokTile = 256;           // compacted tokens are padded to this
 constexpr int kSkew = 34;               // rows between panels: 4352 bytes, see Operand
-constexpr int kTerms = 3;               // bf16 terms of an fp32 value
-constexpr int kPairs = 6;               // term products kept
-__device__ __constant__ const int kPairA[kPairs] = {2, 0, 1, 1, 0, 0};
-__device__ __constant__ const int kPairB[kPairs] = {0, 2, 1, 0, 1, 0};
+constexpr int kTerms = 2;               // 16-bit terms of an fp32 value
+constexpr int kMostPairs = 3;           // term products kept
+constexpr int kFewTokens = 256;         // up to these G is kept in two terms with bf16 too
 
-// v = t[0] + t[1] + t[2] exactly: each term is the nearest bf16 of what is left (8 + 8 + 8 significant bits),
-// |t[1]| <= 2^-8 |v|, |t[2]| <= 2^-16 |v|.  A finite v that would round to infinity is cut off instead;
-// infinities and NaN stay what they are.
-__device__ __forceinline__ void split3(float v, uint16_t (&t)[kTerms]) {
-  constexpr uint32_t kExp = 0x7f800000u;
-  const uint32_t u = __float_as_uint(v);
+// v (already scaled) = t[0] + t[1]: each the nearest fp16 of what is left.  Infinities and NaN stay what they are.
+__device__ __forceinline__ void split_half(float v, uint16_t (&t)[kTerms]) {
+  const _Float16 hi = static_cast<_Float16>(v);
+  const float r = v - static_cast<float>(hi);
+  t[0] = __builtin_bit_cast(uint16_t, hi);
+  t[1] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(r == r ? r : 0.f));   // (inf - inf)
+}
+__device__ __forceinline__ void split_bf(float v, uint16_t (&t)[kTerms]) {
   t[0] = narrow<uint16_t>(v);
-  t[1] = t[2] = 0;
-  if ((u & kExp) == kExp) return;
-  if ((t[0] & 0x7fffu) == 0x7f80u) t[0] = static_cast<uint16_t>(u >> 16);
   const float r = v - widen(t[0]);
-  t[1] = narrow<uint16_t>(r);
-  t[2] = narrow<uint16_t>(r - widen(t[1]));
+  t[1] = narrow<uint16_t>(r == r ? r : 0.f);
 }
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
@@ -85,12 +86,18 @@ struct Operand {
   int rows, planes;        // what may be read: rows, and (K-strided) panels of 64 columns
 };
 
+// What the kernels find in the workspace about the call.
+enum Plan { kCount = 0, kSlicesX = 1, kSlicesW = 2, kSlicesLastW = 3, kScaleW = 4, kScaleX = 5, kScaleG = 6, kPlanInts = 8 };
+
 struct ProductParams {
   Operand A, B;
   int M, N;                // rows of the output on either side (what lies past them is not stored)
   int K;                   // multiple of 64; with k_is_tokens: the compacted count, rounded up, instead
   int k_is_tokens, n_is_tokens;
-  const int* plan;         // [0]: compacted tokens
+  int pairs;               // term products, and the terms of either operand in each
+  int ta[kMostPairs], tb[kMostPairs];
+  const int* plan;         // see Plan
+  int scale_a, scale_b;    // which of its scales the operands carry (fp16 terms)
   int slices_at;           // where in plan the slices of the tiles of the last round stand; 0: not sliced
   // epilogues
   int v0;                  // first vocabulary row of this piece
@@ -101,7 +108,8 @@ struct ProductParams {
   const float* lse;        // compacted
   const float* gl;         // dloss + dlse
   const float* g;          // dloss
-  uint16_t* dl;            // panels [vocabulary / 64][token][64], one or three terms
+  int g_terms;
+  uint16_t* dl;            // panels [vocabulary / 64][token][64], one or two terms
   int64_t pdl;             // elements between them
   float* sums;             // [job][BN][BM]: a slice's sums
   float* over;             // [n][ld_over]: sums over pieces, or null
@@ -130,7 +138,7 @@ __device__ __forceinline__ u32x4_t two_tiles(u32x2_t a, u32x2_t b) {
 }
 
 // Four neighbouring elements (m .. m + 3, of row n of the other side) of a product's output, to where they belong.
-template <bool SPLIT, int EPI>
+template <int EPI>
 __device__ __forceinline__ void put_four(const ProductParams& p, int64_t row, int n, int m, float (&v)[4]) {
   if (EPI == kGradX && p.over != nullptr) {
     float* const to = p.over + n * p.ld_over + m;
@@ -154,7 +162,7 @@ __device__ __forceinline__ void put_four(const ProductParams& p, int64_t row, in
     }
     store_row<4>(to, v, p.M - m);
   };
-  if (SPLIT || p.out_f32) put(static_cast<float*>(p.out) + row * p.dim + m);
+  if (p.out_f32) put(static_cast<float*>(p.out) + row * p.dim + m);
   else put(static_cast<uint16_t*>(p.out) + row * p.dim + m);
 }
 
@@ -167,7 +175,7 @@ __device__ __forceinline__ void fence_schedule() { __builtin_amdgcn_sched_barrie
 // One workgroup stays on a CU (two of the small tile) and takes tile after tile.  The loads run two steps of
 // 64 k ahead of the matrix cores and cross tile borders: a tile's first steps are on their way while the
 // tile before it is finished and stored.
-template <int BM, int BN, int WM, int WN, bool ATR, bool BTR, bool SPLIT, int EPI>
+template <int BM, int BN, int WM, int WN, bool ATR, bool BTR, bool HALF, int EPI>
 __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) {
   constexpr int kW = WM * WN;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;      // 16 x 16 tiles of a wave
@@ -183,7 +191,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
   const int lane = threadIdx.x % kLanes;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
   const int wm = w / WN, wn = w % WN;
-  const int count = p.plan[0];
+  const int count = p.plan[kCount];
 
   // Jobs.  Whole tiles as long as every workgroup gets one; the tiles of the last, partial round are cut along
   // k where that fills the chip, each slice with sums of its own that are added afterwards.  Workgroups b,
@@ -201,7 +209,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
   const int mine = cut - xcd * cut8 < cut8 ? cut - xcd * cut8 : cut8;
   const int job_first = blockIdx.x / 8, job_end = whole8 + (mine > 0 ? mine : 0);
   const int steps1 = ((p.k_is_tokens ? count : p.K) + kBK - 1) / kBK;   // of one pair of terms
-  const int all = SPLIT ? steps1 * kPairs : steps1;
+  const int all = steps1 * p.pairs;
   struct Job {
     int m0, n0, sum, begin, steps;   // sum: which sums, or -1
   };
@@ -252,18 +260,21 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
     }
   };
   Job lj{};
+  auto start_pair = [&]() {
+    la = p.A.p + p.ta[lseg] * p.A.term + (ATR ? 0 : lj.m0 * p.A.row);
+    lb = p.B.p + p.tb[lseg] * p.B.term + (BTR ? 0 : lj.n0 * p.B.row);
+  };
   auto start_load = [&]() {   // the next job with steps, if there is one; else the last loads are repeated
     while (ljob < job_end) {
       const Job j = job_at(ljob);
       if (j.steps > 0) {
         lj = j;
         lleft = j.steps;
-        lseg = SPLIT ? j.begin / steps1 : 0;
+        lseg = j.begin / steps1;
         lk = j.begin - lseg * steps1;
         offsets(p.A, ATR, j.m0, oa);
         offsets(p.B, BTR, j.n0, ob);
-        la = p.A.p + (ATR ? 0 : j.m0 * p.A.row);
-        lb = p.B.p + (BTR ? 0 : j.n0 * p.B.row);
+        start_pair();
         return;
       }
       ljob += stride;
@@ -272,7 +283,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
   const uint32_t as_a = lds_addr(&as[0][0]), bs_a = lds_addr(&bs[0][0]);
   // load i of a step into buffer `buf`
   auto load_a = [&](int i, int buf) {
-    const unsigned char* a = la + lk * p.A.step + (SPLIT ? kPairA[lseg] * p.A.term : 0);
+    const unsigned char* a = la + lk * p.A.step;
     uint32_t o = oa[i];
     if constexpr (ATR) {
       const int plane = lj.m0 / 64 + i * kW / 8;
@@ -285,7 +296,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
     dma16(a, o, as_a + buf * kA + (i * kW + w) * 1024);
   };
   auto load_b = [&](int i, int buf) {
-    const unsigned char* b = lb + lk * p.B.step + (SPLIT ? kPairB[lseg] * p.B.term : 0);
+    const unsigned char* b = lb + lk * p.B.step;
     if constexpr (BTR) {
       const int plane = lj.n0 / 64 + i * kW / 8;
       b += (plane < p.B.planes ? plane : p.B.planes - 1) * p.B.plane;
@@ -302,6 +313,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
       if (++lk == steps1) {
         lk = 0;
         ++lseg;
+        start_pair();
       }
     } else if (ljob < job_end) {
       ljob += stride;
@@ -343,7 +355,11 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
   auto multiply_row = [&](int i, int set) {
 #pragma unroll
     for (int j = 0; j < TN; ++j)
-      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[set][i], fb[set][j], acc[i][j], 0, 0, 0);
+      if constexpr (HALF)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, fa[set][i]),
+                                                           __builtin_bit_cast(f16x8, fb[set][j]), acc[i][j], 0, 0, 0);
+      else
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[set][i], fb[set][j], acc[i][j], 0, 0, 0);
   };
 
   // ---- Two LDS buffers, two sets of fragments.  A step's second half is read while its first half is
@@ -410,6 +426,13 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
     const int wave_m = m0 + wm * TM * 16;
     const int mrow = wave_m + lane / 16 * 4;
     const int ncol = n0 + wn * TN * 16 + lane % 16;
+    // What undoes the operands' scales: exact powers of two, one after the other, since their product may lie
+    // outside fp32.  For the logits it is kept at 2^-126 or more: they are then as good as 0, but 0 times the
+    // mask's -inf would not be -inf.
+    const float* const scales = reinterpret_cast<const float*>(p.plan);
+    const float ua = HALF ? 1.f / scales[p.scale_a] : 1.f, ub = HALF ? 1.f / scales[p.scale_b] : 1.f;
+    const float unit = __builtin_fmaxf(ua * ub, 0x1p-126f);
+    const float to_log2 = kLog2e * unit;
     auto each = [&](int j, auto&& f) {   // accumulator = f(accumulator, row)
 #pragma unroll
       for (int i = 0; i < TM; ++i)
@@ -424,7 +447,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
         const int y = p.tgt[n] - p.v0;   // padded tokens have target -1
         if (__ballot(y >= wave_m && y < wave_m + TM * 16) != 0)
           each(j, [&](float a, int m) {
-            if (m == y) p.tlogit[n] = a;
+            if (m == y) p.tlogit[n] = a * unit;
             return a;
           });
         float mx = -__builtin_inff();
@@ -433,13 +456,13 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
           return a;
         });
         mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16, 64));
-        mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32, 64));
+        mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32, 64)) * unit;
         // exp(a - mx) = 2^(a log2e - c) 2^(c - mx log2e): one multiply-add an element, and the rounding of
         // c = mx log2e taken out of the sum once
         const float ref = mx == -__builtin_inff() ? 0.f : mx, c = ref * kLog2e;
         float s = 0.f;
         each(j, [&](float a, int) {
-          s += __builtin_amdgcn_exp2f(__builtin_fmaf(a, kLog2e, -c));
+          s += __builtin_amdgcn_exp2f(__builtin_fmaf(a, to_log2, -c));
           return a;
         });
         s += __shfl_xor(s, 16, 64);
@@ -451,9 +474,10 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
         const int n = ncol + j * 16;
-        const float lse = p.lse[n], g = p.g[n], c = lse * kLog2e;
-        const float gl = p.gl[n] * __builtin_amdgcn_exp2f(__builtin_fmaf(-lse, kLog2e, c));   // as in the forward pass
-        each(j, [&](float a, int) { return __builtin_amdgcn_exp2f(__builtin_fmaf(a, kLog2e, -c)) * gl; });
+        const float sg = HALF ? scales[kScaleG] : 1.f;
+        const float lse = p.lse[n], g = p.g[n] * sg, c = lse * kLog2e;
+        const float gl = p.gl[n] * sg * __builtin_amdgcn_exp2f(__builtin_fmaf(-lse, kLog2e, c));   // as in the forward pass
+        each(j, [&](float a, int) { return __builtin_amdgcn_exp2f(__builtin_fmaf(a, to_log2, -c)) * gl; });
         const int y = p.tgt[n] - p.v0;
         if (__ballot(y >= wave_m && y < wave_m + TM * 16) != 0) each(j, [&](float a, int m) { return a - (m == y ? g : 0.f); });
         if (m0 + BM > p.M || n0 + BN > count) each(j, [&](float a, int m) { return n < count && m < p.M ? a : 0.f; });
@@ -462,12 +486,15 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
 #pragma unroll
         for (int i = 0; i < TM; i += 2) {
           uint16_t* const at = to + (i / 4 * (p.tok_cap + kSkew)) * 64 + i % 4 * 16;
-          if constexpr (SPLIT) {
+          if (HALF || p.g_terms == 2) {
             uint16_t t[2][4][kTerms];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) split3(acc[i + h][j][e], t[h][e]);
+              for (int e = 0; e < 4; ++e) {
+                if constexpr (HALF) split_half(acc[i + h][j][e], t[h][e]);
+                else split_bf(acc[i + h][j][e], t[h][e]);
+              }
 #pragma unroll
             for (int k = 0; k < kTerms; ++k) {
               u32x2_t d[2];
@@ -492,15 +519,16 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
         if (cur.sum >= 0) {
           float* const to = p.sums + (static_cast<int64_t>(cur.sum) * BN + n - n0) * BM + mrow - m0;
 #pragma unroll
-          for (int i = 0; i < TM; ++i) *reinterpret_cast<f32x4_t*>(to + i * 16) = acc[i][j];
+          for (int i = 0; i < TM; ++i) *reinterpret_cast<f32x4_t*>(to + i * 16) = acc[i][j] * ua * ub;
           continue;
         }
         if (EPI == kGradX ? n >= count : n >= p.N) continue;
         const int64_t row = EPI == kGradX ? static_cast<int64_t>(p.rows[n]) : n;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-          float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-          if (mrow + i * 16 < p.M) put_four<SPLIT, EPI>(p, row, n, mrow + i * 16, v);
+          const f32x4_t d = acc[i][j] * ua * ub;
+          float v[4] = {d[0], d[1], d[2], d[3]};
+          if (mrow + i * 16 < p.M) put_four<EPI>(p, row, n, mrow + i * 16, v);
         }
       }
     }
@@ -511,9 +539,9 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
 
 // Adds the slices of the tiles of the last round, in order: workgroup (tile, share of its n).
 constexpr int kShares = 8;
-template <int BM, int BN, bool SPLIT, int EPI>
+template <int BM, int BN, int EPI>
 __global__ __launch_bounds__(256) void sum_kernel(ProductParams p, int slots) {
-  const int count = p.plan[0], slices = p.plan[p.slices_at];
+  const int count = p.plan[kCount], slices = p.plan[p.slices_at];
   if (slices == 1) return;
   const int tiles_m = (p.M + BM - 1) / BM;
   const int tiles_n = ((p.n_is_tokens ? count : p.N) + BN - 1) / BN;
@@ -539,7 +567,7 @@ __global__ __launch_bounds__(256) void sum_kernel(ProductParams p, int slots) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] += o[e];
     }
-    put_four<SPLIT, EPI>(p, EPI == kGradX ? static_cast<int64_t>(p.rows[n]) : n, n, m, v);
+    put_four<EPI>(p, EPI == kGradX ? static_cast<int64_t>(p.rows[n]) : n, n, m, v);
   }
 }
 
@@ -567,7 +595,7 @@ struct PrepParams {
   const void* x;
   uint16_t* xc;            // panels [term][dpad / 64][tok_cap][64]
   int* tally;              // counted tokens of each group of kGroup, or null: counted again where needed
-  int* plan;               // written: the count, and the slices of dx, of dW, of the last piece's dW
+  int* plan;               // written: the count and the slices; read: the scale of x
   int pairs, steps_x, tile_x, tile_w, tiles_mx, tiles_w, tiles_w_last;
   int* rows;
   int* tgt;
@@ -620,9 +648,10 @@ __global__ __launch_bounds__(256) void tally_kernel(PrepParams p) {
   if (threadIdx.x == 0) p.tally[blockIdx.x] = n;
 }
 
-// 8 elements of a row, laid out: bf16 as it is, fp32 as three terms; past the row's end zeros
+// 8 elements of a row, laid out: bf16 as it is, fp32 scaled and in two fp16 terms; past the row's end zeros
 template <typename T>
-__device__ __forceinline__ void lay_out(const T* row, int64_t col, int64_t dim, uint16_t* to, int64_t term) {
+__device__ __forceinline__ void lay_out(const T* row, int64_t col, int64_t dim, uint16_t* to, int64_t term,
+                                        float scale) {
   if constexpr (sizeof(T) == 2) {
     u32x4_t v = {0, 0, 0, 0};
     if (col + 8 <= dim) {
@@ -638,7 +667,7 @@ __device__ __forceinline__ void lay_out(const T* row, int64_t col, int64_t dim, 
     load_row<8>(row + col, f, dim - col);
     uint16_t t[8][kTerms];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) split3(f[e], t[e]);
+    for (int e = 0; e < 8; ++e) split_half(f[e] * scale, t[e]);
 #pragma unroll
     for (int k = 0; k < kTerms; ++k) {
       u32x4_t v;
@@ -649,8 +678,87 @@ __device__ __forceinline__ void lay_out(const T* row, int64_t col, int64_t dim, 
   }
 }
 
+// The largest finite magnitudes, of the weight, of the counted tokens' x and of their dloss and dloss + dlse
+// (fp32 only): each workgroup's, then all of them into the scales.
+struct RangeParams {
+  PrepParams prep;
+  const float* weight;
+  int64_t elems;
+  uint32_t* part;          // [kRangeBlocks][3]
+};
+constexpr int kRangeBlocks = 1024;
+
+__device__ __forceinline__ uint32_t magnitude(float v) {
+  const uint32_t m = __float_as_uint(v) & 0x7fffffffu;
+  return m < 0x7f800000u ? m : 0u;
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int step = 1; step < kLanes; step *= 2) {
+    const uint32_t o = __shfl_xor(v, step, kLanes);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+__global__ __launch_bounds__(256) void range_kernel(RangeParams r) {
+  __shared__ uint32_t red[4][3];
+  const PrepParams& p = r.prep;
+  const int wave = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+  uint32_t m[3] = {0, 0, 0};
+  auto scan = [&](const float* v, int64_t n, int64_t first, int64_t step, uint32_t& most) {
+#pragma unroll 4
+    for (int64_t i = first * 4; i < n; i += step * 4) {
+      float f[4];
+      load_row<4>(v + i, f, n - i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t a = magnitude(f[e]);
+        most = a > most ? a : most;
+      }
+    }
+  };
+  scan(r.weight, r.elems, static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, int64_t{kRangeBlocks} * 256, m[0]);
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave; t < p.tokens; t += kRangeBlocks * 4) {
+    if (!token_counts(p, t)) continue;
+    scan(static_cast<const float*>(p.x) + t * p.dim, p.dim, lane, kLanes, m[1]);
+    if (p.dloss != nullptr) {
+      const float g = p.dloss[t];
+      const uint32_t a = magnitude(g), b = magnitude(p.dlse != nullptr ? g + p.dlse[t] : g);
+      m[2] = a > m[2] ? a : m[2];
+      m[2] = b > m[2] ? b : m[2];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    m[k] = wave_max(m[k]);
+    if (lane == 0) red[wave][k] = m[k];
+  }
+  __syncthreads();
+  if (threadIdx.x < 3) {
+    uint32_t v = 0;
+    for (int w = 0; w < 4; ++w) v = red[w][threadIdx.x] > v ? red[w][threadIdx.x] : v;
+    r.part[blockIdx.x * 3 + threadIdx.x] = v;
+  }
+}
+
+// wave k: the scale that brings the k-th maximum to [2^14, 2^15), but at most 2^126
+__global__ __launch_bounds__(3 * kLanes) void scale_kernel(const uint32_t* part, int* plan) {
+  const int k = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kRangeBlocks / kLanes; ++i) {
+    const uint32_t v = part[(i * kLanes + lane) * 3 + k];
+    m = v > m ? v : m;
+  }
+  m = wave_max(m);
+  int e = 14 - (static_cast<int>(m >> 23) - 127);
+  e = m == 0 ? 0 : e > 126 ? 126 : e;
+  if (lane == 0) plan[kScaleW + k] = (e + 127) << 23;   // 2^e as fp32
+}
+
 // Which tokens count, in order, and their x as the products read it: in panels of 64 columns, padded with
-// zeros, fp32 as three bf16 terms; after the last one, zero rows up to the end of its tile of 256.
+// zeros, fp32 as two fp16 terms; after the last one, zero rows up to the end of its tile of 256.
 template <typename T>
 __global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
   __shared__ int red[4];
@@ -669,10 +777,11 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
   before = block_count(before, red);
 
   const int64_t term = (p.tok_cap + kSkew) * p.dpad;
+  const float scale = sizeof(T) == 2 ? 1.f : reinterpret_cast<const float*>(p.plan)[kScaleX];
   auto put = [&](int64_t i, int64_t t, bool real) {
     const T* row = static_cast<const T*>(p.x) + t * p.dim;
     for (int64_t c = lane * 8; c < p.dpad; c += kLanes * 8)
-      lay_out<T>(row, c, real ? p.dim : 0, p.xc + (c / 64 * (p.tok_cap + kSkew) + i) * 64 + c % 64, term);
+      lay_out<T>(row, c, real ? p.dim : 0, p.xc + (c / 64 * (p.tok_cap + kSkew) + i) * 64 + c % 64, term, scale);
   };
   if (pad) {
     if (blockIdx.x == static_cast<unsigned>(p.work_blocks) && threadIdx.x < 4) {
@@ -725,11 +834,13 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
 // rows of the weight as the products read them (width not a multiple of 64, or fp32), in panels
 // [term][dpad / 64][rows][64]: 32 rows a workgroup
 template <typename T>
-__global__ __launch_bounds__(256) void weight_kernel(const T* w, uint16_t* to, int64_t rows, int64_t dim, int64_t dpad) {
+__global__ __launch_bounds__(256) void weight_kernel(const T* w, uint16_t* to, int64_t rows, int64_t dim, int64_t dpad,
+                                                     const int* plan) {
   const int64_t r = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x / 8;
   if (r >= rows) return;
+  const float scale = sizeof(T) == 2 ? 1.f : reinterpret_cast<const float*>(plan)[kScaleW];
   for (int64_t c = threadIdx.x % 8 * 8; c < dpad; c += 64)
-    lay_out<T>(w + r * dim, c, dim, to + (c / 64 * (rows + kSkew) + r) * 64 + c % 64, (rows + kSkew) * dpad);
+    lay_out<T>(w + r * dim, c, dim, to + (c / 64 * (rows + kSkew) + r) * 64 + c % 64, (rows + kSkew) * dpad, scale);
 }
 
 // Joins the tiles' (maximum, sum) of a piece with those of the pieces before it; after the last piece, the loss.
@@ -759,7 +870,7 @@ __global__ __launch_bounds__(256) void join_kernel(JoinParams p) {
   __shared__ float2 red[kShareN][TL + 1];
   const int tl = threadIdx.x % TL, share = threadIdx.x / TL;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * TL + tl;
-  const int count = *p.plan;
+  const int count = p.plan[kCount];
   if (static_cast<int64_t>(blockIdx.x) * TL >= count) return;
   float2 r = {-__builtin_inff(), 0.f};
   if (n < count) {
@@ -810,22 +921,25 @@ int64_t sums_bytes(int64_t tiles, int64_t steps, int tile) {
 
 struct XentPlan {
   bool copy_w;             // the weight needs a laid-out copy
-  int terms;
+  int terms, pairs, g_terms, g_pairs;   // of x and the weight, and of G
   int64_t dpad, tok_cap, piece;    // piece: vocabulary rows, a multiple of 256
   int pieces;
   int logits, gx, gw;      // tiles
-  size_t off_plan, off_rows, off_tgt, off_a, off_b, off_c, off_xc, off_tally, off_part, off_w, off_dl, off_over, off_sums, bytes;
+  size_t off_plan, off_range, off_rows, off_tgt, off_a, off_b, off_c, off_xc, off_tally, off_part, off_w, off_dl, off_over, off_sums, bytes;
 };
 
 XentPlan xent_plan(const XentArgs& a, bool grad) {
   XentPlan n{};
   n.terms = a.io ? 1 : kTerms;
+  n.pairs = a.io ? 1 : 3;
+  n.g_terms = !a.io || a.tokens <= kFewTokens ? 2 : 1;
+  n.g_pairs = a.io ? n.g_terms : 3;
   n.dpad = (a.dim + 63) / 64 * 64;
   n.tok_cap = (a.tokens + kTokTile - 1) / kTokTile * kTokTile;
   n.copy_w = !a.io || a.dim % 64 != 0;
   const int64_t vpad = (a.vocab + 255) / 256 * 256;
   int64_t row = 1;   // bytes a vocabulary row of a piece costs
-  if (grad) row += n.tok_cap * 2 * n.terms;
+  if (grad) row += n.tok_cap * 2 * n.g_terms;
   else row += n.tok_cap / 8;   // a partial of 8 bytes per 64 rows
   if (n.copy_w) row += n.dpad * 2 * n.terms;
   n.piece = kPieceBytes / row / 256 * 256;
@@ -841,7 +955,8 @@ XentPlan xent_plan(const XentArgs& a, bool grad) {
   size_t at = 0;
   auto take = [&](size_t b) { const size_t o = at; at += up256(b); return o; };
   const size_t tc = static_cast<size_t>(n.tok_cap);
-  n.off_plan = take(16);
+  n.off_plan = take(kPlanInts * 4);
+  n.off_range = take(a.io ? 0 : size_t{kRangeBlocks} * 3 * 4);
   n.off_rows = take(tc * 4);
   n.off_tgt = take(tc * 4);
   n.off_a = take(tc * 4);
@@ -851,9 +966,9 @@ XentPlan xent_plan(const XentArgs& a, bool grad) {
   n.off_tally = take((tc + kGroup - 1) / kGroup * 4);
   n.off_w = take(n.copy_w ? size_t(n.piece + kSkew) * n.dpad * 2 * n.terms : 0);
   n.off_part = take(grad ? 0 : size_t(n.piece) / 64 * tc * 8);
-  n.off_dl = take(grad ? (tc + kSkew) * n.piece * 2 * n.terms : 0);
+  n.off_dl = take(grad ? (tc + kSkew) * n.piece * 2 * n.g_terms : 0);
   n.off_over = take(grad && n.pieces > 1 ? tc * n.dpad * 4 : 0);
-  const int64_t pairs = a.io ? 1 : kPairs;
+  const int64_t pairs = n.g_pairs;
   const int64_t sx = sums_bytes(tiles_of(a.dim, tok, n.gx), (rows + kBK - 1) / kBK * pairs, n.gx);
   const int64_t sw = sums_bytes(tiles_of(a.dim, rows, n.gw), (tok + kBK - 1) / kBK * pairs, n.gw);
   n.off_sums = take(grad ? static_cast<size_t>(sx > sw ? sx : sw) : 0);   // dx and dW in turn
@@ -861,25 +976,25 @@ XentPlan xent_plan(const XentArgs& a, bool grad) {
   return n;
 }
 
-template <int BM, int WM, int WN, bool ATR, bool BTR, bool SPLIT, int EPI>
+template <int BM, int WM, int WN, bool ATR, bool BTR, bool HALF, int EPI>
 hipError_t product(const ProductParams& p, hipStream_t stream) {
   constexpr int kSlots = slots_of(BM);
   const int64_t tiles = tiles_of(p.M, p.N, BM);
   if (tiles == 0) return hipSuccess;
   const int64_t want = p.slices_at != 0 ? kSlots : (tiles + 7) / 8 * 8;
-  product_kernel<BM, BM, WM, WN, ATR, BTR, SPLIT, EPI>
+  product_kernel<BM, BM, WM, WN, ATR, BTR, HALF, EPI>
       <<<dim3(static_cast<unsigned>(want < kSlots ? want : kSlots)), WM * WN * 64, 0, stream>>>(p);
   if constexpr (EPI == kGradX || EPI == kGradW) {
     const int64_t sliced = tiles < kSlots ? tiles : kSlots;
-    sum_kernel<BM, BM, SPLIT, EPI><<<dim3(static_cast<unsigned>(sliced * kShares)), 256, 0, stream>>>(p, kSlots);
+    sum_kernel<BM, BM, EPI><<<dim3(static_cast<unsigned>(sliced * kShares)), 256, 0, stream>>>(p, kSlots);
   }
   return hipGetLastError();
 }
 
-template <bool ATR, bool BTR, bool SPLIT, int EPI>
+template <bool ATR, bool BTR, bool HALF, int EPI>
 hipError_t product_any(int tile, const ProductParams& p, hipStream_t stream) {
-  return tile == kBig ? product<kBig, 2, 4, ATR, BTR, SPLIT, EPI>(p, stream)
-                      : product<kSmall, 2, 2, ATR, BTR, SPLIT, EPI>(p, stream);
+  return tile == kBig ? product<kBig, 2, 4, ATR, BTR, HALF, EPI>(p, stream)
+                      : product<kSmall, 2, 2, ATR, BTR, HALF, EPI>(p, stream);
 }
 
 template <typename T> hipError_t prep(const XentArgs& a, const XentPlan& n, unsigned char* ws, bool grad, hipStream_t stream) {
@@ -896,7 +1011,7 @@ template <typename T> hipError_t prep(const XentArgs& a, const XentPlan& n, unsi
   p.work_blocks = static_cast<int>((a.tokens + p.per - 1) / p.per);
   if (grad) {
     const int64_t rows = n.piece < a.vocab ? n.piece : a.vocab, last = a.vocab - (n.pieces - 1) * n.piece;
-    p.pairs = a.io ? 1 : kPairs;
+    p.pairs = n.g_pairs;
     p.steps_x = static_cast<int>((rows + kBK - 1) / kBK) * p.pairs;
     p.tile_x = n.gx; p.tile_w = n.gw;
     p.tiles_mx = static_cast<int>((a.dim + n.gx - 1) / n.gx);
@@ -914,11 +1029,16 @@ template <typename T> hipError_t prep(const XentArgs& a, const XentPlan& n, unsi
     p.tally = reinterpret_cast<int*>(ws + n.off_tally);
     tally_kernel<<<dim3(static_cast<unsigned>((a.tokens + kGroup - 1) / kGroup)), 256, 0, stream>>>(p);
   }
+  if constexpr (sizeof(T) == 4) {
+    RangeParams r{p, static_cast<const float*>(a.weight), a.vocab * a.dim, reinterpret_cast<uint32_t*>(ws + n.off_range)};
+    range_kernel<<<dim3(kRangeBlocks), 256, 0, stream>>>(r);
+    scale_kernel<<<dim3(1), 3 * kLanes, 0, stream>>>(r.part, p.plan);
+  }
   prep_kernel<T><<<dim3(static_cast<unsigned>(p.work_blocks + kPadBlocks)), 256, 0, stream>>>(p);
   return hipGetLastError();
 }
 
-// a matrix in panels of 64 columns, [panel][rows][64], one or three of them
+// a matrix in panels of 64 columns, [panel][rows][64], one or two of them
 Operand panels(const void* p, int64_t rows, int64_t cols, bool k_strided) {
   Operand o{};
   o.p = static_cast<const unsigned char*>(p);
@@ -937,8 +1057,17 @@ hipError_t lay_out_weight(const XentArgs& a, const XentPlan& n, unsigned char* w
                           hipStream_t stream) {
   if (!n.copy_w) return hipSuccess;
   weight_kernel<T><<<dim3(static_cast<unsigned>((rows + 31) / 32)), 256, 0, stream>>>(
-      static_cast<const T*>(a.weight) + v0 * a.dim, reinterpret_cast<uint16_t*>(ws + n.off_w), rows, a.dim, n.dpad);
+      static_cast<const T*>(a.weight) + v0 * a.dim, reinterpret_cast<uint16_t*>(ws + n.off_w), rows, a.dim, n.dpad,
+      reinterpret_cast<const int*>(ws + n.off_plan));
   return hipGetLastError();
+}
+
+// the term products, smallest first: (0, 0); with two terms of B alone (0, 1), (0, 0); with two of either (1, 0), (0, 1), (0, 0)
+void set_pairs(ProductParams* p, int pairs) {
+  p->pairs = pairs;
+  p->ta[0] = pairs == 3;
+  p->tb[0] = pairs == 2;
+  p->tb[1] = pairs == 3;
 }
 
 Operand weight_operand(const XentArgs& a, const XentPlan& n, unsigned char* ws, int64_t v0, int64_t rows, bool k_strided) {
@@ -954,7 +1083,7 @@ Operand weight_operand(const XentArgs& a, const XentPlan& n, unsigned char* ws, 
 }
 
 template <typename T> hipError_t xent_fwd_t(const XentArgs& a, hipStream_t stream) {
-  constexpr bool kSplit = sizeof(T) == 4;
+  constexpr bool kHalf = sizeof(T) == 4;
   const XentPlan n = xent_plan(a, false);
   unsigned char* ws = static_cast<unsigned char*>(a.workspace);
   hipError_t e = prep<T>(a, n, ws, false, stream);
@@ -967,13 +1096,15 @@ template <typename T> hipError_t xent_fwd_t(const XentArgs& a, hipStream_t strea
     p.B = panels(ws + n.off_xc, n.tok_cap, n.dpad, false);
     p.M = static_cast<int>(rows); p.N = static_cast<int>(n.tok_cap); p.K = static_cast<int>(n.dpad);
     p.n_is_tokens = 1;
+    set_pairs(&p, n.pairs);
+    p.scale_a = kScaleW; p.scale_b = kScaleX;
     p.plan = reinterpret_cast<int*>(ws + n.off_plan);
     p.tgt = reinterpret_cast<int*>(ws + n.off_tgt);
     p.v0 = static_cast<int>(v0);
     p.part = reinterpret_cast<float2*>(ws + n.off_part);
     p.tok_cap = n.tok_cap;
     p.tlogit = reinterpret_cast<float*>(ws + n.off_a);
-    e = product_any<false, false, kSplit, kLogits>(n.logits, p, stream);
+    e = product_any<false, false, kHalf, kLogits>(n.logits, p, stream);
     if (e != hipSuccess) return e;
     JoinParams j{};
     j.part = p.part; j.tiles = static_cast<int>((rows + n.logits - 1) / n.logits * 2); j.first = k == 0; j.last = k + 1 == n.pieces;
@@ -987,7 +1118,7 @@ template <typename T> hipError_t xent_fwd_t(const XentArgs& a, hipStream_t strea
 }
 
 template <typename T> hipError_t xent_bwd_t(const XentArgs& a, hipStream_t stream) {
-  constexpr bool kSplit = sizeof(T) == 4;
+  constexpr bool kHalf = sizeof(T) == 4;
   const XentPlan n = xent_plan(a, true);
   unsigned char* ws = static_cast<unsigned char*>(a.workspace);
   hipError_t e = prep<T>(a, n, ws, true, stream);
@@ -1004,6 +1135,9 @@ template <typename T> hipError_t xent_bwd_t(const XentArgs& a, hipStream_t strea
     p.B = panels(ws + n.off_xc, n.tok_cap, n.dpad, false);
     p.M = static_cast<int>(rows); p.N = static_cast<int>(n.tok_cap); p.K = static_cast<int>(n.dpad);
     p.n_is_tokens = 1;
+    set_pairs(&p, n.pairs);
+    p.scale_a = kScaleW; p.scale_b = kScaleX;
+    p.g_terms = n.g_terms;
     p.tgt = reinterpret_cast<int*>(ws + n.off_tgt);
     p.v0 = static_cast<int>(v0);
     p.lse = reinterpret_cast<float*>(ws + n.off_a);
@@ -1011,7 +1145,7 @@ template <typename T> hipError_t xent_bwd_t(const XentArgs& a, hipStream_t strea
     p.g = reinterpret_cast<float*>(ws + n.off_c);
     p.dl = dl; p.pdl = (n.tok_cap + kSkew) * rpad;
     p.tok_cap = n.tok_cap;
-    e = product_any<false, false, kSplit, kGradLogits>(n.logits, p, stream);
+    e = product_any<false, false, kHalf, kGradLogits>(n.logits, p, stream);
     if (e != hipSuccess) return e;
     if (a.dx != nullptr) {     // dx += G W: m = width, n = token, k = vocabulary
       ProductParams q{};
@@ -1020,16 +1154,18 @@ template <typename T> hipError_t xent_bwd_t(const XentArgs& a, hipStream_t strea
       q.B = panels(dl, n.tok_cap, rpad, false);
       q.M = static_cast<int>(a.dim); q.N = static_cast<int>(n.tok_cap); q.K = static_cast<int>((rows + 63) / 64 * 64);
       q.n_is_tokens = 1;
-      q.slices_at = 1;
+      set_pairs(&q, n.g_pairs);
+      q.scale_a = kScaleW; q.scale_b = kScaleG;
+      q.slices_at = kSlicesX;
       q.first = k == 0; q.last = k + 1 == n.pieces;
       q.rows = reinterpret_cast<int*>(ws + n.off_rows);
-      q.out = a.dx; q.dim = a.dim; q.out_f32 = kSplit;
+      q.out = a.dx; q.dim = a.dim; q.out_f32 = kHalf;
       q.sums = reinterpret_cast<float*>(ws + n.off_sums);
       if (n.pieces > 1) {
         q.over = reinterpret_cast<float*>(ws + n.off_over);
         q.ld_over = n.dpad;
       }
-      e = product_any<true, false, kSplit, kGradX>(n.gx, q, stream);
+      e = product_any<true, false, kHalf, kGradX>(n.gx, q, stream);
       if (e != hipSuccess) return e;
     }
     if (a.dweight != nullptr) {   // dW of the piece = G^T x: m = width, n = vocabulary row, k = token
@@ -1042,9 +1178,11 @@ template <typename T> hipError_t xent_bwd_t(const XentArgs& a, hipStream_t strea
       q.k_is_tokens = 1;
       q.out = static_cast<unsigned char*>(a.dweight) + v0 * a.dim * gs;
       q.dim = a.dim; q.out_f32 = gs == 4; q.accumulate = a.accumulate;
-      q.slices_at = k + 1 == n.pieces ? 3 : 2;
+      set_pairs(&q, n.g_pairs);
+      q.scale_a = kScaleX; q.scale_b = kScaleG;
+      q.slices_at = k + 1 == n.pieces ? kSlicesLastW : kSlicesW;
       q.sums = reinterpret_cast<float*>(ws + n.off_sums);
-      e = product_any<true, true, kSplit, kGradW>(n.gw, q, stream);
+      e = product_any<true, true, kHalf, kGradW>(n.gw, q, stream);
     }
   }
   return e;

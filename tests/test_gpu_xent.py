@@ -123,6 +123,37 @@ def test_fp32_products_carry_24_bits(M):
         assert (lse - loss - hit).abs().max() < 16 * R.U     # one subtraction of values below 8
 
 
+@pytest.mark.parametrize("ex,ew,eg", [(0, 0, 0), (-70, 66, -90), (90, -92, 100), (-100, -20, 0), (3, -5, -120)])
+def test_fp32_ranges(M, ex, ew, eg):
+    """fp32 inputs of any size, with outliers 2^12 above the rest in some columns: the products keep fp32's accuracy.
+    (The whole tensor's error, in the 2-norm: K roundings of 2^-24 at random add up to sqrt(K) of them; 16 times
+    that, and no more than 2e-6.)"""
+    g = torch.Generator().manual_seed(31)
+    T, V, D = 90, 400, 160
+    x = torch.randn(T, D, generator=g)
+    w = torch.randn(V, D, generator=g) * 0.1
+    x[:, 7] *= 4096.0
+    w[:, 7] /= 4096.0
+    w[:, 11] *= 64.0
+    x[:, 11] /= 64.0
+    y = torch.randint(0, V, (T,), generator=g)
+    dl = (torch.rand(T, generator=g) + 0.5) * 2.0 ** eg
+    x, w = x * 2.0 ** ex, w * 2.0 ** ew
+    loss, lse = M.linear_cross_entropy_fwd(x.cuda(), w.cuda(), y.cuda())
+    grads = M.linear_cross_entropy_bwd(x.cuda(), w.cuda(), y.cuda(), lse, dl.cuda())
+    want = R.cross_entropy(x, w, y, dloss=dl, lse_in=lse.cpu())
+    got = {"loss": loss, "lse": lse, **grads}
+    for k in ("loss", "lse", "dx", "dweight"):
+        ref, out = want[k][0], got[k].cpu().double()
+        # (what lies above fp32's largest number, 2^128, comes out as infinity)
+        over = ref.abs() >= 2.0 ** 128
+        assert torch.equal(out[over], torch.sign(ref[over]) * float("inf")), k
+        ref, out = ref[~over], out[~over]
+        err = float((out - ref).norm())
+        # (what lies below fp32's normal numbers, 2^-126, may come out as 0: at most 2^-126 an element)
+        assert err <= 2e-6 * float(ref.norm()) + 2.0 ** -126 * ref.numel() ** 0.5, (k, err, float(ref.norm()))
+
+
 def test_rows_left_out_are_not_read(M):
     """NaN and infinities in the x of tokens that do not count, and in their dloss, reach nothing."""
     x, w, y, g, gz = make(150, 300, 64, BF16, 0.0, 5)
