@@ -90,18 +90,30 @@ template <int V, typename T> __device__ __forceinline__ void store_row(T* p, con
   }
 }
 
-template <int CTRL> __device__ __forceinline__ float dpp_mov(float v) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+// v of another lane by a DPP move; lanes outside the row mask, or without a source, get 0
+template <int CTRL, int ROWS> __device__ __forceinline__ uint32_t dpp_or_zero(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, true));
+}
+// sum over the lanes up to and including this one: within rows of 16, then across rows (row_bcast)
+__device__ __forceinline__ uint32_t wave_prefix(uint32_t v) {
+  v += dpp_or_zero<0x111, 0xf>(v);   // row_shr:1
+  v += dpp_or_zero<0x112, 0xf>(v);
+  v += dpp_or_zero<0x114, 0xf>(v);
+  v += dpp_or_zero<0x118, 0xf>(v);
+  v += dpp_or_zero<0x142, 0xa>(v);   // row_bcast:15 into rows 1 and 3
+  v += dpp_or_zero<0x143, 0xc>(v);   // row_bcast:31 into rows 2 and 3
+  return v;
 }
 // sum over the wave's 64 lanes, in every lane (the same order of additions every time)
 __device__ __forceinline__ float wave_sum(float v) {
-  v += dpp_mov<0xB1>(v);    // quad_perm [1,0,3,2]
-  v += dpp_mov<0x4E>(v);    // quad_perm [2,3,0,1]
-  v += dpp_mov<0x141>(v);   // row_half_mirror
-  v += dpp_mov<0x140>(v);   // row_mirror
-  v += __shfl_xor(v, 16, 64);
-  v += __shfl_xor(v, 32, 64);
-  return v;
+  auto add = [&](uint32_t o) { v += __uint_as_float(o); };
+  add(dpp_or_zero<0x111, 0xf>(__float_as_uint(v)));
+  add(dpp_or_zero<0x112, 0xf>(__float_as_uint(v)));
+  add(dpp_or_zero<0x114, 0xf>(__float_as_uint(v)));
+  add(dpp_or_zero<0x118, 0xf>(__float_as_uint(v)));
+  add(dpp_or_zero<0x142, 0xa>(__float_as_uint(v)));
+  add(dpp_or_zero<0x143, 0xc>(__float_as_uint(v)));
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
 }
 
 // ids and targets are int32 or int64

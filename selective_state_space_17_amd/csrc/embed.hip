@@ -94,17 +94,6 @@ struct LdsSortParams {
   int64_t total;     // elements of dW to zero; 0: none
 };
 
-// sum over the lanes up to and including this one
-__device__ __forceinline__ uint32_t wave_prefix(uint32_t v) {
-  const int lane = threadIdx.x % kLanes;
-#pragma unroll
-  for (int step = 1; step < kLanes; step *= 2) {
-    const uint32_t o = __shfl_up(v, step, kLanes);
-    v += lane >= step ? o : 0u;
-  }
-  return v;
-}
-
 template <typename G, int E>
 __global__ __launch_bounds__(kLdsThreads) void sort_lds_kernel(LdsSortParams p, G* dweight) {
   constexpr int kPad = E > 1 ? E + 1 : 1;   // words of a thread, and what separates them from the next's
@@ -149,11 +138,10 @@ __global__ __launch_bounds__(kLdsThreads) void sort_lds_kernel(LdsSortParams p, 
       if (lane == kLanes - 1) totals[wave] = upto;
     }
     __syncthreads();
-    if (wave == 0 && lane < kDigits) {
-      uint32_t before = 0;
-      for (int d = 0; d < lane; ++d) before += totals[d];
-      __builtin_amdgcn_wave_barrier();
-      totals[lane] = before;
+    if (wave == 0) {
+      const uint32_t own = lane < kDigits ? totals[lane] : 0u;
+      const uint32_t upto = wave_prefix(own);
+      if (lane < kDigits) totals[lane] = upto - own;
     }
     __syncthreads();
 #pragma unroll
