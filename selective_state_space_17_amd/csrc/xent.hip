@@ -516,13 +516,13 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
         const int n = ncol + j * 16;
+        if (EPI == kGradX ? n >= count : n >= p.N) continue;
         if (cur.sum >= 0) {
           float* const to = p.sums + (static_cast<int64_t>(cur.sum) * BN + n - n0) * BM + mrow - m0;
 #pragma unroll
           for (int i = 0; i < TM; ++i) *reinterpret_cast<f32x4_t*>(to + i * 16) = acc[i][j] * ua * ub;
           continue;
         }
-        if (EPI == kGradX ? n >= count : n >= p.N) continue;
         const int64_t row = EPI == kGradX ? static_cast<int64_t>(p.rows[n]) : n;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {

@@ -45,6 +45,10 @@ CASES = [
     (257, 900, 200, F32, 0.1),
     (300, 2049, 256, BF16, 1.0),
     (513, 1500, 130, BF16, 0.9),
+    (16, 33, 256, BF16, 0.1),
+    (32, 1000, 640, BF16, 0.0),
+    (30, 97, 72, F32, 0.5),
+    (9, 500, 512, F32, 1.0),
 ]
 
 
