@@ -120,5 +120,20 @@ __device__ __forceinline__ float wave_sum(float v) {
 __device__ __forceinline__ int64_t id_at(const void* ids, int id_bytes, int64_t i) {
   return id_bytes == 8 ? static_cast<const int64_t*>(ids)[i] : static_cast<const int32_t*>(ids)[i];
 }
+// those at first, first + step, ...: all loads at once (id_at's branch would have each wait for the one before);
+// from end on the last one again
+template <int E>
+__device__ __forceinline__ void ids_at(const void* ids, int id_bytes, int64_t first, int64_t step, int64_t end,
+                                       int64_t (&v)[E]) {
+  auto all = [&](auto* from) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int64_t i = first + e * step;
+      v[e] = from[i < end ? i : end - 1];
+    }
+  };
+  if (id_bytes == 8) all(static_cast<const int64_t*>(ids));
+  else all(static_cast<const int32_t*>(ids));
+}
 
 }  // namespace mssm

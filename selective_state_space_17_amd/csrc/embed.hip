@@ -6,8 +6,8 @@
 // Both move bytes only.  The lookup reads one row and writes one row per token.  The gradient reads every
 // row of dout once and writes every row of dW once; what makes it more than a copy is that text repeats a
 // few ids very often, so a row of dW may be the sum of one token or of a tenth of the batch.  The tokens
-// are therefore sorted by id (a stable radix sort: equal ids keep their token order, so the sums are taken
-// in a fixed order and the result is the same on every run), and the sorted list is cut into slices of
+// are therefore sorted by id (equal ids keep their token order, so the sums are taken in a fixed order and the
+// result is the same on every run), and the sorted list is cut into slices of
 // sixteen: a wave loads its slice's rows at once, sums the runs of equal ids, writes the rows of runs that lie
 // wholly inside, and leaves the sums of runs that cross a border in the workspace, where a second kernel adds
 // them in order.  No atomics on data, no slice longer than another.  The rows of ids that do not occur are
@@ -69,96 +69,91 @@ __global__ __launch_bounds__(kThreads) void embed_zero_kernel(G* p, int64_t n) {
   zero_rows<G>(p, n, blockIdx.x, gridDim.x, kThreads);
 }
 
-__device__ __forceinline__ uint32_t sort_key(const void* ids, int id_bytes, int64_t vocab, int64_t i) {
-  const int64_t id = id_at(ids, id_bytes, i);
+__device__ __forceinline__ uint32_t sort_key(int64_t id, int64_t vocab) {
   return static_cast<uint32_t>(id < 0 || id > vocab ? vocab : id);
 }
 
 // ------------------------------------------------------------------------------- sort of up to 16384 by id
-// One workgroup sorts the whole list in LDS, while the others zero dW.  A word holds key << 14 | token; four bits
-// of the key a pass.  A thread holds E consecutive words and counts them into counters of its own (LDS adds that
-// return what was there: a word's rank among the thread's equal digits); wave d turns digit d's counters into
-// positions.  A thread's words, and the counters of the threads a lane scans, stand 17 words apart: no bank
-// conflicts either way.
-constexpr int kLdsThreads = 1024, kTokenBits = 14, kLdsMost = 1 << kTokenBits, kDigitBits = 4, kDigits = 1 << kDigitBits;
-constexpr int kLdsWaves = kLdsThreads / kLanes, kLine = kLdsThreads / kLanes;   // counters of a digit that a lane scans
-static_assert(kDigits == kLdsWaves, "one wave to a digit");
+// No passes: a token's place is the number of words key << 14 | token below its own.  A workgroup finds the places
+// of 64 tokens, spread evenly over the batch; it sorts them, looks every word of the batch up between them (six
+// reads of 64 words that stand in 64 banks: no conflicts) and counts the words in each gap; the places are those
+// counts' prefix sums.  Workgroups of the same launch behind them zero dW meanwhile.  16384 ids, table of 50280 x
+// 768 in bf16: 16 us, 11 us without the zeroing, which alone takes 14 us; a radix sort by one workgroup, four bits
+// a pass in LDS, took 26 us beside the same zeroing.  The work grows with the square of the tokens, hence the limit,
+// to which a word has bits for them.
+constexpr int kRankThreads = 1024, kTokenBits = 14, kRankMost = 1 << kTokenBits, kPivots = kLanes;
 
-struct LdsSortParams {
+struct RankParams {
   const void* ids;
   int id_bytes;
   int64_t vocab;
-  int n, passes;
+  int n, groups;     // groups: workgroups with tokens
   uint32_t* keys;
   uint32_t* toks;
   int64_t total;     // elements of dW to zero; 0: none
 };
 
 template <typename G, int E>
-__global__ __launch_bounds__(kLdsThreads) void sort_lds_kernel(LdsSortParams p, G* dweight) {
-  constexpr int kPad = E > 1 ? E + 1 : 1;   // words of a thread, and what separates them from the next's
-  __shared__ uint32_t words[kLdsThreads * kPad];
-  __shared__ uint32_t cnt[kDigits][kLdsThreads / kLine * (kLine + 1)];
-  __shared__ uint32_t totals[kDigits];
-  if (blockIdx.x > 0) {
-    zero_rows<G>(dweight, p.total, blockIdx.x - 1, gridDim.x - 1, kLdsThreads);
+__global__ __launch_bounds__(kRankThreads, 8) void rank_kernel(RankParams p, G* dweight) {
+  __shared__ uint32_t pivots[kPivots], counts[kPivots + 1];
+  if (static_cast<int>(blockIdx.x) >= p.groups) {
+    zero_rows<G>(dweight, p.total, blockIdx.x - p.groups, gridDim.x - p.groups, kRankThreads);
     return;
   }
-  const int tid = threadIdx.x, wave = tid / kLanes, lane = tid % kLanes;
-  auto word_at = [](uint32_t i) -> uint32_t { return E > 1 ? i + i / E : i; };
-  const int mine = tid + tid / kLine;
+  const int tid = threadIdx.x, lane = tid % kLanes;
+  auto word = [&](int64_t id, int i) {   // (what lies past the end sorts last)
+    return i < p.n ? sort_key(id, p.vocab) << kTokenBits | static_cast<uint32_t>(i) : ~0u;
+  };
+  int64_t ids[E], one[1];
+  const int mine = static_cast<int>(blockIdx.x) + lane * p.groups;
+  ids_at<1>(p.ids, p.id_bytes, mine, 0, p.n, one);
+  ids_at<E>(p.ids, p.id_bytes, tid, kRankThreads, p.n, ids);
+  uint32_t v[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int i = e * kLdsThreads + tid;   // (what lies past the end sorts last)
-    words[word_at(i)] = i < p.n ? sort_key(p.ids, p.id_bytes, p.vocab, i) << kTokenBits | static_cast<uint32_t>(i) : ~0u;
+  for (int e = 0; e < E; ++e) v[e] = word(ids[e], e * kRankThreads + tid);
+  if (tid < kLanes) {
+    const uint32_t own = word(one[0], mine);
+    int at = 0;
+#pragma unroll 8
+    for (int l = 0; l < kLanes; ++l) {
+      const uint32_t o = __builtin_amdgcn_readlane(own, l);
+      at += o < own || (o == own && l < lane);
+    }
+    pivots[at] = own;
+    counts[lane] = 0;
+    if (lane == 0) counts[kPivots] = 0;
   }
-  for (int pass = 0; pass < p.passes; ++pass) {
-    const int shift = kTokenBits + pass * kDigitBits;
+  __syncthreads();
+  const uint32_t top = pivots[kPivots - 1];
+  constexpr int kAtOnce = E < 8 ? E : 8;
 #pragma unroll
-    for (int d = 0; d < kDigits; ++d) cnt[d][mine] = 0;
-    __syncthreads();
-    uint32_t v[E], rank[E];
+  for (int e0 = 0; e0 < E; e0 += kAtOnce) {
+    uint32_t below[kAtOnce];   // pivots below the word
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = words[tid * kPad + e];
+    for (int e = 0; e < kAtOnce; ++e) below[e] = 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      rank[e] = __hip_atomic_fetch_add(&cnt[v[e] >> shift & (kDigits - 1)][mine], 1u, __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_WORKGROUP);
-    __syncthreads();
-    {
-      uint32_t c[kLine], s = 0;
+    for (int step = kPivots / 2; step > 0; step /= 2) {
+      uint32_t x[kAtOnce];
 #pragma unroll
-      for (int k = 0; k < kLine; ++k) {
-        c[k] = s;
-        s += cnt[wave][lane * (kLine + 1) + k];
-      }
-      const uint32_t upto = wave_prefix(s);
+      for (int e = 0; e < kAtOnce; ++e) x[e] = pivots[below[e] + step - 1];
 #pragma unroll
-      for (int k = 0; k < kLine; ++k) cnt[wave][lane * (kLine + 1) + k] = upto - s + c[k];
-      if (lane == kLanes - 1) totals[wave] = upto;
+      for (int e = 0; e < kAtOnce; ++e) below[e] += x[e] < v[e0 + e] ? step : 0;
     }
-    __syncthreads();
-    if (wave == 0) {
-      const uint32_t own = lane < kDigits ? totals[lane] : 0u;
-      const uint32_t upto = wave_prefix(own);
-      if (lane < kDigits) totals[lane] = upto - own;
-    }
-    __syncthreads();
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const uint32_t d = v[e] >> shift & (kDigits - 1);
-      words[word_at(totals[d] + cnt[d][mine] + rank[e])] = v[e];   // (all words are in registers)
+    for (int e = 0; e < kAtOnce; ++e) {
+      below[e] += top < v[e0 + e];
+      if (v[e0 + e] != ~0u)
+        __hip_atomic_fetch_add(&counts[below[e]], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     }
-    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
   }
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int i = e * kLdsThreads + tid;
-    if (i < p.n) {
-      const uint32_t v = words[word_at(i)];
-      p.keys[i] = v >> kTokenBits;
-      p.toks[i] = v & (kLdsMost - 1);
-    }
+  __syncthreads();
+  if (tid >= kLanes) return;
+  const uint32_t own = pivots[lane];
+  const uint32_t at = wave_prefix(counts[lane]) - 1;   // the words up to this one, but for itself
+  if (own != ~0u) {
+    p.keys[at] = own >> kTokenBits;
+    p.toks[at] = own & (kRankMost - 1);
   }
 }
 
@@ -181,7 +176,7 @@ struct SortParams {
 };
 
 __device__ __forceinline__ uint32_t key_at(const SortParams& p, int i) {
-  return p.ids == nullptr ? p.keys[i] : sort_key(p.ids, p.id_bytes, p.vocab, i);
+  return p.ids == nullptr ? p.keys[i] : sort_key(id_at(p.ids, p.id_bytes, i), p.vocab);
 }
 
 __global__ __launch_bounds__(kThreads) void sort_hist_kernel(SortParams p) {
@@ -365,10 +360,11 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedGradParams p)
   if (lo > 0 && p.keys[lo - 1] == key) return;              // the run began in an earlier slice
   // the last slice the run reaches into: its first key is still the run's
   int64_t have = s + 1, not_in = p.slices;
-  while (not_in - have > 1) {
-    const int64_t mid = (have + not_in) / 2;
-    if (p.keys[mid * kSlice] == key) have = mid;
-    else not_in = mid;
+  while (not_in - have > 1) {   // 63 or 64 places between, a lane each
+    const int64_t step = (not_in - have + kLanes - 1) / kLanes, at = have + (lane + 1) * step;
+    const int in = __popcll(__ballot(at < not_in && p.keys[at < not_in ? at * kSlice : 0] == key));
+    have += in * step;
+    not_in = have + step < not_in ? have + step : not_in;
   }
   const int parts = static_cast<int>(have - s) + 1;          // the first from the second half of its line
   const int64_t col = (static_cast<int64_t>(blockIdx.y) * kLanes + lane) * V;
@@ -432,16 +428,15 @@ template <typename T, typename G> hipError_t embed_bwd_t(const EmbedArgs& a, hip
 
   const int64_t total = a.accumulate ? 0 : a.vocab * a.dim;
   EmbedGradParams g{};
-  if (n > 0 && n <= kLdsMost && a.vocab < (int64_t{1} << (32 - kTokenBits)) - 1) {
-    LdsSortParams sp{a.ids, a.id_bytes, a.vocab, n, 1, buf[0], buf[1], total};
-    while ((int64_t{1} << (kDigitBits * sp.passes)) <= a.vocab) ++sp.passes;   // the keys are 0 .. vocab
-    const int64_t want = (total + kLdsThreads * 32 - 1) / (kLdsThreads * 32);
-    const dim3 grid(1 + static_cast<unsigned>(want < 2048 ? want : 2048));
+  if (n > 0 && n <= kRankMost && a.vocab < (int64_t{1} << (32 - kTokenBits)) - 1) {
+    const RankParams rp{a.ids, a.id_bytes, a.vocab, n, (n + kPivots - 1) / kPivots, buf[0], buf[1], total};
+    const int64_t want = (total + kRankThreads * 32 - 1) / (kRankThreads * 32);
+    const dim3 grid(rp.groups + static_cast<unsigned>(want < 2048 ? want : 2048));
     G* const dw = static_cast<G*>(a.dweight);
-    if (n <= kLdsThreads) sort_lds_kernel<G, 1><<<grid, kLdsThreads, 0, stream>>>(sp, dw);
-    else if (n <= 4 * kLdsThreads) sort_lds_kernel<G, 4><<<grid, kLdsThreads, 0, stream>>>(sp, dw);
-    else if (n <= 8 * kLdsThreads) sort_lds_kernel<G, 8><<<grid, kLdsThreads, 0, stream>>>(sp, dw);
-    else sort_lds_kernel<G, 16><<<grid, kLdsThreads, 0, stream>>>(sp, dw);
+    if (n <= kRankThreads) rank_kernel<G, 1><<<grid, kRankThreads, 0, stream>>>(rp, dw);
+    else if (n <= 4 * kRankThreads) rank_kernel<G, 4><<<grid, kRankThreads, 0, stream>>>(rp, dw);
+    else if (n <= 8 * kRankThreads) rank_kernel<G, 8><<<grid, kRankThreads, 0, stream>>>(rp, dw);
+    else rank_kernel<G, 16><<<grid, kRankThreads, 0, stream>>>(rp, dw);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     g.keys = buf[0];

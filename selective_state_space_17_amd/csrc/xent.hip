@@ -621,9 +621,23 @@ __host__ __device__ constexpr int slots_of(int tile) { return tile == kBig ? kCU
 constexpr int kPadBlocks = 16;
 constexpr int kGroup = 4096;
 
-__device__ __forceinline__ bool token_counts(const PrepParams& p, int64_t t) {
-  const int64_t y = id_at(p.targets, p.id_bytes, t);
+__device__ __forceinline__ bool target_counts(const PrepParams& p, int64_t y) {
   return y >= 0 && y < p.vocab && y != p.ignore;
+}
+__device__ __forceinline__ bool token_counts(const PrepParams& p, int64_t t) {
+  return target_counts(p, id_at(p.targets, p.id_bytes, t));
+}
+// how many of a thread's tokens lo + tid, lo + tid + 256, ... below hi count, E at a time
+template <int E>
+__device__ __forceinline__ int counted(const PrepParams& p, int64_t lo, int64_t hi) {
+  int n = 0;
+  for (int64_t t = lo + threadIdx.x; t < hi; t += E * 256) {
+    int64_t y[E];
+    ids_at<E>(p.targets, p.id_bytes, t, 256, hi, y);
+#pragma unroll
+    for (int e = 0; e < E; ++e) n += t + e * 256 < hi && target_counts(p, y[e]);
+  }
+  return n;
 }
 
 // the sum of every thread's n over the workgroup of 256
@@ -638,13 +652,7 @@ __device__ __forceinline__ int block_count(int n, int* red) {
 __global__ __launch_bounds__(256) void tally_kernel(PrepParams p) {
   __shared__ int red[4];
   const int64_t lo = static_cast<int64_t>(blockIdx.x) * kGroup;
-  int n = 0;
-#pragma unroll
-  for (int i = 0; i < kGroup / 256; ++i) {
-    const int64_t t = lo + i * 256 + threadIdx.x;
-    n += t < p.tokens && token_counts(p, t);
-  }
-  n = block_count(n, red);
+  const int n = block_count(counted<kGroup / 256>(p, lo, lo + kGroup < p.tokens ? lo + kGroup : p.tokens), red);
   if (threadIdx.x == 0) p.tally[blockIdx.x] = n;
 }
 
@@ -772,8 +780,7 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
     for (int g = threadIdx.x; g < groups; g += 256) before += p.tally[g];
     from = static_cast<int64_t>(groups) * kGroup;
   }
-#pragma unroll 4
-  for (int64_t t = from + threadIdx.x; t < lo; t += 256) before += token_counts(p, t);
+  before += counted<8>(p, from, lo);
   before = block_count(before, red);
 
   const int64_t term = (p.tok_cap + kSkew) * p.dpad;
