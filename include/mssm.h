@@ -491,7 +491,7 @@ int mssm_ssd_mimo_plan(const mssm_ssd_desc* desc, int32_t rank, int32_t* route);
  *                  taken in fp32 and rounded once), as for a head tied to the
  *                  embedding or gradients gathered over several batches.
  * The gradient is summed in fp32 over the tokens sorted by id, in token order:
- * the same result on every run.  tokens may be 0, up to 2^26 - 1; vocab up to
+ * the same result on every run.  tokens may be 0, up to 2^26 - 4; vocab up to
  * 2^30; dim up to 2^20 (MSSM_ERR_UNSUPPORTED above); scale finite.  workspace
  * (the gradient only): at least mssm_embedding_bwd_workspace_size(desc) bytes,
  * 256-byte aligned.  Element-aligned pointers.  Other rules as
@@ -534,9 +534,10 @@ size_t mssm_embedding_bwd_workspace_size(const mssm_embedding_desc* desc);
  *   dweight, dbias     : [dim] fp32, overwritten; dbias nullable (NULL for the RMS norm)
  * io_dtype MSSM_BF16 takes either res_dtype, MSSM_F32 takes MSSM_F32.  eps is
  * positive.  rows may be 0 (the backward pass then writes zero dweight and
- * dbias), up to 2^26 - 1 of at most 256 columns, 2^22 - 1 of more; dim up to
+ * dbias), up to 2^26 - 4 of at most 256 columns, 2^22 - 1 of more; dim up to
  * 2^20.  Statistics and sums are fp32, in a fixed order: the same result on
- * every run.  workspace (the gradients only): at least
+ * every run (the mean of squares is one of them: it overflows for values
+ * beyond about 1e19).  workspace (the gradients only): at least
  * mssm_norm_bwd_workspace_size(desc) bytes, 256-byte aligned.  Element-aligned
  * pointers.  Other rules as mssm_selective_scan_fwd. */
 #define MSSM_LAYER_NORM 0
@@ -577,9 +578,14 @@ size_t mssm_norm_bwd_workspace_size(const mssm_norm_desc* desc);
  *   dx      : [tokens, dim] (io_dtype);  dweight : [vocab, dim] in grad_dtype,
  *             io_dtype or MSSM_F32, overwritten, or added to with accumulate != 0
  *             (in fp32, rounded once); one of dx and dweight may be NULL
- * Products are summed in fp32.  With MSSM_BF16 G is rounded to bf16, whatever
- * grad_dtype; with MSSM_F32 every product carries 24 bits.  All sums are taken
- * in a fixed order: the same result on every run.
+ * Products are summed in fp32.  With MSSM_BF16 G is rounded to bf16 once,
+ * whatever grad_dtype (for up to 256 tokens it keeps 16 bits).  With MSSM_F32
+ * x, weight and G enter the matrix cores as two fp16 terms each, under a power
+ * of two that fits each matrix: a value keeps 23 bits or more where it is
+ * within 2^-16 of its matrix's largest finite magnitude, and is right to 2^-39
+ * of that magnitude below.  A NaN among a token's logits, or one of +infinity,
+ * makes its loss and lse NaN.  All sums are taken in a fixed order: the same
+ * result on every run.
  * tokens may be 0, up to 2^26 - 1; vocab up to 2^30; dim up to 2^20.  bf16
  * weight of a dim that is a multiple of 64 must be 16-byte aligned (it is read
  * in place; any other weight is laid out piece by piece in the workspace

@@ -10,7 +10,8 @@ using mssm::set_err;
 
 namespace {
 
-constexpr int64_t kMaxTokens = (int64_t{1} << 26) - 1;   // a wave per token fits a 1-D grid's 32-bit work-item count
+constexpr int64_t kMaxTokens = (int64_t{1} << 26) - 1;
+constexpr int64_t kMaxWaves = (int64_t{1} << 26) - 4;    // a wave a row, four to a workgroup: a 32-bit work-item count
 constexpr int64_t kMaxVocab = int64_t{1} << 30;
 constexpr int64_t kMaxDim = int64_t{1} << 20;
 
@@ -52,7 +53,7 @@ int validate_embedding(const mssm_embedding_desc* d) {
   if (!mul_ok(d->tokens, d->dim, &t) || !mul_ok(t, 16, &t)) return MSSM_ERR_INVALID_ARG;
   if (!mul_ok(d->vocab, d->dim, &t) || !mul_ok(t, 4, &t)) return MSSM_ERR_INVALID_ARG;
   if (!io_ok(d->io_dtype) || (d->id_bytes != 4 && d->id_bytes != 8)) return MSSM_ERR_UNSUPPORTED;
-  if (d->tokens > kMaxTokens || d->vocab > kMaxVocab || d->dim > kMaxDim) return MSSM_ERR_UNSUPPORTED;
+  if (d->tokens > kMaxWaves || d->vocab > kMaxVocab || d->dim > kMaxDim) return MSSM_ERR_UNSUPPORTED;
   return MSSM_OK;
 }
 
@@ -73,7 +74,7 @@ int validate_norm(const mssm_norm_desc* d) {
   if (!io_ok(d->io_dtype) || !io_ok(d->res_dtype)) return MSSM_ERR_UNSUPPORTED;
   if (d->io_dtype == MSSM_F32 && d->res_dtype != MSSM_F32) return MSSM_ERR_UNSUPPORTED;
   // a wave per row up to 256 columns, a workgroup of up to 1024 threads above: 32-bit work-item counts
-  if (d->rows > (d->dim <= 256 ? kMaxTokens : (int64_t{1} << 22) - 1) || d->dim > kMaxDim) return MSSM_ERR_UNSUPPORTED;
+  if (d->rows > (d->dim <= 256 ? kMaxWaves : (int64_t{1} << 22) - 1) || d->dim > kMaxDim) return MSSM_ERR_UNSUPPORTED;
   return MSSM_OK;
 }
 
@@ -88,7 +89,7 @@ int validate_xent(const mssm_cross_entropy_desc* d) {
   if (d == nullptr) return MSSM_ERR_INVALID_ARG;
   if (d->tokens < 0 || d->vocab <= 0 || d->dim <= 0 || d->flags != 0) return MSSM_ERR_INVALID_ARG;
   int64_t t = 0;
-  // (the workspace holds up to three bf16 terms of either operand, padded)
+  // (the workspace holds up to two 16-bit terms of either operand, padded)
   if (!mul_ok(d->tokens, d->dim, &t) || !mul_ok(t, 64, &t)) return MSSM_ERR_INVALID_ARG;
   if (!mul_ok(d->vocab, d->dim, &t) || !mul_ok(t, 64, &t)) return MSSM_ERR_INVALID_ARG;
   if (!io_ok(d->io_dtype) || (d->id_bytes != 4 && d->id_bytes != 8)) return MSSM_ERR_UNSUPPORTED;

@@ -8,7 +8,7 @@
 // The logits [tokens, vocab] are never kept.  The forward pass forms them tile by tile on the matrix cores
 // and keeps, per token and tile, the maximum and the sum of exponentials (and the target's logit); a second
 // kernel joins those.  The gradients take the vocabulary in pieces: a piece's logits are formed again, G of
-// the piece goes to the workspace in bf16, and two more products take it to dx (summed over the pieces in
+// the piece goes to the workspace in 16-bit terms, and two more products take it to dx (summed over the pieces in
 // fp32) and to the piece's rows of dW.
 //
 // One tiled product serves all four: out[m, n] = sum_k A[m, k] B[n, k] with m on the weight's side (so that
@@ -19,10 +19,12 @@
 // bf16 inputs enter the matrix cores as they are; products are summed in fp32.  G is rounded to bf16 (the
 // gradients' own type) once; for up to 256 tokens, where few roundings average out and the weight's bytes are what
 // the time goes into, it is kept in two bf16 terms.
-// fp32 inputs are split into two fp16 terms, v s = hi + lo to within 2^-24 of v s, and a product is the three term
-// products hi lo + lo hi + hi hi (what is left out is below 2^-24 of the product), summed in fp32, smallest first.
-// s is a power of two for each matrix that brings its largest finite magnitude to [2^14, 2^15): fp16's range then
-// reaches 2^-40 below that, where a value's own 24 bits end.  Three fp16 products take a fifth of the time of one
+// fp32 inputs are split into two fp16 terms, v s = hi + lo: exact for three values in four, one unit in the last of
+// 24 bits off (2^-23) for the rest.  A product is the three term products hi lo + lo hi + hi hi, summed in fp32; lo
+// lo is left out, below 2^-22 of the product (2^-25 in the mean square).  Over a row of products both vanish beside
+// the roundings of the sum.  s is a power of two for each matrix that brings its largest finite magnitude to [2^14,
+// 2^15): fp16's smallest step then lies 2^39 below the largest value, so values down to 2^-16 of it keep the bits
+// said, smaller ones are right to 2^-39 of the largest.  Three fp16 products take a fifth of the time of one
 // product at the matrix cores' fp32 rate, a sixteenth of fp16's; with three bf16 terms and six products the fp32
 // step of 1001 x 1000 x 32003 took 1.47 ms.
 #include <type_traits>
@@ -82,7 +84,7 @@ __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t l
 struct Operand {
   const unsigned char* p;
   int64_t row, step, plane;
-  int64_t term;            // between the bf16 terms of a split operand
+  int64_t term;            // between the terms of a split operand
   int rows, planes;        // what may be read: rows, and (K-strided) panels of 64 columns
 };
 

@@ -99,10 +99,10 @@ def cross_entropy(x, weight, targets, ignore_id=-100, dloss=None, dlse=None, lse
     xk, yk = xd[kept].to(F64), y[kept].long()
     logits = xk @ w.T
     mag = xk.abs() @ w.abs().T
-    # bf16 products are exact in fp32; fp32 ones are six term products, what they leave out below 2^-23 of the
-    # product.  Every addition inside the matrix cores may lose a whole step: 2 u each.
-    terms = dim * (1 if io == torch.bfloat16 else 6) + 64
-    e_l = mag * (2 * terms * U + (0 if io == torch.bfloat16 else 2.0 ** -23))
+    # bf16 products are exact in fp32; fp32 ones are three products of fp16 terms: either factor may be 2^-23 off and
+    # 2^-22 of the product is left out.  Every addition inside the matrix cores may lose a whole step: 2 u each.
+    terms = dim * (1 if io == torch.bfloat16 else 3) + 64
+    e_l = mag * (2 * terms * U + (0 if io == torch.bfloat16 else 2.0 ** -21))
     top = e_l.max(1).values if kept.numel() else torch.zeros(0, dtype=F64)
     lse = torch.logsumexp(logits, 1)
     # the logits' error, the exponentials (8 u with the argument's rounding: u per unit of the argument) and their sums
@@ -125,13 +125,14 @@ def cross_entropy(x, weight, targets, ignore_id=-100, dloss=None, dlse=None, lse
     e_g = p * gl.abs()[:, None] * (1.01 * e_l + (8 + 2 * arg.abs()) * U + 2 * U) + U * gr.abs() + U * (one * g.abs()[:, None])
     stored = 2.0 ** -8 if io == torch.bfloat16 else 2.0 ** -23    # G as the products read it
     e_g = e_g + gr.abs() * stored
-    times = 1 if io == torch.bfloat16 else 6
+    times = 1 if io == torch.bfloat16 else 3
+    split = 0 if io == torch.bfloat16 else 2.0 ** -21
     m_dx, m_dw = gr.abs() @ w.abs(), gr.abs().T @ xk.abs()
     dx = torch.zeros(y.numel(), dim, dtype=F64).index_copy(0, kept, gr @ w)
     e_dx = torch.zeros(y.numel(), dim, dtype=F64).index_copy(
-        0, kept, e_g @ w.abs() + m_dx * (2 * (vocab * times + 64) * U))
+        0, kept, e_g @ w.abs() + m_dx * (2 * (vocab * times + 64) * U + split))
     dw = gr.T @ xk
-    e_dw = e_g.T @ xk.abs() + m_dw * (2 * (kept.numel() * times + 64) * U)
+    e_dw = e_g.T @ xk.abs() + m_dw * (2 * (kept.numel() * times + 64) * U + split)
     if old is not None:
         dw = dw + old.to(F64)
         e_dw = e_dw + U * dw.abs()

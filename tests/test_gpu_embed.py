@@ -45,6 +45,12 @@ CASES = [
     (2049, 511, 96, BF16, "text", torch.int64),
     (4097, 512, 36, F32, "one", torch.int64),
     (5000, 300, 520, BF16, "two", torch.int64),
+    (4096, 262142, 4, BF16, "text", torch.int64),
+    (4200, 262143, 4, BF16, "text", torch.int32),
+    (8192, 40, 12, F32, "pad", torch.int32),
+    (8193, 5000, 16, BF16, "text", torch.int64),
+    (16383, 9, 8, F32, "pad", torch.int32),
+    (16384, 50000, 24, BF16, "one", torch.int64),
     (16385, 50000, 40, F32, "text", torch.int32),
     (40000, 1000, 24, BF16, "pad", torch.int64),
 ]
@@ -68,6 +74,15 @@ def test_embedding(M, case):
         old = torch.randn(vocab, dim, generator=torch.Generator().manual_seed(5)).to(gd)
         got = M.embedding_bwd(ids.cuda(), dout.cuda(), vocab, scale=scale, dweight=old.cuda(), accumulate=True)
         R.check(got, R.embedding_bwd(ids, dout, vocab, scale, old, gd)["dweight"], f"accumulated {gd}")
+
+
+def test_most_tokens(M):
+    """As many tokens as a call takes: all that the largest grid holds."""
+    n = (1 << 26) - 4
+    weight = torch.arange(1, 6, dtype=F32, device="cuda")[:, None]
+    ids = torch.arange(n, dtype=torch.int32, device="cuda") % 5
+    out = M.embedding_fwd(ids, weight)
+    assert torch.equal(out[:, 0], ids + 1.0)
 
 
 def test_scale_one_is_a_copy(M):

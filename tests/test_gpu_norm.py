@@ -143,6 +143,17 @@ def test_constant_and_huge_rows(M):
     assert torch.equal(M.rms_norm_fwd(torch.zeros(2, 64).cuda(), w.cuda()).cpu(), torch.zeros(2, 64))
 
 
+def test_most_rows(M):
+    """As many rows as a call takes, of one column: the layer norm of a single value is the bias."""
+    n = (1 << 26) - 4
+    x = torch.arange(n, dtype=F32, device="cuda")[:, None] - n / 2
+    w, b = torch.ones(1, device="cuda"), torch.full((1,), 0.75, device="cuda")
+    out = M.layer_norm_fwd(x, w, b)
+    assert bool((out == 0.75).all())
+    want = M.rms_norm_fwd(x, w)     # x / sqrt(x^2 + eps): the sign, but for x = 0
+    assert bool(((want - torch.sign(x)).abs() < 1e-4).all())
+
+
 def test_a_row_of_nan_stays_alone(M):
     x = torch.randn(6, 300)
     clean = M.layer_norm_fwd(x.cuda(), torch.ones(300).cuda()).cpu()

@@ -76,6 +76,8 @@ def test_embedding_arguments():
     d = desc(E)
     for scale in (float("nan"), float("inf")):
         assert embed_fwd(desc(E, scale=scale)) == INV
+    most = (1 << 26) - 4
+    assert embed_fwd(desc(E, tokens=most + 1, dim=1)) == UNS and embed_fwd(desc(E, tokens=most, dim=1), ids=None) == INV
     assert embed_fwd(d, ids=None) == INV and embed_fwd(d, weight=None) == INV and embed_fwd(d, out=None) == INV
     assert embed_fwd(d, ids=AT[0] + 4) == MIS and embed_fwd(d, weight=AT[1] + 1) == MIS and embed_fwd(d, out=AT[2] + 1) == MIS
     assert embed_fwd(d, out=AT[1]) == INV and embed_fwd(d, out=AT[0] - 100) == INV
@@ -96,6 +98,8 @@ def test_norm_arguments():
     assert norm_fwd(desc(N, io_dtype=M.MSSM_F32, res_dtype=M.MSSM_BF16)) == UNS
     assert norm_fwd(desc(N, res_dtype=3)) == UNS
     assert norm_fwd(desc(N, rows=1 << 22, dim=257)) == UNS
+    most = (1 << 26) - 4
+    assert norm_fwd(desc(N, rows=most + 1, dim=1)) == UNS and norm_fwd(desc(N, rows=most, dim=1), x=None) == INV
     rms = desc(N, kind=M.MSSM_RMS_NORM)
     assert norm_fwd(rms, mean=None) == INV, "the RMS norm has no bias"
     assert norm_fwd(rms, bias=None) == INV, "nor a mean"
