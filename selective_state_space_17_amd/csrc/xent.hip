@@ -177,6 +177,15 @@ __device__ __forceinline__ void fence_schedule() { __builtin_amdgcn_sched_barrie
 // One workgroup stays on a CU (two of the small tile) and takes tile after tile.  The loads run two steps of
 // 64 k ahead of the matrix cores and cross tile borders: a tile's first steps are on their way while the
 // tile before it is finished and stored.
+// Bound by the matrix cores at the clock that the power limit leaves them (1.8 to 1.9 GHz): 16384 x 2048 x 131072 in
+// bf16 runs at 1.32 PFLOP/s (logits, 6.6 ms; a library product of the same sizes, which writes them, at 1.40), 1.20
+// (G), 1.31 (dx) and 1.27 (dW), with the matrix cores busy 69, 60, 66 and 64 % of the cycles and no LDS bank
+// conflicts; 7373 x 768 x 50280 at 1.01 PFLOP/s (565 us; the library: 0.82).  With few tokens bound by the weight's
+// bytes: 16 x 2560 x 50280 in 49 us, 5.2 TB/s with part of the weight left in the 256 MB cache by the call before (a
+// kernel that streamed the weight straight into registers was no faster).  Tried and slower: a ring of five
+// buffers of 32 k (8.3 against 7.5 ms for the logits at the time), two groups of waves taking turns (8.8 ms), 32 x
+// 32 x 16 instructions (8.6 ms, spills), all loads in a step's first two rows (7.9 ms), G stored past the cache
+// (1.78 against 1.55 ms a piece).
 template <int BM, int BN, int WM, int WN, bool ATR, bool BTR, bool HALF, int EPI>
 __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) {
   constexpr int kW = WM * WN;
