@@ -100,7 +100,7 @@ struct ProductParams {
   int ta[kMostPairs], tb[kMostPairs];
   const int* plan;         // see Plan
   int scale_a, scale_b;    // which of its scales the operands carry (fp16 terms)
-  int slices_at;           // where in plan the slices of the tiles of the last round stand; 0: not sliced
+  int slices_at;           // dx, dW: where in plan the slices of the tiles of the last round stand
   // epilogues
   int v0;                  // first vocabulary row of this piece
   const int* tgt;          // compacted targets
@@ -187,7 +187,7 @@ __device__ __forceinline__ void fence_schedule() { __builtin_amdgcn_sched_barrie
 // 32 x 16 instructions (8.6 ms, spills), all loads in a step's first two rows (7.9 ms), G stored past the cache
 // (1.78 against 1.55 ms a piece).
 template <int BM, int BN, int WM, int WN, bool ATR, bool BTR, bool HALF, int EPI>
-__global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) {
+__global__ __launch_bounds__(WM * WN * 64, 2) void product_kernel(ProductParams p) {
   constexpr int kW = WM * WN;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;      // 16 x 16 tiles of a wave
   constexpr int LA = BM / 8 / kW, LB = BN / 8 / kW;        // 1 KB loads of a wave per step
@@ -212,8 +212,9 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
   const int tiles_m = (p.M + BM - 1) / BM;
   const int tiles_n = ((p.n_is_tokens ? count : p.N) + BN - 1) / BN;
   const int tiles = tiles_m * tiles_n;
-  const int whole = p.slices_at != 0 ? tiles / static_cast<int>(gridDim.x) * static_cast<int>(gridDim.x) : 0;
-  const int slices = p.slices_at != 0 ? p.plan[p.slices_at] : 1;
+  constexpr bool kSliced = EPI == kGradX || EPI == kGradW;
+  const int whole = kSliced ? tiles / static_cast<int>(gridDim.x) * static_cast<int>(gridDim.x) : 0;
+  const int slices = kSliced ? p.plan[p.slices_at] : 1;
   const int rest = tiles - whole, cut = rest * slices;
   const int xcd = blockIdx.x % 8, stride = gridDim.x / 8;
   const int whole8 = whole / 8, cut8 = (cut + 7) / 8;      // of an XCD
@@ -227,8 +228,8 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
   auto job_at = [&](int i) {
     Job j;
     int tile;
-    if (i < whole8) {
-      tile = xcd * whole8 + i;
+    if (!kSliced || i < whole8) {
+      tile = kSliced ? xcd * whole8 + i : xcd * cut8 + i;
       j.sum = -1;
       j.begin = 0;
       j.steps = all;
@@ -456,11 +457,15 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(ProductParams p) 
         const int n = ncol + j * 16;
         if (m0 + BM > p.M) each(j, [&](float a, int m) { return m < p.M ? a : -__builtin_inff(); });
         const int y = p.tgt[n] - p.v0;   // padded tokens have target -1
-        if (__ballot(y >= wave_m && y < wave_m + TM * 16) != 0)
+        if (__ballot(y >= wave_m && y < wave_m + TM * 16) != 0) {
+          float hit = 0.f;   // (one store: as many as there are rows cost each wave 0.8 us a tile)
           each(j, [&](float a, int m) {
-            if (m == y) p.tlogit[n] = a * unit;
+            hit = m == y ? a : hit;
             return a;
           });
+          const int at = y - mrow;
+          if (at >= 0 && at < TM * 16 && at % 16 < 4) p.tlogit[n] = hit * unit;
+        }
         float mx = -__builtin_inff();
         each(j, [&](float a, int) {
           mx = __builtin_fmaxf(mx, a);
@@ -999,7 +1004,7 @@ hipError_t product(const ProductParams& p, hipStream_t stream) {
   constexpr int kSlots = slots_of(BM);
   const int64_t tiles = tiles_of(p.M, p.N, BM);
   if (tiles == 0) return hipSuccess;
-  const int64_t want = p.slices_at != 0 ? kSlots : (tiles + 7) / 8 * 8;
+  const int64_t want = EPI == kGradX || EPI == kGradW ? kSlots : (tiles + 7) / 8 * 8;
   product_kernel<BM, BM, WM, WN, ATR, BTR, HALF, EPI>
       <<<dim3(static_cast<unsigned>(want < kSlots ? want : kSlots)), WM * WN * 64, 0, stream>>>(p);
   if constexpr (EPI == kGradX || EPI == kGradW) {
