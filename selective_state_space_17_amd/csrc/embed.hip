@@ -57,17 +57,23 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(EmbedParams p) {
 }
 
 // ---------------------------------------------------------------------------------------- rows without a token
-template <typename G>
-__device__ __forceinline__ void zero_rows(G* p, int64_t n, int64_t block, int64_t blocks, int threads) {
-  constexpr int V = 16 / sizeof(G);
-  const float z[V] = {};
-  const int64_t step = blocks * threads * V;
-  for (int64_t i = (block * threads + threadIdx.x) * V; i < n; i += step) store_row<V>(p + i, z, n - i);
+// What a launch zeroes with the workgroups behind its own: n units of two bytes.
+struct Zeros {
+  uint16_t* p;
+  int64_t n;
+};
+__device__ __forceinline__ void zero_rows(const Zeros& z, int64_t block, int64_t blocks, int threads) {
+  const float none[8] = {};
+  const int64_t step = blocks * threads * 8;
+  for (int64_t i = (block * threads + threadIdx.x) * 8; i < z.n; i += step) store_row<8>(z.p + i, none, z.n - i);
+}
+unsigned zero_blocks(const Zeros& z, int threads) {
+  const int64_t want = (z.n + threads * 32 - 1) / (threads * 32);
+  return static_cast<unsigned>(want < 2048 ? want : 2048);
 }
 
-template <typename G>
-__global__ __launch_bounds__(kThreads) void embed_zero_kernel(G* p, int64_t n) {
-  zero_rows<G>(p, n, blockIdx.x, gridDim.x, kThreads);
+__global__ __launch_bounds__(kThreads) void embed_zero_kernel(Zeros z) {
+  zero_rows(z, blockIdx.x, gridDim.x, kThreads);
 }
 
 __device__ __forceinline__ uint32_t sort_key(int64_t id, int64_t vocab) {
@@ -91,14 +97,13 @@ struct RankParams {
   int n, groups;     // groups: workgroups with tokens
   uint32_t* keys;
   uint32_t* toks;
-  int64_t total;     // elements of dW to zero; 0: none
+  Zeros zeros;
 };
 
-template <typename G, int E>
-__global__ __launch_bounds__(kRankThreads, 8) void rank_kernel(RankParams p, G* dweight) {
+template <int E> __global__ __launch_bounds__(kRankThreads, 8) void rank_kernel(RankParams p) {
   __shared__ uint32_t pivots[kPivots], counts[kPivots + 1];
   if (static_cast<int>(blockIdx.x) >= p.groups) {
-    zero_rows<G>(dweight, p.total, blockIdx.x - p.groups, gridDim.x - p.groups, kRankThreads);
+    zero_rows(p.zeros, blockIdx.x - p.groups, gridDim.x - p.groups, kRankThreads);
     return;
   }
   const int tid = threadIdx.x, lane = tid % kLanes;
@@ -159,7 +164,8 @@ __global__ __launch_bounds__(kRankThreads, 8) void rank_kernel(RankParams p, G* 
 }
 
 // ---------------------------------------------------------------------------------- sort of any number by id
-// Least-significant-digit radix sort of (id, token) pairs, ids outside [0, vocab) sorted last as `vocab`.
+// Least-significant-digit radix sort of (id, token) pairs, ids outside [0, vocab) sorted last as `vocab`.  Each of
+// its launches, few workgroups that wait for memory, zeroes a share of dW beside.
 constexpr int kTile = 1024;                    // pairs per workgroup
 constexpr int kPerWave = kTile / kWaves;       // a wave's pairs are consecutive, so its order is the input's
 constexpr int kMaxDigits = 512;
@@ -174,6 +180,7 @@ struct SortParams {
   uint32_t* out_toks;
   uint32_t* hist;          // [digit][tile]
   int n, tiles, shift, bits;
+  Zeros zeros;
 };
 
 __device__ __forceinline__ uint32_t key_at(const SortParams& p, int i) {
@@ -182,6 +189,10 @@ __device__ __forceinline__ uint32_t key_at(const SortParams& p, int i) {
 
 __global__ __launch_bounds__(kThreads) void sort_hist_kernel(SortParams p) {
   __shared__ uint32_t cnt[kMaxDigits];
+  if (static_cast<int>(blockIdx.x) >= p.tiles) {
+    zero_rows(p.zeros, blockIdx.x - p.tiles, gridDim.x - p.tiles, kThreads);
+    return;
+  }
   const int digits = 1 << p.bits;
   for (int d = threadIdx.x; d < digits; d += kThreads) cnt[d] = 0;
   __syncthreads();
@@ -195,8 +206,12 @@ __global__ __launch_bounds__(kThreads) void sort_hist_kernel(SortParams p) {
 
 // exclusive prefix sum of n counts in place, one workgroup
 constexpr int kScanThreads = 1024;
-__global__ __launch_bounds__(kScanThreads) void sort_scan_kernel(uint32_t* v, int64_t n) {
+__global__ __launch_bounds__(kScanThreads) void sort_scan_kernel(uint32_t* v, int64_t n, Zeros zeros) {
   __shared__ uint32_t part[kScanThreads];
+  if (blockIdx.x > 0) {
+    zero_rows(zeros, blockIdx.x - 1, gridDim.x - 1, kScanThreads);
+    return;
+  }
   const int64_t per = (n + kScanThreads - 1) / kScanThreads;
   const int64_t lo = threadIdx.x * per, hi = lo + per < n ? lo + per : n;
   uint32_t s = 0;
@@ -229,6 +244,10 @@ __device__ __forceinline__ uint64_t same_digit(uint32_t digit, int bits, bool on
 
 __global__ __launch_bounds__(kThreads) void sort_scatter_kernel(SortParams p) {
   __shared__ uint32_t at[kWaves][kMaxDigits];   // where the wave's next pair of each digit goes
+  if (static_cast<int>(blockIdx.x) >= p.tiles) {
+    zero_rows(p.zeros, blockIdx.x - p.tiles, gridDim.x - p.tiles, kThreads);
+    return;
+  }
   const int wave = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
   const int digits = 1 << p.bits;
   for (int d = threadIdx.x; d < digits; d += kThreads)
@@ -430,30 +449,33 @@ template <typename T, typename G> hipError_t embed_bwd_t(const EmbedArgs& a, hip
   uint32_t* hist = reinterpret_cast<uint32_t*>(ws + 4 * up256(size_t(n) * 4));
   float* part = reinterpret_cast<float*>(ws + 4 * up256(size_t(n) * 4) + up256((size_t(1) << bits) * tiles * 4));
 
-  const int64_t total = a.accumulate ? 0 : a.vocab * a.dim;
+  const Zeros all{static_cast<uint16_t*>(a.dweight), a.accumulate ? 0 : a.vocab * a.dim * static_cast<int64_t>(sizeof(G) / 2)};
   EmbedGradParams g{};
-  if (n > 0 && n <= kRankMost && a.vocab < (int64_t{1} << (32 - kTokenBits)) - 1) {
-    const RankParams rp{a.ids, a.id_bytes, a.vocab, n, (n + kPivots - 1) / kPivots, buf[0], buf[1], total};
-    const int64_t want = (total + kRankThreads * 32 - 1) / (kRankThreads * 32);
-    const dim3 grid(rp.groups + static_cast<unsigned>(want < 2048 ? want : 2048));
-    G* const dw = static_cast<G*>(a.dweight);
-    if (n <= kRankThreads) rank_kernel<G, 1><<<grid, kRankThreads, 0, stream>>>(rp, dw);
-    else if (n <= 4 * kRankThreads) rank_kernel<G, 4><<<grid, kRankThreads, 0, stream>>>(rp, dw);
-    else if (n <= 8 * kRankThreads) rank_kernel<G, 8><<<grid, kRankThreads, 0, stream>>>(rp, dw);
-    else rank_kernel<G, 16><<<grid, kRankThreads, 0, stream>>>(rp, dw);
+  if (n == 0) {
+    if (all.n > 0) embed_zero_kernel<<<dim3(zero_blocks(all, kThreads)), kThreads, 0, stream>>>(all);
+    return hipGetLastError();
+  }
+  if (n <= kRankMost && a.vocab < (int64_t{1} << (32 - kTokenBits)) - 1) {
+    const RankParams rp{a.ids, a.id_bytes, a.vocab, n, (n + kPivots - 1) / kPivots, buf[0], buf[1], all};
+    const dim3 grid(rp.groups + zero_blocks(all, kRankThreads));
+    if (n <= kRankThreads) rank_kernel<1><<<grid, kRankThreads, 0, stream>>>(rp);
+    else if (n <= 4 * kRankThreads) rank_kernel<4><<<grid, kRankThreads, 0, stream>>>(rp);
+    else if (n <= 8 * kRankThreads) rank_kernel<8><<<grid, kRankThreads, 0, stream>>>(rp);
+    else rank_kernel<16><<<grid, kRankThreads, 0, stream>>>(rp);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     g.keys = buf[0];
     g.toks = buf[1];
   } else {
-    if (total > 0) {
-      const int64_t want = (total + kThreads * 32 - 1) / (kThreads * 32);
-      embed_zero_kernel<G><<<dim3(static_cast<unsigned>(want < 8192 ? want : 8192)), kThreads, 0, stream>>>(
-          static_cast<G*>(a.dweight), total);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
-    if (n == 0) return hipSuccess;
+    const int launches = 3 * passes;
+    const int64_t share = ((all.n + launches - 1) / launches + 7) / 8 * 8;   // of a launch, in whole stores
+    int64_t done = 0;
+    auto next = [&]() {
+      const int64_t left = all.n - done;
+      const Zeros z{all.p + done, left < share ? left : share};
+      done += z.n;
+      return z;
+    };
     SortParams sp{};
     sp.n = n; sp.tiles = tiles; sp.bits = bits; sp.vocab = a.vocab; sp.hist = hist; sp.id_bytes = a.id_bytes;
     for (int k = 0; k < passes; ++k) {
@@ -463,9 +485,13 @@ template <typename T, typename G> hipError_t embed_bwd_t(const EmbedArgs& a, hip
       sp.out_keys = buf[(k & 1) ? 2 : 0];
       sp.out_toks = buf[(k & 1) ? 3 : 1];
       sp.shift = k * bits;
-      sort_hist_kernel<<<dim3(tiles), kThreads, 0, stream>>>(sp);
-      sort_scan_kernel<<<dim3(1), kScanThreads, 0, stream>>>(hist, (int64_t{1} << bits) * tiles);
-      sort_scatter_kernel<<<dim3(tiles), kThreads, 0, stream>>>(sp);
+      sp.zeros = next();
+      sort_hist_kernel<<<dim3(tiles + zero_blocks(sp.zeros, kThreads)), kThreads, 0, stream>>>(sp);
+      const Zeros z = next();
+      sort_scan_kernel<<<dim3(1 + zero_blocks(z, kScanThreads)), kScanThreads, 0, stream>>>(
+          hist, (int64_t{1} << bits) * tiles, z);
+      sp.zeros = next();
+      sort_scatter_kernel<<<dim3(tiles + zero_blocks(sp.zeros, kThreads)), kThreads, 0, stream>>>(sp);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }

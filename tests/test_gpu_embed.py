@@ -76,6 +76,21 @@ def test_embedding(M, case):
         R.check(got, R.embedding_bwd(ids, dout, vocab, scale, old, gd)["dweight"], f"accumulated {gd}")
 
 
+@pytest.mark.parametrize("dim", [1, 3, 8, 33])
+@pytest.mark.parametrize("vocab", [7, 509, 1009, 300007])
+@pytest.mark.parametrize("tokens", [5, 1100, 16384, 16400])
+def test_rows_without_a_token_are_zeroed(M, tokens, vocab, dim):
+    """Every element of every other row, whatever stood there, and nothing behind the table."""
+    for dtype in (BF16, F32):
+        buf = torch.full((vocab * dim + 64,), 3.0, dtype=dtype, device="cuda")
+        ids = torch.full((tokens,), vocab // 2, device="cuda")
+        dout = torch.zeros(tokens, dim, dtype=dtype, device="cuda")
+        dout[0] = 1.0
+        dw = M.embedding_bwd(ids, dout, vocab, dweight=buf[:vocab * dim].view(vocab, dim))
+        assert float(dw.float().sum()) == dim and bool((dw[vocab // 2] == 1).all())
+        assert int((dw != 0).sum()) == dim and bool((buf[vocab * dim:] == 3).all())
+
+
 def test_most_tokens(M):
     """As many tokens as a call takes: all that the largest grid holds."""
     n = (1 << 26) - 4
