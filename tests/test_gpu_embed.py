@@ -53,6 +53,8 @@ CASES = [
     (16384, 50000, 24, BF16, "one", torch.int64),
     (16385, 50000, 40, F32, "text", torch.int32),
     (40000, 1000, 24, BF16, "pad", torch.int64),
+    (70000, 131072, 8, BF16, "text", torch.int64),
+    (200001, 70000, 4, F32, "text", torch.int32),
 ]
 
 
