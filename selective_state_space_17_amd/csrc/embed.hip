@@ -86,8 +86,8 @@ __device__ __forceinline__ uint32_t sort_key(int64_t id, int64_t vocab) {
 // reads of 64 words that stand in 64 banks: no conflicts) and counts the words in each gap; the places are those
 // counts' prefix sums.  Workgroups of the same launch behind them zero dW meanwhile.  16384 ids, table of 50280 x
 // 768 in bf16: 16 us, 11 us without the zeroing, which alone takes 14 us; a radix sort by one workgroup, four bits
-// a pass in LDS, took 26 us beside the same zeroing.  The work grows with the square of the tokens, hence the limit,
-// to which a word has bits for them.
+// a pass in LDS, took 26 us beside the same zeroing.  The work grows with the square of the tokens; at the limit, to
+// which a word has bits for them, the whole gradient takes 35 us, one token above, sorted as below, 51 us.
 constexpr int kRankThreads = 1024, kTokenBits = 14, kRankMost = 1 << kTokenBits, kPivots = kLanes;
 
 struct RankParams {
@@ -165,7 +165,8 @@ template <int E> __global__ __launch_bounds__(kRankThreads, 8) void rank_kernel(
 
 // ---------------------------------------------------------------------------------- sort of any number by id
 // Least-significant-digit radix sort of (id, token) pairs, ids outside [0, vocab) sorted last as `vocab`.  Each of
-// its launches, few workgroups that wait for memory, zeroes a share of dW beside.
+// its launches, few workgroups that wait for memory, zeroes a share of dW beside.  Up to nine bits a pass: 65536 ids of
+// a table of 50280 take two passes of three launches, 6 + 6 + 7 us each, of 82 us for the gradient (768 columns).
 constexpr int kTile = 1024;                    // pairs per workgroup
 constexpr int kPerWave = kTile / kWaves;       // a wave's pairs are consecutive, so its order is the input's
 constexpr int kMaxDigits = 512;
@@ -183,8 +184,20 @@ struct SortParams {
   Zeros zeros;
 };
 
-__device__ __forceinline__ uint32_t key_at(const SortParams& p, int i) {
-  return p.ids == nullptr ? p.keys[i] : sort_key(id_at(p.ids, p.id_bytes, i), p.vocab);
+// keys first, first + step, ..., all loads at once; past the end the last one again
+template <int E> __device__ __forceinline__ void keys_at(const SortParams& p, int64_t first, int64_t step, uint32_t (&key)[E]) {
+  if (p.ids == nullptr) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int64_t i = first + e * step;
+      key[e] = p.keys[i < p.n ? i : p.n - 1];
+    }
+  } else {
+    int64_t id[E];
+    ids_at<E>(p.ids, p.id_bytes, first, step, p.n, id);
+#pragma unroll
+    for (int e = 0; e < E; ++e) key[e] = sort_key(id[e], p.vocab);
+  }
 }
 
 __global__ __launch_bounds__(kThreads) void sort_hist_kernel(SortParams p) {
@@ -196,9 +209,12 @@ __global__ __launch_bounds__(kThreads) void sort_hist_kernel(SortParams p) {
   const int digits = 1 << p.bits;
   for (int d = threadIdx.x; d < digits; d += kThreads) cnt[d] = 0;
   __syncthreads();
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * kTile;
-  for (int e = threadIdx.x; e < kTile; e += kThreads)
-    if (base + e < p.n) atomicAdd(&cnt[(key_at(p, static_cast<int>(base) + e) >> p.shift) & (digits - 1)], 1u);
+  const int64_t mine = static_cast<int64_t>(blockIdx.x) * kTile + threadIdx.x;
+  uint32_t key[kTile / kThreads];
+  keys_at(p, mine, kThreads, key);
+#pragma unroll
+  for (int e = 0; e < kTile / kThreads; ++e)
+    if (mine + e * kThreads < p.n) atomicAdd(&cnt[(key[e] >> p.shift) & (digits - 1)], 1u);
   __syncthreads();
   for (int d = threadIdx.x; d < digits; d += kThreads)
     p.hist[static_cast<int64_t>(d) * p.tiles + blockIdx.x] = cnt[d];
@@ -282,10 +298,18 @@ __global__ __launch_bounds__(kThreads) void sort_scatter_kernel(SortParams p) {
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) at[w][d] = 0;
   __syncthreads();
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kTile + wave * kPerWave;
-  for (int e = lane; e < kPerWave; e += kLanes)
-    if (first + e < p.n)
-      atomicAdd(&at[wave][(key_at(p, static_cast<int>(first) + e) >> p.shift) & (digits - 1)], 1u);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kTile + wave * kPerWave + lane;
+  constexpr int kEach = kPerWave / kLanes;
+  uint32_t key[kEach], tok[kEach];
+  keys_at(p, first, kLanes, key);
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int64_t i = first + e * kLanes;
+    tok[e] = p.ids != nullptr ? static_cast<uint32_t>(i) : p.toks[i < p.n ? i : p.n - 1];
+  }
+#pragma unroll
+  for (int e = 0; e < kEach; ++e)
+    if (first + e * kLanes < p.n) atomicAdd(&at[wave][(key[e] >> p.shift) & (digits - 1)], 1u);
   __syncthreads();
   for (int d = threadIdx.x; d < digits; d += kThreads) {
     uint32_t run = p.hist[static_cast<int64_t>(d) * p.tiles + blockIdx.x];
@@ -298,17 +322,16 @@ __global__ __launch_bounds__(kThreads) void sort_scatter_kernel(SortParams p) {
   }
   __syncthreads();
   volatile uint32_t* const mine = at[wave];
-  for (int e = lane; e < kPerWave; e += kLanes) {
-    const bool on = first + e < p.n;
-    const int i = static_cast<int>(first) + e;
-    const uint32_t key = on ? key_at(p, i) : 0u;
-    const uint32_t digit = (key >> p.shift) & (digits - 1);
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const bool on = first + e * kLanes < p.n;
+    const uint32_t digit = (key[e] >> p.shift) & (digits - 1);
     const uint64_t m = same_digit(digit, p.bits, on);
     const int rank = __popcll(m & ((1ull << lane) - 1));
     if (on) {
       const uint32_t to = mine[digit] + rank;
-      p.out_keys[to] = key;
-      p.out_toks[to] = p.ids != nullptr ? static_cast<uint32_t>(i) : p.toks[i];
+      p.out_keys[to] = key[e];
+      p.out_toks[to] = tok[e];
     }
     __builtin_amdgcn_wave_barrier();
     if (on && rank == 0) mine[digit] += __popcll(m);
