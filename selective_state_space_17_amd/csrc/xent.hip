@@ -178,9 +178,9 @@ __device__ __forceinline__ void fence_schedule() { __builtin_amdgcn_sched_barrie
 // 64 k ahead of the matrix cores and cross tile borders: a tile's first steps are on their way while the
 // tile before it is finished and stored.
 // Bound by the matrix cores at the clock that the power limit leaves them (1.8 to 1.9 GHz): 16384 x 2048 x 131072 in
-// bf16 runs at 1.32 PFLOP/s (logits, 6.6 ms; a library product of the same sizes, which writes them, at 1.40), 1.20
-// (G), 1.31 (dx) and 1.27 (dW), with the matrix cores busy 69, 60, 66 and 64 % of the cycles and no LDS bank
-// conflicts; 7373 x 768 x 50280 at 1.01 PFLOP/s (565 us; the library: 0.82).  With few tokens bound by the weight's
+// bf16 runs at 1.32 PFLOP/s (logits, 6.6 ms; a library product of the same sizes, which writes them, at 1.40), 1.21
+// (G), 1.28 (dx) and 1.23 (dW), with the matrix cores busy 69, 60, 66 and 64 % of the cycles and no LDS bank
+// conflicts; 7373 x 768 x 50280 at 1.03 PFLOP/s (553 us; the library: 0.82).  With few tokens bound by the weight's
 // bytes: 16 x 2560 x 50280 in 49 us, 5.2 TB/s with part of the weight left in the 256 MB cache by the call before (a
 // kernel that streamed the weight straight into registers was no faster).  Tried and slower: a ring of five
 // buffers of 32 k (8.3 against 7.5 ms for the logits at the time), two groups of waves taking turns (8.8 ms), 32 x
