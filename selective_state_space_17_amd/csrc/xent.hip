@@ -611,7 +611,8 @@ struct PrepParams {
   const void* x;
   uint16_t* xc;            // panels [term][dpad / 64][tok_cap][64]
   int* tally;              // counted tokens of each group of kGroup, or null: counted again where needed
-  int* plan;               // written: the count and the slices; read: the scale of x
+  int* plan;               // written: the count, the slices, the scales
+  const uint32_t* range;   // fp32: the largest magnitudes, see range_kernel
   int pairs, steps_x, tile_x, tile_w, tiles_mx, tiles_w, tiles_w_last;
   int* rows;
   int* tgt;
@@ -703,12 +704,12 @@ __device__ __forceinline__ void lay_out(const T* row, int64_t col, int64_t dim, 
 }
 
 // The largest finite magnitudes, of the weight, of the counted tokens' x and of their dloss and dloss + dlse
-// (fp32 only): each workgroup's, then all of them into the scales.
+// (fp32 only), each workgroup's.
 struct RangeParams {
   PrepParams prep;
   const float* weight;
   int64_t elems;
-  uint32_t* part;          // [kRangeBlocks][3]
+  uint32_t* part;          // [3][kRangeBlocks]
 };
 constexpr int kRangeBlocks = 1024;
 
@@ -762,23 +763,26 @@ __global__ __launch_bounds__(256) void range_kernel(RangeParams r) {
   if (threadIdx.x < 3) {
     uint32_t v = 0;
     for (int w = 0; w < 4; ++w) v = red[w][threadIdx.x] > v ? red[w][threadIdx.x] : v;
-    r.part[blockIdx.x * 3 + threadIdx.x] = v;
+    r.part[threadIdx.x * kRangeBlocks + blockIdx.x] = v;
   }
 }
 
-// wave k: the scale that brings the k-th maximum to [2^14, 2^15), but at most 2^126
-__global__ __launch_bounds__(3 * kLanes) void scale_kernel(const uint32_t* part, int* plan) {
-  const int k = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+// 2^e as fp32 that brings the k-th maximum to [2^14, 2^15), but at most 2^126; for a workgroup of 256
+__device__ __forceinline__ uint32_t scale_of(const uint32_t* range, int k, uint32_t (&red)[4]) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kRangeBlocks / kLanes; ++i) {
-    const uint32_t v = part[(i * kLanes + lane) * 3 + k];
+  for (int i = 0; i < kRangeBlocks / 256; ++i) {
+    const uint32_t v = range[k * kRangeBlocks + i * 256 + threadIdx.x];
     m = v > m ? v : m;
   }
   m = wave_max(m);
-  int e = 14 - (static_cast<int>(m >> 23) - 127);
-  e = m == 0 ? 0 : e > 126 ? 126 : e;
-  if (lane == 0) plan[kScaleW + k] = (e + 127) << 23;   // 2^e as fp32
+  __syncthreads();
+  if (threadIdx.x % kLanes == 0) red[threadIdx.x / kLanes] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w) m = red[w] > m ? red[w] : m;
+  const int e = 14 - (static_cast<int>(m >> 23) - 127);
+  return static_cast<uint32_t>((m == 0 ? 0 : e > 126 ? 126 : e) + 127) << 23;
 }
 
 // Which tokens count, in order, and their x as the products read it: in panels of 64 columns, padded with
@@ -800,7 +804,16 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
   before = block_count(before, red);
 
   const int64_t term = (p.tok_cap + kSkew) * p.dpad;
-  const float scale = sizeof(T) == 2 ? 1.f : reinterpret_cast<const float*>(p.plan)[kScaleX];
+  float scale = 1.f;
+  if constexpr (sizeof(T) == 4) {   // (every workgroup finds the scale of x for itself: a launch between took 5 us)
+    __shared__ uint32_t most[4];
+    scale = __uint_as_float(scale_of(p.range, 1, most));
+    if (blockIdx.x == static_cast<unsigned>(p.work_blocks)) {
+      const uint32_t w = scale_of(p.range, 0, most), g = scale_of(p.range, 2, most);
+      if (threadIdx.x < 3)
+        p.plan[kScaleW + threadIdx.x] = static_cast<int>(threadIdx.x == 0 ? w : threadIdx.x == 1 ? __float_as_uint(scale) : g);
+    }
+  }
   auto put = [&](int64_t i, int64_t t, bool real) {
     const T* row = static_cast<const T*>(p.x) + t * p.dim;
     for (int64_t c = lane * 8; c < p.dpad; c += kLanes * 8)
@@ -1055,7 +1068,7 @@ template <typename T> hipError_t prep(const XentArgs& a, const XentPlan& n, unsi
   if constexpr (sizeof(T) == 4) {
     RangeParams r{p, static_cast<const float*>(a.weight), a.vocab * a.dim, reinterpret_cast<uint32_t*>(ws + n.off_range)};
     range_kernel<<<dim3(kRangeBlocks), 256, 0, stream>>>(r);
-    scale_kernel<<<dim3(1), 3 * kLanes, 0, stream>>>(r.part, p.plan);
+    p.range = r.part;
   }
   prep_kernel<T><<<dim3(static_cast<unsigned>(p.work_blocks + kPadBlocks)), 256, 0, stream>>>(p);
   return hipGetLastError();
