@@ -39,6 +39,9 @@ CASES = [
     (1, 7, 8, BF16, "text", torch.int32),
     (2, 3, 333, BF16, "pad", torch.int64),
     (63, 100, 64, F32, "pad", torch.int64),
+    (33, 5, 600, BF16, "pad", torch.int64),
+    (64, 40, 1030, F32, "text", torch.int32),
+    (61, 7, 1544, BF16, "two", torch.int32),
     (64, 100, 130, BF16, "one", torch.int64),
     (65, 513, 68, F32, "two", torch.int32),
     (1000, 70000, 20, BF16, "text", torch.int64),
