@@ -64,25 +64,28 @@ struct Zeros {
   int64_t n;
 };
 constexpr int kZeroBlocks = 1 << 20;   // (a launch has less than 2^32 threads)
-constexpr int kZeroStores = 4;   // of a thread at a time
+// Stores of a thread at a time: one where zeroing is all that a launch does (716 MB at 6.6 TB/s; four: 5.9), four
+// beside a sort, whose workgroups then wait for fewer others (16384 x 768 of 50280: 34.2 us; one: 37.1).
+constexpr int kStoresAlone = 1, kStoresBeside = 4;
+template <int STORES = kStoresBeside>
 __device__ __forceinline__ void zero_rows(const Zeros& z, int64_t block, int64_t blocks, int threads) {
   const float none[8] = {};
-  const int64_t piece = static_cast<int64_t>(threads) * 8 * kZeroStores;
+  const int64_t piece = static_cast<int64_t>(threads) * 8 * STORES;
   for (int64_t at = block * piece; at < z.n; at += blocks * piece) {
 #pragma unroll
-    for (int k = 0; k < kZeroStores; ++k) {
+    for (int k = 0; k < STORES; ++k) {
       const int64_t i = at + (k * threads + threadIdx.x) * 8;
       store_row<8>(z.p + i, none, z.n - i);
     }
   }
 }
-unsigned zero_blocks(const Zeros& z, int threads) {
-  const int64_t piece = static_cast<int64_t>(threads) * 8 * kZeroStores, want = (z.n + piece - 1) / piece;
+unsigned zero_blocks(const Zeros& z, int threads, int stores = kStoresBeside) {
+  const int64_t piece = static_cast<int64_t>(threads) * 8 * stores, want = (z.n + piece - 1) / piece;
   return static_cast<unsigned>(want < kZeroBlocks ? want : kZeroBlocks);
 }
 
 __global__ __launch_bounds__(kThreads) void embed_zero_kernel(Zeros z) {
-  zero_rows(z, blockIdx.x, gridDim.x, kThreads);
+  zero_rows<kStoresAlone>(z, blockIdx.x, gridDim.x, kThreads);
 }
 
 __device__ __forceinline__ uint32_t sort_key(int64_t id, int64_t vocab) {
@@ -381,7 +384,7 @@ __device__ __forceinline__ void write_grad(G* row, const float (&acc)[V], float 
 // Up to 64 tokens need no sort: a wave for every token and chunk of 64 V columns compares the token's id with all
 // others', and where none before it has that id adds the rows of those that do, in order.  Two launches instead of
 // three, which is what so small a call's time is: 64 x 768 of 50280 in bf16 15 us (25 by the sort below), 38 x 1856
-// of 96414 in fp32, where 716 MB of zeros are the work, 121 us (142).
+// of 96414 in fp32, where 716 MB of zeros are the work, 108 us (142).
 constexpr int kFew = kLanes;
 template <typename T, typename G, int V>
 __global__ __launch_bounds__(kThreads) void embed_few_kernel(EmbedGradParams p, const void* ids, int id_bytes) {
@@ -554,7 +557,7 @@ template <typename T, typename G> hipError_t embed_bwd_t(const EmbedArgs& a, hip
   constexpr int kV = 16 / sizeof(T);
   const unsigned chunks = static_cast<unsigned>((a.dim + kLanes * kV - 1) / (kLanes * kV));
   if (n <= kFew) {
-    if (all.n > 0) embed_zero_kernel<<<dim3(zero_blocks(all, kThreads)), kThreads, 0, stream>>>(all);
+    if (all.n > 0) embed_zero_kernel<<<dim3(zero_blocks(all, kThreads, kStoresAlone)), kThreads, 0, stream>>>(all);
     if (n > 0)
       embed_few_kernel<T, G, kV><<<dim3((n + kWaves - 1) / kWaves, chunks), kThreads, 0, stream>>>(g, a.ids, a.id_bytes);
     return hipGetLastError();
