@@ -767,7 +767,9 @@ __global__ __launch_bounds__(256) void range_kernel(RangeParams r) {
   }
 }
 
-// 2^e as fp32 that brings the k-th maximum to [2^14, 2^15), but at most 2^126; for a workgroup of 256
+// 2^e as fp32 that brings the k-th maximum to [2^14, 2^15), but at most 2^126; for a workgroup of 256.  That of
+// dloss and dloss + dlse to half as much: the target's element of G, p (dloss + dlse) - dloss, is up to their sum,
+// and fp16 ends at 65504.
 __device__ __forceinline__ uint32_t scale_of(const uint32_t* range, int k, uint32_t (&red)[4]) {
   uint32_t m = 0;
 #pragma unroll
@@ -781,7 +783,7 @@ __device__ __forceinline__ uint32_t scale_of(const uint32_t* range, int k, uint3
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < 4; ++w) m = red[w] > m ? red[w] : m;
-  const int e = 14 - (static_cast<int>(m >> 23) - 127);
+  const int e = (k == 2 ? 13 : 14) - (static_cast<int>(m >> 23) - 127);
   return static_cast<uint32_t>((m == 0 ? 0 : e > 126 ? 126 : e) + 127) << 23;
 }
 

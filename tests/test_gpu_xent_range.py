@@ -1,0 +1,41 @@
+"""Cross entropy of fp32 inputs on the GPU where magnitudes lie far apart, element by element against the plain 64-bit
+forms in model_ops."""
+import pytest
+import torch
+
+import model_ops as R
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+F32 = torch.float32
+
+
+@pytest.fixture(scope="module")
+def M():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import selective_state_space_17_amd as m
+    return m
+
+
+def gradients(M, x, w, y, dl, dz=None):
+    loss, lse = M.linear_cross_entropy_fwd(x.cuda(), w.cuda(), y.cuda())
+    got = M.linear_cross_entropy_bwd(x.cuda(), w.cuda(), y.cuda(), lse, dl.cuda(), dlse=None if dz is None else dz.cuda())
+    return got, R.cross_entropy(x, w, y, dloss=dl, dlse=dz, lse_in=lse.cpu())
+
+
+@pytest.mark.parametrize("share", [0.99985, 0.9999, 0.99999, 1.0 - 2.0 ** -24])
+def test_loss_and_lse_gradients_of_opposite_signs(M, share):
+    """dlse = -2 dloss of a certain token: the target's element of G, p (dloss + dlse) - dloss, is twice as large as
+    either of its two parts, for a dloss just below a power of two."""
+    g = torch.Generator().manual_seed(17)
+    T, V, D = 24, 150, 64
+    w = torch.randn(V, D, generator=g)
+    y = torch.randint(0, V, (T,), generator=g)
+    x = 4 * w[y] + 0.1 * torch.randn(T, D, generator=g)
+    dl = 0.1 + 0.8 * torch.rand(T, generator=g)
+    dl[5] = share
+    say("dlse against dloss", share)
+    got, ref = gradients(M, x, w, y, dl, -2 * dl)
+    R.check(got["dx"], ref["dx"], "dx")
+    R.check(got["dweight"], ref["dweight"], "dweight")
