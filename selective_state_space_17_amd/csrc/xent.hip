@@ -438,11 +438,13 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void product_kernel(ProductParams 
     const int wave_m = m0 + wm * TM * 16;
     const int mrow = wave_m + lane / 16 * 4;
     const int ncol = n0 + wn * TN * 16 + lane % 16;
-    // What undoes the operands' scales: exact powers of two, one after the other, since their product may lie
-    // outside fp32.  For the logits it is kept at 2^-126 or more: they are then as good as 0, but 0 times the
-    // mask's -inf would not be -inf.
+    // What undoes the operands' scales: their product may lie outside fp32, so two powers of two, one after the
+    // other, each half of it: what is in between lies between the accumulator and the result, and overflows only if
+    // one of them does.  For the logits the product is kept at 2^-126 or more: they are then as good as 0, but 0
+    // times the mask's -inf would not be -inf.
     const float* const scales = reinterpret_cast<const float*>(p.plan);
-    const float ua = HALF ? 1.f / scales[p.scale_a] : 1.f, ub = HALF ? 1.f / scales[p.scale_b] : 1.f;
+    const int back = HALF ? 254 - (__float_as_uint(scales[p.scale_a]) >> 23) - (__float_as_uint(scales[p.scale_b]) >> 23) : 0;
+    const float ua = __uint_as_float((127 + back / 2) << 23), ub = __uint_as_float((127 + back - back / 2) << 23);
     const float unit = __builtin_fmaxf(ua * ub, 0x1p-126f);
     const float to_log2 = kLog2e * unit;
     auto each = [&](int j, auto&& f) {   // accumulator = f(accumulator, row)

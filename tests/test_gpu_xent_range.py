@@ -39,3 +39,21 @@ def test_loss_and_lse_gradients_of_opposite_signs(M, share):
     got, ref = gradients(M, x, w, y, dl, -2 * dl)
     R.check(got["dx"], ref["dx"], "dx")
     R.check(got["dweight"], ref["dweight"], "dweight")
+
+
+@pytest.mark.parametrize("ex,ew,eg", [(112, -114, -60), (-116, 113, -70), (118, -120, 4), (-119, 116, 3)])
+def test_one_matrix_near_the_largest_numbers(M, ex, ew, eg):
+    """x or the weight near fp32's largest numbers, the gradient of the logits small, and the products of the two well
+    inside fp32: nothing on the way may overflow.  (Norms as for inputs of any size: sqrt(K) roundings of 2^-24 at
+    random, 16 times that.)"""
+    g = torch.Generator().manual_seed(41)
+    T, V, D = 90, 400, 160
+    x, w = torch.randn(T, D, generator=g) * 2.0 ** ex, torch.randn(V, D, generator=g) * 2.0 ** ew
+    y = torch.randint(0, V, (T,), generator=g)
+    dl = (torch.rand(T, generator=g) + 0.5) * 2.0 ** eg
+    say("one matrix near the largest numbers", ex, ew, eg)
+    got, ref = gradients(M, x, w, y, dl)
+    for k in ("dx", "dweight"):
+        want, out = ref[k][0], got[k].cpu().double()
+        assert float(want.abs().max()) < 2.0 ** 127, "the case itself overflows"
+        assert float((out - want).norm()) <= 2e-6 * float(want.norm()) + 2.0 ** -126 * want.numel() ** 0.5, k
