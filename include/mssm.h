@@ -580,19 +580,24 @@ size_t mssm_norm_bwd_workspace_size(const mssm_norm_desc* desc);
  *             (in fp32, rounded once); one of dx and dweight may be NULL
  * Products are summed in fp32.  With MSSM_BF16 G is rounded to bf16 once,
  * whatever grad_dtype (for up to 256 tokens it keeps 16 bits).  With MSSM_F32
- * x, weight and G enter the matrix cores as two fp16 terms each, under a power
- * of two that fits each matrix: a value keeps 23 bits or more where it is
- * within 2^-16 of its matrix's largest finite magnitude, and is right to 2^-39
- * of that magnitude below.  A NaN among a token's logits, or one of +infinity,
+ * x, weight and G carry a power of two each that fits them (G's fits dloss).
+ * In the logits x and weight are two fp16 terms each: a value keeps 23 bits or
+ * more where it is within 2^-16 of its matrix's largest finite magnitude, and
+ * is right to 2^-39 of that magnitude below; an infinity among them makes its
+ * logits NaN.  In the gradients' products all three are three bf16 terms each,
+ * all 24 bits of what is within 2^-124 of the largest magnitude (G: of the
+ * largest dloss), the products summed in fp32 under those powers of two.
+ * A NaN among a token's logits, or one of +infinity,
  * makes its loss and lse NaN.  All sums are taken in a fixed order: the same
  * result on every run.
  * tokens may be 0, up to 2^26 - 1; vocab up to 2^30; dim up to 2^20.  bf16
  * weight of a dim that is a multiple of 64 must be 16-byte aligned (it is read
  * in place; any other weight is laid out piece by piece in the workspace
  * first), other pointers element-aligned.  workspace: at least the bytes the
- * size queries ask, 256-byte aligned; it holds the counted tokens' x, a piece
- * of at most about 896 MiB (but 256 vocabulary rows at least) of G or partial
- * sums and laid-out weight, up to 128 MiB of sums over parts of k, and where
+ * size queries ask, 256-byte aligned; it holds the counted tokens' x (for
+ * MSSM_F32 gradients twice, 4 and 6 bytes a value), a piece of at most about
+ * 896 MiB (but 256 vocabulary rows at least) of G or partial sums and laid-out
+ * weight, up to 128 MiB of sums over parts of k, and where
  * the vocabulary takes several pieces dx in fp32.  Other rules as mssm_selective_scan_fwd. */
 typedef struct {
     int64_t tokens, vocab, dim;

@@ -19,14 +19,17 @@
 // bf16 inputs enter the matrix cores as they are; products are summed in fp32.  G is rounded to bf16 (the
 // gradients' own type) once; for up to 256 tokens, where few roundings average out and the weight's bytes are what
 // the time goes into, it is kept in two bf16 terms.
-// fp32 inputs are split into two fp16 terms, v s = hi + lo: exact for three values in four, one unit in the last of
-// 24 bits off (2^-23) for the rest.  A product is the three term products hi lo + lo hi + hi hi, summed in fp32; lo
-// lo is left out, below 2^-22 of the product (2^-25 in the mean square).  Over a row of products both vanish beside
-// the roundings of the sum.  s is a power of two for each matrix that brings its largest finite magnitude to [2^14,
-// 2^15): fp16's smallest step then lies 2^39 below the largest value, so values down to 2^-16 of it keep the bits
-// said, smaller ones are right to 2^-39 of the largest.  Three fp16 products take a fifth of the time of one
-// product at the matrix cores' fp32 rate, a sixteenth of fp16's; with three bf16 terms and six products the fp32
-// step of 1001 x 1000 x 32003 took 1.47 ms.
+// fp32 matrices carry a power of two each, s, that brings their largest finite magnitude to [2^14, 2^15).  x and the
+// weight enter the logits as two fp16 terms, v s = hi + lo: exact for three values in four, one unit in the last of 24
+// bits off (2^-23) for the rest.  A product is the three term products hi lo + lo hi + hi hi, summed in fp32; lo lo is
+// left out, below 2^-22 of the product (2^-25 in the mean square).  Over a row of products both vanish beside the
+// roundings of the sum.  fp16's smallest step lies 2^39 below the largest value, so values down to 2^-16 of it keep the
+// bits said, smaller ones are right to 2^-39 of the largest.  That serves the logits, whose absolute error is what
+// counts, and not the gradients: a word's row of dW is made of p dloss with p down to 1e-30, and its error relative to
+// its own size is what an optimiser sees.  There x, the weight and G enter as three bf16 terms, all 24 bits of what is
+// within 2^-124 of the largest, and a product is the six term products whose places add up to two at most (what is left
+// out is below 2^-23 of the product, 2^-26 in the mean square).  One product at the matrix cores' fp32 rate, a sixteenth
+// of fp16's, would take 2.7 times the time of six.
 #include <type_traits>
 
 #include "device_util.h"
@@ -46,8 +49,9 @@ constexpr int kRow = kBK * 2;           // bytes of a row of a step
 constexpr int kPlane = 64 * kRow;       // LDS tiles are planes of 64 rows x 128 bytes
 constexpr int kTokTile = 256;           // compacted tokens are padded to this
 constexpr int kSkew = 34;               // rows between panels: 4352 bytes, see Operand
-constexpr int kTerms = 2;               // 16-bit terms of an fp32 value
-constexpr int kMostPairs = 3;           // term products kept
+constexpr int kTerms = 2;               // fp16 terms of an fp32 value in the logits
+constexpr int kFineTerms = 3;           // bf16 terms of an fp32 value in the gradients' products
+constexpr int kMostPairs = 6;           // term products kept
 constexpr int kFewTokens = 256;         // up to these G is kept in two terms with bf16 too
 
 // v (already scaled) = t[0] + t[1]: each the nearest fp16 of what is left.  Infinities and NaN stay what they are.
@@ -57,10 +61,14 @@ __device__ __forceinline__ void split_half(float v, uint16_t (&t)[kTerms]) {
   t[0] = __builtin_bit_cast(uint16_t, hi);
   t[1] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(r == r ? r : 0.f));   // (inf - inf)
 }
-__device__ __forceinline__ void split_bf(float v, uint16_t (&t)[kTerms]) {
-  t[0] = narrow<uint16_t>(v);
-  const float r = v - widen(t[0]);
-  t[1] = narrow<uint16_t>(r == r ? r : 0.f);
+// the same in bf16 terms
+__device__ __forceinline__ void split_bf(float v, uint16_t (&t)[kFineTerms]) {
+#pragma unroll
+  for (int k = 0; k < kFineTerms; ++k) {
+    t[k] = narrow<uint16_t>(v);
+    v -= widen(t[k]);
+    v = v == v ? v : 0.f;
+  }
 }
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
@@ -99,7 +107,7 @@ struct ProductParams {
   int pairs;               // term products, and the terms of either operand in each
   int ta[kMostPairs], tb[kMostPairs];
   const int* plan;         // see Plan
-  int scale_a, scale_b;    // which of its scales the operands carry (fp16 terms)
+  int scale_a, scale_b;    // fp32: which of its scales the operands carry
   int slices_at;           // dx, dW: where in plan the slices of the tiles of the last round stand
   // epilogues
   int v0;                  // first vocabulary row of this piece
@@ -111,7 +119,7 @@ struct ProductParams {
   const float* gl;         // dloss + dlse
   const float* g;          // dloss
   int g_terms;
-  uint16_t* dl;            // panels [vocabulary / 64][token][64], one or two terms
+  uint16_t* dl;            // panels [vocabulary / 64][token][64], one to three terms
   int64_t pdl;             // elements between them
   float* sums;             // [job][BN][BM]: a slice's sums
   float* over;             // [n][ld_over]: sums over pieces, or null
@@ -186,7 +194,7 @@ __device__ __forceinline__ void fence_schedule() { __builtin_amdgcn_sched_barrie
 // buffers of 32 k (8.3 against 7.5 ms for the logits at the time), two groups of waves taking turns (8.8 ms), 32 x
 // 32 x 16 instructions (8.6 ms, spills), all loads in a step's first two rows (7.9 ms), G stored past the cache
 // (1.78 against 1.55 ms a piece).
-template <int BM, int BN, int WM, int WN, bool ATR, bool BTR, bool HALF, int EPI>
+template <int BM, int BN, int WM, int WN, bool ATR, bool BTR, bool FP32, int EPI>
 __global__ __launch_bounds__(WM * WN * 64, 2) void product_kernel(ProductParams p) {
   constexpr int kW = WM * WN;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;      // 16 x 16 tiles of a wave
@@ -367,7 +375,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void product_kernel(ProductParams 
   auto multiply_row = [&](int i, int set) {
 #pragma unroll
     for (int j = 0; j < TN; ++j)
-      if constexpr (HALF)
+      if constexpr (FP32 && !kSliced)
         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, fa[set][i]),
                                                            __builtin_bit_cast(f16x8, fb[set][j]), acc[i][j], 0, 0, 0);
       else
@@ -443,7 +451,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void product_kernel(ProductParams 
     // one of them does.  For the logits the product is kept at 2^-126 or more: they are then as good as 0, but 0
     // times the mask's -inf would not be -inf.
     const float* const scales = reinterpret_cast<const float*>(p.plan);
-    const int back = HALF ? 254 - (__float_as_uint(scales[p.scale_a]) >> 23) - (__float_as_uint(scales[p.scale_b]) >> 23) : 0;
+    const int back = FP32 ? 254 - (__float_as_uint(scales[p.scale_a]) >> 23) - (__float_as_uint(scales[p.scale_b]) >> 23) : 0;
     const float ua = __uint_as_float((127 + back / 2) << 23), ub = __uint_as_float((127 + back - back / 2) << 23);
     const float unit = __builtin_fmaxf(ua * ub, 0x1p-126f);
     const float to_log2 = kLog2e * unit;
@@ -492,7 +500,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void product_kernel(ProductParams 
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
         const int n = ncol + j * 16;
-        const float sg = HALF ? scales[kScaleG] : 1.f;
+        const float sg = FP32 ? scales[kScaleG] : 1.f;
         const float lse = p.lse[n], g = p.g[n] * sg, c = lse * kLog2e;
         const float gl = p.gl[n] * sg * __builtin_amdgcn_exp2f(__builtin_fmaf(-lse, kLog2e, c));   // as in the forward pass
         each(j, [&](float a, int) { return __builtin_amdgcn_exp2f(__builtin_fmaf(a, to_log2, -c)) * gl; });
@@ -504,22 +512,24 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void product_kernel(ProductParams 
 #pragma unroll
         for (int i = 0; i < TM; i += 2) {
           uint16_t* const at = to + (i / 4 * (p.tok_cap + kSkew)) * 64 + i % 4 * 16;
-          if (HALF || p.g_terms == 2) {
-            uint16_t t[2][4][kTerms];
+          if (FP32 || p.g_terms == 2) {
+            // term after term of what is left
+            f32x4_t r[2] = {acc[i][j], acc[i + 1][j]};
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if constexpr (HALF) split_half(acc[i + h][j][e], t[h][e]);
-                else split_bf(acc[i + h][j][e], t[h][e]);
-              }
-#pragma unroll
-            for (int k = 0; k < kTerms; ++k) {
+            for (int k = 0; k < (FP32 ? kFineTerms : 2); ++k) {
               u32x2_t d[2];
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                d[h] = u32x2_t{t[h][0][k] | static_cast<uint32_t>(t[h][1][k]) << 16,
-                               t[h][2][k] | static_cast<uint32_t>(t[h][3][k]) << 16};
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                  float a, b;
+                  d[h][e / 2] = pack_bf16(r[h][e], r[h][e + 1]);
+                  split_bf16(d[h][e / 2], a, b);
+                  a = r[h][e] - a;
+                  b = r[h][e + 1] - b;
+                  r[h][e] = a == a ? a : 0.f;   // (inf - inf)
+                  r[h][e + 1] = b == b ? b : 0.f;
+                }
               *reinterpret_cast<u32x4_t*>(at + k * p.pdl) = two_tiles(d[0], d[1]);
             }
           } else {
@@ -612,6 +622,7 @@ struct PrepParams {
   int64_t ignore, vocab, tokens, dim, dpad, tok_cap;
   const void* x;
   uint16_t* xc;            // panels [term][dpad / 64][tok_cap][64]
+  uint16_t* xf;            // fp32 gradients: the same in bf16 terms, or null
   int* tally;              // counted tokens of each group of kGroup, or null: counted again where needed
   int* plan;               // written: the count, the slices, the scales
   const uint32_t* range;   // fp32: the largest magnitudes, see range_kernel
@@ -675,10 +686,11 @@ __global__ __launch_bounds__(256) void tally_kernel(PrepParams p) {
   if (threadIdx.x == 0) p.tally[blockIdx.x] = n;
 }
 
-// 8 elements of a row, laid out: bf16 as it is, fp32 scaled and in two fp16 terms; past the row's end zeros
+// 8 elements of a row, laid out: bf16 as it is, fp32 scaled and in two fp16 terms, and with `fine` in three bf16 terms
+// there; past the row's end zeros
 template <typename T>
-__device__ __forceinline__ void lay_out(const T* row, int64_t col, int64_t dim, uint16_t* to, int64_t term,
-                                        float scale) {
+__device__ __forceinline__ void lay_out(const T* row, int64_t col, int64_t dim, uint16_t* to, uint16_t* fine,
+                                        int64_t term, float scale) {
   if constexpr (sizeof(T) == 2) {
     u32x4_t v = {0, 0, 0, 0};
     if (col + 8 <= dim) {
@@ -692,16 +704,22 @@ __device__ __forceinline__ void lay_out(const T* row, int64_t col, int64_t dim, 
   } else {
     float f[8];
     load_row<8>(row + col, f, dim - col);
-    uint16_t t[8][kTerms];
+    auto put = [&](auto n, uint16_t* at, auto&& split) {
+      constexpr int kN = decltype(n)::value;
+      uint16_t t[8][kN];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) split_half(f[e] * scale, t[e]);
+      for (int e = 0; e < 8; ++e) split(f[e], t[e]);
 #pragma unroll
-    for (int k = 0; k < kTerms; ++k) {
-      u32x4_t v;
+      for (int k = 0; k < kN; ++k) {
+        u32x4_t v;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = t[2 * e][k] | static_cast<uint32_t>(t[2 * e + 1][k]) << 16;
-      *reinterpret_cast<u32x4_t*>(to + k * term) = v;
-    }
+        for (int e = 0; e < 4; ++e) v[e] = t[2 * e][k] | static_cast<uint32_t>(t[2 * e + 1][k]) << 16;
+        *reinterpret_cast<u32x4_t*>(at + k * term) = v;
+      }
+    };
+    put(std::integral_constant<int, kTerms>{}, to, [&](float v, auto& t) { split_half(v * scale, t); });
+    if (fine != nullptr)
+      put(std::integral_constant<int, kFineTerms>{}, fine, [&](float v, auto& t) { split_bf(v * scale, t); });
   }
 }
 
@@ -769,9 +787,7 @@ __global__ __launch_bounds__(256) void range_kernel(RangeParams r) {
   }
 }
 
-// 2^e as fp32 that brings the k-th maximum to [2^14, 2^15), but at most 2^126; for a workgroup of 256.  That of
-// dloss and dloss + dlse to half as much: the target's element of G, p (dloss + dlse) - dloss, is up to their sum,
-// and fp16 ends at 65504.
+// 2^e as fp32 that brings the k-th maximum to [2^14, 2^15), but at most 2^126; for a workgroup of 256
 __device__ __forceinline__ uint32_t scale_of(const uint32_t* range, int k, uint32_t (&red)[4]) {
   uint32_t m = 0;
 #pragma unroll
@@ -785,12 +801,13 @@ __device__ __forceinline__ uint32_t scale_of(const uint32_t* range, int k, uint3
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < 4; ++w) m = red[w] > m ? red[w] : m;
-  const int e = (k == 2 ? 13 : 14) - (static_cast<int>(m >> 23) - 127);
+  const int e = 14 - (static_cast<int>(m >> 23) - 127);
   return static_cast<uint32_t>((m == 0 ? 0 : e > 126 ? 126 : e) + 127) << 23;
 }
 
 // Which tokens count, in order, and their x as the products read it: in panels of 64 columns, padded with
-// zeros, fp32 as two fp16 terms; after the last one, zero rows up to the end of its tile of 256.
+// zeros, fp32 as two fp16 terms (and for the gradients three bf16 terms beside); after the last one, zero rows up to
+// the end of its tile of 256.
 template <typename T>
 __global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
   __shared__ int red[4];
@@ -820,8 +837,10 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
   }
   auto put = [&](int64_t i, int64_t t, bool real) {
     const T* row = static_cast<const T*>(p.x) + t * p.dim;
-    for (int64_t c = lane * 8; c < p.dpad; c += kLanes * 8)
-      lay_out<T>(row, c, real ? p.dim : 0, p.xc + (c / 64 * (p.tok_cap + kSkew) + i) * 64 + c % 64, term, scale);
+    for (int64_t c = lane * 8; c < p.dpad; c += kLanes * 8) {
+      const int64_t at = (c / 64 * (p.tok_cap + kSkew) + i) * 64 + c % 64;
+      lay_out<T>(row, c, real ? p.dim : 0, p.xc + at, p.xf != nullptr ? p.xf + at : nullptr, term, scale);
+    }
   };
   if (pad) {
     if (blockIdx.x == static_cast<unsigned>(p.work_blocks) && threadIdx.x < 4) {
@@ -872,15 +891,17 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
 }
 
 // rows of the weight as the products read them (width not a multiple of 64, or fp32), in panels
-// [term][dpad / 64][rows][64]: 32 rows a workgroup
+// [term][dpad / 64][rows][64]: 32 rows a workgroup; `fine`: see lay_out
 template <typename T>
-__global__ __launch_bounds__(256) void weight_kernel(const T* w, uint16_t* to, int64_t rows, int64_t dim, int64_t dpad,
-                                                     const int* plan) {
+__global__ __launch_bounds__(256) void weight_kernel(const T* w, uint16_t* to, uint16_t* fine, int64_t rows, int64_t dim,
+                                                     int64_t dpad, const int* plan) {
   const int64_t r = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x / 8;
   if (r >= rows) return;
   const float scale = sizeof(T) == 2 ? 1.f : reinterpret_cast<const float*>(plan)[kScaleW];
-  for (int64_t c = threadIdx.x % 8 * 8; c < dpad; c += 64)
-    lay_out<T>(w + r * dim, c, dim, to + (c / 64 * (rows + kSkew) + r) * 64 + c % 64, (rows + kSkew) * dpad, scale);
+  for (int64_t c = threadIdx.x % 8 * 8; c < dpad; c += 64) {
+    const int64_t at = (c / 64 * (rows + kSkew) + r) * 64 + c % 64;
+    lay_out<T>(w + r * dim, c, dim, to + at, fine != nullptr ? fine + at : nullptr, (rows + kSkew) * dpad, scale);
+  }
 }
 
 // Joins the tiles' (maximum, sum) of a piece with those of the pieces before it; after the last piece, the loss.
@@ -937,7 +958,8 @@ __global__ __launch_bounds__(256) void join_kernel(JoinParams p) {
 
 // ---------------------------------------------------------------------------------------------- host side
 constexpr size_t up256(size_t b) { return (b + 255) / 256 * 256; }
-constexpr int64_t kPieceBytes = int64_t{896} << 20;   // of a piece's G (or partial sums) and laid-out weight
+// of a piece's G (or partial sums) and laid-out weight, and of the bf16 terms of x, which leave the rest half at least
+constexpr int64_t kPieceBytes = int64_t{896} << 20;
 
 int64_t tiles_of(int64_t m, int64_t n, int tile) { return (m + tile - 1) / tile * ((n + tile - 1) / tile); }
 
@@ -961,19 +983,21 @@ int64_t sums_bytes(int64_t tiles, int64_t steps, int tile) {
 
 struct XentPlan {
   bool copy_w;             // the weight needs a laid-out copy
-  int terms, pairs, g_terms, g_pairs;   // of x and the weight, and of G
+  int terms, pairs;        // in the logits
+  int fine, g_terms, g_pairs;           // fp32 gradients: bf16 terms of x and the weight (else 0: read as in the logits); of G
   int64_t dpad, tok_cap, piece;    // piece: vocabulary rows, a multiple of 256
   int pieces;
   int logits, gx, gw;      // tiles
-  size_t off_plan, off_range, off_rows, off_tgt, off_a, off_b, off_c, off_xc, off_tally, off_part, off_w, off_dl, off_over, off_sums, bytes;
+  size_t off_plan, off_range, off_rows, off_tgt, off_a, off_b, off_c, off_xc, off_xf, off_tally, off_part, off_w, off_wf, off_dl, off_over, off_sums, bytes;
 };
 
 XentPlan xent_plan(const XentArgs& a, bool grad) {
   XentPlan n{};
   n.terms = a.io ? 1 : kTerms;
   n.pairs = a.io ? 1 : 3;
-  n.g_terms = !a.io || a.tokens <= kFewTokens ? 2 : 1;
-  n.g_pairs = a.io ? n.g_terms : 3;
+  n.fine = a.io || !grad ? 0 : kFineTerms;
+  n.g_terms = !a.io ? kFineTerms : a.tokens <= kFewTokens ? 2 : 1;
+  n.g_pairs = a.io ? n.g_terms : kMostPairs;
   n.dpad = (a.dim + 63) / 64 * 64;
   n.tok_cap = (a.tokens + kTokTile - 1) / kTokTile * kTokTile;
   n.copy_w = !a.io || a.dim % 64 != 0;
@@ -981,8 +1005,9 @@ XentPlan xent_plan(const XentArgs& a, bool grad) {
   int64_t row = 1;   // bytes a vocabulary row of a piece costs
   if (grad) row += n.tok_cap * 2 * n.g_terms;
   else row += n.tok_cap / 8;   // a partial of 8 bytes per 64 rows
-  if (n.copy_w) row += n.dpad * 2 * n.terms;
-  n.piece = kPieceBytes / row / 256 * 256;
+  if (n.copy_w) row += n.dpad * 2 * (n.terms + n.fine);
+  const int64_t fine_x = (n.tok_cap + kSkew) * n.dpad * 2 * n.fine;
+  n.piece = (fine_x < kPieceBytes / 2 ? kPieceBytes - fine_x : kPieceBytes / 2) / row / 256 * 256;
   if (n.piece < 256) n.piece = 256;
   if (n.piece > vpad) n.piece = vpad;
   n.pieces = static_cast<int>((a.vocab + n.piece - 1) / n.piece);
@@ -1003,8 +1028,10 @@ XentPlan xent_plan(const XentArgs& a, bool grad) {
   n.off_b = take(tc * (grad ? 4 : 8));
   n.off_c = take(tc * 4);
   n.off_xc = take((tc + kSkew) * n.dpad * 2 * n.terms);
+  n.off_xf = take(static_cast<size_t>(fine_x));
   n.off_tally = take((tc + kGroup - 1) / kGroup * 4);
   n.off_w = take(n.copy_w ? size_t(n.piece + kSkew) * n.dpad * 2 * n.terms : 0);
+  n.off_wf = take(size_t(n.piece + kSkew) * n.dpad * 2 * n.fine);
   n.off_part = take(grad ? 0 : size_t(n.piece) / 64 * tc * 8);
   n.off_dl = take(grad ? (tc + kSkew) * n.piece * 2 * n.g_terms : 0);
   n.off_over = take(grad && n.pieces > 1 ? tc * n.dpad * 4 : 0);
@@ -1016,13 +1043,13 @@ XentPlan xent_plan(const XentArgs& a, bool grad) {
   return n;
 }
 
-template <int BM, int WM, int WN, bool ATR, bool BTR, bool HALF, int EPI>
+template <int BM, int WM, int WN, bool ATR, bool BTR, bool FP32, int EPI>
 hipError_t product(const ProductParams& p, hipStream_t stream) {
   constexpr int kSlots = slots_of(BM);
   const int64_t tiles = tiles_of(p.M, p.N, BM);
   if (tiles == 0) return hipSuccess;
   const int64_t want = EPI == kGradX || EPI == kGradW ? kSlots : (tiles + 7) / 8 * 8;
-  product_kernel<BM, BM, WM, WN, ATR, BTR, HALF, EPI>
+  product_kernel<BM, BM, WM, WN, ATR, BTR, FP32, EPI>
       <<<dim3(static_cast<unsigned>(want < kSlots ? want : kSlots)), WM * WN * 64, 0, stream>>>(p);
   if constexpr (EPI == kGradX || EPI == kGradW) {
     const int64_t sliced = tiles < kSlots ? tiles : kSlots;
@@ -1031,10 +1058,10 @@ hipError_t product(const ProductParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <bool ATR, bool BTR, bool HALF, int EPI>
+template <bool ATR, bool BTR, bool FP32, int EPI>
 hipError_t product_any(int tile, const ProductParams& p, hipStream_t stream) {
-  return tile == kBig ? product<kBig, 2, 4, ATR, BTR, HALF, EPI>(p, stream)
-                      : product<kSmall, 2, 2, ATR, BTR, HALF, EPI>(p, stream);
+  return tile == kBig ? product<kBig, 2, 4, ATR, BTR, FP32, EPI>(p, stream)
+                      : product<kSmall, 2, 2, ATR, BTR, FP32, EPI>(p, stream);
 }
 
 template <typename T> hipError_t prep(const XentArgs& a, const XentPlan& n, unsigned char* ws, bool grad, hipStream_t stream) {
@@ -1057,6 +1084,7 @@ template <typename T> hipError_t prep(const XentArgs& a, const XentPlan& n, unsi
     p.tiles_mx = static_cast<int>((a.dim + n.gx - 1) / n.gx);
     p.tiles_w = static_cast<int>(tiles_of(a.dim, rows, n.gw));
     p.tiles_w_last = static_cast<int>(tiles_of(a.dim, last, n.gw));
+    if (n.fine != 0) p.xf = reinterpret_cast<uint16_t*>(ws + n.off_xf);
     p.lse = a.lse_in; p.dloss = a.dloss; p.dlse = a.dlse; p.dx = a.dx;
     p.c_lse = reinterpret_cast<float*>(ws + n.off_a);
     p.c_gl = reinterpret_cast<float*>(ws + n.off_b);
@@ -1091,27 +1119,31 @@ Operand panels(const void* p, int64_t rows, int64_t cols, bool k_strided) {
   return o;
 }
 
-// the piece's rows of the weight, laid out first where they cannot be read in place
+// the piece's rows of the weight, laid out first where they cannot be read in place (fp32 with dx: for both products)
 template <typename T>
 hipError_t lay_out_weight(const XentArgs& a, const XentPlan& n, unsigned char* ws, int64_t v0, int64_t rows,
                           hipStream_t stream) {
   if (!n.copy_w) return hipSuccess;
   weight_kernel<T><<<dim3(static_cast<unsigned>((rows + 31) / 32)), 256, 0, stream>>>(
-      static_cast<const T*>(a.weight) + v0 * a.dim, reinterpret_cast<uint16_t*>(ws + n.off_w), rows, a.dim, n.dpad,
+      static_cast<const T*>(a.weight) + v0 * a.dim, reinterpret_cast<uint16_t*>(ws + n.off_w),
+      n.fine != 0 && a.dx != nullptr ? reinterpret_cast<uint16_t*>(ws + n.off_wf) : nullptr, rows, a.dim, n.dpad,
       reinterpret_cast<const int*>(ws + n.off_plan));
   return hipGetLastError();
 }
 
-// the term products, smallest first: (0, 0); with two terms of B alone (0, 1), (0, 0); with two of either (1, 0), (0, 1), (0, 0)
+// the term products (of A, of B), smallest first: one term of either; two of B alone; two of either; three of either
 void set_pairs(ProductParams* p, int pairs) {
+  constexpr int kOf[4][kMostPairs][2] = {{{0, 0}}, {{0, 1}, {0, 0}}, {{1, 0}, {0, 1}, {0, 0}},
+                                         {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}}};
   p->pairs = pairs;
-  p->ta[0] = pairs == 3;
-  p->tb[0] = pairs == 2;
-  p->tb[1] = pairs == 3;
+  for (int i = 0; i < pairs; ++i) {
+    p->ta[i] = kOf[pairs < 4 ? pairs - 1 : 3][i][0];
+    p->tb[i] = kOf[pairs < 4 ? pairs - 1 : 3][i][1];
+  }
 }
 
 Operand weight_operand(const XentArgs& a, const XentPlan& n, unsigned char* ws, int64_t v0, int64_t rows, bool k_strided) {
-  if (n.copy_w) return panels(ws + n.off_w, rows, n.dpad, k_strided);
+  if (n.copy_w) return panels(ws + (n.fine != 0 && k_strided ? n.off_wf : n.off_w), rows, n.dpad, k_strided);
   Operand o{};
   o.p = static_cast<const unsigned char*>(a.weight) + v0 * a.dim * 2;
   o.row = a.dim * 2;
@@ -1123,7 +1155,7 @@ Operand weight_operand(const XentArgs& a, const XentPlan& n, unsigned char* ws, 
 }
 
 template <typename T> hipError_t xent_fwd_t(const XentArgs& a, hipStream_t stream) {
-  constexpr bool kHalf = sizeof(T) == 4;
+  constexpr bool kFp32 = sizeof(T) == 4;
   const XentPlan n = xent_plan(a, false);
   unsigned char* ws = static_cast<unsigned char*>(a.workspace);
   hipError_t e = prep<T>(a, n, ws, false, stream);
@@ -1144,7 +1176,7 @@ template <typename T> hipError_t xent_fwd_t(const XentArgs& a, hipStream_t strea
     p.part = reinterpret_cast<float2*>(ws + n.off_part);
     p.tok_cap = n.tok_cap;
     p.tlogit = reinterpret_cast<float*>(ws + n.off_a);
-    e = product_any<false, false, kHalf, kLogits>(n.logits, p, stream);
+    e = product_any<false, false, kFp32, kLogits>(n.logits, p, stream);
     if (e != hipSuccess) return e;
     JoinParams j{};
     j.part = p.part; j.tiles = static_cast<int>((rows + n.logits - 1) / n.logits * 2); j.first = k == 0; j.last = k + 1 == n.pieces;
@@ -1158,7 +1190,7 @@ template <typename T> hipError_t xent_fwd_t(const XentArgs& a, hipStream_t strea
 }
 
 template <typename T> hipError_t xent_bwd_t(const XentArgs& a, hipStream_t stream) {
-  constexpr bool kHalf = sizeof(T) == 4;
+  constexpr bool kFp32 = sizeof(T) == 4;
   const XentPlan n = xent_plan(a, true);
   unsigned char* ws = static_cast<unsigned char*>(a.workspace);
   hipError_t e = prep<T>(a, n, ws, true, stream);
@@ -1185,7 +1217,7 @@ template <typename T> hipError_t xent_bwd_t(const XentArgs& a, hipStream_t strea
     p.g = reinterpret_cast<float*>(ws + n.off_c);
     p.dl = dl; p.pdl = (n.tok_cap + kSkew) * rpad;
     p.tok_cap = n.tok_cap;
-    e = product_any<false, false, kHalf, kGradLogits>(n.logits, p, stream);
+    e = product_any<false, false, kFp32, kGradLogits>(n.logits, p, stream);
     if (e != hipSuccess) return e;
     if (a.dx != nullptr) {     // dx += G W: m = width, n = token, k = vocabulary
       ProductParams q{};
@@ -1199,20 +1231,20 @@ template <typename T> hipError_t xent_bwd_t(const XentArgs& a, hipStream_t strea
       q.slices_at = kSlicesX;
       q.first = k == 0; q.last = k + 1 == n.pieces;
       q.rows = reinterpret_cast<int*>(ws + n.off_rows);
-      q.out = a.dx; q.dim = a.dim; q.out_f32 = kHalf;
+      q.out = a.dx; q.dim = a.dim; q.out_f32 = kFp32;
       q.sums = reinterpret_cast<float*>(ws + n.off_sums);
       if (n.pieces > 1) {
         q.over = reinterpret_cast<float*>(ws + n.off_over);
         q.ld_over = n.dpad;
       }
-      e = product_any<true, false, kHalf, kGradX>(n.gx, q, stream);
+      e = product_any<true, false, kFp32, kGradX>(n.gx, q, stream);
       if (e != hipSuccess) return e;
     }
     if (a.dweight != nullptr) {   // dW of the piece = G^T x: m = width, n = vocabulary row, k = token
       ProductParams q{};
       const size_t gs = a.grad_io ? sizeof(T) : 4;
       q.plan = p.plan;
-      q.A = panels(ws + n.off_xc, n.tok_cap, n.dpad, true);
+      q.A = panels(ws + (n.fine != 0 ? n.off_xf : n.off_xc), n.tok_cap, n.dpad, true);
       q.B = panels(dl, n.tok_cap, rpad, true);
       q.M = static_cast<int>(a.dim); q.N = static_cast<int>(rows);
       q.k_is_tokens = 1;
@@ -1222,7 +1254,7 @@ template <typename T> hipError_t xent_bwd_t(const XentArgs& a, hipStream_t strea
       q.scale_a = kScaleX; q.scale_b = kScaleG;
       q.slices_at = k + 1 == n.pieces ? kSlicesLastW : kSlicesW;
       q.sums = reinterpret_cast<float*>(ws + n.off_sums);
-      e = product_any<true, true, kHalf, kGradW>(n.gw, q, stream);
+      e = product_any<true, true, kFp32, kGradW>(n.gw, q, stream);
     }
   }
   return e;

@@ -57,3 +57,52 @@ def test_one_matrix_near_the_largest_numbers(M, ex, ew, eg):
         want, out = ref[k][0], got[k].cpu().double()
         assert float(want.abs().max()) < 2.0 ** 127, "the case itself overflows"
         assert float((out - want).norm()) <= 2e-6 * float(want.norm()) + 2.0 ** -126 * want.numel() ** 0.5, k
+
+
+def test_gradients_of_unlikely_words(M):
+    """Logits from 0 down to -70: a word's row of dweight is made of p dloss, from p = 1e-2 down to 1e-32, and an
+    optimiser that divides by a row's own size sees the smallest as well as the largest.  Every element within the
+    relative bound of its own products; tokens of tiny dloss likewise."""
+    g = torch.Generator().manual_seed(5)
+    T, V, D = 70, 300, 20
+    w, x = 0.05 * torch.randn(V, D, generator=g), torch.randn(T, D, generator=g)
+    w[:, 0] = -torch.linspace(0, 70 / 8, V)
+    x[:, 0] = 8.0
+    y = torch.randint(0, 5, (T,), generator=g)
+    dl = 0.5 + torch.rand(T, generator=g)
+    dl[10:20] *= 2.0 ** -50
+    for dz in (None, 0.1 * torch.randn(T, generator=g) * dl):
+        say("unlikely words", dz is not None)
+        got, ref = gradients(M, x, w, y, dl, dz)
+        assert float(ref["dweight"][0].abs().min(1).values.max()) > 0 and float(ref["dweight"][0][-1].abs().max()) < 1e-28
+        R.check(got["dweight"], ref["dweight"], "dweight")
+        R.check(got["dx"], ref["dx"], "dx")
+
+
+def test_gradients_of_columns_far_below_the_others(M):
+    """Columns of x and of the weight 2^-45 below the rest: their gradients are right to their own size."""
+    g = torch.Generator().manual_seed(6)
+    T, V, D = 150, 260, 70
+    x, w = torch.randn(T, D, generator=g), torch.randn(V, D, generator=g) * D ** -0.5
+    x[:, 3:6] *= 2.0 ** -45
+    w[:, 40:44] *= 2.0 ** -45
+    y = torch.randint(0, V, (T,), generator=g)
+    got, ref = gradients(M, x, w, y, 0.5 + torch.rand(T, generator=g))
+    R.check(got["dweight"], ref["dweight"], "dweight")
+    R.check(got["dx"], ref["dx"], "dx")
+
+
+def test_gradients_of_the_largest_numbers(M):
+    """Values of the largest binade, some of which round up to infinity in 8 bits, stay what they are."""
+    g = torch.Generator().manual_seed(7)
+    T, V, D = 20, 64, 64
+    top = float(torch.finfo(F32).max)
+    x, w = torch.zeros(T, D), torch.zeros(V, D)
+    x[:, 0] = torch.where(torch.arange(T) % 2 == 0, top, top * (1 - 2.0 ** -9))
+    x[:, 1] = 2.0 ** 110
+    w[:, 1] = torch.randn(V, generator=g) * 2.0 ** -110
+    y = torch.randint(0, V, (T,), generator=g)
+    dl = 2.0 ** -10 * (0.5 + torch.rand(T, generator=g))
+    got, ref = gradients(M, x, w, y, dl)
+    R.check(got["dweight"], ref["dweight"], "dweight")
+    R.check(got["dx"], ref["dx"], "dx")
