@@ -1,5 +1,6 @@
 """Cross entropy at sizes where every product takes more than one round of tiles over the chip: workgroups that go from
-tile to tile, whole tiles ahead of a last round that is cut along k, several bands of token tiles.  Against the plain 64-bit forms in model_ops, element by element, in 64 bits on the
+tile to tile, whole tiles ahead of a last round that is cut along k, several bands of token tiles, and a vocabulary that
+the forward pass takes in pieces.  Against the plain 64-bit forms in model_ops, element by element, in 64 bits on the
 GPU."""
 import pytest
 import torch
@@ -84,3 +85,32 @@ def test_more_than_one_round(M, sizes, io):
     ref = reference(x, w, y, dloss=dl, dlse=dz, lse_in=lse, old=old, grad_dtype=F32)
     got = M.linear_cross_entropy_bwd(x, w, y, lse, dl, dlse=dz, want_dx=False, dweight=old, accumulate=True)
     R.check(got["dweight"], ref["dweight"], "accumulated dweight")
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_forward_in_pieces(M, io):
+    """A million tokens, nearly all left out, and a vocabulary of several pieces in the forward pass: the maximum and sum
+    carried between pieces, targets in each of them."""
+    T, V, D = 1 << 20, 15000, 8
+    need = M.linear_cross_entropy_fwd_workspace_size(T, V, D, M.MSSM_BF16 if io == BF16 else M.MSSM_F32)
+    assert need < V // 64 * T * 8, "the partial sums of the whole vocabulary would fit: it is one piece"
+    g = torch.Generator().manual_seed(18)
+    keep = torch.randperm(T, generator=g)[:300].sort().values
+    y = torch.full((T,), -100)
+    y[keep] = torch.randint(0, V, (300,), generator=g)
+    y[keep[:6]] = torch.tensor([0, V - 1, V // 2, 5119, 5120, 10240])
+    x = torch.randn(T, D, generator=g).to(io)
+    w = torch.randn(V, D, generator=g)
+    w[7000:7010] *= 4.0      # the largest logits of most tokens lie in the middle piece
+    w = w.to(io)
+    dl = torch.rand(T, generator=g)
+    say("forward in pieces", io)
+    loss, lse = M.linear_cross_entropy_fwd(x.cuda(), w.cuda(), y.cuda())
+    want = R.cross_entropy(x[keep], w, y[keep], dloss=dl[keep], lse_in=lse.cpu()[keep])
+    R.check(loss[keep.cuda()], want["loss"], "loss")
+    R.check(lse[keep.cuda()], want["lse"], "lse")
+    assert int((loss != 0).sum()) <= 300
+    grads = M.linear_cross_entropy_bwd(x.cuda(), w.cuda(), y.cuda(), lse, dl.cuda())
+    R.check(grads["dx"][keep.cuda()], want["dx"], "dx")
+    R.check(grads["dweight"], want["dweight"], "dweight")
+    assert int((grads["dx"] != 0).any(1).sum()) <= 300
