@@ -601,18 +601,27 @@ __global__ __launch_bounds__(256) void sum_kernel(ProductParams p, int slots) {
 
 // How many slices the tiles of the last round are cut into: the least time, in steps of a workgroup.  A slice
 // costs some four steps more (its start, its sums' way out) and the addition some eight.  At most two rounds
-// of slices, which bounds the sums' memory.
-__device__ int pick_slices(int tiles, int steps, int slots) {
+// of slices, which bounds the sums' memory.  Of a workgroup of 256, every thread with some of the up to 1024 counts:
+// one thread after another's three divisions took 150 us for 64 x 128 x 131072.
+__device__ int pick_slices(int tiles, int steps, int slots, uint64_t (&red)[4]) {
   const int rest = tiles % slots;
-  int best = 1, least = steps;
-  for (int s = 2; rest > 0 && rest * s <= 2 * slots && steps / s >= 4; ++s) {
-    const int time = (rest * s + slots - 1) / slots * ((steps + s - 1) / s + 4) + 8;
-    if (time < least) {
-      least = time;
-      best = s;
-    }
+  uint64_t best = ~0ull;   // time and, for equal times, the fewer slices
+  for (int s = 1 + threadIdx.x; s == 1 || (rest > 0 && rest * s <= 2 * slots && steps / s >= 4); s += 256) {
+    const int time = s == 1 ? steps : (rest * s + slots - 1) / slots * ((steps + s - 1) / s + 4) + 8;
+    const uint64_t mine = static_cast<uint64_t>(time) << 32 | static_cast<uint32_t>(s);
+    best = mine < best ? mine : best;
   }
-  return best;
+#pragma unroll
+  for (int step = 1; step < kLanes; step *= 2) {
+    const uint64_t o = __shfl_xor(best, step, kLanes);
+    best = o < best ? o : best;
+  }
+  __syncthreads();
+  if (threadIdx.x % kLanes == 0) red[threadIdx.x / kLanes] = best;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w) best = red[w] < best ? red[w] : best;
+  return static_cast<int>(best & 0xffffffffu);
 }
 
 // -------------------------------------------------------------------------------------- around the products
@@ -843,14 +852,22 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
     }
   };
   if (pad) {
-    if (blockIdx.x == static_cast<unsigned>(p.work_blocks) && threadIdx.x < 4) {
-      const int steps_w = (before + kBK - 1) / kBK * p.pairs;
-      const int tiles_x = p.tiles_mx * ((before + p.tile_x - 1) / p.tile_x);
-      p.plan[threadIdx.x] = threadIdx.x == 0   ? before
-                            : p.c_lse == nullptr ? 1
-                            : threadIdx.x == 1 ? pick_slices(tiles_x, p.steps_x, slots_of(p.tile_x))
-                            : threadIdx.x == 2 ? pick_slices(p.tiles_w, steps_w, slots_of(p.tile_w))
-                                               : pick_slices(p.tiles_w_last, steps_w, slots_of(p.tile_w));
+    if (blockIdx.x == static_cast<unsigned>(p.work_blocks)) {
+      __shared__ uint64_t least[4];
+      int slices[3] = {1, 1, 1};
+      if (p.c_lse != nullptr) {
+        const int steps_w = (before + kBK - 1) / kBK * p.pairs;
+        const int tiles_x = p.tiles_mx * ((before + p.tile_x - 1) / p.tile_x);
+        slices[0] = pick_slices(tiles_x, p.steps_x, slots_of(p.tile_x), least);
+        slices[1] = pick_slices(p.tiles_w, steps_w, slots_of(p.tile_w), least);
+        slices[2] = p.tiles_w_last == p.tiles_w ? slices[1] : pick_slices(p.tiles_w_last, steps_w, slots_of(p.tile_w), least);
+      }
+      if (threadIdx.x == 0) {
+        p.plan[kCount] = before;
+        p.plan[kSlicesX] = slices[0];
+        p.plan[kSlicesW] = slices[1];
+        p.plan[kSlicesLastW] = slices[2];
+      }
     }
     const int64_t end = (before + kTokTile - 1) / kTokTile * int64_t{kTokTile};
     for (int64_t i = before + (blockIdx.x - p.work_blocks) * 4 + wave; i < end; i += kPadBlocks * 4) {
