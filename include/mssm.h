@@ -579,13 +579,16 @@ size_t mssm_norm_bwd_workspace_size(const mssm_norm_desc* desc);
  *             io_dtype or MSSM_F32, overwritten, or added to with accumulate != 0
  *             (in fp32, rounded once); one of dx and dweight may be NULL
  * Products are summed in fp32.  With MSSM_BF16 G is rounded to bf16 once,
- * whatever grad_dtype (for up to 256 tokens it keeps 16 bits).  With MSSM_F32
+ * whatever grad_dtype, which leaves the gradients a relative error of some
+ * 1.7e-3 in the mean square beside their own rounding; for up to 256 tokens, and with
+ * MSSM_CROSS_ENTROPY_FINE_G for any number, it keeps 16 bits (twice the work of
+ * the two products with G, half as much again for a training step).  With MSSM_F32
  * x, weight and G carry a power of two each that fits them (G's fits dloss).
  * In the logits x and weight are two fp16 terms each: a value keeps 23 bits or
  * more where it is within 2^-16 of its matrix's largest finite magnitude, and
  * is right to 2^-39 of that magnitude below; an infinity among them makes its
  * logits NaN.  In the gradients' products all three are three bf16 terms each,
- * all 24 bits of what is within 2^-124 of the largest magnitude (G: of the
+ * all 24 bits of what is within 2^-117 of the largest magnitude (G: of the
  * largest dloss), the products summed in fp32 under those powers of two.
  * A NaN among a token's logits, or one of +infinity,
  * makes its loss and lse NaN.  All sums are taken in a fixed order: the same
@@ -599,12 +602,13 @@ size_t mssm_norm_bwd_workspace_size(const mssm_norm_desc* desc);
  * 896 MiB (but 256 vocabulary rows at least) of G or partial sums and laid-out
  * weight, up to 128 MiB of sums over parts of k, and where
  * the vocabulary takes several pieces dx in fp32.  Other rules as mssm_selective_scan_fwd. */
+#define MSSM_CROSS_ENTROPY_FINE_G 2u
 typedef struct {
     int64_t tokens, vocab, dim;
     int64_t ignore_id;
     int32_t io_dtype;   /* mssm_dtype */
     int32_t id_bytes;   /* 4 or 8 */
-    uint32_t flags;     /* reserved, must be 0 */
+    uint32_t flags;     /* 0 or MSSM_CROSS_ENTROPY_FINE_G (the forward pass ignores it) */
 } mssm_cross_entropy_desc;
 
 int mssm_linear_cross_entropy_fwd(const mssm_cross_entropy_desc* desc, const void* x, const void* weight,

@@ -57,6 +57,7 @@ class CrossEntropyDesc(ctypes.Structure):
 
 MSSM_LAYER_NORM = 0
 MSSM_RMS_NORM = 1
+MSSM_CROSS_ENTROPY_FINE_G = 2
 
 
 # every exported symbol and its ctypes signature (checked against include/mssm.h by the tests)
@@ -1050,12 +1051,12 @@ def linear_cross_entropy_fwd_workspace_size(tokens, vocab, dim, io_dtype=MSSM_BF
     return lib.mssm_linear_cross_entropy_fwd_workspace_size(ctypes.byref(d))
 
 
-def linear_cross_entropy_bwd_workspace_size(tokens, vocab, dim, io_dtype=MSSM_BF16) -> int:
-    d = CrossEntropyDesc(tokens, vocab, dim, -100, io_dtype, 8, 0)
+def linear_cross_entropy_bwd_workspace_size(tokens, vocab, dim, io_dtype=MSSM_BF16, fine: bool = False) -> int:
+    d = CrossEntropyDesc(tokens, vocab, dim, -100, io_dtype, 8, MSSM_CROSS_ENTROPY_FINE_G if fine else 0)
     return lib.mssm_linear_cross_entropy_bwd_workspace_size(ctypes.byref(d))
 
 
-def _xent_args(x, weight, targets, ignore_id, cur):
+def _xent_args(x, weight, targets, ignore_id, cur, fine=False):
     if x.dim() < 1 or weight.dim() != 2 or x.shape[-1] != weight.shape[1]:
         raise ValueError("x must be [..., dim] and weight [vocab, dim]")
     vocab, dim = weight.shape
@@ -1063,7 +1064,7 @@ def _xent_args(x, weight, targets, ignore_id, cur):
     _check_place("x", x, cur)
     _check_gpu("weight", weight, x.dtype, (vocab, dim), cur)
     _check_gpu("targets", targets, targets.dtype, x.shape[:-1], cur)
-    return CrossEntropyDesc(targets.numel(), vocab, dim, ignore_id, io, nb, 0)
+    return CrossEntropyDesc(targets.numel(), vocab, dim, ignore_id, io, nb, MSSM_CROSS_ENTROPY_FINE_G if fine else 0)
 
 
 def linear_cross_entropy_fwd(x, weight, targets, ignore_id: int = -100, loss=None, lse=None, workspace=None,
@@ -1093,17 +1094,18 @@ def linear_cross_entropy_fwd(x, weight, targets, ignore_id: int = -100, loss=Non
 
 def linear_cross_entropy_bwd(x, weight, targets, lse, dloss, dlse=None, ignore_id: int = -100, want_dx: bool = True,
                              want_dweight: bool = True, dx=None, dweight=None, accumulate: bool = False,
-                             workspace=None, stream=None):
+                             workspace=None, stream=None, fine: bool = False):
     """Gradients of sum(loss * dloss) + sum(lse * dlse) with respect to x and weight
     (mssm_linear_cross_entropy_bwd).
 
     lse: as linear_cross_entropy_fwd returned it; dloss, dlse: float32 of targets' shape (dlse None: zero).
     dweight: [vocab, dim] in x's type or float32 (allocated in x's type when None), overwritten, or added to
-    when accumulate (a head tied to the embedding, several batches).  Returns a dict of dx and dweight (None
-    for one that is not wanted)."""
+    when accumulate (a head tied to the embedding, several batches).  fine: with bfloat16 the logits' gradient
+    keeps 16 bits before its products with weight and x, as it does anyway for up to 256 tokens, instead of
+    bfloat16's 8.  Returns a dict of dx and dweight (None for one that is not wanted)."""
     torch = _torch()
     cur = torch.cuda.current_device()
-    d = _xent_args(x, weight, targets, ignore_id, cur)
+    d = _xent_args(x, weight, targets, ignore_id, cur, fine)
     shape = tuple(targets.shape)
     _check_gpu("lse", lse, torch.float32, shape, cur)
     _check_gpu("dloss", dloss, torch.float32, shape, cur)

@@ -87,9 +87,10 @@ mssm::NormArgs norm_args(const mssm_norm_desc& d) {
 
 int validate_xent(const mssm_cross_entropy_desc* d) {
   if (d == nullptr) return MSSM_ERR_INVALID_ARG;
-  if (d->tokens < 0 || d->vocab <= 0 || d->dim <= 0 || d->flags != 0) return MSSM_ERR_INVALID_ARG;
+  if (d->tokens < 0 || d->vocab <= 0 || d->dim <= 0) return MSSM_ERR_INVALID_ARG;
+  if ((d->flags & ~MSSM_CROSS_ENTROPY_FINE_G) != 0) return MSSM_ERR_INVALID_ARG;
   int64_t t = 0;
-  // (the workspace holds up to two 16-bit terms of either operand, padded)
+  // (the workspace holds up to five 16-bit terms of either operand, padded)
   if (!mul_ok(d->tokens, d->dim, &t) || !mul_ok(t, 64, &t)) return MSSM_ERR_INVALID_ARG;
   if (!mul_ok(d->vocab, d->dim, &t) || !mul_ok(t, 64, &t)) return MSSM_ERR_INVALID_ARG;
   if (!io_ok(d->io_dtype) || (d->id_bytes != 4 && d->id_bytes != 8)) return MSSM_ERR_UNSUPPORTED;
@@ -106,6 +107,7 @@ mssm::XentArgs xent_args(const mssm_cross_entropy_desc& d, const void* x, const 
   mssm::XentArgs a{};
   a.tokens = d.tokens; a.vocab = d.vocab; a.dim = d.dim; a.ignore = d.ignore_id; a.io = d.io_dtype;
   a.id_bytes = d.id_bytes; a.x = x; a.weight = weight; a.targets = targets;
+  a.fine_g = (d.flags & MSSM_CROSS_ENTROPY_FINE_G) != 0;
   return a;
 }
 

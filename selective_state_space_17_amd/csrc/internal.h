@@ -216,6 +216,7 @@ struct XentArgs {
   int64_t tokens, vocab, dim;
   int64_t ignore;
   int io;                // 0 fp32, 1 bf16
+  int fine_g;            // bf16: the logits' gradient in two terms whatever the tokens
   int id_bytes;          // 4 or 8
   const void* x;
   const void* weight;

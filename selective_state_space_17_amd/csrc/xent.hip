@@ -18,7 +18,9 @@
 //
 // bf16 inputs enter the matrix cores as they are; products are summed in fp32.  G is rounded to bf16 (the
 // gradients' own type) once; for up to 256 tokens, where few roundings average out and the weight's bytes are what
-// the time goes into, it is kept in two bf16 terms.
+// the time goes into, or where the caller asks for it, it is kept in two bf16 terms.  (8192 x 768 x 50280, relative
+// errors of dx in the 2-norm: 2.34e-3 with one rounding of G, 1.66e-3 with two terms, which is dx's own rounding; loss
+// and gradients 2.12 and 3.33 ms.)
 // fp32 matrices carry a power of two each, s, that brings their largest finite magnitude to [2^14, 2^15).  x and the
 // weight enter the logits as two fp16 terms, v s = hi + lo: exact for three values in four, one unit in the last of 24
 // bits off (2^-23) for the rest.  A product is the three term products hi lo + lo hi + hi hi, summed in fp32; lo lo is
@@ -27,7 +29,7 @@
 // bits said, smaller ones are right to 2^-39 of the largest.  That serves the logits, whose absolute error is what
 // counts, and not the gradients: a word's row of dW is made of p dloss with p down to 1e-30, and its error relative to
 // its own size is what an optimiser sees.  There x, the weight and G enter as three bf16 terms, all 24 bits of what is
-// within 2^-124 of the largest, and a product is the six term products whose places add up to two at most (what is left
+// within 2^-117 of the largest, and a product is the six term products whose places add up to two at most (what is left
 // out is below 2^-23 of the product, 2^-26 in the mean square).  One product at the matrix cores' fp32 rate, a sixteenth
 // of fp16's, would take 2.7 times the time of six.
 #include <type_traits>
@@ -1013,7 +1015,7 @@ XentPlan xent_plan(const XentArgs& a, bool grad) {
   n.terms = a.io ? 1 : kTerms;
   n.pairs = a.io ? 1 : 3;
   n.fine = a.io || !grad ? 0 : kFineTerms;
-  n.g_terms = !a.io ? kFineTerms : a.tokens <= kFewTokens ? 2 : 1;
+  n.g_terms = !a.io ? kFineTerms : a.tokens <= kFewTokens || a.fine_g ? 2 : 1;
   n.g_pairs = a.io ? n.g_terms : kMostPairs;
   n.dpad = (a.dim + 63) / 64 * 64;
   n.tok_cap = (a.tokens + kTokTile - 1) / kTokTile * kTokTile;

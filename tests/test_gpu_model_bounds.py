@@ -82,3 +82,19 @@ def test_few_tokens_keep_sixteen_bits_of_g(M, tokens, vocab, dim):
     dl, dz = torch.rand(tokens, generator=g) + 0.5, 0.1 * torch.randn(tokens, generator=g)
     say("sixteen bits", tokens, vocab, dim)
     sixteen_bits(M, x, w, y, dl, dz, M.linear_cross_entropy_bwd)
+
+
+@pytest.mark.parametrize("tokens,vocab,dim", [(257, 300, 64), (300, 2049, 100), (2100, 5000, 512)])
+def test_more_tokens_keep_sixteen_bits_of_g_on_request(M, tokens, vocab, dim):
+    g = torch.Generator().manual_seed(tokens)
+    x, w = torch.randn(tokens, dim, generator=g).to(BF16), (1.5 * dim ** -0.5 * torch.randn(vocab, dim, generator=g)).to(BF16)
+    y = torch.randint(0, vocab, (tokens,), generator=g)
+    y[1::7] = -100
+    dl, dz = torch.rand(tokens, generator=g) + 0.5, 0.1 * torch.randn(tokens, generator=g)
+    say("sixteen bits on request", tokens, vocab, dim)
+    sixteen_bits(M, x, w, y, dl, dz, lambda *a, **kw: M.linear_cross_entropy_bwd(*a, fine=True, **kw))
+    need = M.linear_cross_entropy_bwd_workspace_size(tokens, vocab, dim, fine=True)
+    assert need > M.linear_cross_entropy_bwd_workspace_size(tokens, vocab, dim)
+    with pytest.raises(M.MssmError):
+        ws = torch.empty(need - 256, dtype=torch.uint8, device="cuda")
+        sixteen_bits(M, x, w, y, dl, dz, lambda *a, **kw: M.linear_cross_entropy_bwd(*a, fine=True, workspace=ws, **kw))
