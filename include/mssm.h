@@ -580,17 +580,17 @@ size_t mssm_norm_bwd_workspace_size(const mssm_norm_desc* desc);
  *             (in fp32, rounded once); one of dx and dweight may be NULL
  * Products are summed in fp32.  With MSSM_BF16 G is rounded to bf16 once,
  * whatever grad_dtype, which leaves the gradients a relative error of some
- * 1.7e-3 in the mean square beside their own rounding; for up to 256 tokens, and with
- * MSSM_CROSS_ENTROPY_FINE_G for any number, it keeps 16 bits (twice the work of
- * the two products with G, half as much again for a training step).  With MSSM_F32
- * x, weight and G carry a power of two each that fits them (G's fits dloss).
- * In the logits x and weight are two fp16 terms each: a value keeps 23 bits or
- * more where it is within 2^-16 of its matrix's largest finite magnitude, and
- * is right to 2^-39 of that magnitude below; an infinity among them makes its
- * logits NaN.  In the gradients' products all three are three bf16 terms each,
- * all 24 bits of what is within 2^-117 of the largest magnitude (G: of the
- * largest dloss), the products summed in fp32 under those powers of two.
- * A NaN among a token's logits, or one of +infinity,
+ * 1.7e-3 in the mean square beside their own rounding; for up to 256 tokens
+ * (those left out included), and with MSSM_CROSS_ENTROPY_FINE_G for any number,
+ * it keeps 16 bits (twice the work of the two products with G, half as much
+ * again for a training step).  With MSSM_F32 x, weight and G carry a power of
+ * two each that fits them (G's fits dloss).  In the logits x and weight are two
+ * fp16 terms each: a value keeps 23 bits or more where it is within 2^-16 of its
+ * matrix's largest finite magnitude, and is right to 2^-39 of that magnitude
+ * below; an infinity among them makes its logits NaN.  In the gradients'
+ * products all three are three bf16 terms each, all 24 bits of what is within
+ * 2^-117 of the largest magnitude (G: of the largest dloss), summed in fp32
+ * under those powers of two.  A NaN among a token's logits, or one of +infinity,
  * makes its loss and lse NaN.  All sums are taken in a fixed order: the same
  * result on every run.
  * tokens may be 0, up to 2^26 - 1; vocab up to 2^30; dim up to 2^20.  bf16
@@ -600,8 +600,8 @@ size_t mssm_norm_bwd_workspace_size(const mssm_norm_desc* desc);
  * size queries ask, 256-byte aligned; it holds the counted tokens' x (for
  * MSSM_F32 gradients twice, 4 and 6 bytes a value), a piece of at most about
  * 896 MiB (but 256 vocabulary rows at least) of G or partial sums and laid-out
- * weight, up to 128 MiB of sums over parts of k, and where
- * the vocabulary takes several pieces dx in fp32.  Other rules as mssm_selective_scan_fwd. */
+ * weight, up to 128 MiB of sums over parts of k, and where the vocabulary takes
+ * several pieces dx in fp32.  Other rules as mssm_selective_scan_fwd. */
 #define MSSM_CROSS_ENTROPY_FINE_G 2u
 typedef struct {
     int64_t tokens, vocab, dim;

@@ -99,7 +99,7 @@ __device__ __forceinline__ uint32_t sort_key(int64_t id, int64_t vocab) {
 // counts' prefix sums.  Workgroups of the same launch behind them zero dW meanwhile.  16384 ids, table of 50280 x
 // 768 in bf16: 16 us, 11 us without the zeroing, which alone takes 14 us; a radix sort by one workgroup, four bits
 // a pass in LDS, took 26 us beside the same zeroing.  The work grows with the square of the tokens; at the limit, to
-// which a word has bits for them, the whole gradient takes 35 us, one token above, sorted as below, 51 us.
+// which a word has bits for them, the whole gradient takes 35 us, one token above, sorted as below, 52 us.
 constexpr int kRankThreads = 1024, kTokenBits = 14, kRankMost = 1 << kTokenBits, kPivots = kLanes;
 
 struct RankParams {
@@ -178,7 +178,7 @@ template <int E> __global__ __launch_bounds__(kRankThreads, 8) void rank_kernel(
 // ---------------------------------------------------------------------------------- sort of any number by id
 // Least-significant-digit radix sort of (id, token) pairs, ids outside [0, vocab) sorted last as `vocab`.  Each of
 // its launches, few workgroups that wait for memory, zeroes a share of dW beside.  Up to nine bits a pass: 65536 ids of
-// a table of 50280 take two passes of three launches, 6 + 6 + 7 us each, of 82 us for the gradient (768 columns).
+// a table of 50280 take two passes of three launches, 6 + 6 + 7 us each, of 84 us for the gradient (768 columns).
 constexpr int kTile = 1024;                    // pairs per workgroup
 constexpr int kPerWave = kTile / kWaves;       // a wave's pairs are consecutive, so its order is the input's
 constexpr int kMaxDigits = 512;
@@ -470,7 +470,7 @@ __global__ __launch_bounds__(kThreads) void embed_grad_kernel(EmbedGradParams p)
 
 // Runs that cross slices: the workgroup of the slice where such a run begins adds its parts, each wave a
 // quarter of them in order, the quarters in order.  6 us for the same sizes (a launch, two rounds of probes for the
-// run's end, up to a hundred parts); halving the interval instead of 64 places at once took 7.5 us.
+// run's end, up to a hundred parts) and more with the longest run: 40 us where every id is the same.  Halving the interval instead of 64 places at once took 7.5 us.
 template <typename G, int V>
 __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedGradParams p) {
   __shared__ float red[kWaves][kLanes * V];

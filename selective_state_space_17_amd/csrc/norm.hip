@@ -16,8 +16,9 @@
 // Measured, where a large copy reaches 5.1 to 5.2 TB/s: RMS norm of 32768 x 2560, bf16 with an fp32 stream, forward
 // 183 us (1.01 GB, 5.5 TB/s), gradients 250 us (1.34 GB, 5.4 TB/s) and 5 us of sums.  Layer norm of 16384 x 768 in
 // bf16: 15, 19 and 4 us (50 and 75 MB: launches and the first loads' latency are a third of it); 5001 x 1023 in
-// fp32, whose rows start at any element: 16, 21 and 5 us.  Loading the gradients' next row ahead spilled registers
-// (287 us).
+// fp32, whose rows start at any element: 16, 21 and 5 us.  Loading the gradients' next row ahead took 287 us at 2560
+// columns: a kernel with a workgroup a row is compiled for 1024 threads, the most that a row takes, and its 128
+// registers spilled.
 #include <type_traits>
 
 #include "device_util.h"
@@ -253,7 +254,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormParams 
 }
 
 // Rows too wide for one workgroup's registers: the row is read again for each of its passes (from the L2,
-// where it still is).
+// where it still is), an element a lane: layer norm of 4096 x 20000 in bf16 224 us, gradients 307 us, 1.5 TB/s.
 constexpr int kWideThreads = 1024;
 template <typename T, typename R>
 __global__ __launch_bounds__(kWideThreads) void norm_fwd_wide_kernel(NormParams p) {
