@@ -602,8 +602,9 @@ __global__ __launch_bounds__(256) void sum_kernel(ProductParams p, int slots) {
 }
 
 // How many slices the tiles of the last round are cut into: the least time, in steps of a workgroup.  A slice
-// costs some four steps more (its start, its sums' way out) and the addition some eight.  At most two rounds
-// of slices, which bounds the sums' memory.  Of a workgroup of 256, every thread with some of the up to 1024 counts:
+// costs some four steps more (its start, its sums' way out) and the addition some eight (of a few slices; of hundreds,
+// which only a tile or two of very many steps come to, far more: 83 us of 165 at 64 x 128 x 131072).  At most two
+// rounds of slices, which bounds the sums' memory.  Of a workgroup of 256, every thread with some of the up to 1024 counts:
 // one thread after another's three divisions took 150 us for 64 x 128 x 131072.
 __device__ int pick_slices(int tiles, int steps, int slots, uint64_t (&red)[4]) {
   const int rest = tiles % slots;
