@@ -1,5 +1,5 @@
 """Cross entropy of fp32 inputs on the GPU where magnitudes lie far apart, element by element against the plain 64-bit
-forms in model_ops."""
+forms in model_ops; its gradients captured and replayed."""
 import pytest
 import torch
 
@@ -106,3 +106,41 @@ def test_gradients_of_the_largest_numbers(M):
     got, ref = gradients(M, x, w, y, dl)
     R.check(got["dweight"], ref["dweight"], "dweight")
     R.check(got["dx"], ref["dx"], "dx")
+
+
+@pytest.mark.parametrize("io,fine", [(F32, False), (torch.bfloat16, True)])
+def test_captured_and_replayed(M, io, fine):
+    """Loss and gradients with three terms of fp32, or 16 bits of G, captured: every replay equals the eager result, on
+    changed inputs too, with eager work between."""
+    g = torch.Generator().manual_seed(9)
+    T, V, D = 700, 900, 130
+    sets = []
+    for _ in range(2):
+        y = torch.randint(-40, V, (T,), generator=g)
+        sets.append([t.cuda() for t in (torch.randn(T, D, generator=g).to(io), (torch.randn(V, D, generator=g) * 0.1).to(io), y,
+                                        torch.rand(T, generator=g), 0.1 * torch.randn(T, generator=g))])
+    x, w, y, dl, dz = (t.clone() for t in sets[0])
+
+    def run():
+        loss, lse = M.linear_cross_entropy_fwd(x, w, y)
+        got = M.linear_cross_entropy_bwd(x, w, y, lse, dl, dlse=dz, fine=fine)
+        return [loss, lse, got["dx"], got["dweight"]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run()
+    for i in range(4):
+        for a, b in zip((x, w, y, dl, dz), sets[i % 2]):
+            a.copy_(b)
+        for t in held:
+            t.fill_(3)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for k, (a, b) in enumerate(zip(held, run())):
+            assert torch.equal(a, b), f"replay {i}, output {k}"
