@@ -17,7 +17,10 @@
  *  - what stands on either side of the scans in a language model (embedding,
  *    blocks with a norm in front and a residual stream, norm, tied head; "Mamba-2 y state-space
  *    models", 4.3), for training and serving: mssm_embedding_fwd and _bwd,
- *    mssm_norm_fwd and _bwd, mssm_linear_cross_entropy_fwd and _bwd.
+ *    mssm_norm_fwd and _bwd, mssm_linear_cross_entropy_fwd and _bwd;
+ *  - the blocks' projections in 8 bits: mssm_norm_fp8_fwd, mssm_fp8_linear_fwd
+ *    and _bwd, and matrices kept in 8 bits between the two (mssm_fp8_quantize,
+ *    mssm_fp8_transpose, mssm_fp8_dequantize).
  *
  *  1. mssm_selective_scan_fwd -- the Mamba-1 selective scan.  Defined by the
  *     linear state recurrence h_t = A h_{t-1} + B x_t with readout y_t = C h_t
@@ -620,6 +623,105 @@ int mssm_linear_cross_entropy_bwd(const mssm_cross_entropy_desc* desc, const voi
                                   void* dx, void* dweight, int32_t grad_dtype, int32_t accumulate, void* workspace,
                                   size_t workspace_bytes, void* stream);
 size_t mssm_linear_cross_entropy_bwd_workspace_size(const mssm_cross_entropy_desc* desc);
+
+/* Matrices in 8 bits: the input and output projections of the blocks
+ * ("Mamba-2 y state-space models", 4.3) and the activations that their
+ * gradients need.  A matrix X [rows, cols] is
+ *   codes  : [rows][128 * blocks] bytes, blocks = ceil(cols / 128): OCP e4m3
+ *            (finite values up to 448, one NaN), zeros past cols
+ *   scales : one byte b for each block of 128, e8m0: 2^(b - 127)
+ *            MSSM_FP8_ROWS:   of 128 columns of a row, [blocks][lines],
+ *                             lines = rows rounded up to a multiple of 4 (the
+ *                             bytes past rows: 127)
+ *            MSSM_FP8_SQUARE: of 128 x 128, [blocks][ceil(rows / 128)]
+ * and stands for codes * scales.  Rounding: the scale is the least power of two
+ * that brings the block's largest finite magnitude to 448 or less (2^-126 at
+ * the least; 1 where all finite values are 0), a code X / scale to nearest even:
+ * 2^-4 of the value at most, 2^-10 of the scale below 2^-6 of it.  NaN and
+ * infinities become NaN, and touch no other value.  A kernel that reads a
+ * matrix in 8 bits takes codes past cols to be zeros.
+ *   mssm_fp8_quantize   : X (io_dtype) to 8 bits, to the transposed matrix
+ *                         [cols, rows] in 8 bits, or to both in one read; one
+ *                         pair of outputs may be NULL.  MSSM_FP8_SQUARE: the
+ *                         same values either way; MSSM_FP8_ROWS: the transposed
+ *                         one has its blocks along X's columns.
+ *   mssm_fp8_transpose  : a matrix of MSSM_FP8_ROWS to the transposed one of
+ *                         MSSM_FP8_ROWS.  Scales are powers of two: a value keeps
+ *                         its code's bits but below 2^-6 of its new block's scale.
+ *   mssm_fp8_dequantize : values back (io_dtype, rounded once; exact in fp32, and
+ *                         in bf16 from 2^-126 on)
+ * (mssm_fp8_transpose takes no notice of io_dtype.)
+ * rows may be 0; rows and cols up to 2^22 (MSSM_ERR_UNSUPPORTED above).  codes
+ * are 16-byte, scales 4-byte, others element-aligned.  Other rules as
+ * mssm_selective_scan_fwd. */
+#define MSSM_FP8_ROWS 0
+#define MSSM_FP8_SQUARE 1
+typedef struct {
+    int64_t rows, cols;
+    int32_t io_dtype;   /* mssm_dtype */
+    int32_t kind;       /* MSSM_FP8_ROWS or MSSM_FP8_SQUARE */
+    uint32_t flags;     /* reserved, must be 0 */
+} mssm_fp8_desc;
+
+int mssm_fp8_quantize(const mssm_fp8_desc* desc, const void* x, void* codes, void* scales, void* codes_t,
+                      void* scales_t, void* stream);
+int mssm_fp8_transpose(const mssm_fp8_desc* desc, const void* codes, const void* scales, void* codes_t, void* scales_t,
+                       void* stream);
+int mssm_fp8_dequantize(const mssm_fp8_desc* desc, const void* codes, const void* scales, void* out, void* stream);
+
+/* mssm_norm_fwd with its output in 8 bits, rounded once from fp32: codes and
+ * scales of out [rows, dim], MSSM_FP8_ROWS.  (Gradients: mssm_norm_bwd, with
+ * dout the gradient of the values that codes and scales stand for.)  codes are
+ * 16-byte, scales 4-byte aligned; other rules as mssm_norm_fwd. */
+int mssm_norm_fp8_fwd(const mssm_norm_desc* desc, const void* x, const void* residual, const float* weight,
+                      const float* bias, void* codes, void* scales, void* residual_out, float* mean, float* rstd,
+                      void* stream);
+
+/* A linear layer in 8 bits and its gradients.  With Q(.) a matrix's rounding to
+ * 8 bits (MSSM_FP8_ROWS; above):
+ *     out[t,n]     = sum_k x[t,k] weight[n,k]
+ *     dx[t,k]      = sum_n Q(dout)[t,n] weight[n,k]
+ *     dweight[n,k] (+)= sum_t Q(dout^T)[n,t] Q(x^T)[k,t]
+ *   x        : [tokens, in_features], in 8 bits (x_dtype MSSM_E4M3: codes, and
+ *              x_scales; MSSM_FP8_ROWS), or, the forward pass only, in x_dtype
+ *              with x_scales NULL: Q(x) is then taken on the way
+ *   weight   : [out_features, in_features] in 8 bits, of weight_kind
+ *   weight_t : the transposed weight [in_features, out_features] in 8 bits, of
+ *              weight_kind; required for dx (mssm_fp8_quantize of
+ *              MSSM_FP8_SQUARE writes both from one read)
+ *   out, dout, dx : [tokens, ...] in io_dtype
+ *   dweight  : [out_features, in_features] in grad_dtype, io_dtype or MSSM_F32,
+ *              overwritten, or added to with accumulate != 0 (in fp32, rounded
+ *              once).  One of dx and dweight may be NULL.
+ * x as the forward pass took it in 8 bits is all that the gradients need of it.
+ * Sums are fp32, in a fixed order: the same result on every run.  Results in
+ * bf16 come from the 8-bit matrix instructions, which drop what lies some 14
+ * bits below the largest of 8 neighbouring products (2^-13 of it at most each:
+ * some 1e-5 of the result in the mean square); results in fp32 from products
+ * that are kept whole, at up to twice the time.  A NaN reaches the
+ * outputs that its row or column enters.
+ * tokens may be 0 (dweight is then zeroed, or left as it is with accumulate),
+ * up to 2^22; features up to 2^20 (MSSM_ERR_UNSUPPORTED above).  codes are
+ * 16-byte, scales 4-byte, others element-aligned.  workspace: at least the
+ * bytes that the size queries ask for the same desc (the gradients: for the
+ * outputs wanted), 256-byte aligned.  Other rules as mssm_selective_scan_fwd. */
+#define MSSM_E4M3 2
+typedef struct {
+    int64_t tokens, in_features, out_features;
+    int32_t x_dtype;      /* MSSM_E4M3, or for the forward pass an mssm_dtype */
+    int32_t io_dtype;     /* mssm_dtype */
+    int32_t weight_kind;  /* MSSM_FP8_ROWS or MSSM_FP8_SQUARE */
+    uint32_t flags;       /* reserved, must be 0 */
+} mssm_fp8_linear_desc;
+
+int mssm_fp8_linear_fwd(const mssm_fp8_linear_desc* desc, const void* x, const void* x_scales, const void* weight,
+                        const void* weight_scales, void* out, void* workspace, size_t workspace_bytes, void* stream);
+size_t mssm_fp8_linear_fwd_workspace_size(const mssm_fp8_linear_desc* desc);
+int mssm_fp8_linear_bwd(const mssm_fp8_linear_desc* desc, const void* x, const void* x_scales, const void* weight_t,
+                        const void* weight_t_scales, const void* dout, void* dx, void* dweight, int32_t grad_dtype,
+                        int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+size_t mssm_fp8_linear_bwd_workspace_size(const mssm_fp8_linear_desc* desc, int32_t want_dx, int32_t want_dweight,
+                                          int32_t grad_dtype);
 
 /* Static text for a status code (never NULL). */
 const char* mssm_status_string(int status);

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import Any, NamedTuple, Optional, Tuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmssm.so")
@@ -55,9 +55,23 @@ class CrossEntropyDesc(ctypes.Structure):
                 ("flags", ctypes.c_uint32)]
 
 
+class Fp8Desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
+                ("kind", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class Fp8LinearDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("in_features", ctypes.c_int64), ("out_features", ctypes.c_int64),
+                ("x_dtype", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("weight_kind", ctypes.c_int32),
+                ("flags", ctypes.c_uint32)]
+
+
 MSSM_LAYER_NORM = 0
 MSSM_RMS_NORM = 1
 MSSM_CROSS_ENTROPY_FINE_G = 2
+MSSM_FP8_ROWS = 0
+MSSM_FP8_SQUARE = 1
+MSSM_E4M3 = 2
 
 
 # every exported symbol and its ctypes signature (checked against include/mssm.h by the tests)
@@ -99,6 +113,15 @@ SIGNATURES = {
     "mssm_linear_cross_entropy_bwd": (_I, [ctypes.POINTER(CrossEntropyDesc)] + [_P] * 8 +
                                       [ctypes.c_int32, ctypes.c_int32, _P, _SZ, _P]),
     "mssm_linear_cross_entropy_bwd_workspace_size": (_SZ, [ctypes.POINTER(CrossEntropyDesc)]),
+    "mssm_fp8_quantize": (_I, [ctypes.POINTER(Fp8Desc)] + [_P] * 6),
+    "mssm_fp8_transpose": (_I, [ctypes.POINTER(Fp8Desc)] + [_P] * 5),
+    "mssm_fp8_dequantize": (_I, [ctypes.POINTER(Fp8Desc)] + [_P] * 4),
+    "mssm_norm_fp8_fwd": (_I, [ctypes.POINTER(NormDesc)] + [_P] * 10),
+    "mssm_fp8_linear_fwd": (_I, [ctypes.POINTER(Fp8LinearDesc)] + [_P] * 6 + [_SZ, _P]),
+    "mssm_fp8_linear_fwd_workspace_size": (_SZ, [ctypes.POINTER(Fp8LinearDesc)]),
+    "mssm_fp8_linear_bwd": (_I, [ctypes.POINTER(Fp8LinearDesc)] + [_P] * 7 +
+                            [ctypes.c_int32, ctypes.c_int32, _P, _SZ, _P]),
+    "mssm_fp8_linear_bwd_workspace_size": (_SZ, [ctypes.POINTER(Fp8LinearDesc)] + [ctypes.c_int32] * 3),
     "mssm_status_string": (ctypes.c_char_p, [_I]),
     "mssm_last_error_detail": (ctypes.c_char_p, []),
     "mssm_abi_version": (_I, []),
@@ -942,7 +965,7 @@ def rms_norm_fwd(x, weight, residual=None, eps: float = 1e-5, return_residual: b
 
 
 def _norm_fwd(kind, x, weight, bias, residual, eps, return_residual, residual_dtype, return_stats, out, residual_out,
-              stream):
+              stream, fp8=False):
     torch = _torch()
     if x.dim() < 1:
         raise ValueError("x must be [..., dim]")
@@ -961,7 +984,12 @@ def _norm_fwd(kind, x, weight, bias, residual, eps, return_residual, residual_dt
     res = _res_code(rdt, xt)
     if residual is not None:
         _check_gpu("residual", residual, rdt, shape, cur)
-    if out is None:
+    if fp8:
+        if out is None:
+            out = _fp8_empty(stream, rows, dim)
+        else:
+            _fp8_expect("out", out, rows, dim, False, cur)
+    elif out is None:
         out = _empty(stream, shape, xt, x)
     else:
         _check_gpu("out", out, xt, shape, cur)
@@ -977,10 +1005,15 @@ def _norm_fwd(kind, x, weight, bias, residual, eps, return_residual, residual_dt
         if kind == MSSM_LAYER_NORM:
             mean = _empty(stream, shape[:-1], torch.float32, rstd)
     d = NormDesc(rows, dim, eps, kind, io, res, 0)
-    st = lib.mssm_norm_fwd(ctypes.byref(d), x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias),
-                           out.data_ptr(), _ptr(residual_out), _ptr(mean), _ptr(rstd), _stream_on(stream, cur))
+    if fp8:
+        st = lib.mssm_norm_fp8_fwd(ctypes.byref(d), x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias),
+                                   out.codes.data_ptr(), out.scales.data_ptr(), _ptr(residual_out), _ptr(mean),
+                                   _ptr(rstd), _stream_on(stream, cur))
+    else:
+        st = lib.mssm_norm_fwd(ctypes.byref(d), x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias),
+                               out.data_ptr(), _ptr(residual_out), _ptr(mean), _ptr(rstd), _stream_on(stream, cur))
     if st != MSSM_OK:
-        raise MssmError(st, "mssm_norm_fwd")
+        raise MssmError(st, "mssm_norm_fp8_fwd" if fp8 else "mssm_norm_fwd")
     if return_stats:
         stats = (mean, rstd) if kind == MSSM_LAYER_NORM else (rstd,)
         return (out, residual_out, *stats) if return_residual else (out, *stats)
@@ -1134,4 +1167,257 @@ def linear_cross_entropy_bwd(x, weight, targets, lse, dloss, dlse=None, ignore_i
                                            ws_bytes, _stream_on(stream, cur))
     if st != MSSM_OK:
         raise MssmError(st, "mssm_linear_cross_entropy_bwd")
+    return {"dx": dx, "dweight": dweight}
+
+
+# --------------------------------------------------------------------------
+# The 8-bit linear layer
+# --------------------------------------------------------------------------
+class Fp8Matrix(NamedTuple):
+    """A matrix [rows, cols] in 8 bits (include/mssm.h).
+
+    codes: float8_e4m3fn [rows, 128 * blocks], blocks = ceil(cols / 128), zeros past cols; scales: float8_e8m0fnu,
+    a power of two for each block of 128 columns of a row, [blocks, rows rounded up to 4], or with square for
+    each 128 x 128, [blocks, ceil(rows / 128)].  The values are codes * scales."""
+    codes: Any
+    scales: Any
+    cols: int
+    square: bool = False
+
+
+def _fp8_shapes(rows, cols, square):
+    blocks = -(-cols // 128)
+    return (rows, 128 * blocks), (blocks, -(-rows // 128) if square else -(-rows // 4) * 4)
+
+
+def _fp8_empty(stream, rows, cols, square=False) -> Fp8Matrix:
+    torch = _torch()
+    codes, scales = _fp8_shapes(rows, cols, square)
+    return Fp8Matrix(_empty(stream, codes, torch.float8_e4m3fn), _empty(stream, scales, torch.float8_e8m0fnu), cols,
+                     square)
+
+
+def _fp8_expect(name, m, rows, cols, square, cur) -> None:
+    torch = _torch()
+    if not isinstance(m, Fp8Matrix):
+        raise TypeError(f"{name} must be an Fp8Matrix, got {type(m).__name__}")
+    if m.cols != cols:
+        raise ValueError(f"{name} must have {cols} columns, got {m.cols}")
+    if bool(m.square) != square:
+        raise ValueError(f"{name} must have a scale for each {'128 x 128' if square else '128 columns of a row'}")
+    codes, scales = _fp8_shapes(rows, cols, square)
+    _check_gpu(name + ".codes", m.codes, torch.float8_e4m3fn, codes, cur)
+    _check_gpu(name + ".scales", m.scales, torch.float8_e8m0fnu, scales, cur)
+
+
+def _fp8_check(name, m, cur) -> int:
+    """Rows of a matrix whose own sizes define the problem."""
+    if not isinstance(m, Fp8Matrix):
+        raise TypeError(f"{name} must be an Fp8Matrix, got {type(m).__name__}")
+    if m.codes.dim() != 2 or m.cols <= 0:
+        raise ValueError(f"{name} must have codes [rows, 128 * blocks] and at least one column")
+    rows = m.codes.shape[0]
+    _fp8_expect(name, m, rows, m.cols, bool(m.square), cur)
+    return rows
+
+
+def _fp8_kind(square) -> int:
+    return MSSM_FP8_SQUARE if square else MSSM_FP8_ROWS
+
+
+def fp8_quantize(x, square: bool = False, transposed: bool = False, both: bool = False, out=None, stream=None):
+    """x [rows, cols] (float32 or bfloat16) in 8 bits (mssm_fp8_quantize): an Fp8Matrix, with transposed that of
+    x's transpose [cols, rows], with both the two of them from one read.
+
+    square: a scale for each 128 x 128 (a weight, whose transpose then has the same values) instead of for
+    each 128 columns of a row.  out: what is returned, to be written over."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, cols]")
+    rows, cols = x.shape
+    io = _codes(x.dtype)
+    square = bool(square)
+    cur = _torch().cuda.current_device()
+    _check_place("x", x, cur)
+    m = t = None
+    if out is not None:
+        m, t = out if both else (None, out) if transposed else (out, None)
+    if both or not transposed:
+        if m is None:
+            m = _fp8_empty(stream, rows, cols, square)
+        else:
+            _fp8_expect("out", m, rows, cols, square, cur)
+    if both or transposed:
+        if rows == 0:
+            raise ValueError("the transpose of no rows has no columns")
+        if t is None:
+            t = _fp8_empty(stream, cols, rows, square)
+        else:
+            _fp8_expect("out", t, cols, rows, square, cur)
+    d = Fp8Desc(rows, cols, io, _fp8_kind(square), 0)
+    st = lib.mssm_fp8_quantize(ctypes.byref(d), x.data_ptr(), _ptr(m and m.codes), _ptr(m and m.scales),
+                               _ptr(t and t.codes), _ptr(t and t.scales), _stream_on(stream, cur))
+    if st != MSSM_OK:
+        raise MssmError(st, "mssm_fp8_quantize")
+    return (m, t) if both else t if transposed else m
+
+
+def fp8_transpose(m, out=None, stream=None) -> Fp8Matrix:
+    """The transpose of an Fp8Matrix with scales of rows, with scales of its own rows (mssm_fp8_transpose): the
+    values that m stands for, but below 2^-6 of their new block's scale, where they are rounded to 2^-9 of it."""
+    cur = _torch().cuda.current_device()
+    rows = _fp8_check("m", m, cur)
+    if m.square:
+        raise ValueError("m must have a scale for each 128 columns of a row")
+    if rows == 0:
+        raise ValueError("the transpose of no rows has no columns")
+    if out is None:
+        out = _fp8_empty(stream, m.cols, rows)
+    else:
+        _fp8_expect("out", out, m.cols, rows, False, cur)
+    d = Fp8Desc(rows, m.cols, MSSM_F32, MSSM_FP8_ROWS, 0)
+    st = lib.mssm_fp8_transpose(ctypes.byref(d), m.codes.data_ptr(), m.scales.data_ptr(), out.codes.data_ptr(),
+                                out.scales.data_ptr(), _stream_on(stream, cur))
+    if st != MSSM_OK:
+        raise MssmError(st, "mssm_fp8_transpose")
+    return out
+
+
+def fp8_dequantize(m, dtype=None, out=None, stream=None):
+    """The values [rows, cols] that an Fp8Matrix stands for, in dtype (float32 or bfloat16, the default)
+    (mssm_fp8_dequantize)."""
+    torch = _torch()
+    cur = torch.cuda.current_device()
+    rows = _fp8_check("m", m, cur)
+    dtype = dtype or (torch.bfloat16 if out is None else out.dtype)
+    io = _codes(dtype)
+    if out is None:
+        out = _empty(stream, (rows, m.cols), dtype)
+    else:
+        _check_gpu("out", out, dtype, (rows, m.cols), cur)
+    d = Fp8Desc(rows, m.cols, io, _fp8_kind(m.square), 0)
+    st = lib.mssm_fp8_dequantize(ctypes.byref(d), m.codes.data_ptr(), m.scales.data_ptr(), out.data_ptr(),
+                                 _stream_on(stream, cur))
+    if st != MSSM_OK:
+        raise MssmError(st, "mssm_fp8_dequantize")
+    return out
+
+
+def layer_norm_fp8_fwd(x, weight, bias=None, residual=None, eps: float = 1e-5, return_residual: bool = False,
+                       residual_dtype=None, return_stats: bool = False, out=None, residual_out=None, stream=None):
+    """layer_norm_fwd with its output in 8 bits, rounded once from float32 (mssm_norm_fp8_fwd): out is an Fp8Matrix
+    [rows, dim], rows the product of x's leading sizes."""
+    return _norm_fwd(MSSM_LAYER_NORM, x, weight, bias, residual, eps, return_residual, residual_dtype, return_stats,
+                     out, residual_out, stream, fp8=True)
+
+
+def rms_norm_fp8_fwd(x, weight, residual=None, eps: float = 1e-5, return_residual: bool = False, residual_dtype=None,
+                     return_stats: bool = False, out=None, residual_out=None, stream=None):
+    """rms_norm_fwd with its output in 8 bits, rounded once from float32 (mssm_norm_fp8_fwd): out is an Fp8Matrix
+    [rows, dim], rows the product of x's leading sizes."""
+    return _norm_fwd(MSSM_RMS_NORM, x, weight, None, residual, eps, return_residual, residual_dtype, return_stats,
+                     out, residual_out, stream, fp8=True)
+
+
+def fp8_linear_fwd_workspace_size(tokens, in_features, out_features, x_dtype=MSSM_E4M3, io_dtype=MSSM_BF16) -> int:
+    d = Fp8LinearDesc(tokens, in_features, out_features, x_dtype, io_dtype, MSSM_FP8_SQUARE, 0)
+    return lib.mssm_fp8_linear_fwd_workspace_size(ctypes.byref(d))
+
+
+def fp8_linear_bwd_workspace_size(tokens, in_features, out_features, io_dtype=MSSM_BF16, grad_dtype=None,
+                                  want_dx: bool = True, want_dweight: bool = True) -> int:
+    d = Fp8LinearDesc(tokens, in_features, out_features, MSSM_E4M3, io_dtype, MSSM_FP8_SQUARE, 0)
+    return lib.mssm_fp8_linear_bwd_workspace_size(ctypes.byref(d), int(want_dx), int(want_dweight),
+                                                  io_dtype if grad_dtype is None else grad_dtype)
+
+
+def fp8_linear_fwd(x, weight, out_dtype=None, out=None, workspace=None, stream=None):
+    """x @ weight.T in 8 bits (mssm_fp8_linear_fwd).
+
+    x: Fp8Matrix [tokens, in] with scales of rows, or a float32 or bfloat16 tensor [..., in], which is rounded
+    as fp8_quantize would; weight: Fp8Matrix [out, in], square or not.  out_dtype: bfloat16 (the default)
+    or float32, which also keeps more of the sums.  Returns [tokens, out], for a tensor x [..., out]."""
+    torch = _torch()
+    cur = torch.cuda.current_device()
+    n = _fp8_check("weight", weight, cur)
+    k = weight.cols
+    if isinstance(x, Fp8Matrix):
+        tokens = _fp8_check("x", x, cur)
+        _fp8_expect("x", x, tokens, k, False, cur)
+        xd, xp, xs, shape = MSSM_E4M3, x.codes.data_ptr(), x.scales.data_ptr(), (tokens, n)
+    else:
+        if x.dim() < 1 or x.shape[-1] != k:
+            raise ValueError(f"x must be [..., {k}]")
+        xd, tokens = _codes(x.dtype), x.numel() // k
+        _check_place("x", x, cur)
+        xp, xs, shape = x.data_ptr(), None, (*x.shape[:-1], n)
+    out_dtype = out_dtype or (torch.bfloat16 if out is None else out.dtype)
+    io = _codes(out_dtype)
+    if out is None:
+        out = _empty(stream, shape, out_dtype)
+    else:
+        _check_gpu("out", out, out_dtype, shape, cur)
+    d = Fp8LinearDesc(tokens, k, n, xd, io, _fp8_kind(weight.square), 0)
+    ws, ws_bytes, _keep = _workspace(lib.mssm_fp8_linear_fwd_workspace_size(ctypes.byref(d)), workspace, stream)
+    st = lib.mssm_fp8_linear_fwd(ctypes.byref(d), xp, xs, weight.codes.data_ptr(), weight.scales.data_ptr(),
+                                 out.data_ptr(), ws, ws_bytes, _stream_on(stream, cur))
+    if st != MSSM_OK:
+        raise MssmError(st, "mssm_fp8_linear_fwd")
+    return out
+
+
+def fp8_linear_bwd(x, weight_t, dout, want_dx: bool = True, want_dweight: bool = True, dx=None, dweight=None,
+                   dweight_dtype=None, accumulate: bool = False, workspace=None, stream=None):
+    """Gradients of fp8_linear_fwd (mssm_fp8_linear_bwd), from its input as it was kept in 8 bits.
+
+    x: Fp8Matrix [tokens, in] with scales of rows (None without dweight); weight_t: the transposed weight, Fp8Matrix
+    [in, out], square or not (None without dx); dout: [tokens, out] (or any leading sizes), float32 or bfloat16,
+    which is rounded to 8 bits along the sums that it enters.  dweight: [out, in] in dout's type or float32
+    (allocated in dweight_dtype, else dout's, when None), overwritten, or added to when accumulate.
+    Returns a dict of dx [tokens, in] in dout's type and dweight (None for one that is not wanted)."""
+    torch = _torch()
+    cur = torch.cuda.current_device()
+    if not want_dx and not want_dweight:
+        raise ValueError("nothing to compute: want_dx and want_dweight are both False")
+    if dout.dim() < 1 or dout.shape[-1] == 0:
+        raise ValueError("dout must be [..., out]")
+    io, n = _codes(dout.dtype), dout.shape[-1]
+    tokens = dout.numel() // n
+    _check_place("dout", dout, cur)
+    if want_dx and weight_t is None:
+        raise ValueError("weight_t is required for dx")
+    if want_dweight and x is None:
+        raise ValueError("x is required for dweight")
+    k = _fp8_check("weight_t", weight_t, cur) if weight_t is not None else x.cols
+    square = weight_t is not None and bool(weight_t.square)
+    if weight_t is not None:
+        _fp8_expect("weight_t", weight_t, k, n, square, cur)
+    if x is not None:
+        _fp8_check("x", x, cur)
+        _fp8_expect("x", x, tokens, k, False, cur)
+    if want_dx:
+        dx = _empty(stream, (*dout.shape[:-1], k), dout.dtype) if dx is None else dx
+        _check_gpu("dx", dx, dout.dtype, (*dout.shape[:-1], k), cur)
+    else:
+        dx = None
+    gd = io
+    if want_dweight:
+        if dweight is None:
+            if accumulate:
+                raise ValueError("accumulate adds to dweight, which must be given")
+            dweight = _empty(stream, (n, k), dweight_dtype or dout.dtype)
+        elif dweight_dtype is not None and dweight.dtype != dweight_dtype:
+            raise TypeError(f"dweight_dtype is {dweight_dtype}, but dweight is {dweight.dtype}")
+        gd = _grad_code("dweight", dweight, dout.dtype)
+        _check_gpu("dweight", dweight, dweight.dtype, (n, k), cur)
+    else:
+        dweight = None
+    d = Fp8LinearDesc(tokens, k, n, MSSM_E4M3, io, _fp8_kind(square), 0)
+    ws, ws_bytes, _keep = _workspace(
+        lib.mssm_fp8_linear_bwd_workspace_size(ctypes.byref(d), int(want_dx), int(want_dweight), gd), workspace, stream)
+    st = lib.mssm_fp8_linear_bwd(ctypes.byref(d), _ptr(x and x.codes), _ptr(x and x.scales),
+                                 _ptr(weight_t and weight_t.codes), _ptr(weight_t and weight_t.scales),
+                                 dout.data_ptr(), _ptr(dx), _ptr(dweight), gd, int(accumulate), ws, ws_bytes,
+                                 _stream_on(stream, cur))
+    if st != MSSM_OK:
+        raise MssmError(st, "mssm_fp8_linear_bwd")
     return {"dx": dx, "dweight": dweight}

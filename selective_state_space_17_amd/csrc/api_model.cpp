@@ -3,10 +3,12 @@
 #include "../../include/mssm.h"
 
 #include "checks.h"
+#include "fp8_util.h"
 #include "internal.h"
 
 using namespace mssm::checks;
-using mssm::set_err;
+using mssm::fp8_blocks;
+using mssm::fp8_lines;
 
 namespace {
 
@@ -14,36 +16,6 @@ constexpr int64_t kMaxTokens = (int64_t{1} << 26) - 1;
 constexpr int64_t kMaxWaves = (int64_t{1} << 26) - 4;    // a wave a row, four to a workgroup: a 32-bit work-item count
 constexpr int64_t kMaxVocab = int64_t{1} << 30;
 constexpr int64_t kMaxDim = int64_t{1} << 20;
-
-bool io_ok(int32_t t) { return t == MSSM_F32 || t == MSSM_BF16; }
-int64_t size_of(int32_t t) { return t == MSSM_BF16 ? 2 : 4; }
-
-int done(hipError_t e) {
-  if (e == hipSuccess) return MSSM_OK;
-  set_err(e);
-  return MSSM_ERR_HIP;
-}
-
-struct Buf {
-  const void* p;
-  int64_t bytes;
-};
-// no output may overlap an input or another output
-template <int NI, int NO> bool disjoint(const Buf (&in)[NI], const Buf (&out)[NO]) {
-  for (int o = 0; o < NO; ++o) {
-    for (int i = 0; i < NI; ++i)
-      if (overlap(out[o].p, out[o].bytes, in[i].p, in[i].bytes)) return false;
-    for (int k = 0; k < o; ++k)
-      if (overlap(out[o].p, out[o].bytes, out[k].p, out[k].bytes)) return false;
-  }
-  return true;
-}
-
-int workspace_status(const void* ws, size_t have, size_t need) {
-  if (need == 0) return MSSM_OK;
-  if (ws == nullptr || have < need) return MSSM_ERR_WORKSPACE;
-  return aligned(ws, 256) ? MSSM_OK : MSSM_ERR_MISALIGNED;
-}
 
 int validate_embedding(const mssm_embedding_desc* d) {
   if (d == nullptr) return MSSM_ERR_INVALID_ARG;
@@ -157,26 +129,42 @@ int mssm_embedding_bwd(const mssm_embedding_desc* desc, const void* ids, const v
   return done(mssm::embed_bwd_launch(a, static_cast<hipStream_t>(stream)));
 }
 
-int mssm_norm_fwd(const mssm_norm_desc* desc, const void* x, const void* residual, const float* weight,
-                  const float* bias, void* out, void* residual_out, float* mean, float* rstd, void* stream) {
+// the forward pass with either output: out, or codes and scales
+static int norm_fwd(const mssm_norm_desc* desc, const void* x, const void* residual, const float* weight,
+                    const float* bias, void* out, void* codes, void* scales, bool fp8, void* residual_out, float* mean,
+                    float* rstd, void* stream) {
   const int v = validate_norm(desc);
   if (v != MSSM_OK) return v;
   const mssm_norm_desc& d = *desc;
   if (d.kind == MSSM_RMS_NORM && (bias != nullptr || mean != nullptr)) return MSSM_ERR_INVALID_ARG;
   if (residual != nullptr && residual_out == nullptr) return MSSM_ERR_INVALID_ARG;
   if (d.rows == 0) return MSSM_OK;
-  if (x == nullptr || weight == nullptr || out == nullptr) return MSSM_ERR_INVALID_ARG;
+  if (x == nullptr || weight == nullptr || (fp8 ? codes == nullptr || scales == nullptr : out == nullptr))
+    return MSSM_ERR_INVALID_ARG;
   const int64_t es = size_of(d.io_dtype), rs = size_of(d.res_dtype), n = d.rows * d.dim;
   if (!aligned(x, es) || !aligned(out, es) || !aligned(residual, rs) || !aligned(residual_out, rs) ||
-      !aligned(weight, 4) || !aligned(bias, 4) || !aligned(mean, 4) || !aligned(rstd, 4))
+      !aligned(weight, 4) || !aligned(bias, 4) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(codes, 16) ||
+      !aligned(scales, 4))
     return MSSM_ERR_MISALIGNED;
   const Buf in[] = {{x, n * es}, {residual, n * rs}, {weight, d.dim * 4}, {bias, d.dim * 4}};
-  const Buf outs[] = {{out, n * es}, {residual_out, n * rs}, {mean, d.rows * 4}, {rstd, d.rows * 4}};
+  const Buf outs[] = {{out, n * es}, {residual_out, n * rs}, {mean, d.rows * 4}, {rstd, d.rows * 4},
+                      {codes, d.rows * fp8_blocks(d.dim) * mssm::kBlock}, {scales, fp8_blocks(d.dim) * fp8_lines(d.rows)}};
   if (!disjoint(in, outs)) return MSSM_ERR_INVALID_ARG;
   mssm::NormArgs a = norm_args(d);
   a.x = x; a.residual = residual; a.weight = weight; a.bias = bias; a.out = out; a.residual_out = residual_out;
-  a.mean = mean; a.rstd = rstd;
+  a.mean = mean; a.rstd = rstd; a.codes = codes; a.scales = scales;
   return done(mssm::norm_fwd_launch(a, static_cast<hipStream_t>(stream)));
+}
+
+int mssm_norm_fwd(const mssm_norm_desc* desc, const void* x, const void* residual, const float* weight,
+                  const float* bias, void* out, void* residual_out, float* mean, float* rstd, void* stream) {
+  return norm_fwd(desc, x, residual, weight, bias, out, nullptr, nullptr, false, residual_out, mean, rstd, stream);
+}
+
+int mssm_norm_fp8_fwd(const mssm_norm_desc* desc, const void* x, const void* residual, const float* weight,
+                      const float* bias, void* codes, void* scales, void* residual_out, float* mean, float* rstd,
+                      void* stream) {
+  return norm_fwd(desc, x, residual, weight, bias, nullptr, codes, scales, true, residual_out, mean, rstd, stream);
 }
 
 size_t mssm_norm_bwd_workspace_size(const mssm_norm_desc* desc) {

@@ -205,6 +205,8 @@ struct NormArgs {
   float* dweight;
   float* dbias;            // nullable
   void* workspace;
+  void* codes;             // forward: out in 8 bits instead of `out`, with scales
+  void* scales;
 };
 
 hipError_t norm_fwd_launch(const NormArgs& a, hipStream_t stream);
@@ -238,5 +240,43 @@ struct XentArgs {
 size_t xent_workspace_bytes(const XentArgs& a, bool grad);
 hipError_t xent_fwd_launch(const XentArgs& a, hipStream_t stream);
 hipError_t xent_bwd_launch(const XentArgs& a, hipStream_t stream);
+
+// ---------------------------------------------------------------------------
+// 8-bit linear layer
+// ---------------------------------------------------------------------------
+// a matrix in 8 bits (layout: fp8_util.h), or a plain one where scales is null
+struct Fp8View {
+  void* codes = nullptr;
+  void* scales = nullptr;
+};
+
+struct Fp8Args {
+  int64_t rows, cols;
+  int io;                // x or out: 0 fp32, 1 bf16
+  int square;            // blocks of 128 x 128 instead of 128 of a row
+  const void* x;         // quantize: [rows, cols]
+  void* out;             // dequantize: [rows, cols]
+  Fp8View m;             // quantize: output, nullable; else input
+  Fp8View t;             // the transposed matrix in 8 bits: output, nullable for quantize
+};
+
+hipError_t fp8_quantize_launch(const Fp8Args& a, hipStream_t stream);
+hipError_t fp8_transpose_launch(const Fp8Args& a, hipStream_t stream);
+hipError_t fp8_dequantize_launch(const Fp8Args& a, hipStream_t stream);
+
+// out[r, c] (+)= sum over k of R[r, k] C[c, k]
+struct Fp8ProductArgs {
+  int64_t rows, cols, k;
+  Fp8View r;             // row scales
+  Fp8View c;
+  int square;            // C's scales
+  void* out;             // [rows, cols]
+  int out_io;            // 0 fp32, 1 bf16
+  int accumulate;
+  void* workspace;
+};
+
+size_t fp8_product_workspace_bytes(const Fp8ProductArgs& a);
+hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream);
 
 }  // namespace mssm

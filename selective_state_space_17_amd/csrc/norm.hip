@@ -21,7 +21,7 @@
 // registers spilled.
 #include <type_traits>
 
-#include "device_util.h"
+#include "fp8_util.h"
 #include "internal.h"
 
 namespace mssm {
@@ -40,6 +40,8 @@ struct NormParams {
   void* residual_out;       // nullable
   float* mean;              // nullable
   float* rstd;              // forward: nullable
+  unsigned char* codes;     // out in 8 bits instead: see fp8_util.h
+  unsigned char* scales;
   // backward
   const void* h;
   const void* dout;
@@ -75,7 +77,23 @@ template <typename T, typename R> __device__ __forceinline__ float norm_at(const
   return p.residual_out != nullptr ? rounded<R>(v) : v;
 }
 
-template <typename T, typename R, int V, int C, bool WAVE>
+// 8 neighbouring values of a row's output to 8 bits, 16 lanes together: a thread owns 8 columns an access and a row
+// starts with a wave's first thread, so a block of 128 columns is one row of 16 lanes.  y is 0 past the row's end.
+__device__ __forceinline__ void put_fp8(const NormParams& p, int64_t row, int col, const float (&y)[8]) {
+  const int blocks = static_cast<int>(fp8_blocks(p.dim));
+  uint32_t scale;
+  const u32x2_t codes = fp8_block_codes(y, scale);
+  if (col >= blocks * kBlock) return;
+  *reinterpret_cast<u32x2_t*>(p.codes + row * blocks * kBlock + col) = codes;
+  if (threadIdx.x % 16 == 0) {
+    unsigned char* const to = p.scales + col / kBlock * fp8_lines(p.rows) + row;
+    *to = static_cast<unsigned char>(scale);
+    if (row == p.rows - 1)
+      for (int64_t i = 1; row + i < fp8_lines(p.rows); ++i) to[i] = kOne;
+  }
+}
+
+template <typename T, typename R, int V, int C, bool WAVE, bool FP8>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_fwd_kernel(NormParams p) {
   __shared__ float red[2][kMaxWaves];
   const int per = WAVE ? blockDim.x / kLanes : 1;            // rows at a time
@@ -138,8 +156,13 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_fwd_kernel(NormParams 
   for (int c = 0; c < C; ++c) {
     const int col = (c * tr + tid) * V;
     const int left = p.dim - col;
+    float y[V];
+    if (FP8) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) y[i] = 0.f;
+    }
     if (left > 0) {
-      float w[V], y[V];
+      float w[V];
       load_row<V>(p.weight + col, w, left);
 #pragma unroll
       for (int i = 0; i < V; ++i) y[i] = (h[c][i] - mu) * rs * w[i];
@@ -149,8 +172,14 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_fwd_kernel(NormParams 
 #pragma unroll
         for (int i = 0; i < V; ++i) y[i] += b[i];
       }
-      store_row<V>(static_cast<T*>(p.out) + base + col, y, left);
+      if constexpr (FP8) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[i] = i < left ? y[i] : 0.f;   // (a row of NaN: its padding stays 0)
+      } else {
+        store_row<V>(static_cast<T*>(p.out) + base + col, y, left);
+      }
     }
+    if constexpr (FP8) put_fp8(p, row, col, y);
   }
 }
 
@@ -256,7 +285,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormParams 
 // Rows too wide for one workgroup's registers: the row is read again for each of its passes (from the L2,
 // where it still is), an element a lane: layer norm of 4096 x 20000 in bf16 224 us, gradients 307 us, 1.5 TB/s.
 constexpr int kWideThreads = 1024;
-template <typename T, typename R>
+template <typename T, typename R, bool FP8>
 __global__ __launch_bounds__(kWideThreads) void norm_fwd_wide_kernel(NormParams p) {
   __shared__ float red[2][kMaxWaves];
   const int64_t base = static_cast<int64_t>(blockIdx.x) * p.dim;
@@ -278,6 +307,25 @@ __global__ __launch_bounds__(kWideThreads) void norm_fwd_wide_kernel(NormParams 
   if (threadIdx.x == 0) {
     if (p.mean != nullptr) p.mean[blockIdx.x] = mu;
     if (p.rstd != nullptr) p.rstd[blockIdx.x] = rs;
+  }
+  if constexpr (FP8) {
+    const int most = static_cast<int>(fp8_blocks(p.dim)) * kBlock;
+    for (int c0 = 0; c0 < most; c0 += kWideThreads * 8) {   // (every thread: blocks are found 16 lanes together)
+      const int col = c0 + threadIdx.x * 8;
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = col + i;
+        y[i] = 0.f;
+        if (c < p.dim) {
+          const float v = at(c);
+          if (p.residual_out != nullptr) static_cast<R*>(p.residual_out)[base + c] = narrow<R>(v);
+          y[i] = (v - mu) * rs * p.weight[c] + (p.bias != nullptr ? p.bias[c] : 0.f);
+        }
+      }
+      put_fp8(p, blockIdx.x, col, y);
+    }
+    return;
   }
   for (int c = threadIdx.x; c < p.dim; c += kWideThreads) {
     const float v = at(c);
@@ -400,21 +448,25 @@ NormParams params(const NormArgs& a) {
   p.residual_out = a.residual_out; p.mean = a.mean; p.rstd = a.rstd;
   p.h = a.h; p.dout = a.dout; p.dresidual = a.dresidual; p.dx = a.dx; p.dresidual_in = a.dresidual_in;
   p.part = static_cast<float*>(a.workspace);
+  p.codes = static_cast<unsigned char*>(a.codes); p.scales = static_cast<unsigned char*>(a.scales);
   return p;
 }
 
-template <typename T, typename R> hipError_t norm_fwd_t(const NormArgs& a, hipStream_t stream) {
+template <typename T, typename R, bool FP8> hipError_t norm_fwd_out(const NormArgs& a, hipStream_t stream) {
   const NormParams p = params(a);
   const NormPlan n = norm_plan(a.dim);
   if (n.wide) {
-    norm_fwd_wide_kernel<T, R><<<dim3(static_cast<unsigned>(a.rows)), kWideThreads, 0, stream>>>(p);
+    norm_fwd_wide_kernel<T, R, FP8><<<dim3(static_cast<unsigned>(a.rows)), kWideThreads, 0, stream>>>(p);
     return hipGetLastError();
   }
   const int64_t blocks = n.wave ? (a.rows + 3) / 4 : a.rows;
   return norm_dispatch(n, [&](auto C, auto W) {
-    norm_fwd_kernel<T, R, kVec, decltype(C)::value, decltype(W)::value>
+    norm_fwd_kernel<T, R, kVec, decltype(C)::value, decltype(W)::value, FP8>
         <<<dim3(static_cast<unsigned>(blocks)), n.threads, 0, stream>>>(p);
   });
+}
+template <typename T, typename R> hipError_t norm_fwd_t(const NormArgs& a, hipStream_t stream) {
+  return a.codes != nullptr ? norm_fwd_out<T, R, true>(a, stream) : norm_fwd_out<T, R, false>(a, stream);
 }
 
 template <typename T, typename R> hipError_t norm_bwd_t(const NormArgs& a, hipStream_t stream) {

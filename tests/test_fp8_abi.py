@@ -1,0 +1,159 @@
+"""Refusals of the 8-bit entry points: every argument check runs on the host before anything is enqueued (no GPU
+needed; the addresses are never read)."""
+import ctypes
+
+import pytest
+import torch
+
+import fp8_ops as Q
+import selective_state_space_17_amd as M
+
+BASE = 0x7F0000000000
+MB = 1 << 20
+AT = [BASE + i * 100 * MB for i in range(16)]
+INV, UNS, MIS, WS = M.MSSM_ERR_INVALID_ARG, M.MSSM_ERR_UNSUPPORTED, M.MSSM_ERR_MISALIGNED, M.MSSM_ERR_WORKSPACE
+MOST = 1 << 22
+
+
+def ref(d):
+    return None if d is None else ctypes.byref(d)
+
+
+def mat(**kw):
+    return M.Fp8Desc(**{**dict(rows=8, cols=200, io_dtype=M.MSSM_BF16, kind=M.MSSM_FP8_ROWS, flags=0), **kw})
+
+
+def lin(**kw):
+    return M.Fp8LinearDesc(**{**dict(tokens=8, in_features=200, out_features=70, x_dtype=M.MSSM_E4M3,
+                                     io_dtype=M.MSSM_BF16, weight_kind=M.MSSM_FP8_SQUARE, flags=0), **kw})
+
+
+def quantize(d, x=AT[0], codes=AT[1], scales=AT[2], codes_t=AT[3], scales_t=AT[4]):
+    return M.lib.mssm_fp8_quantize(ref(d), x, codes, scales, codes_t, scales_t, None)
+
+
+def transpose(d, codes=AT[1], scales=AT[2], codes_t=AT[3], scales_t=AT[4]):
+    return M.lib.mssm_fp8_transpose(ref(d), codes, scales, codes_t, scales_t, None)
+
+
+def dequantize(d, codes=AT[1], scales=AT[2], out=AT[3]):
+    return M.lib.mssm_fp8_dequantize(ref(d), codes, scales, out, None)
+
+
+def fwd(d, x=AT[0], xs=AT[1], w=AT[2], ws=AT[3], out=AT[4], work=AT[5], nb=90 * MB):
+    return M.lib.mssm_fp8_linear_fwd(ref(d), x, xs, w, ws, out, work, nb, None)
+
+
+def bwd(d, x=AT[0], xs=AT[1], wt=AT[2], wts=AT[3], dout=AT[4], dx=AT[5], dw=AT[6], gd=M.MSSM_BF16, acc=0, work=AT[7],
+        nb=90 * MB):
+    return M.lib.mssm_fp8_linear_bwd(ref(d), x, xs, wt, wts, dout, dx, dw, gd, acc, work, nb, None)
+
+
+@pytest.mark.parametrize("call", [quantize, transpose, dequantize])
+def test_matrix_descriptors(call):
+    assert call(None) == INV
+    for kw, want in (({"rows": -1}, INV), ({"cols": 0}, INV), ({"cols": -3}, INV), ({"flags": 1}, INV), ({"kind": 2}, INV),
+                     ({"io_dtype": 7}, UNS), ({"rows": MOST + 1}, UNS), ({"cols": MOST + 1}, UNS),
+                     ({"rows": 1 << 62}, UNS)):
+        assert call(mat(**kw)) == want, kw
+
+
+@pytest.mark.parametrize("call", [fwd, bwd])
+def test_linear_descriptors(call):
+    assert call(None) == INV
+    for kw, want in (({"tokens": -1}, INV), ({"in_features": 0}, INV), ({"out_features": 0}, INV), ({"flags": 4}, INV),
+                     ({"weight_kind": 2}, INV), ({"x_dtype": 3}, UNS), ({"io_dtype": M.MSSM_E4M3}, UNS),
+                     ({"tokens": MOST + 1}, UNS), ({"in_features": MB + 1}, UNS), ({"out_features": MB + 1}, UNS)):
+        assert call(lin(**kw)) == want, kw
+
+
+def test_matrix_arguments():
+    d = mat()
+    for k in ("x", "codes", "scales", "codes_t", "scales_t"):
+        assert quantize(d, **{k: None}) == INV, k
+    assert quantize(d, codes=None, scales=None, codes_t=None, scales_t=None) == INV
+    assert quantize(d, x=AT[0] + 1) == MIS and quantize(d, codes=AT[1] + 8) == MIS and quantize(d, scales=AT[2] + 2) == MIS
+    assert quantize(d, codes_t=AT[3] + 4) == MIS and quantize(d, scales_t=AT[4] + 1) == MIS
+    assert quantize(d, codes=AT[0]) == INV and quantize(d, codes_t=AT[1]) == INV and quantize(d, scales_t=AT[2]) == INV
+    # 200 codes of a row of 256: the padding belongs to the matrix
+    assert quantize(d, scales=AT[1] + 8 * 256 - 4) == INV
+    assert transpose(mat(kind=M.MSSM_FP8_SQUARE)) == UNS
+    for k in ("codes", "scales", "codes_t", "scales_t"):
+        assert transpose(d, **{k: None}) == INV, k
+    assert transpose(d, codes=AT[1] + 1) == MIS and transpose(d, codes_t=AT[1]) == INV
+    for k in ("codes", "scales", "out"):
+        assert dequantize(d, **{k: None}) == INV, k
+    assert dequantize(d, out=AT[3] + 1) == MIS and dequantize(d, out=AT[1]) == INV and dequantize(d, out=AT[2]) == INV
+    for call in (quantize, transpose, dequantize):
+        assert call(mat(rows=0)) == M.MSSM_OK
+    assert quantize(mat(rows=0), None, None, None, None, None) == M.MSSM_OK
+
+
+def test_norm_arguments():
+    def norm(d, x=AT[0], r=AT[1], w=AT[2], b=AT[3], codes=AT[4], scales=AT[5], ro=AT[6], mean=AT[7], rstd=AT[8]):
+        return M.lib.mssm_norm_fp8_fwd(ref(d), x, r, w, b, codes, scales, ro, mean, rstd, None)
+
+    def desc(**kw):
+        return M.NormDesc(**{**dict(rows=8, dim=200, eps=1e-5, kind=M.MSSM_LAYER_NORM, io_dtype=M.MSSM_BF16,
+                                    res_dtype=M.MSSM_F32, flags=0), **kw})
+
+    assert norm(None) == INV and norm(desc(rows=-1)) == INV and norm(desc(eps=0.0)) == INV and norm(desc(io_dtype=2)) == UNS
+    d = desc()
+    for k in ("x", "w", "codes", "scales", "ro"):
+        assert norm(d, **{k: None}) == INV, k
+    assert norm(d, codes=AT[4] + 8) == MIS and norm(d, scales=AT[5] + 2) == MIS and norm(d, x=AT[0] + 1) == MIS
+    assert norm(d, codes=AT[0]) == INV and norm(d, scales=AT[4]) == INV and norm(d, scales=AT[4] + 8 * 256 - 4) == INV
+    assert norm(desc(kind=M.MSSM_RMS_NORM)) == INV
+    assert norm(desc(rows=0), x=None, codes=None, scales=None) == M.MSSM_OK
+
+
+def test_linear_arguments():
+    d = lin()
+    for k in ("x", "xs", "w", "ws", "out"):
+        assert fwd(d, **{k: None}) == INV, k
+    assert fwd(d, x=AT[0] + 8) == MIS and fwd(d, xs=AT[1] + 2) == MIS and fwd(d, w=AT[2] + 4) == MIS
+    assert fwd(d, out=AT[4] + 1) == MIS and fwd(d, out=AT[0]) == INV and fwd(d, out=AT[3]) == INV
+    plain = lin(x_dtype=M.MSSM_BF16)
+    assert fwd(plain) == INV, "a plain x has no scales"
+    need = M.fp8_linear_fwd_workspace_size(8, 200, 70, M.MSSM_BF16)
+    assert need > 0
+    for kw, want in ((dict(x=AT[0] + 1), MIS), (dict(nb=need - 1), WS), (dict(work=None), WS), (dict(work=AT[5] + 16), MIS),
+                     (dict(work=AT[2]), INV), (dict(work=AT[4]), INV)):
+        assert fwd(plain, xs=None, **kw) == want, kw
+    for t in (M.MSSM_E4M3, M.MSSM_F32):
+        assert fwd(lin(tokens=0, x_dtype=t), x=None, xs=None, out=None, work=None, nb=0) == M.MSSM_OK
+    for k in ("x", "xs", "wt", "wts", "dout"):
+        assert bwd(d, **{k: None}) == INV, k
+    assert bwd(d, dx=None, dw=None) == INV
+    assert bwd(plain) == UNS and bwd(d, gd=9) == UNS and bwd(lin(io_dtype=M.MSSM_F32), gd=M.MSSM_BF16) == UNS
+    assert bwd(d, x=AT[0] + 1) == MIS and bwd(d, wts=AT[3] + 2) == MIS and bwd(d, dx=AT[5] + 1) == MIS
+    assert bwd(d, dx=AT[4]) == INV and bwd(d, dw=AT[0]) == INV and bwd(d, dw=AT[5]) == INV and bwd(d, work=AT[6]) == INV
+    need = M.fp8_linear_bwd_workspace_size(8, 200, 70)
+    assert need > 0 and bwd(d, nb=need - 1) == WS and bwd(d, work=AT[7] + 64) == MIS
+    assert M.fp8_linear_bwd_workspace_size(8, 200, 70, want_dweight=False) < need
+    assert M.fp8_linear_bwd_workspace_size(8, 0, 70) == 0 and M.fp8_linear_fwd_workspace_size(-1, 5, 5) == 0
+    # each desc's own query: what is wanted decides
+    one = M.fp8_linear_bwd_workspace_size(8, 200, 70, want_dx=False)
+    assert bwd(d, dx=None, wt=None, wts=None, work=None, nb=0) == WS and one < need
+
+
+def test_workspaces_hold_what_the_sizes_say():
+    """In bytes per value: the input once, or the output's gradient twice and the input once, and sums bounded."""
+    t, k, n = 32768, 2560, 10240
+    assert M.fp8_linear_fwd_workspace_size(t, k, n, M.MSSM_BF16) < 1.02 * t * k + (256 << 20)
+    assert M.fp8_linear_bwd_workspace_size(t, k, n) < 1.02 * (2 * t * n + t * k) + (256 << 20)
+    assert M.fp8_linear_fwd_workspace_size(MOST, MB, MB, M.MSSM_F32) > 0
+
+
+def test_plain_rounding():
+    """The plain form's rounding against torch's own conversion, at every code, midpoint and power of two."""
+    v = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    mid = (v[1:] + v[:-1]) / 2
+    x = torch.cat([v, mid, torch.nextafter(mid, mid + 1), torch.nextafter(mid, mid - 1), torch.rand(4096) * 448])
+    x = torch.cat([x, -x])
+    assert torch.equal(Q.e4m3(x.double()), x.to(torch.float8_e4m3fn).double())
+    top = torch.tensor([0.0, 448.0, 448.0001, 2.0 ** -149, 3.4e38, 1.75, 1.76], dtype=torch.float32)
+    # 2^-126 at the least; 1.75 = 448 x 2^-8
+    assert Q.scale_byte(top.double()).tolist() == [127, 127, 128, 1, 247, 119, 120]
+    m = Q.quantize(torch.randn(130, 300), True)
+    assert m[0].shape == (130, 384) and m[1].shape == (3, 2) and Q.values(m).shape == (130, 300)
