@@ -9,6 +9,7 @@
 // rounding).  fp32 results are to be better than that: the codes are widened to bf16, which holds them and their
 // scales exactly, and the bf16 instructions' sums keep fp32's bits, at half the rate.
 #include <type_traits>
+#include <utility>
 
 #include "fp8_util.h"
 #include "internal.h"
@@ -16,6 +17,7 @@
 namespace mssm {
 namespace {
 
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
@@ -28,15 +30,11 @@ struct Fp8Params {
   int square;
   void* out;
   int accumulate;
+  // tiles: see tile_product_kernel
+  int tiles_c, tiles_r, whole, slices;
+  float* sums;                   // [slice][BR][BC]
 };
 
-// a lane's 32 codes of a row's block; which k a lane holds does not matter as long as both sides agree, as the scales
-// are the same for all of the block
-__device__ __forceinline__ i32x8_t codes_at(const unsigned char* p) {
-  const u32x4_t a = *reinterpret_cast<const u32x4_t*>(p), b = *reinterpret_cast<const u32x4_t*>(p + 16);
-  return i32x8_t{static_cast<int>(a[0]), static_cast<int>(a[1]), static_cast<int>(a[2]), static_cast<int>(a[3]),
-                 static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]), static_cast<int>(b[3])};
-}
 // 8 codes (words 2 q and 2 q + 1) times s, as bf16: exact
 __device__ __forceinline__ bf16x8_t wide_codes(const i32x8_t& v, int q, float s) {
   bf16x8_t o;
@@ -49,68 +47,393 @@ __device__ __forceinline__ bf16x8_t wide_codes(const i32x8_t& v, int q, float s)
   return o;
 }
 
-// C's rows are the matrix instructions' rows, so that a lane's four accumulators are neighbours in the output.
-// Four waves, each 32 x 32 of a tile of 64 x 64, the operands straight from global memory.
-template <typename T> __global__ __launch_bounds__(256) void simple_product_kernel(Fp8Params p) {
-  const int lane = threadIdx.x % kLanes, wave = threadIdx.x / kLanes;
-  const int64_t tiles_c = (p.cols + 63) / 64;
-  const int64_t c0 = blockIdx.x % tiles_c * 64 + wave % 2 * 32, r0 = blockIdx.x / tiles_c * 64 + wave / 2 * 32;
-  int64_t rr[2], cc[2];
+// -------------------------------------------------------------------------------------------------- tiles
+constexpr int kRow = kBlock;             // bytes of a row of a step
+constexpr int kBand = 4;                 // tiles of R side by side in the order of tiles
+
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));   // low half of a flat LDS address
+}
+// lane l's 16 bytes at base + off go to LDS offset lds + 16 l (base and lds are wave-uniform).  Written as asm
+// so that the compiler does not wait for these loads before the LDS reads of the other buffer; they are
+// waited for by count.  No output register: nothing can be overwritten while a load is in flight.
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory", "m0");
+}
+__device__ __forceinline__ u32x4_t lds_at(uint32_t addr) {
+  return *(__attribute__((address_space(3))) const u32x4_t*)static_cast<uintptr_t>(addr);
+}
+// the scheduler keeps what stands before this before it
+__device__ __forceinline__ void fence_schedule() { __builtin_amdgcn_sched_barrier(0); }
+
+template <int... I, typename F> __device__ __forceinline__ void unrolled(std::integer_sequence<int, I...>, F&& f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F> __device__ __forceinline__ void unrolled(F&& f) {
+  unrolled(std::make_integer_sequence<int, N>{}, f);
+}
+
+// where tile `tile` of the order below lies
+struct Place {
+  int c0, r0;
+};
+template <int BC, int BR> __device__ __forceinline__ Place place_of(const Fp8Params& p, int tile) {
+  const int band = tile / (p.tiles_c * kBand);
+  const int left = p.tiles_r - band * kBand, wide = left < kBand ? left : kBand;
+  const int in_band = tile - band * p.tiles_c * kBand;
+  // (the same for all lanes, which the divisions hide from the compiler)
+  return {__builtin_amdgcn_readfirstlane(in_band / wide * BC),
+          __builtin_amdgcn_readfirstlane((band * kBand + in_band % wide) * BR)};
+}
+
+// 8 neighbouring elements of a row of the output, the first `left` of which exist, to where they belong
+template <typename T> __device__ __forceinline__ void put(T* to, float (&v)[8], int64_t left, int accumulate) {
+  if (accumulate) {
+    float o[8];
+    load_row<8>(to, o, left);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t r = r0 + i * 16 + lane % 16, c = c0 + i * 16 + lane % 16;
-    rr[i] = r < p.rows ? r : p.rows - 1;
-    cc[i] = c < p.cols ? c : p.cols - 1;
+    for (int e = 0; e < 8; ++e) v[e] += o[e];
   }
-  f32x4_t acc[2][2] = {};
-  for (int s = 0; s < p.steps; ++s) {
-    i32x8_t a[2], b[2];
-    int sa[2], sb[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      a[i] = codes_at(p.c + cc[i] * p.pitch + s * kBlock + lane / 16 * 32);
-      b[i] = codes_at(p.r + rr[i] * p.pitch + s * kBlock + lane / 16 * 32);
-      sa[i] = p.cs[s * p.c_lines + (p.square ? cc[i] / kBlock : cc[i])];
-      sb[i] = p.rs[s * p.r_lines + rr[i]];
-    }
-    if constexpr (std::is_same_v<T, float>) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide_codes(a[i], q, fp8_power(sa[i])),
-                                                                wide_codes(b[j], q, fp8_power(sb[j])), acc[i][j], 0, 0, 0);
+  store_row<8>(to, v, left);
+}
+
+// C's rows are the matrix instructions' rows: a lane's accumulators are neighbours in the output.
+//
+// One workgroup stays on a CU (two of the small tile) and takes tile after tile, each 128 k (a block) a step, from two
+// LDS buffers filled by loads that run two steps ahead and cross the borders of tiles.  A step is two halves of 64 k:
+// the second half's fragments are read while the first is multiplied; between the halves every wave has read all of
+// the step's buffer, so one barrier there frees it for the loads two steps ahead and publishes the next step's, whose
+// first half is read while the second is multiplied.
+//
+// A wave holds TC x TR tiles of 32 x 32.  Row i of tile t is row TC i + t of its share: a lane's scales for its tiles
+// are then TC neighbouring bytes of memory, one word, from which the instruction picks a byte; and what a lane holds of
+// an output row are runs of 4 TC neighbouring elements.
+template <int BC, int BR, int WC, int WR, typename T>
+__global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params p) {
+  constexpr bool kFine = std::is_same_v<T, float>;
+  constexpr int kW = WC * WR;
+  constexpr int TC = BC / WC / 32, TR = BR / WR / 32;      // 32 x 32 tiles of a wave
+  constexpr int LC = BC / 8 / kW, LR = BR / 8 / kW;        // 1 KB loads of a wave per step
+  constexpr int kRows = TC;                                // rows of multiplications in a half
+  constexpr int kLoads = (LC + LR + kRows - 1) / kRows;    // loads between two of them
+  constexpr int kReads = (TC + TR + kRows - 1) / kRows;    // fragments read there
+  static_assert(LC * 8 * kW == BC && LR * 8 * kW == BR, "loads split evenly over the waves");
+  static_assert(TC == 2 || TC == 4, "a lane's scales of C are a word or half of one");
+  static_assert(TR == 2 || TR == 4, "and those of R");
+  constexpr int kC = BC * kRow, kR = BR * kRow;            // bytes of a buffer
+  __shared__ __attribute__((aligned(128))) unsigned char cbuf[2][kC];
+  __shared__ __attribute__((aligned(128))) unsigned char rbuf[2][kR];
+
+  const int lane = threadIdx.x % kLanes;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
+  const int wc = w / WR, wr = w % WR;
+
+  // Jobs.  Whole tiles as long as every workgroup gets one; the tiles of the last, partial round are cut along k where
+  // that fills the chip, each slice with sums of its own that are added afterwards.  Workgroups b, b + 8, ... share an
+  // XCD and its L2: each XCD takes a contiguous range of an order that walks bands of 4 tiles of R, C outer.
+  const int tiles = p.tiles_c * p.tiles_r;
+  const int rest = tiles - p.whole, cut = rest * p.slices;
+  const int xcd = blockIdx.x % 8, stride = gridDim.x / 8;
+  const int whole8 = p.whole / 8, cut8 = (cut + 7) / 8;    // of an XCD
+  const int mine = cut - xcd * cut8 < cut8 ? cut - xcd * cut8 : cut8;
+  const int job_first = blockIdx.x / 8, job_end = whole8 + (mine > 0 ? mine : 0);
+  struct Job {
+    int c0, r0, sum, begin, steps;   // sum: which sums, or -1
+  };
+  auto job_at = [&](int i) {
+    Job j;
+    int tile;
+    if (i < whole8) {
+      tile = xcd * whole8 + i;
+      j.sum = -1;
+      j.begin = 0;
+      j.steps = p.steps;
     } else {
+      const int c = xcd * cut8 + i - whole8;
+      const int slice = c / rest;
+      tile = p.whole + c - slice * rest;
+      j.sum = p.slices > 1 ? c : -1;
+      // (steps < 2^16, slices <= 2 workgroups)
+      j.begin = __builtin_amdgcn_readfirstlane(p.steps * slice / p.slices);
+      j.steps = __builtin_amdgcn_readfirstlane(p.steps * (slice + 1) / p.slices) - j.begin;
+    }
+    const Place at = place_of<BC, BR>(p, tile);
+    j.c0 = at.c0;
+    j.r0 = at.r0;
+    return j;
+  };
+
+  // ---- loads.  A load is 8 rows x 128 bytes, a lane's part row lane / 8 and the 16-byte chunk lane % 8 as stored.  The
+  // chunk it holds is xor-ed with the row's low three bits, which keeps the reads below free of bank conflicts.  LDS row
+  // 32 t + i of a wave's share holds row TC i + t of it.  Rows past the matrix are its last row again.
+  const int lrow = lane / 8;
+  const uint32_t chunk = static_cast<uint32_t>(((lane % 8) ^ lrow) * 16);
+  int ljob = job_first, lleft = 0, lk = 0;   // job and step of the next loads
+  const unsigned char *lc = nullptr, *lr = nullptr;
+  uint32_t oc[LC], orr[LR];
+  int64_t lsc = 0, lsr = 0;                  // where the scales of the next loads stand, of step 0
+  const uint32_t pitch = static_cast<uint32_t>(p.pitch);
+  auto offsets = [&](int64_t rows, int of, auto& off) {   // rows: of the matrix, from the tile's first on
+    const int last = rows < 256 ? static_cast<int>(rows) - 1 : 255;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < static_cast<int>(sizeof(off) / sizeof(off[0])); ++i) {
+      const int at = (i * kW + w) * 8 + lrow;
+      const int r = at / (32 * of) * (32 * of) + at % 32 * of + at / 32 % of;
+      off[i] = static_cast<uint32_t>(r < last ? r : last) * pitch + chunk;   // (pitch <= 2^22)
+    }
+  };
+  auto start_load = [&]() {   // the next job with steps, if there is one; else the last loads are repeated
+    while (ljob < job_end) {
+      const Job j = job_at(ljob);
+      if (j.steps > 0) {
+        lleft = j.steps;
+        lk = j.begin;
+        offsets(p.cols - j.c0, TC, oc);
+        offsets(p.rows - j.r0, TR, orr);
+        lc = p.c + static_cast<int64_t>(j.c0) * p.pitch;
+        lr = p.r + static_cast<int64_t>(j.r0) * p.pitch;
+        const int64_t c = j.c0 + wc * (32 * TC) + lane % 32 * TC, r = j.r0 + wr * (32 * TR) + lane % 32 * TR;
+        if (p.square) {
+          const int64_t b = (j.c0 + wc * (32 * TC)) / kBlock;
+          lsc = b < p.c_lines ? b : p.c_lines - 1;
+        } else {
+          lsc = c < p.c_lines ? c : p.c_lines - TC;
+        }
+        lsr = r < p.r_lines ? r : p.r_lines - TR;
+        return;
+      }
+      ljob += stride;
+    }
+  };
+  const uint32_t c_lds = lds_addr(&cbuf[0][0]), r_lds = lds_addr(&rbuf[0][0]);
+  auto load_one = [&](int i, int buf) {
+    const int64_t k = static_cast<int64_t>(lk) * kRow;
+    if (i < LC) dma16(lc + k, oc[i < LC ? i : 0], c_lds + buf * kC + (i * kW + w) * 1024);
+    else dma16(lr + k, orr[i - LC < LR && i >= LC ? i - LC : 0], r_lds + buf * kR + ((i - LC) * kW + w) * 1024);
+  };
+  auto bytes_at = [&](const unsigned char* at, int of) {
+    return of == 4 ? *reinterpret_cast<const uint32_t*>(at) : static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(at));
+  };
+  struct Scales {
+    uint32_t c, r;
+  };
+  auto load_scales = [&]() {
+    Scales s;
+    const unsigned char* const at = p.cs + lk * p.c_lines + lsc;
+    s.c = p.square ? static_cast<uint32_t>(*at) * 0x01010101u : bytes_at(at, TC);
+    s.r = bytes_at(p.rs + lk * p.r_lines + lsr, TR);
+    return s;
+  };
+  auto loaded = [&]() {   // after a step's last load
+    if (lleft > 1) {
+      --lleft;
+      ++lk;
+    } else if (ljob < job_end) {
+      ljob += stride;
+      start_load();
+    }
+  };
+
+  // ---- fragments: a lane's 32 codes are chunks 4 h + 2 (lane / 32) and the next of its row
+  uint32_t fc_at[2][2], fr_at[2][2];   // by half and chunk
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[i], b[j], acc[i][j], 0, 0, 0, sa[i], 0, sb[j]);
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int i = lane % 32;
+      const uint32_t at = i * kRow + (((h * 4 + lane / 32 * 2 + q) ^ (i & 7)) << 4);
+      fc_at[h][q] = c_lds + at + wc * TC * 32 * kRow;
+      fr_at[h][q] = r_lds + at + wr * TR * 32 * kRow;
+    }
+  f32x16_t acc[TC][TR];
+  i32x8_t fc[2][TC], fr[2][TR];
+  auto frag = [&](const uint32_t (&at)[2], uint32_t more) {
+    const u32x4_t a = lds_at(at[0] + more), b = lds_at(at[1] + more);
+    return i32x8_t{static_cast<int>(a[0]), static_cast<int>(a[1]), static_cast<int>(a[2]), static_cast<int>(a[3]),
+                   static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]), static_cast<int>(b[3])};
+  };
+  auto read_one = [&](int q, int h, int buf) {
+    if (q < TR) fr[h][q < TR ? q : 0] = frag(fr_at[h], buf * kR + (q < TR ? q : 0) * 32 * kRow);
+    else fc[h][q - TR < TC && q >= TR ? q - TR : 0] = frag(fc_at[h], buf * kC + (q - TR) * 32 * kRow);
+  };
+  auto multiply_row = [&](auto i, int h, const Scales& s) {
+    constexpr int I = decltype(i)::value;
+    if constexpr (kFine) {
+      const float sc = fp8_power((s.c >> (8 * I)) & 255u);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const bf16x8_t a = wide_codes(fc[h][I], q, sc);
+#pragma unroll
+        for (int j = 0; j < TR; ++j)
+          acc[I][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, wide_codes(fr[h][j], q, fp8_power((s.r >> (8 * j)) & 255u)),
+                                                              acc[I][j], 0, 0, 0);
+      }
+    } else {
+      unrolled<TR>([&](auto j) {
+        constexpr int J = decltype(j)::value;
+        acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fc[h][I], fr[h][J], acc[I][J], 0, 0, I,
+                                                                    static_cast<int>(s.c), J, static_cast<int>(s.r));
+        // stays here: the compiler knows of no reason not to move a multiplication to where its result is used
+        asm volatile("" : "+v"(acc[I][J]));
+      });
+    }
+  };
+
+  start_load();
+  Scales now{}, next{}, coming{};   // of the step that is multiplied, the next one, and the one whose loads are on their way
+  if (lleft > 0) {   // (no steps at all where k is empty: the tiles are then stored as zeros)
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+      for (int q = 0; q < LC + LR; ++q) load_one(q, b);
+      (b == 0 ? now : coming) = load_scales();
+      loaded();
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
+  int buf = 0;
+#pragma unroll
+  for (int q = 0; q < TC + TR; ++q) read_one(q, 0, 0);
+  for (int job = job_first; job < job_end; job += stride) {
+    const Job cur = job_at(job);
+#pragma unroll
+    for (int i = 0; i < TC; ++i)
+#pragma unroll
+      for (int j = 0; j < TR; ++j) acc[i][j] = f32x16_t{};
+    for (int s = 0; s < cur.steps; ++s, buf ^= 1) {
+      fence_schedule();
+      unrolled<TC>([&](auto i) {
+        multiply_row(i, 0, now);
+        fence_schedule();
+#pragma unroll
+        for (int q = i * kReads; q < (i + 1) * kReads && q < TC + TR; ++q) read_one(q, 1, buf);
+        fence_schedule();
+      });
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      next = coming;
+      fence_schedule();
+      unrolled<TC>([&](auto i) {
+        multiply_row(i, 1, now);
+        fence_schedule();
+#pragma unroll
+        for (int q = i * kLoads; q < (i + 1) * kLoads && q < LC + LR; ++q) load_one(q, buf);
+        if (i == TC - 1) coming = load_scales();
+#pragma unroll
+        for (int q = i * kReads; q < (i + 1) * kReads && q < TC + TR; ++q) read_one(q, 0, buf ^ 1);
+        fence_schedule();
+      });
+      now = next;
+      loaded();
+    }
+
+    // accumulator e = 4 q + f of tile (i, j): C's row TC (8 q + 4 (lane / 32) + f) + i and R's row TR (lane % 32) + j of
+    // the wave's shares
+    const int wave_c = wc * TC * 32 + lane / 32 * 4 * TC, wave_r = wr * TR * 32 + lane % 32 * TR;
+    auto each = [&](auto&& to) {   // every run of 8 neighbouring elements: (row of the tile, column of it, values)
+#pragma unroll
+      for (int j = 0; j < TR; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int h = 0; h < TC / 2; ++h) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = acc[e % TC][j][4 * q + (8 * h + e) / TC];
+            to(wave_r + j, wave_c + 8 * TC * q + 8 * h, v);
+          }
+    };
+    if (cur.sum >= 0) {
+      float* const to = p.sums + static_cast<int64_t>(cur.sum) * BR * BC;
+      each([&](int r, int c, float (&v)[8]) { store_row<8>(to + r * BC + c, v); });
+    } else {
+      T* const to = static_cast<T*>(p.out) + cur.r0 * p.cols + cur.c0;
+      const int64_t rows = p.rows - cur.r0, cols = p.cols - cur.c0;
+      if (rows >= BR && cols >= BC && !p.accumulate)
+        each([&](int r, int c, float (&v)[8]) { store_row<8>(to + r * p.cols + c, v); });
+      else
+        each([&](int r, int c, float (&v)[8]) {
+          if (r < rows) put(to + r * p.cols + c, v, cols - c, p.accumulate);
+        });
     }
   }
+  // the last loads may still be on their way into this workgroup's LDS
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// Adds the slices of the tiles of the last round, in order: workgroup (tile, share of its rows).
+constexpr int kShares = 8;
+template <int BC, int BR, typename T> __global__ __launch_bounds__(256) void slices_kernel(Fp8Params p) {
+  const int t = blockIdx.x / kShares, rest = p.tiles_c * p.tiles_r - p.whole;
+  const Place at = place_of<BC, BR>(p, p.whole + t);
+  const int c = threadIdx.x % (BC / 8) * 8;
+  const int64_t left = p.cols - at.c0 - c;
+  if (left <= 0) return;
+  constexpr int kRowsOf = BR / kShares, kAtOnce = 256 / (BC / 8);
+  const int first = blockIdx.x % kShares * kRowsOf + threadIdx.x / (BC / 8);
+  for (int i = 0; i < kRowsOf; i += kAtOnce) {
+    const int64_t row = static_cast<int64_t>(at.r0) + first + i;
+    if (row >= p.rows) return;
+    float v[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < p.slices; ++s) {
+      float o[8];
+      load_row<8>(p.sums + ((static_cast<int64_t>(s) * rest + t) * BR + first + i) * BC + c, o);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t r = r0 + j * 16 + lane % 16, c = c0 + i * 16 + lane / 16 * 4;
-      if (r >= p.rows) continue;
-      T* const to = static_cast<T*>(p.out) + r * p.cols + c;
-      float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-      if (p.accumulate) {
-        float o[4];
-        load_row<4>(to, o, p.cols - c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += o[e];
-      }
-      store_row<4>(to, v, p.cols - c);
+      for (int e = 0; e < 8; ++e) v[e] += o[e];
     }
+    put(static_cast<T*>(p.out) + row * p.cols + at.c0 + c, v, left, p.accumulate);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------- plan
+struct Tiling {
+  int bc, br;              // tile
+  int grid;                // workgroups
+  int64_t tiles;
+  int whole, slices;
+  int64_t cost;
+};
+
+// Slices of the last, partial round: the least time, in steps of a workgroup.  A slice costs some four steps more (its
+// start, its sums' way out) and the addition some eight.  At most two rounds of slices, which bounds the sums' memory.
+Tiling tiling(const Fp8ProductArgs& a, int bc, int br, int grid, int64_t weight) {
+  Tiling t{bc, br, grid, 0, 0, 1, 0};
+  t.tiles = ((a.cols + bc - 1) / bc) * ((a.rows + br - 1) / br);
+  const int64_t steps = fp8_blocks(a.k), rest = t.tiles % grid;
+  int64_t best = rest > 0 ? steps : 0;
+  for (int64_t s = 2; rest > 0 && rest * s <= 2 * grid && steps / s >= 4; ++s) {
+    const int64_t time = (rest * s + grid - 1) / grid * ((steps + s - 1) / s + 4) + 8;
+    if (time < best) {
+      best = time;
+      t.slices = static_cast<int>(s);
+    }
+  }
+  t.whole = static_cast<int>(t.tiles - rest);
+  t.cost = weight * (t.tiles / grid * steps + best);
+  return t;
+}
+
+constexpr int kCus = 256;
+// Tiles of 256 x 256, one workgroup to a CU, or of 128 x 128, two to a CU.
+Tiling pick(const Fp8ProductArgs& a) {
+  const Tiling small = tiling(a, 128, 128, 2 * kCus, 5);
+  if (!a.out_io) return small;
+  const Tiling large = tiling(a, 256, 256, kCus, 8);
+  return large.cost <= small.cost ? large : small;
 }
 
 }  // namespace
 
-size_t fp8_product_workspace_bytes(const Fp8ProductArgs&) { return 0; }
+size_t fp8_product_workspace_bytes(const Fp8ProductArgs& a) {
+  if (a.rows == 0 || a.cols == 0) return 0;
+  const Tiling t = pick(a);
+  return t.slices > 1 ? static_cast<size_t>(t.tiles - t.whole) * t.slices * t.bc * t.br * 4 : 0;
+}
 
 hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream) {
   if (a.rows == 0 || a.cols == 0) return hipSuccess;
@@ -121,9 +444,24 @@ hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream) {
   p.steps = static_cast<int>(fp8_blocks(a.k)); p.pitch = fp8_blocks(a.k) * kBlock;
   p.r_lines = fp8_lines(a.rows); p.c_lines = a.square ? fp8_blocks(a.cols) : fp8_lines(a.cols);
   p.out = a.out; p.accumulate = a.accumulate;
-  const int64_t tiles = ((a.rows + 63) / 64) * ((a.cols + 63) / 64);
-  if (a.out_io) simple_product_kernel<uint16_t><<<dim3(static_cast<unsigned>(tiles)), 256, 0, stream>>>(p);
-  else simple_product_kernel<float><<<dim3(static_cast<unsigned>(tiles)), 256, 0, stream>>>(p);
+  const Tiling t = pick(a);
+  p.tiles_c = static_cast<int>((a.cols + t.bc - 1) / t.bc); p.tiles_r = static_cast<int>((a.rows + t.br - 1) / t.br);
+  p.whole = t.whole; p.slices = t.slices; p.sums = static_cast<float*>(a.workspace);
+  const dim3 sum_grid(static_cast<unsigned>((t.tiles - t.whole) * kShares));
+  auto go = [&](auto bc, auto br, auto waves_c, auto waves_r, auto io) {
+    constexpr int kBC = decltype(bc)::value, kBR = decltype(br)::value;
+    constexpr int kWC = decltype(waves_c)::value, kWR = decltype(waves_r)::value;
+    using T = decltype(io);
+    tile_product_kernel<kBC, kBR, kWC, kWR, T><<<dim3(t.grid), kWC * kWR * kLanes, 0, stream>>>(p);
+    if (t.slices > 1) slices_kernel<kBC, kBR, T><<<sum_grid, 256, 0, stream>>>(p);
+  };
+  using Two = std::integral_constant<int, 2>;
+  using Four = std::integral_constant<int, 4>;
+  using Small = std::integral_constant<int, 128>;
+  using Large = std::integral_constant<int, 256>;
+  if (t.bc == 256) go(Large{}, Large{}, Two{}, Four{}, uint16_t{});
+  else if (a.out_io) go(Small{}, Small{}, Two{}, Two{}, uint16_t{});
+  else go(Small{}, Small{}, Two{}, Two{}, float{});
   return hipGetLastError();
 }
 

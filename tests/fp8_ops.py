@@ -74,12 +74,12 @@ def same(got, want, what):
     assert not bad.any(), f"{what}: {int(bad.sum())} codes differ, the first at {torch.nonzero(bad)[0].tolist()}"
 
 
-def product(r, c, out_dtype, old=None, chunk=64):
+def product(r, c, out_dtype, old=None, chunk=64, device="cpu"):
     """sum_k r[., k] c[., k] of two matrices of values, and its bound.
 
     fp32: products of e4m3 numbers are exact in fp32 and are summed there; every addition inside the matrix cores may
     lose a whole step, 2 u.  bf16: besides, of 8 neighbouring products each may lose 2^-13 of the largest."""
-    rv, cv = values(r), values(c)
+    rv, cv = values(r).to(device), values(c).to(device)
     k = rv.shape[1]
     ref, mag = rv @ cv.T, rv.abs() @ cv.abs().T
     bound = mag * 2 * (k + 64) * U
@@ -89,12 +89,12 @@ def product(r, c, out_dtype, old=None, chunk=64):
         lost = torch.zeros_like(ref)
         for i in range(0, ref.shape[0], chunk):
             for j in range(0, ref.shape[1], chunk):
-                top = torch.zeros(a[i:i + chunk].shape[0], b[j:j + chunk].shape[0], a.shape[1], dtype=F64)
+                top = torch.zeros(a[i:i + chunk].shape[0], b[j:j + chunk].shape[0], a.shape[1], dtype=F64, device=device)
                 for e in range(8):
                     top = torch.maximum(top, a[i:i + chunk, None, :, e] * b[None, j:j + chunk, :, e])
                 lost[i:i + chunk, j:j + chunk] = top.sum(2)
         bound = bound + lost * 8 * 2.0 ** -13
     if old is not None:
-        ref = ref + old.to(F64)
+        ref = ref + old.to(device, F64)
         bound = bound + U * ref.abs()
-    return ref, bound * 1.01 + ref.abs() * half_step(out_dtype)
+    return ref.cpu(), (bound * 1.01 + ref.abs() * half_step(out_dtype)).cpu()

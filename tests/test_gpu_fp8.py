@@ -210,6 +210,37 @@ def test_linear_fwd(M, shape, out_dtype):
     assert torch.equal(got, M.fp8_linear_fwd(xg, wg, out_dtype=out_dtype)), "differs between two calls"
 
 
+# enough tiles for every kernel: whole rounds and a last one, whole or cut along k, ragged on either side
+TILES = [(4100, 260, 5000), (9000, 129, 3001), (2048, 1408, 2048), (2300, 1000, 2500), (300, 4096, 520), (5000, 8, 4000),
+         (1500, 2900, 1300)]
+
+
+@pytest.mark.parametrize("square", [False, True], ids=["rows", "square"])
+@pytest.mark.parametrize("out_dtype", [BF16, F32], ids=str)
+@pytest.mark.parametrize("shape", TILES, ids=str)
+def test_linear_fwd_of_many_tiles(M, shape, out_dtype, square):
+    tokens, k, n = shape
+    say("fp8 linear of many tiles", shape, out_dtype, square)
+    x, w = operands(gen(tokens + k + n), tokens, k, n, square)
+    got = M.fp8_linear_fwd(Q.to_gpu(M, x), Q.to_gpu(M, w), out_dtype=out_dtype)
+    R.check(got, Q.product(x, w, out_dtype, chunk=512, device="cuda"), "out")
+
+
+@pytest.mark.parametrize("shape", [(3000, 2100, 2400), (20000, 300, 200)], ids=str)
+def test_linear_bwd_of_many_tiles(M, shape):
+    tokens, k, n = shape
+    say("fp8 linear gradients of many tiles", shape)
+    g = gen(17)
+    x, w = operands(g, *shape)
+    wt = Q.quantize(Q.values(w).T, True)
+    dout = spread(g, tokens, n, F32).mul(1e-3).to(BF16)
+    old = torch.randn(n, k, generator=g).to(BF16)
+    got = M.fp8_linear_bwd(Q.to_gpu(M, x), Q.to_gpu(M, wt), dout.cuda(), dweight=old.cuda(), accumulate=True)
+    R.check(got["dx"], Q.product(Q.quantize(dout), wt, BF16, chunk=512, device="cuda"), "dx")
+    want = Q.product(Q.quantize(dout.T), Q.quantize(Q.values(x).T), BF16, old=old, chunk=512, device="cuda")
+    R.check(got["dweight"], want, "dweight")
+
+
 @pytest.mark.parametrize("io", [BF16, F32], ids=str)
 @pytest.mark.parametrize("shape", [(1, 1, 5), (1, 2560, 640), (3, 333, 130), (16, 640, 256), (40, 1000, 96), (300, 384, 200)],
                          ids=str)
