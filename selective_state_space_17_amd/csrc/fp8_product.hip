@@ -165,10 +165,11 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
   };
 
   // ---- loads.  A load is 8 rows x 128 bytes, a lane's part row lane / 8 and the 16-byte chunk lane % 8 as stored.  The
-  // chunk it holds is xor-ed with the row's low three bits, which keeps the reads below free of bank conflicts.  LDS row
-  // 32 t + i of a wave's share holds row TC i + t of it.  Rows past the matrix are its last row again.
+  // chunk it holds is xor-ed with bits 1 to 3 of the row: the reads below, where 32 lanes read one chunk of 32 rows, are
+  // served 16 lanes, 256 bytes, at a time, two rows of 128 bytes side by side (with the low three bits every read took
+  // two turns).  LDS row 32 t + i of a wave's share holds row TC i + t of it.  Rows past the matrix are its last row again.
   const int lrow = lane / 8;
-  const uint32_t chunk = static_cast<uint32_t>(((lane % 8) ^ lrow) * 16);
+  const uint32_t chunk = static_cast<uint32_t>(((lane % 8) ^ (w * 4 + lrow / 2) % 8) * 16);   // (kW is even)
   int ljob = job_first, lleft = 0, lk = 0;   // job and step of the next loads
   const unsigned char *lc = nullptr, *lr = nullptr;
   uint32_t oc[LC], orr[LR];
@@ -242,7 +243,7 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int i = lane % 32;
-      const uint32_t at = i * kRow + (((h * 4 + lane / 32 * 2 + q) ^ (i & 7)) << 4);
+      const uint32_t at = i * kRow + (((h * 4 + lane / 32 * 2 + q) ^ (i / 2 % 8)) << 4);
       fc_at[h][q] = c_lds + at + wc * TC * 32 * kRow;
       fr_at[h][q] = r_lds + at + wr * TR * 32 * kRow;
     }
