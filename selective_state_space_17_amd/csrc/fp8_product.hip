@@ -48,7 +48,8 @@ __device__ __forceinline__ bf16x8_t wide_codes(const i32x8_t& v, int q, float s)
 }
 
 // -------------------------------------------------------------------------------------------------- tiles
-constexpr int kRow = kBlock;             // bytes of a row of a step
+constexpr int kRow = kBlock / 2;         // bytes of a row of half a step
+constexpr int kRing = 4;                 // halves in LDS
 constexpr int kBand = 4;                 // tiles of R side by side in the order of tiles
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
@@ -61,8 +62,18 @@ __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t l
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :: "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory", "m0");
 }
-__device__ __forceinline__ u32x4_t lds_at(uint32_t addr) {
-  return *(__attribute__((address_space(3))) const u32x4_t*)static_cast<uintptr_t>(addr);
+// the same with up to four bytes a lane, each of which becomes a word at lds + 4 l
+template <int BYTES> __device__ __forceinline__ void dma_word(const void* base, uint32_t off, uint32_t lds) {
+  const uint32_t to = __builtin_amdgcn_readfirstlane(lds);
+  if constexpr (BYTES == 4)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" :: "v"(off), "s"(base), "s"(to) : "memory", "m0");
+  else if constexpr (BYTES == 2)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_ushort %0, %1" :: "v"(off), "s"(base), "s"(to) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, %1" :: "v"(off), "s"(base), "s"(to) : "memory", "m0");
+}
+template <typename V> __device__ __forceinline__ V lds_at(uint32_t addr) {
+  return *(__attribute__((address_space(3))) const V*)static_cast<uintptr_t>(addr);
 }
 // the scheduler keeps what stands before this before it
 __device__ __forceinline__ void fence_schedule() { __builtin_amdgcn_sched_barrier(0); }
@@ -100,11 +111,12 @@ template <typename T> __device__ __forceinline__ void put(T* to, float (&v)[8], 
 
 // C's rows are the matrix instructions' rows: a lane's accumulators are neighbours in the output.
 //
-// One workgroup stays on a CU (two of the small tile) and takes tile after tile, each 128 k (a block) a step, from two
-// LDS buffers filled by loads that run two steps ahead and cross the borders of tiles.  A step is two halves of 64 k:
-// the second half's fragments are read while the first is multiplied; between the halves every wave has read all of
-// the step's buffer, so one barrier there frees it for the loads two steps ahead and publishes the next step's, whose
-// first half is read while the second is multiplied.
+// One workgroup stays on a CU (two of the small tile) and takes tile after tile, each 128 k (a block) a step, in halves
+// of 64 k.  Four halves are in LDS or on their way there.  While a half is multiplied from registers the next one's
+// fragments are read, and the place that it was read from before takes the loads of the half four ahead; one barrier
+// after each half, before which a wave waits for its loads of the half after the next, by count.  So a load has three
+// halves of multiplications to arrive in, and crosses the borders of tiles (with two whole steps in LDS and a barrier a
+// step it had two: 497 us at 8192^3).
 //
 // A wave holds TC x TR tiles of 32 x 32.  Row i of tile t is row TC i + t of its share: a lane's scales for its tiles
 // are then TC neighbouring bytes of memory, one word, from which the instruction picks a byte; and what a lane holds of
@@ -114,16 +126,19 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
   constexpr bool kFine = std::is_same_v<T, float>;
   constexpr int kW = WC * WR;
   constexpr int TC = BC / WC / 32, TR = BR / WR / 32;      // 32 x 32 tiles of a wave
-  constexpr int LC = BC / 8 / kW, LR = BR / 8 / kW;        // 1 KB loads of a wave per step
-  constexpr int kRows = TC;                                // rows of multiplications in a half
-  constexpr int kLoads = (LC + LR + kRows - 1) / kRows;    // loads between two of them
-  constexpr int kReads = (TC + TR + kRows - 1) / kRows;    // fragments read there
-  static_assert(LC * 8 * kW == BC && LR * 8 * kW == BR, "loads split evenly over the waves");
+  constexpr int LC = BC / 16 / kW, LR = BR / 16 / kW;      // 1 KB loads of a wave per half
+  constexpr int kLoads = (LC + LR + TC - 1) / TC;          // loads between two rows of multiplications
+  constexpr int kReads = (TC + TR + TC - 1) / TC;          // fragments read there
+  constexpr int kAhead = 2 * (LC + LR) + 2;                // loads of two neighbouring halves, scales among them
+  constexpr int kStores = TC * TR * static_cast<int>(sizeof(T));   // a whole tile's stores of a wave, 16 bytes a lane
+  static_assert(LC * 16 * kW == BC && LR * 16 * kW == BR, "loads split evenly over the waves");
   static_assert(TC == 2 || TC == 4, "a lane's scales of C are a word or half of one");
-  static_assert(TR == 2 || TR == 4, "and those of R");
-  constexpr int kC = BC * kRow, kR = BR * kRow;            // bytes of a buffer
-  __shared__ __attribute__((aligned(128))) unsigned char cbuf[2][kC];
-  __shared__ __attribute__((aligned(128))) unsigned char rbuf[2][kR];
+  static_assert(TR == 2, "and those of R half of one");
+  static_assert(kAhead + kStores < 64, "what the wait instruction can count");
+  constexpr int kC = BC * kRow, kR = BR * kRow;            // bytes of a half
+  __shared__ __attribute__((aligned(256))) unsigned char cbuf[kRing][kC];
+  __shared__ __attribute__((aligned(256))) unsigned char rbuf[kRing][kR];
+  __shared__ uint32_t sbuf[kRing / 2][kW][2][kLanes];      // scales of a step, each wave's own: C's, R's
 
   const int lane = threadIdx.x % kLanes;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
@@ -164,22 +179,21 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
     return j;
   };
 
-  // ---- loads.  A load is 8 rows x 128 bytes, a lane's part row lane / 8 and the 16-byte chunk lane % 8 as stored.  The
-  // chunk it holds is xor-ed with bits 1 to 3 of the row: the reads below, where 32 lanes read one chunk of 32 rows, are
-  // served 16 lanes, 256 bytes, at a time, two rows of 128 bytes side by side (with the low three bits every read took
-  // two turns).  LDS row 32 t + i of a wave's share holds row TC i + t of it.  Rows past the matrix are its last row again.
-  const int lrow = lane / 8;
-  const uint32_t chunk = static_cast<uint32_t>(((lane % 8) ^ (w * 4 + lrow / 2) % 8) * 16);   // (kW is even)
+  // ---- loads.  A load is 16 rows x 64 bytes, a lane's part row lane / 4 and the 16-byte chunk lane % 4 as stored.  The
+  // chunk it holds is xor-ed with bits 2 and 3 of the row: the reads below, where 32 lanes read one chunk of 32 rows, are
+  // served 16 lanes, 256 bytes, at a time, four rows of 64 bytes side by side.  LDS row 32 t + i of a wave's share holds
+  // row TC i + t of it.  Rows past the matrix are its last row again.
+  const int lrow = lane / 4;
+  const uint32_t chunk = static_cast<uint32_t>(((lane % 4) ^ (lane / 16)) * 16);
   int ljob = job_first, lleft = 0, lk = 0;   // job and step of the next loads
-  const unsigned char *lc = nullptr, *lr = nullptr;
-  uint32_t oc[LC], orr[LR];
-  int64_t lsc = 0, lsr = 0;                  // where the scales of the next loads stand, of step 0
+  const unsigned char *lc = nullptr, *lr = nullptr, *lcs = nullptr, *lrs = nullptr;
+  uint32_t oc[LC], orr[LR], ocs = 0, ors = 0;
   const uint32_t pitch = static_cast<uint32_t>(p.pitch);
   auto offsets = [&](int64_t rows, int of, auto& off) {   // rows: of the matrix, from the tile's first on
     const int last = rows < 256 ? static_cast<int>(rows) - 1 : 255;
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(off) / sizeof(off[0])); ++i) {
-      const int at = (i * kW + w) * 8 + lrow;
+      const int at = (i * kW + w) * 16 + lrow;
       const int r = at / (32 * of) * (32 * of) + at % 32 * of + at / 32 % of;
       off[i] = static_cast<uint32_t>(r < last ? r : last) * pitch + chunk;   // (pitch <= 2^22)
     }
@@ -194,37 +208,34 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
         offsets(p.rows - j.r0, TR, orr);
         lc = p.c + static_cast<int64_t>(j.c0) * p.pitch;
         lr = p.r + static_cast<int64_t>(j.r0) * p.pitch;
-        const int64_t c = j.c0 + wc * (32 * TC) + lane % 32 * TC, r = j.r0 + wr * (32 * TR) + lane % 32 * TR;
-        if (p.square) {
-          const int64_t b = (j.c0 + wc * (32 * TC)) / kBlock;
-          lsc = b < p.c_lines ? b : p.c_lines - 1;
-        } else {
-          lsc = c < p.c_lines ? c : p.c_lines - TC;
-        }
-        lsr = r < p.r_lines ? r : p.r_lines - TR;
+        const int c = wc * (32 * TC) + lane % 32 * TC, r = wr * (32 * TR) + lane % 32 * TR;
+        const int64_t left_c = p.c_lines - j.c0 - TC, left_r = p.r_lines - j.r0 - TR;
+        lcs = p.cs + (p.square ? j.c0 / kBlock : j.c0);
+        lrs = p.rs + j.r0;
+        if (p.square) ocs = j.c0 / kBlock + wc * (32 * TC) / kBlock < p.c_lines ? wc * (32 * TC) / kBlock : 0;
+        else ocs = c < left_c ? c : static_cast<int>(left_c);
+        ors = r < left_r ? r : static_cast<int>(left_r);
         return;
       }
       ljob += stride;
     }
   };
   const uint32_t c_lds = lds_addr(&cbuf[0][0]), r_lds = lds_addr(&rbuf[0][0]);
-  auto load_one = [&](int i, int buf) {
-    const int64_t k = static_cast<int64_t>(lk) * kRow;
-    if (i < LC) dma16(lc + k, oc[i < LC ? i : 0], c_lds + buf * kC + (i * kW + w) * 1024);
-    else dma16(lr + k, orr[i - LC < LR && i >= LC ? i - LC : 0], r_lds + buf * kR + ((i - LC) * kW + w) * 1024);
+  const uint32_t s_lds = lds_addr(&sbuf[0][w][0][0]);
+  constexpr int kScales = sizeof(sbuf[0]);
+  // load i of half h of a step into the place of half h of steps of parity `turn`
+  auto load_one = [&](int i, int h, int turn) {
+    const int64_t k = static_cast<int64_t>(lk) * kBlock + h * kRow;
+    const int slot = 2 * turn + h;
+    if (i < LC) dma16(lc + k, oc[i < LC ? i : 0], c_lds + slot * kC + (i * kW + w) * 1024);
+    else dma16(lr + k, orr[i - LC < LR && i >= LC ? i - LC : 0], r_lds + slot * kR + ((i - LC) * kW + w) * 1024);
   };
-  auto bytes_at = [&](const unsigned char* at, int of) {
-    return of == 4 ? *reinterpret_cast<const uint32_t*>(at) : static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(at));
-  };
-  struct Scales {
-    uint32_t c, r;
-  };
-  auto load_scales = [&]() {
-    Scales s;
-    const unsigned char* const at = p.cs + lk * p.c_lines + lsc;
-    s.c = p.square ? static_cast<uint32_t>(*at) * 0x01010101u : bytes_at(at, TC);
-    s.r = bytes_at(p.rs + lk * p.r_lines + lsr, TR);
-    return s;
+  auto load_scales = [&](int turn) {
+    const uint32_t to = s_lds + turn * kScales;
+    const unsigned char* const c = lcs + lk * p.c_lines;
+    if (p.square) dma_word<1>(c, ocs, to);
+    else dma_word<TC>(c, ocs, to);
+    dma_word<TR>(lrs + lk * p.r_lines, ors, to + 4 * kLanes);
   };
   auto loaded = [&]() {   // after a step's last load
     if (lleft > 1) {
@@ -236,27 +247,32 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
     }
   };
 
-  // ---- fragments: a lane's 32 codes are chunks 4 h + 2 (lane / 32) and the next of its row
-  uint32_t fc_at[2][2], fr_at[2][2];   // by half and chunk
+  // ---- fragments: a lane's 32 codes are chunks 2 (lane / 32) and the next of its row
+  uint32_t fc_at[2], fr_at[2];   // by chunk
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int i = lane % 32;
-      const uint32_t at = i * kRow + (((h * 4 + lane / 32 * 2 + q) ^ (i / 2 % 8)) << 4);
-      fc_at[h][q] = c_lds + at + wc * TC * 32 * kRow;
-      fr_at[h][q] = r_lds + at + wr * TR * 32 * kRow;
-    }
+  for (int q = 0; q < 2; ++q) {
+    const int i = lane % 32;
+    const uint32_t at = i * kRow + (((lane / 32 * 2 + q) ^ (i / 4 % 4)) << 4);
+    fc_at[q] = c_lds + at + wc * TC * 32 * kRow;
+    fr_at[q] = r_lds + at + wr * TR * 32 * kRow;
+  }
   f32x16_t acc[TC][TR];
   i32x8_t fc[2][TC], fr[2][TR];
   auto frag = [&](const uint32_t (&at)[2], uint32_t more) {
-    const u32x4_t a = lds_at(at[0] + more), b = lds_at(at[1] + more);
+    const u32x4_t a = lds_at<u32x4_t>(at[0] + more), b = lds_at<u32x4_t>(at[1] + more);
     return i32x8_t{static_cast<int>(a[0]), static_cast<int>(a[1]), static_cast<int>(a[2]), static_cast<int>(a[3]),
                    static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]), static_cast<int>(b[3])};
   };
-  auto read_one = [&](int q, int h, int buf) {
-    if (q < TR) fr[h][q < TR ? q : 0] = frag(fr_at[h], buf * kR + (q < TR ? q : 0) * 32 * kRow);
-    else fc[h][q - TR < TC && q >= TR ? q - TR : 0] = frag(fc_at[h], buf * kC + (q - TR) * 32 * kRow);
+  auto read_one = [&](int q, int h, int slot) {
+    if (q < TR) fr[h][q < TR ? q : 0] = frag(fr_at, slot * kR + (q < TR ? q : 0) * 32 * kRow);
+    else fc[h][q - TR < TC && q >= TR ? q - TR : 0] = frag(fc_at, slot * kC + (q - TR) * 32 * kRow);
+  };
+  struct Scales {
+    uint32_t c, r;
+  };
+  auto read_scales = [&](int turn) {
+    const uint32_t at = s_lds + turn * kScales + lane * 4;
+    return Scales{lds_at<uint32_t>(at) * (p.square ? 0x01010101u : 1u), lds_at<uint32_t>(at + 4 * kLanes)};
   };
   auto multiply_row = [&](auto i, int h, const Scales& s) {
     constexpr int I = decltype(i)::value;
@@ -281,53 +297,62 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
     }
   };
 
-  start_load();
-  Scales now{}, next{}, coming{};   // of the step that is multiplied, the next one, and the one whose loads are on their way
-  if (lleft > 0) {   // (no steps at all where k is empty: the tiles are then stored as zeros)
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-#pragma unroll
-      for (int q = 0; q < LC + LR; ++q) load_one(q, b);
-      (b == 0 ? now : coming) = load_scales();
-      loaded();
+  int stored = 0;   // halves whose wait may leave the last tile's stores outstanding too
+  // the end of a half: this wave's reads of the next one are done, and its loads of the one after that have arrived
+  auto turn_over = [&]() {
+    if (stored > 0) {
+      --stored;
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kAhead + kStores) : "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kAhead) : "memory");
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-  }
-  int buf = 0;
+    fence_schedule();
+  };
+  start_load();
+  Scales now{}, next{};
+  if (lleft > 0) {   // (no steps at all where k is empty: the tiles are then stored as zeros)
 #pragma unroll
-  for (int q = 0; q < TC + TR; ++q) read_one(q, 0, 0);
+    for (int turn = 0; turn < 2; ++turn) {
+      load_scales(turn);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < LC + LR; ++q) load_one(q, h, turn);
+      loaded();
+    }
+    turn_over();
+#pragma unroll
+    for (int q = 0; q < TC + TR; ++q) read_one(q, 0, 0);
+    now = read_scales(0);
+    turn_over();
+  }
+  int turn = 0;   // parity of the step, counted over all tiles
   for (int job = job_first; job < job_end; job += stride) {
     const Job cur = job_at(job);
 #pragma unroll
     for (int i = 0; i < TC; ++i)
 #pragma unroll
       for (int j = 0; j < TR; ++j) acc[i][j] = f32x16_t{};
-    for (int s = 0; s < cur.steps; ++s, buf ^= 1) {
+    for (int s = 0; s < cur.steps; ++s, turn ^= 1) {
       fence_schedule();
-      unrolled<TC>([&](auto i) {
-        multiply_row(i, 0, now);
-        fence_schedule();
 #pragma unroll
-        for (int q = i * kReads; q < (i + 1) * kReads && q < TC + TR; ++q) read_one(q, 1, buf);
-        fence_schedule();
-      });
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      next = coming;
-      fence_schedule();
-      unrolled<TC>([&](auto i) {
-        multiply_row(i, 1, now);
-        fence_schedule();
+      for (int h = 0; h < 2; ++h) {
+        if (h == 0) load_scales(turn);
+        else next = read_scales(turn ^ 1);
+        unrolled<TC>([&](auto i) {
+          multiply_row(i, h, now);
+          fence_schedule();
 #pragma unroll
-        for (int q = i * kLoads; q < (i + 1) * kLoads && q < LC + LR; ++q) load_one(q, buf);
-        if (i == TC - 1) coming = load_scales();
+          for (int q = i * kLoads; q < (i + 1) * kLoads && q < LC + LR; ++q) load_one(q, h, turn);
 #pragma unroll
-        for (int q = i * kReads; q < (i + 1) * kReads && q < TC + TR; ++q) read_one(q, 0, buf ^ 1);
-        fence_schedule();
-      });
+          for (int q = i * kReads; q < (i + 1) * kReads && q < TC + TR; ++q)
+            read_one(q, h ^ 1, h == 0 ? 2 * turn + 1 : 2 * (turn ^ 1));
+          fence_schedule();
+        });
+        turn_over();
+      }
       now = next;
       loaded();
     }
@@ -354,12 +379,14 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
     } else {
       T* const to = static_cast<T*>(p.out) + cur.r0 * p.cols + cur.c0;
       const int64_t rows = p.rows - cur.r0, cols = p.cols - cur.c0;
-      if (rows >= BR && cols >= BC && !p.accumulate)
+      if (rows >= BR && cols >= BC && !p.accumulate) {
         each([&](int r, int c, float (&v)[8]) { store_row<8>(to + r * p.cols + c, v); });
-      else
+        stored = 2;
+      } else {
         each([&](int r, int c, float (&v)[8]) {
           if (r < rows) put(to + r * p.cols + c, v, cols - c, p.accumulate);
         });
+      }
     }
   }
   // the last loads may still be on their way into this workgroup's LDS
