@@ -277,14 +277,23 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
   auto multiply_row = [&](auto i, int h, const Scales& s) {
     constexpr int I = decltype(i)::value;
     if constexpr (kFine) {
-      const float sc = fp8_power((s.c >> (8 * I)) & 255u);
+      // 16 k at a time, every fragment widened once
+      float sc[TC], sr[TR];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const bf16x8_t a = wide_codes(fc[h][I], q, sc);
+      for (int c = 0; c < TC; ++c) sc[c] = fp8_power((s.c >> (8 * c)) & 255u);
 #pragma unroll
-        for (int j = 0; j < TR; ++j)
-          acc[I][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, wide_codes(fr[h][j], q, fp8_power((s.r >> (8 * j)) & 255u)),
-                                                              acc[I][j], 0, 0, 0);
+      for (int r = 0; r < TR; ++r) sr[r] = fp8_power((s.r >> (8 * r)) & 255u);
+#pragma unroll
+      for (int q = I * 4 / TC; q < (I + 1) * 4 / TC; ++q) {
+        bf16x8_t b[TR];
+#pragma unroll
+        for (int r = 0; r < TR; ++r) b[r] = wide_codes(fr[h][r], q, sr[r]);
+#pragma unroll
+        for (int c = 0; c < TC; ++c) {
+          const bf16x8_t a = wide_codes(fc[h][c], q, sc[c]);
+#pragma unroll
+          for (int r = 0; r < TR; ++r) acc[c][r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b[r], acc[c][r], 0, 0, 0);
+        }
       }
     } else {
       unrolled<TR>([&](auto j) {
@@ -380,7 +389,41 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
       T* const to = static_cast<T*>(p.out) + cur.r0 * p.cols + cur.c0;
       const int64_t rows = p.rows - cur.r0, cols = p.cols - cur.c0;
       if (rows >= BR && cols >= BC && !p.accumulate) {
-        each([&](int r, int c, float (&v)[8]) { store_row<8>(to + r * p.cols + c, v); });
+        if constexpr (kFine) {
+          each([&](int r, int c, float (&v)[8]) { store_row<8>(to + r * p.cols + c, v); });
+        } else {
+          // A run of a row is 16 (TC 2) or 32 bytes of lane l and as many after it of lane l + 32.  Pieces of 16 bytes change
+          // places between lanes 16 apart, so that a store writes 64 bytes of each of 16 rows, past the cache: kept there,
+          // the output pushed the operands out of it (32768 x 2560 x 10240, which writes 671 MB: 817 us, as here 767; past
+          // the cache but in pieces of 32 bytes 955).
+          constexpr bool kTwo = TC == 4;             // a run is two pieces: they change places, else runs q and q + 1
+          const int row16 = lane / 16 % 2;
+#pragma unroll
+          for (int j = 0; j < TR; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; q += kTwo ? 1 : 2) {
+              u32x4_t piece[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int at = (kTwo ? 8 * h : 0) + 2 * e, run = 4 * (kTwo ? q : q + h);
+                  piece[h][e] = pack_bf16(acc[at % TC][j][run + at / TC], acc[(at + 1) % TC][j][run + (at + 1) / TC]);
+                }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const auto t = __builtin_amdgcn_permlane16_swap(piece[0][e], piece[1][e], false, false);
+                piece[0][e] = t[0];
+                piece[1][e] = t[1];
+              }
+              const int c = wave_c + 8 * TC * q + row16 * (kTwo ? 8 : 8 * TC);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int r = wr * TR * 32 + (lane % 16 + 16 * h) * TR + j;
+                __builtin_nontemporal_store(piece[h], reinterpret_cast<u32x4_u*>(to + r * p.cols + c));
+              }
+            }
+        }
         stored = 2;
       } else {
         each([&](int r, int c, float (&v)[8]) {
@@ -450,7 +493,6 @@ constexpr int kCus = 256;
 // Tiles of 256 x 256, one workgroup to a CU, or of 128 x 128, two to a CU.
 Tiling pick(const Fp8ProductArgs& a) {
   const Tiling small = tiling(a, 128, 128, 2 * kCus, 5);
-  if (!a.out_io) return small;
   const Tiling large = tiling(a, 256, 256, kCus, 8);
   return large.cost <= small.cost ? large : small;
 }
@@ -487,7 +529,8 @@ hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream) {
   using Four = std::integral_constant<int, 4>;
   using Small = std::integral_constant<int, 128>;
   using Large = std::integral_constant<int, 256>;
-  if (t.bc == 256) go(Large{}, Large{}, Two{}, Four{}, uint16_t{});
+  if (t.bc == 256 && a.out_io) go(Large{}, Large{}, Two{}, Four{}, uint16_t{});
+  else if (t.bc == 256) go(Large{}, Large{}, Two{}, Four{}, float{});
   else if (a.out_io) go(Small{}, Small{}, Two{}, Two{}, uint16_t{});
   else go(Small{}, Small{}, Two{}, Two{}, float{});
   return hipGetLastError();
