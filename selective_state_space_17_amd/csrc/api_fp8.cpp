@@ -67,14 +67,16 @@ struct Pieces {
 struct Fwd {
   mssm::Fp8ProductArgs product{};
   size_t bytes = 0;
-  Fp8View x;   // where a plain x goes
+  bool rounds = false;   // a plain x goes through
+  Fp8View x;
 };
 Fwd plan_fwd(const mssm_fp8_linear_desc& d, void* workspace) {
   Fwd f;
   Pieces w{static_cast<unsigned char*>(workspace)};
-  if (d.x_dtype != MSSM_E4M3) f.x = w.matrix(d.tokens, d.in_features);
   f.product.rows = d.tokens; f.product.cols = d.out_features; f.product.k = d.in_features;
-  f.product.square = d.weight_kind == MSSM_FP8_SQUARE; f.product.out_io = d.io_dtype;
+  f.product.square = d.weight_kind == MSSM_FP8_SQUARE; f.product.out_io = d.io_dtype; f.product.r_io = d.x_dtype;
+  f.rounds = d.x_dtype != MSSM_E4M3 && !mssm::fp8_product_takes_plain(f.product);
+  if (f.rounds) f.x = w.matrix(d.tokens, d.in_features);
   f.product.workspace = w.take(mssm::fp8_product_workspace_bytes(f.product));
   f.bytes = w.used;
   return f;
@@ -195,7 +197,7 @@ int mssm_fp8_linear_fwd(const mssm_fp8_linear_desc* desc, const void* x, const v
   if (!disjoint(in, outs)) return MSSM_ERR_INVALID_ARG;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   f.product.r = {const_cast<void*>(x), const_cast<void*>(x_scales)};
-  if (plain) {
+  if (f.rounds) {
     mssm::Fp8Args q{};
     q.rows = d.tokens; q.cols = d.in_features; q.io = d.x_dtype; q.x = x; q.m = f.x;
     const int e = done(mssm::fp8_quantize_launch(q, s));

@@ -23,7 +23,7 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
 struct Fp8Params {
   const unsigned char *r, *rs, *c, *cs;
-  int64_t rows, cols;
+  int64_t rows, cols, k;
   int64_t r_lines, c_lines;      // of the scales
   int64_t pitch;                 // bytes of a row of either
   int steps;                     // of 128 k
@@ -49,28 +49,28 @@ __device__ __forceinline__ bf16x8_t wide_codes(const i32x8_t& v, int q, float s)
 
 // -------------------------------------------------------------------------------------------------- tiles
 constexpr int kRow = kBlock / 2;         // bytes of a row of half a step
-constexpr int kRing = 4;                 // halves in LDS
 constexpr int kBand = 4;                 // tiles of R side by side in the order of tiles
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));   // low half of a flat LDS address
 }
-// lane l's 16 bytes at base + off go to LDS offset lds + 16 l (base and lds are wave-uniform).  Written as asm
-// so that the compiler does not wait for these loads before the LDS reads of the other buffer; they are
-// waited for by count.  No output register: nothing can be overwritten while a load is in flight.
-__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               :: "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory", "m0");
-}
-// the same with up to four bytes a lane, each of which becomes a word at lds + 4 l
-template <int BYTES> __device__ __forceinline__ void dma_word(const void* base, uint32_t off, uint32_t lds) {
-  const uint32_t to = __builtin_amdgcn_readfirstlane(lds);
-  if constexpr (BYTES == 4)
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" :: "v"(off), "s"(base), "s"(to) : "memory", "m0");
+// Lane l's 16 bytes at base + off + OFF go to LDS offset lds + LDS + 16 l; with fewer bytes each becomes a word at + 4 l
+// (base and lds are wave-uniform; the instruction adds its offset to either address).  Written as asm so that the compiler does not wait for these loads before the LDS
+// reads of the other halves; they are waited for by count.  No output register: nothing can be overwritten while a load
+// is in flight.
+template <int BYTES, int LDS, int OFF> __device__ __forceinline__ void dma(const void* base, uint32_t off, uint32_t lds) {
+  if constexpr (BYTES == 16)
+    asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 offset:%4"
+                 :: "v"(off), "s"(base), "s"(lds), "n"(LDS - OFF), "n"(OFF) : "memory", "m0", "scc");
+  else if constexpr (BYTES == 4)
+    asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1 offset:%4"
+                 :: "v"(off), "s"(base), "s"(lds), "n"(LDS - OFF), "n"(OFF) : "memory", "m0", "scc");
   else if constexpr (BYTES == 2)
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_ushort %0, %1" :: "v"(off), "s"(base), "s"(to) : "memory", "m0");
+    asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_ushort %0, %1 offset:%4"
+                 :: "v"(off), "s"(base), "s"(lds), "n"(LDS - OFF), "n"(OFF) : "memory", "m0", "scc");
   else
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, %1" :: "v"(off), "s"(base), "s"(to) : "memory", "m0");
+    asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, %1 offset:%4"
+                 :: "v"(off), "s"(base), "s"(lds), "n"(LDS - OFF), "n"(OFF) : "memory", "m0", "scc");
 }
 template <typename V> __device__ __forceinline__ V lds_at(uint32_t addr) {
   return *(__attribute__((address_space(3))) const V*)static_cast<uintptr_t>(addr);
@@ -111,17 +111,17 @@ template <typename T> __device__ __forceinline__ void put(T* to, float (&v)[8], 
 
 // C's rows are the matrix instructions' rows: a lane's accumulators are neighbours in the output.
 //
-// One workgroup stays on a CU (two of the small tile) and takes tile after tile, each 128 k (a block) a step, in halves
-// of 64 k.  Four halves are in LDS or on their way there.  While a half is multiplied from registers the next one's
+// A workgroup stays on a CU (two of the small tile) and takes tile after tile, each 128 k (a block) a step, in halves of
+// 64 k.  Four halves are in LDS or on their way there.  While a half is multiplied from registers the next one's
 // fragments are read, and the place that it was read from before takes the loads of the half four ahead; one barrier
 // after each half, before which a wave waits for its loads of the half after the next, by count.  So a load has three
 // halves of multiplications to arrive in, and crosses the borders of tiles (with two whole steps in LDS and a barrier a
-// step it had two: 497 us at 8192^3).
+// step it had two: 497 us at 8192^3, where this takes 448; a ring of eight halves was no faster).
 //
 // A wave holds TC x TR tiles of 32 x 32.  Row i of tile t is row TC i + t of its share: a lane's scales for its tiles
 // are then TC neighbouring bytes of memory, one word, from which the instruction picks a byte; and what a lane holds of
 // an output row are runs of 4 TC neighbouring elements.
-template <int BC, int BR, int WC, int WR, typename T>
+template <int BC, int BR, int WC, int WR, bool SQUARE, typename T>
 __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params p) {
   constexpr bool kFine = std::is_same_v<T, float>;
   constexpr int kW = WC * WR;
@@ -136,10 +136,11 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
   static_assert(TR == 2, "and those of R half of one");
   static_assert(kAhead + kStores < 64, "what the wait instruction can count");
   constexpr int kC = BC * kRow, kR = BR * kRow;            // bytes of a half
-  __shared__ __attribute__((aligned(256))) unsigned char cbuf[kRing][kC];
-  __shared__ __attribute__((aligned(256))) unsigned char rbuf[kRing][kR];
-  __shared__ uint32_t sbuf[kRing / 2][kW][2][kLanes];      // scales of a step, each wave's own: C's, R's
-
+  // LDS: four halves of C, four of R, the scales of two steps, each wave's own (C's, R's).  The ring's two steps lie a power
+  // of two apart, so that an exclusive or takes an address from one to the other.
+  constexpr int kS = kW * 2 * kLanes * 4;
+  __shared__ __attribute__((aligned(4 * kC))) unsigned char lds[4 * kC + 4 * kR + 2 * kS];
+  static_assert((kC & (kC - 1)) == 0 && kC == kR && (kS & (kS - 1)) == 0, "powers of two");
   const int lane = threadIdx.x % kLanes;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
   const int wc = w / WR, wr = w % WR;
@@ -185,7 +186,7 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
   // row TC i + t of it.  Rows past the matrix are its last row again.
   const int lrow = lane / 4;
   const uint32_t chunk = static_cast<uint32_t>(((lane % 4) ^ (lane / 16)) * 16);
-  int ljob = job_first, lleft = 0, lk = 0;   // job and step of the next loads
+  int ljob = job_first, lleft = 0;           // job of the next loads, and its steps that they have not come to
   const unsigned char *lc = nullptr, *lr = nullptr, *lcs = nullptr, *lrs = nullptr;
   uint32_t oc[LC], orr[LR], ocs = 0, ors = 0;
   const uint32_t pitch = static_cast<uint32_t>(p.pitch);
@@ -203,16 +204,15 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
       const Job j = job_at(ljob);
       if (j.steps > 0) {
         lleft = j.steps;
-        lk = j.begin;
         offsets(p.cols - j.c0, TC, oc);
         offsets(p.rows - j.r0, TR, orr);
-        lc = p.c + static_cast<int64_t>(j.c0) * p.pitch;
-        lr = p.r + static_cast<int64_t>(j.r0) * p.pitch;
+        lc = p.c + static_cast<int64_t>(j.c0) * p.pitch + j.begin * kBlock;
+        lr = p.r + static_cast<int64_t>(j.r0) * p.pitch + j.begin * kBlock;
         const int c = wc * (32 * TC) + lane % 32 * TC, r = wr * (32 * TR) + lane % 32 * TR;
         const int64_t left_c = p.c_lines - j.c0 - TC, left_r = p.r_lines - j.r0 - TR;
-        lcs = p.cs + (p.square ? j.c0 / kBlock : j.c0);
-        lrs = p.rs + j.r0;
-        if (p.square) ocs = j.c0 / kBlock + wc * (32 * TC) / kBlock < p.c_lines ? wc * (32 * TC) / kBlock : 0;
+        lcs = p.cs + j.begin * p.c_lines + (SQUARE ? j.c0 / kBlock : j.c0);
+        lrs = p.rs + j.begin * p.r_lines + j.r0;
+        if (SQUARE) ocs = j.c0 / kBlock + wc * (32 * TC) / kBlock < p.c_lines ? wc * (32 * TC) / kBlock : 0;
         else ocs = c < left_c ? c : static_cast<int>(left_c);
         ors = r < left_r ? r : static_cast<int>(left_r);
         return;
@@ -220,27 +220,29 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
       ljob += stride;
     }
   };
-  const uint32_t c_lds = lds_addr(&cbuf[0][0]), r_lds = lds_addr(&rbuf[0][0]);
-  const uint32_t s_lds = lds_addr(&sbuf[0][w][0][0]);
-  constexpr int kScales = sizeof(sbuf[0]);
-  // load i of half h of a step into the place of half h of steps of parity `turn`
-  auto load_one = [&](int i, int h, int turn) {
-    const int64_t k = static_cast<int64_t>(lk) * kBlock + h * kRow;
-    const int slot = 2 * turn + h;
-    if (i < LC) dma16(lc + k, oc[i < LC ? i : 0], c_lds + slot * kC + (i * kW + w) * 1024);
-    else dma16(lr + k, orr[i - LC < LR && i >= LC ? i - LC : 0], r_lds + slot * kR + ((i - LC) * kW + w) * 1024);
+  const uint32_t c_lds = lds_addr(lds), r_lds = c_lds + 4 * kC, s_lds = r_lds + 4 * kR + w * (2 * kLanes * 4);
+  // where the ring's step that takes loads lies
+  uint32_t c_to = __builtin_amdgcn_readfirstlane(c_lds + w * 1024), r_to = c_to + 4 * kC, s_to = __builtin_amdgcn_readfirstlane(s_lds);
+  // load i of half h of a step
+  auto load_one = [&](auto i, auto h) {
+    constexpr int I = decltype(i)::value, H = decltype(h)::value;
+    if constexpr (I < LC) dma<16, H * kC + I * kW * 1024, H * kRow>(lc, oc[I], c_to);
+    else dma<16, H * kR + (I - LC) * kW * 1024, H * kRow>(lr, orr[I - LC], r_to);
   };
-  auto load_scales = [&](int turn) {
-    const uint32_t to = s_lds + turn * kScales;
-    const unsigned char* const c = lcs + lk * p.c_lines;
-    if (p.square) dma_word<1>(c, ocs, to);
-    else dma_word<TC>(c, ocs, to);
-    dma_word<TR>(lrs + lk * p.r_lines, ors, to + 4 * kLanes);
+  auto load_scales = [&]() {
+    dma<SQUARE ? 1 : TC, 0, 0>(lcs, ocs, s_to);
+    dma<TR, 4 * kLanes, 0>(lrs, ors, s_to);
   };
   auto loaded = [&]() {   // after a step's last load
+    c_to ^= 2 * kC;
+    r_to ^= 2 * kR;
+    s_to ^= kS;
     if (lleft > 1) {
       --lleft;
-      ++lk;
+      lc += kBlock;
+      lr += kBlock;
+      lcs += p.c_lines;
+      lrs += p.r_lines;
     } else if (ljob < job_end) {
       ljob += stride;
       start_load();
@@ -248,7 +250,7 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
   };
 
   // ---- fragments: a lane's 32 codes are chunks 2 (lane / 32) and the next of its row
-  uint32_t fc_at[2], fr_at[2];   // by chunk
+  uint32_t fc_at[2], fr_at[2], fs_at = s_lds + lane * 4;   // by chunk; of the step that is multiplied
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int i = lane % 32;
@@ -263,16 +265,16 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
     return i32x8_t{static_cast<int>(a[0]), static_cast<int>(a[1]), static_cast<int>(a[2]), static_cast<int>(a[3]),
                    static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]), static_cast<int>(b[3])};
   };
-  auto read_one = [&](int q, int h, int slot) {
-    if (q < TR) fr[h][q < TR ? q : 0] = frag(fr_at, slot * kR + (q < TR ? q : 0) * 32 * kRow);
-    else fc[h][q - TR < TC && q >= TR ? q - TR : 0] = frag(fc_at, slot * kC + (q - TR) * 32 * kRow);
+  auto read_one = [&](auto q, auto h) {   // fragment q of half h into set h
+    constexpr int Q = decltype(q)::value, H = decltype(h)::value;
+    if constexpr (Q < TR) fr[H][Q] = frag(fr_at, H * kR + Q * 32 * kRow);
+    else fc[H][Q - TR] = frag(fc_at, H * kC + (Q - TR) * 32 * kRow);
   };
   struct Scales {
     uint32_t c, r;
   };
-  auto read_scales = [&](int turn) {
-    const uint32_t at = s_lds + turn * kScales + lane * 4;
-    return Scales{lds_at<uint32_t>(at) * (p.square ? 0x01010101u : 1u), lds_at<uint32_t>(at + 4 * kLanes)};
+  auto read_scales = [&]() {
+    return Scales{lds_at<uint32_t>(fs_at) * (SQUARE ? 0x01010101u : 1u), lds_at<uint32_t>(fs_at + 4 * kLanes)};
   };
   auto multiply_row = [&](auto i, int h, const Scales& s) {
     constexpr int I = decltype(i)::value;
@@ -319,49 +321,60 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
     asm volatile("" ::: "memory");
     fence_schedule();
   };
+  using Zero = std::integral_constant<int, 0>;
   start_load();
-  Scales now{}, next{};
+  Scales now{};
   if (lleft > 0) {   // (no steps at all where k is empty: the tiles are then stored as zeros)
 #pragma unroll
     for (int turn = 0; turn < 2; ++turn) {
-      load_scales(turn);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int q = 0; q < LC + LR; ++q) load_one(q, h, turn);
+      load_scales();
+      unrolled<2>([&](auto h) { unrolled<LC + LR>([&](auto q) { load_one(q, h); }); });
       loaded();
     }
     turn_over();
-#pragma unroll
-    for (int q = 0; q < TC + TR; ++q) read_one(q, 0, 0);
-    now = read_scales(0);
+    unrolled<TC + TR>([&](auto q) { read_one(q, Zero{}); });
+    now = read_scales();
     turn_over();
   }
-  int turn = 0;   // parity of the step, counted over all tiles
   for (int job = job_first; job < job_end; job += stride) {
     const Job cur = job_at(job);
 #pragma unroll
     for (int i = 0; i < TC; ++i)
 #pragma unroll
       for (int j = 0; j < TR; ++j) acc[i][j] = f32x16_t{};
-    for (int s = 0; s < cur.steps; ++s, turn ^= 1) {
+    for (int s = 0; s < cur.steps; ++s) {
+      Scales next;
       fence_schedule();
+      unrolled<2>([&](auto h) {
+        constexpr int H = decltype(h)::value;
+        if constexpr (H == 0) {
+          load_scales();
+        } else {
+          // the next half is the next step's first
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (h == 0) load_scales(turn);
-        else next = read_scales(turn ^ 1);
+          for (int q = 0; q < 2; ++q) {
+            fc_at[q] ^= 2 * kC;
+            fr_at[q] ^= 2 * kR;
+          }
+          fs_at ^= kS;
+          next = read_scales();
+        }
         unrolled<TC>([&](auto i) {
-          multiply_row(i, h, now);
+          constexpr int I = decltype(i)::value;
+          multiply_row(i, H, now);
           fence_schedule();
-#pragma unroll
-          for (int q = i * kLoads; q < (i + 1) * kLoads && q < LC + LR; ++q) load_one(q, h, turn);
-#pragma unroll
-          for (int q = i * kReads; q < (i + 1) * kReads && q < TC + TR; ++q)
-            read_one(q, h ^ 1, h == 0 ? 2 * turn + 1 : 2 * (turn ^ 1));
+          unrolled<kLoads>([&](auto q) {
+            constexpr int Q = I * kLoads + decltype(q)::value;
+            if constexpr (Q < LC + LR) load_one(std::integral_constant<int, Q>{}, h);
+          });
+          unrolled<kReads>([&](auto q) {
+            constexpr int Q = I * kReads + decltype(q)::value;
+            if constexpr (Q < TC + TR) read_one(std::integral_constant<int, Q>{}, std::integral_constant<int, H ^ 1>{});
+          });
           fence_schedule();
         });
         turn_over();
-      }
+      });
       now = next;
       loaded();
     }
@@ -384,7 +397,10 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
     };
     if (cur.sum >= 0) {
       float* const to = p.sums + static_cast<int64_t>(cur.sum) * BR * BC;
-      each([&](int r, int c, float (&v)[8]) { store_row<8>(to + r * BC + c, v); });
+      const int64_t rows = p.rows - cur.r0;
+      each([&](int r, int c, float (&v)[8]) {
+        if (r < rows) store_row<8>(to + r * BC + c, v);
+      });
     } else {
       T* const to = static_cast<T*>(p.out) + cur.r0 * p.cols + cur.c0;
       const int64_t rows = p.rows - cur.r0, cols = p.cols - cur.c0;
@@ -461,8 +477,155 @@ template <int BC, int BR, typename T> __global__ __launch_bounds__(256) void sli
   }
 }
 
+// ------------------------------------------------------------------------------------------- few rows
+// For up to some hundred rows the time goes into C's bytes and into latency, not into multiplications.  A workgroup owns
+// a tile of 16 CT x 16 RT; its waves take k's blocks in turn, the operands straight from global memory (C's bytes serve
+// once, R's come from the L2), and their sums are added in LDS in the waves' order, a thread 8 neighbouring elements.  No
+// barrier and no wait for another wave before that.
+// As above, row i of tile t is row CT i + t of C's 16 CT and RT i + t of R's.
+// X: R's type, E4m3 or, for RT = 1, a plain one: a lane has a quarter of a row's block and rounds it itself, in each
+// workgroup again, which saves a launch and the way through memory.
+struct E4m3 {};
+
+template <int N> __device__ __forceinline__ uint32_t scales_at(const unsigned char* at) {
+  if constexpr (N == 4) return *reinterpret_cast<const uint32_t*>(at);
+  else if constexpr (N == 2) return *reinterpret_cast<const uint16_t*>(at);
+  else return *at;
+}
+// a lane's 32 codes of a row's block: 16 of either half, so that a load's four lanes of a row read 64 bytes on end (which k
+// a lane holds does not matter as long as both sides agree: the scales are the same for all of the block)
+__device__ __forceinline__ i32x8_t codes_at(const unsigned char* p) {
+  const u32x4_t a = *reinterpret_cast<const u32x4_t*>(p), b = *reinterpret_cast<const u32x4_t*>(p + 64);
+  return i32x8_t{static_cast<int>(a[0]), static_cast<int>(a[1]), static_cast<int>(a[2]), static_cast<int>(a[3]),
+                 static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]), static_cast<int>(b[3])};
+}
+
+template <int CT, int RT, int NW, typename X, typename T>
+__global__ __launch_bounds__(NW * 64) void few_product_kernel(Fp8Params p) {
+  constexpr bool kFine = std::is_same_v<T, float>, kPlain = !std::is_same_v<X, E4m3>;
+  static_assert(!kPlain || RT == 1, "plain rows are rounded by the lane that multiplies them");
+  constexpr int kC = 16 * CT, kR = 16 * RT, kPad = kC + 4;   // a row in LDS: off the banks of the next
+  constexpr int kDepth = CT + RT <= 4 ? 4 : 2;               // blocks on their way at a time
+  __shared__ __attribute__((aligned(16))) float sums[NW][kR][kPad];
+  const int lane = threadIdx.x % kLanes, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
+  const int i16 = lane % 16, part = lane / 16;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x % p.tiles_c) * kC, r0 = static_cast<int64_t>(blockIdx.x / p.tiles_c) * kR;
+  const unsigned char *ca[CT], *ra[RT];
+#pragma unroll
+  for (int t = 0; t < CT; ++t) {
+    const int64_t c = c0 + i16 * CT + t;
+    ca[t] = p.c + (c < p.cols ? c : p.cols - 1) * p.pitch + part * 16;
+  }
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int64_t r = r0 + i16 * RT + t, row = r < p.rows ? r : p.rows - 1;
+    ra[t] = p.r + (kPlain ? row * p.k * static_cast<int64_t>(sizeof(X)) : row * p.pitch + part * 16);
+  }
+  const int64_t cs = p.square ? c0 / kBlock : c0 + i16 * CT < p.c_lines - CT ? c0 + i16 * CT : p.c_lines - CT;
+  const int64_t rs = r0 + i16 * RT < p.r_lines - RT ? r0 + i16 * RT : p.r_lines - RT;
+  struct Step {
+    i32x8_t c[CT], r[RT];
+    uint32_t sc, sr;
+  };
+  auto load = [&](int s) {
+    Step v;
+#pragma unroll
+    for (int t = 0; t < CT; ++t) v.c[t] = codes_at(ca[t] + static_cast<int64_t>(s) * kBlock);
+    v.sc = p.square ? p.cs[s * p.c_lines + cs] * 0x01010101u : scales_at<CT>(p.cs + s * p.c_lines + cs);
+    if constexpr (kPlain) {
+      float top = 0.f, x[4][8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t at = static_cast<int64_t>(s) * kBlock + part * 16 + e / 2 * 64 + e % 2 * 8;
+        load_row<8>(reinterpret_cast<const X*>(ra[0]) + at, x[e], p.k - at);
+#pragma unroll
+        for (int f = 0; f < 8; ++f) top = __builtin_fmaxf(top, finite_abs(x[e][f]));
+      }
+      top = __builtin_fmaxf(top, __shfl_xor(top, 16, kLanes));
+      top = __builtin_fmaxf(top, __shfl_xor(top, 32, kLanes));
+      v.sr = fp8_scale(top);
+      const float inv = fp8_inverse(v.sr);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v.r[0][2 * e] = static_cast<int>(fp8_codes(x[e][0] * inv, x[e][1] * inv, x[e][2] * inv, x[e][3] * inv));
+        v.r[0][2 * e + 1] = static_cast<int>(fp8_codes(x[e][4] * inv, x[e][5] * inv, x[e][6] * inv, x[e][7] * inv));
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < RT; ++t) v.r[t] = codes_at(ra[t] + static_cast<int64_t>(s) * kBlock);
+      v.sr = scales_at<RT>(p.rs + s * p.r_lines + rs);
+    }
+    return v;
+  };
+  f32x4_t acc[CT][RT] = {};
+  auto multiply = [&](const Step& v) {
+    if constexpr (kFine) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        bf16x8_t b[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) b[r] = wide_codes(v.r[r], q, fp8_power((v.sr >> (8 * r)) & 255u));
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          const bf16x8_t a = wide_codes(v.c[c], q, fp8_power((v.sc >> (8 * c)) & 255u));
+#pragma unroll
+          for (int r = 0; r < RT; ++r) acc[c][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[r], acc[c][r], 0, 0, 0);
+        }
+      }
+    } else {
+      unrolled<CT>([&](auto c) {
+        unrolled<RT>([&](auto r) {
+          constexpr int C = decltype(c)::value, R = decltype(r)::value;
+          acc[C][R] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v.c[C], v.r[R], acc[C][R], 0, 0, C,
+                                                                       static_cast<int>(v.sc), R, static_cast<int>(v.sr));
+        });
+      });
+    }
+  };
+  // kDepth blocks are loaded together (past the last one: the last again) and then multiplied
+  for (int s = w; s < p.steps; s += NW * kDepth) {
+    Step v[kDepth];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      const int at = s + d * NW;
+      v[d] = load(at < p.steps ? at : p.steps - 1);
+    }
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d)
+      if (s + d * NW < p.steps) multiply(v[d]);
+  }
+  // accumulator e of tile (i, j): C's row CT (4 part + e) + i and R's row RT i16 + j
+#pragma unroll
+  for (int j = 0; j < RT; ++j)
+#pragma unroll
+    for (int q = 0; q < CT; ++q) {
+      f32x4_t v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = acc[(4 * q + e) % CT][j][(4 * q + e) / CT];
+      *reinterpret_cast<f32x4_t*>(&sums[w][i16 * RT + j][part * 4 * CT + 4 * q]) = v;
+    }
+  __syncthreads();
+  constexpr int kRuns = kC / 8;
+  for (int i = threadIdx.x; i < kR * kRuns; i += NW * kLanes) {
+    const int r = i / kRuns, c = i % kRuns * 8;
+    const int64_t row = r0 + r, left = p.cols - c0 - c;
+    if (row >= p.rows || left <= 0) continue;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = sums[0][r][c + e];
+#pragma unroll
+    for (int k = 1; k < NW; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += sums[k][r][c + e];
+    put(static_cast<T*>(p.out) + row * p.cols + c0 + c, v, left, p.accumulate);
+  }
+}
+
 // ---------------------------------------------------------------------------------------------- plan
+enum Kind { kLarge, kSmall, kFew64, kFew32, kFew16 };
+
 struct Tiling {
+  Kind kind;
   int bc, br;              // tile
   int grid;                // workgroups
   int64_t tiles;
@@ -472,8 +635,8 @@ struct Tiling {
 
 // Slices of the last, partial round: the least time, in steps of a workgroup.  A slice costs some four steps more (its
 // start, its sums' way out) and the addition some eight.  At most two rounds of slices, which bounds the sums' memory.
-Tiling tiling(const Fp8ProductArgs& a, int bc, int br, int grid, int64_t weight) {
-  Tiling t{bc, br, grid, 0, 0, 1, 0};
+Tiling tiling(const Fp8ProductArgs& a, Kind kind, int bc, int br, int grid, int64_t weight) {
+  Tiling t{kind, bc, br, grid, 0, 0, 1, 0};
   t.tiles = ((a.cols + bc - 1) / bc) * ((a.rows + br - 1) / br);
   const int64_t steps = fp8_blocks(a.k), rest = t.tiles % grid;
   int64_t best = rest > 0 ? steps : 0;
@@ -490,14 +653,24 @@ Tiling tiling(const Fp8ProductArgs& a, int bc, int br, int grid, int64_t weight)
 }
 
 constexpr int kCus = 256;
+Tiling few(const Fp8ProductArgs& a, Kind kind, int side) {
+  Tiling t{kind, side, side, 0, 0, 0, 1, 0};
+  t.tiles = ((a.cols + side - 1) / side) * ((a.rows + side - 1) / side);
+  t.grid = static_cast<int>(t.tiles);
+  return t;
+}
 // Tiles of 256 x 256, one workgroup to a CU, or of 128 x 128, two to a CU.
 Tiling pick(const Fp8ProductArgs& a) {
-  const Tiling small = tiling(a, 128, 128, 2 * kCus, 5);
-  const Tiling large = tiling(a, 256, 256, kCus, 8);
+  if (a.rows <= 16) return few(a, kFew16, 16);
+  const Tiling small = tiling(a, kSmall, 128, 128, 2 * kCus, 5);
+  if (!a.out_io) return small;
+  const Tiling large = tiling(a, kLarge, 256, 256, kCus, 8);
   return large.cost <= small.cost ? large : small;
 }
 
 }  // namespace
+
+bool fp8_product_takes_plain(const Fp8ProductArgs& a) { return pick(a).kind == kFew16; }
 
 size_t fp8_product_workspace_bytes(const Fp8ProductArgs& a) {
   if (a.rows == 0 || a.cols == 0) return 0;
@@ -510,29 +683,40 @@ hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream) {
   Fp8Params p{};
   p.r = static_cast<const unsigned char*>(a.r.codes); p.rs = static_cast<const unsigned char*>(a.r.scales);
   p.c = static_cast<const unsigned char*>(a.c.codes); p.cs = static_cast<const unsigned char*>(a.c.scales);
-  p.rows = a.rows; p.cols = a.cols; p.square = a.square;
+  p.rows = a.rows; p.cols = a.cols; p.k = a.k; p.square = a.square;
   p.steps = static_cast<int>(fp8_blocks(a.k)); p.pitch = fp8_blocks(a.k) * kBlock;
   p.r_lines = fp8_lines(a.rows); p.c_lines = a.square ? fp8_blocks(a.cols) : fp8_lines(a.cols);
   p.out = a.out; p.accumulate = a.accumulate;
   const Tiling t = pick(a);
   p.tiles_c = static_cast<int>((a.cols + t.bc - 1) / t.bc); p.tiles_r = static_cast<int>((a.rows + t.br - 1) / t.br);
   p.whole = t.whole; p.slices = t.slices; p.sums = static_cast<float*>(a.workspace);
-  const dim3 sum_grid(static_cast<unsigned>((t.tiles - t.whole) * kShares));
-  auto go = [&](auto bc, auto br, auto waves_c, auto waves_r, auto io) {
-    constexpr int kBC = decltype(bc)::value, kBR = decltype(br)::value;
-    constexpr int kWC = decltype(waves_c)::value, kWR = decltype(waves_r)::value;
-    using T = decltype(io);
-    tile_product_kernel<kBC, kBR, kWC, kWR, T><<<dim3(t.grid), kWC * kWR * kLanes, 0, stream>>>(p);
-    if (t.slices > 1) slices_kernel<kBC, kBR, T><<<sum_grid, 256, 0, stream>>>(p);
+  const dim3 grid(static_cast<unsigned>(t.grid)), sum_grid(static_cast<unsigned>((t.tiles - t.whole) * kShares));
+  auto go = [&](auto out) {
+    using T = decltype(out);
+    switch (t.kind) {
+      case kLarge:
+        if constexpr (std::is_same_v<T, uint16_t>) {
+          if (p.square) tile_product_kernel<256, 256, 2, 4, true, T><<<grid, 512, 0, stream>>>(p);
+          else tile_product_kernel<256, 256, 2, 4, false, T><<<grid, 512, 0, stream>>>(p);
+          if (t.slices > 1) slices_kernel<256, 256, T><<<sum_grid, 256, 0, stream>>>(p);
+        }
+        break;
+      case kSmall:
+        if (p.square) tile_product_kernel<128, 128, 2, 2, true, T><<<grid, 256, 0, stream>>>(p);
+        else tile_product_kernel<128, 128, 2, 2, false, T><<<grid, 256, 0, stream>>>(p);
+        if (t.slices > 1) slices_kernel<128, 128, T><<<sum_grid, 256, 0, stream>>>(p);
+        break;
+      case kFew64: few_product_kernel<4, 4, 4, E4m3, T><<<grid, 256, 0, stream>>>(p); break;
+      case kFew32: few_product_kernel<2, 2, 8, E4m3, T><<<grid, 512, 0, stream>>>(p); break;
+      case kFew16:
+        if (a.r.scales != nullptr) few_product_kernel<1, 1, 8, E4m3, T><<<grid, 512, 0, stream>>>(p);
+        else if (a.r_io) few_product_kernel<1, 1, 8, uint16_t, T><<<grid, 512, 0, stream>>>(p);
+        else few_product_kernel<1, 1, 8, float, T><<<grid, 512, 0, stream>>>(p);
+        break;
+    }
   };
-  using Two = std::integral_constant<int, 2>;
-  using Four = std::integral_constant<int, 4>;
-  using Small = std::integral_constant<int, 128>;
-  using Large = std::integral_constant<int, 256>;
-  if (t.bc == 256 && a.out_io) go(Large{}, Large{}, Two{}, Four{}, uint16_t{});
-  else if (t.bc == 256) go(Large{}, Large{}, Two{}, Four{}, float{});
-  else if (a.out_io) go(Small{}, Small{}, Two{}, Two{}, uint16_t{});
-  else go(Small{}, Small{}, Two{}, Two{}, float{});
+  if (a.out_io) go(uint16_t{});
+  else go(float{});
   return hipGetLastError();
 }
 

@@ -267,7 +267,8 @@ hipError_t fp8_dequantize_launch(const Fp8Args& a, hipStream_t stream);
 // out[r, c] (+)= sum over k of R[r, k] C[c, k]
 struct Fp8ProductArgs {
   int64_t rows, cols, k;
-  Fp8View r;             // row scales
+  Fp8View r;             // row scales; a plain matrix (r_io: 0 fp32, 1 bf16) without scales where that is taken
+  int r_io;
   Fp8View c;
   int square;            // C's scales
   void* out;             // [rows, cols]
@@ -276,6 +277,8 @@ struct Fp8ProductArgs {
   void* workspace;
 };
 
+// whether R may be a plain matrix, which is then rounded on the way (the sizes and out_io decide)
+bool fp8_product_takes_plain(const Fp8ProductArgs& a);
 size_t fp8_product_workspace_bytes(const Fp8ProductArgs& a);
 hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream);
 

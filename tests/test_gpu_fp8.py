@@ -492,6 +492,8 @@ def test_refusals(M):
     x = torch.randn(6, 200).cuda()
     w = M.fp8_quantize(torch.randn(70, 200).cuda(), square=True)
     q = M.fp8_quantize(x)
+    many = torch.randn(300, 200).cuda()      # (a few plain rows need no workspace)
+    assert M.fp8_linear_fwd_workspace_size(300, 200, 70, M.MSSM_F32) > 256
     d = torch.randn(6, 70).cuda()
     wt = M.fp8_quantize(torch.randn(200, 70).cuda(), square=True)
     for call in (lambda: M.fp8_quantize(x.half()), lambda: M.fp8_dequantize(q, torch.float16),
@@ -515,10 +517,10 @@ def test_refusals(M):
                  lambda: M.fp8_linear_bwd(q, wt, d, want_dx=False, want_dweight=False),
                  lambda: M.fp8_quantize(torch.zeros(0, 5).cuda(), transposed=True),
                  lambda: M.rms_norm_fp8_fwd(x, torch.ones(200).cuda(), out=w),
-                 lambda: M.fp8_linear_fwd(x, w, workspace=torch.zeros(4096, dtype=torch.uint8))):
+                 lambda: M.fp8_linear_fwd(many, w, workspace=torch.zeros(1 << 20, dtype=torch.uint8))):
         with pytest.raises(ValueError):
             call()
     with pytest.raises(M.MssmError):
-        M.fp8_linear_fwd(x, w, workspace=torch.zeros(256, dtype=torch.uint8).cuda())
+        M.fp8_linear_fwd(many, w, workspace=torch.zeros(256, dtype=torch.uint8).cuda())
     with pytest.raises(M.MssmError):
         M.fp8_quantize(x, out=M.Fp8Matrix(x.view(torch.float8_e4m3fn).reshape(-1)[:1536].view(6, 256), q.scales, 200))
