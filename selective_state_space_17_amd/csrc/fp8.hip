@@ -1,7 +1,7 @@
 // Matrices kept in 8 bits with a power of two for each block of 128 (fp8_util.h): rounded from fp32 or bf16, in either
 // order or both from one read; laid out the other way from 8 bits; read back.
 //
-// A workgroup takes tiles of 128 x 128, so that a tile is one block along either axis: a thread holds 8 rows x 8
+// A workgroup takes tiles of 128 x 128, so that a tile is one block along either axis: a thread holds 4 rows x 8
 // columns in registers, finds the largest magnitudes of its rows (over 16 lanes) and of its columns (over the
 // workgroup), and rounds with either; the transposed codes change places in LDS.  Bound by memory: each input is read
 // once and each output written once.
@@ -28,67 +28,97 @@ struct TileParams {
 };
 
 constexpr int kThreads = 256;
+constexpr int kTileThreads = 512;
+constexpr int kHigh = 4;   // rows of a thread
 struct E4m3 {};   // the type of inputs that are in 8 bits
 
-template <typename T, bool SQUARE> __global__ __launch_bounds__(kThreads) void tile_kernel(TileParams p) {
-  __shared__ float tops[4][kBlock];
-  __shared__ __attribute__((aligned(16))) uint64_t turned[kBlock][16];   // [column][8 rows], its place xor-ed with the chunk
+template <typename T, bool SQUARE> __global__ __launch_bounds__(kTileThreads, 4) void tile_kernel(TileParams p) {
+  constexpr int kWaves = kTileThreads / kLanes;
+  __shared__ __attribute__((aligned(16))) uint32_t tops[kWaves][kBlock];
+  __shared__ __attribute__((aligned(16))) uint32_t turned[kBlock][kBlock / kHigh];   // [column][4 rows], the place xor-ed
   const int chunk = threadIdx.x % 16, rg = threadIdx.x / 16;
   const int wave = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
   const int64_t pitch = static_cast<int64_t>(p.tiles_c) * kBlock;            // of the codes
   const int64_t tiles_r = fp8_blocks(p.rows), pitch_t = tiles_r * kBlock;    // of the transposed ones
   const int64_t lines = fp8_lines(p.rows), lines_t = fp8_lines(p.cols);
   for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
-    const int64_t tr = tile / p.tiles_c, r0 = tr * kBlock + rg * 8;
+    const int64_t tr = tile / p.tiles_c, r0 = tr * kBlock + rg * kHigh;
     const int tc = static_cast<int>(tile - tr * p.tiles_c), c0 = tc * kBlock + chunk * 8;
-    float v[8][8];
+    float v[kHigh][8];
+    if constexpr (std::is_same_v<T, E4m3>) {
+      u32x2_t q[kHigh];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t r = r0 + i;
-      if constexpr (std::is_same_v<T, E4m3>) {
-        u32x2_t q = {0, 0};
-        float s = 1.f;
-        if (r < p.rows) {
-          q = *reinterpret_cast<const u32x2_t*>(static_cast<const unsigned char*>(p.x) + r * pitch + c0);
-          s = fp8_power(p.x_scales[tc * lines + r]);
-        }
+      for (int i = 0; i < kHigh; ++i)
+        q[i] = r0 + i < p.rows
+                   ? *reinterpret_cast<const u32x2_t*>(static_cast<const unsigned char*>(p.x) + (r0 + i) * pitch + c0)
+                   : u32x2_t{0, 0};
+      const uint32_t s = r0 < lines ? *reinterpret_cast<const uint32_t*>(p.x_scales + tc * lines + r0) : 0;
+#pragma unroll
+      for (int i = 0; i < kHigh; ++i) {
+        const float power = r0 + i < p.rows ? fp8_power((s >> (8 * i)) & 255u) : 0.f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float f[4];
-          fp8_values(q[h], f);
+          fp8_values(q[i][h], f);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[i][4 * h + e] = f[e] * s;
+          for (int e = 0; e < 4; ++e) v[i][4 * h + e] = f[e] * power;
         }
-      } else {
-        load_row<8>(static_cast<const T*>(p.x) + r * p.cols + c0, v[i], r < p.rows ? p.cols - c0 : 0);
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kHigh; ++i)
+        load_row<8>(static_cast<const T*>(p.x) + (r0 + i) * p.cols + c0, v[i], r0 + i < p.rows ? p.cols - c0 : 0);
     }
-    float col_top[8];
-    if (SQUARE || p.codes_t != nullptr) {
+    // largest magnitudes of this thread's part of its rows and columns
+    uint32_t row_top[kHigh] = {}, col_top[8] = {}, most = 0;
+#pragma unroll
+    for (int i = 0; i < kHigh; ++i) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float t = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t = __builtin_fmaxf(t, finite_abs(v[i][j]));
-        t = __builtin_fmaxf(t, __shfl_xor(t, 16, kLanes));
-        col_top[j] = __builtin_fmaxf(t, __shfl_xor(t, 32, kLanes));
+        const uint32_t m = magnitude(v[i][j]);
+        row_top[i] = larger(row_top[i], m);
+        col_top[j] = larger(col_top[j], m);
       }
+      most = larger(most, row_top[i]);
+    }
+    if (most >= kInfinite) {
+#pragma unroll
+      for (int i = 0; i < kHigh; ++i) row_top[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) col_top[j] = 0;
+#pragma unroll
+      for (int i = 0; i < kHigh; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          row_top[i] = larger(row_top[i], finite_magnitude(v[i][j]));
+          col_top[j] = larger(col_top[j], finite_magnitude(v[i][j]));
+        }
+    }
+    if (SQUARE || p.codes_t != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) col_top[j] = column4_max(col_top[j]);
       __syncthreads();   // (the tile before may still be read)
       if (lane < 16) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) tops[wave][chunk * 8 + j] = col_top[j];
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<u32x4_t*>(&tops[wave][chunk * 8 + 4 * h]) =
+              u32x4_t{col_top[4 * h], col_top[4 * h + 1], col_top[4 * h + 2], col_top[4 * h + 3]};
       }
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int w = 0; w < kWaves; ++w)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) col_top[j] = __builtin_fmaxf(col_top[j], tops[w][chunk * 8 + j]);
+        for (int h = 0; h < 2; ++h) {
+          const u32x4_t t = *reinterpret_cast<const u32x4_t*>(&tops[w][chunk * 8 + 4 * h]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) col_top[4 * h + e] = larger(col_top[4 * h + e], t[e]);
+        }
     }
     uint32_t all = 0;
     if constexpr (SQUARE) {
-      float t = 0.f;
+      uint32_t t = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t = __builtin_fmaxf(t, col_top[j]);
+      for (int j = 0; j < 8; ++j) t = larger(t, col_top[j]);
       all = fp8_scale(row16_max(t));
       if (threadIdx.x == 0) {
         if (p.codes != nullptr) p.scales[tc * tiles_r + tr] = static_cast<unsigned char>(all);
@@ -96,42 +126,39 @@ template <typename T, bool SQUARE> __global__ __launch_bounds__(kThreads) void t
       }
     }
     if (p.codes != nullptr) {
+      uint32_t word = 0;   // the scales of the four rows (1 for the rows that pad the lines)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t r = r0 + i;
-        u32x2_t q;
-        if constexpr (SQUARE) {
-          const float s = fp8_inverse(all);
-          q = u32x2_t{fp8_codes(v[i][0] * s, v[i][1] * s, v[i][2] * s, v[i][3] * s),
-                      fp8_codes(v[i][4] * s, v[i][5] * s, v[i][6] * s, v[i][7] * s)};
-        } else {
-          uint32_t scale;
-          q = fp8_block_codes(v[i], scale);   // (1 for the rows that pad the scales' lines)
-          if (chunk == 0 && r < lines) p.scales[tc * lines + r] = static_cast<unsigned char>(scale);
-        }
-        if (r < p.rows) *reinterpret_cast<u32x2_t*>(p.codes + r * pitch + c0) = q;
+      for (int i = 0; i < kHigh; ++i) {
+        const uint32_t scale = SQUARE ? all : fp8_scale(row16_max(row_top[i]));
+        word |= scale << (8 * i);
+        if (r0 + i < p.rows)
+          *reinterpret_cast<u32x2_t*>(p.codes + (r0 + i) * pitch + c0) =
+              u32x2_t{fp8_codes(v[i][0], v[i][1], v[i][2], v[i][3], scale),
+                      fp8_codes(v[i][4], v[i][5], v[i][6], v[i][7], scale)};
       }
+      if (!SQUARE && chunk == 0 && r0 < lines) *reinterpret_cast<uint32_t*>(p.scales + tc * lines + r0) = word;
     }
     if (p.codes_t != nullptr) {
+      uint32_t word[2] = {0, 0};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t scale = SQUARE ? all : fp8_scale(col_top[j]);
-        const float s = fp8_inverse(scale);
-        const int64_t c = c0 + j;
-        if (!SQUARE && rg == 0 && c < lines_t) p.scales_t[tr * lines_t + c] = static_cast<unsigned char>(scale);
-        const uint64_t lo = fp8_codes(v[0][j] * s, v[1][j] * s, v[2][j] * s, v[3][j] * s);
-        const uint64_t hi = fp8_codes(v[4][j] * s, v[5][j] * s, v[6][j] * s, v[7][j] * s);
-        turned[chunk * 8 + j][rg ^ chunk] = lo | hi << 32;
+        word[j / 4] |= scale << (8 * (j % 4));
+        // (a place is 4 rows, and the ways of 16 lanes differ in their chunk's low three bits)
+        turned[chunk * 8 + j][rg ^ (chunk % 8 * 4)] = fp8_codes(v[0][j], v[1][j], v[2][j], v[3][j], scale);
+      }
+      if (!SQUARE && rg == 0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (c0 + 4 * h < lines_t) *reinterpret_cast<uint32_t*>(p.scales_t + tr * lines_t + c0 + 4 * h) = word[h];
       }
       __syncthreads();
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c = k * 32 + threadIdx.x / 8, pair = threadIdx.x % 8 * 2;
-        const uint64_t a = turned[c][pair ^ (c / 8)], b = turned[c][(pair + 1) ^ (c / 8)];
+      for (int k = 0; k < 2; ++k) {
+        const int c = k * 64 + threadIdx.x / 8, at = threadIdx.x % 8 * 4;
+        const u32x4_t q = *reinterpret_cast<const u32x4_t*>(&turned[c][at ^ (c / 8 % 8 * 4)]);
         if (tc * kBlock + c < p.cols)
-          *reinterpret_cast<u32x4_t*>(p.codes_t + (tc * static_cast<int64_t>(kBlock) + c) * pitch_t + tr * kBlock + pair * 8) =
-              u32x4_t{static_cast<uint32_t>(a), static_cast<uint32_t>(a >> 32), static_cast<uint32_t>(b),
-                      static_cast<uint32_t>(b >> 32)};
+          *reinterpret_cast<u32x4_t*>(p.codes_t + (tc * static_cast<int64_t>(kBlock) + c) * pitch_t + tr * kBlock + at * 4) = q;
       }
     }
   }
@@ -183,7 +210,7 @@ hipError_t fp8_quantize_launch(const Fp8Args& a, hipStream_t stream) {
   TileParams p = tile_params(a);
   p.x = a.x;
   p.codes = static_cast<unsigned char*>(a.m.codes); p.scales = static_cast<unsigned char*>(a.m.scales);
-  auto go = [&](auto kernel) { kernel<<<dim3(grid(p.tiles)), kThreads, 0, stream>>>(p); };
+  auto go = [&](auto kernel) { kernel<<<dim3(grid(p.tiles)), kTileThreads, 0, stream>>>(p); };
   if (a.io) go(a.square ? tile_kernel<uint16_t, true> : tile_kernel<uint16_t, false>);
   else go(a.square ? tile_kernel<float, true> : tile_kernel<float, false>);
   return hipGetLastError();
@@ -193,7 +220,7 @@ hipError_t fp8_transpose_launch(const Fp8Args& a, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
   TileParams p = tile_params(a);
   p.x = a.m.codes; p.x_scales = static_cast<const unsigned char*>(a.m.scales);
-  tile_kernel<E4m3, false><<<dim3(grid(p.tiles)), kThreads, 0, stream>>>(p);
+  tile_kernel<E4m3, false><<<dim3(grid(p.tiles)), kTileThreads, 0, stream>>>(p);
   return hipGetLastError();
 }
 

@@ -483,8 +483,8 @@ template <int BC, int BR, typename T> __global__ __launch_bounds__(256) void sli
 // once, R's come from the L2), and their sums are added in LDS in the waves' order, a thread 8 neighbouring elements.  No
 // barrier and no wait for another wave before that.
 // As above, row i of tile t is row CT i + t of C's 16 CT and RT i + t of R's.
-// X: R's type, E4m3 or, for RT = 1, a plain one: a lane has a quarter of a row's block and rounds it itself, in each
-// workgroup again, which saves a launch and the way through memory.
+// X: R's type, E4m3 or a plain one for up to 16 rows that fit into LDS in 8 bits: each workgroup rounds them again while
+// its first loads of C are on their way, which saves a launch (1 x 2560 x 10240: TODO).
 struct E4m3 {};
 
 template <int N> __device__ __forceinline__ uint32_t scales_at(const unsigned char* at) {
@@ -501,12 +501,13 @@ __device__ __forceinline__ i32x8_t codes_at(const unsigned char* p) {
 }
 
 template <int CT, int RT, int NW, typename X, typename T>
-__global__ __launch_bounds__(NW * 64) void few_product_kernel(Fp8Params p) {
+__global__ __launch_bounds__(NW * 64, CT * RT == 1 ? 4 : 2) void few_product_kernel(Fp8Params p) {
   constexpr bool kFine = std::is_same_v<T, float>, kPlain = !std::is_same_v<X, E4m3>;
-  static_assert(!kPlain || RT == 1, "plain rows are rounded by the lane that multiplies them");
+  static_assert(!kPlain || RT == 1, "up to 16 plain rows");
   constexpr int kC = 16 * CT, kR = 16 * RT, kPad = kC + 4;   // a row in LDS: off the banks of the next
-  constexpr int kDepth = CT + RT <= 4 ? 4 : 2;               // blocks on their way at a time
+  constexpr int kDepth = CT + RT <= 4 ? 4 : 2;    // blocks on their way at a time
   __shared__ __attribute__((aligned(16))) float sums[NW][kR][kPad];
+  extern __shared__ __attribute__((aligned(16))) unsigned char plain[];   // [rows][pitch + 16], [rows][blocks] scales
   const int lane = threadIdx.x % kLanes, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
   const int i16 = lane % 16, part = lane / 16;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x % p.tiles_c) * kC, r0 = static_cast<int64_t>(blockIdx.x / p.tiles_c) * kR;
@@ -519,7 +520,7 @@ __global__ __launch_bounds__(NW * 64) void few_product_kernel(Fp8Params p) {
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const int64_t r = r0 + i16 * RT + t, row = r < p.rows ? r : p.rows - 1;
-    ra[t] = p.r + (kPlain ? row * p.k * static_cast<int64_t>(sizeof(X)) : row * p.pitch + part * 16);
+    ra[t] = kPlain ? plain + row * (p.pitch + 16) + part * 16 : p.r + row * p.pitch + part * 16;
   }
   const int64_t cs = p.square ? c0 / kBlock : c0 + i16 * CT < p.c_lines - CT ? c0 + i16 * CT : p.c_lines - CT;
   const int64_t rs = r0 + i16 * RT < p.r_lines - RT ? r0 + i16 * RT : p.r_lines - RT;
@@ -527,35 +528,16 @@ __global__ __launch_bounds__(NW * 64) void few_product_kernel(Fp8Params p) {
     i32x8_t c[CT], r[RT];
     uint32_t sc, sr;
   };
-  auto load = [&](int s) {
-    Step v;
+  auto load_c = [&](int s, Step& v) {
 #pragma unroll
     for (int t = 0; t < CT; ++t) v.c[t] = codes_at(ca[t] + static_cast<int64_t>(s) * kBlock);
     v.sc = p.square ? p.cs[s * p.c_lines + cs] * 0x01010101u : scales_at<CT>(p.cs + s * p.c_lines + cs);
-    if constexpr (kPlain) {
-      float top = 0.f, x[4][8];
+  };
+  auto load_r = [&](int s, Step& v) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t at = static_cast<int64_t>(s) * kBlock + part * 16 + e / 2 * 64 + e % 2 * 8;
-        load_row<8>(reinterpret_cast<const X*>(ra[0]) + at, x[e], p.k - at);
-#pragma unroll
-        for (int f = 0; f < 8; ++f) top = __builtin_fmaxf(top, finite_abs(x[e][f]));
-      }
-      top = __builtin_fmaxf(top, __shfl_xor(top, 16, kLanes));
-      top = __builtin_fmaxf(top, __shfl_xor(top, 32, kLanes));
-      v.sr = fp8_scale(top);
-      const float inv = fp8_inverse(v.sr);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v.r[0][2 * e] = static_cast<int>(fp8_codes(x[e][0] * inv, x[e][1] * inv, x[e][2] * inv, x[e][3] * inv));
-        v.r[0][2 * e + 1] = static_cast<int>(fp8_codes(x[e][4] * inv, x[e][5] * inv, x[e][6] * inv, x[e][7] * inv));
-      }
-    } else {
-#pragma unroll
-      for (int t = 0; t < RT; ++t) v.r[t] = codes_at(ra[t] + static_cast<int64_t>(s) * kBlock);
-      v.sr = scales_at<RT>(p.rs + s * p.r_lines + rs);
-    }
-    return v;
+    for (int t = 0; t < RT; ++t) v.r[t] = codes_at(ra[t] + static_cast<int64_t>(s) * kBlock);
+    if constexpr (kPlain) v.sr = plain[p.rows * (p.pitch + 16) + (i16 < p.rows ? i16 : p.rows - 1) * p.steps + s];
+    else v.sr = scales_at<RT>(p.rs + s * p.r_lines + rs);
   };
   f32x4_t acc[CT][RT] = {};
   auto multiply = [&](const Step& v) {
@@ -583,13 +565,28 @@ __global__ __launch_bounds__(NW * 64) void few_product_kernel(Fp8Params p) {
     }
   };
   // kDepth blocks are loaded together (past the last one: the last again) and then multiplied
-  for (int s = w; s < p.steps; s += NW * kDepth) {
-    Step v[kDepth];
+  Step v[kDepth];
+  auto load = [&](int s) {
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-      const int at = s + d * NW;
-      v[d] = load(at < p.steps ? at : p.steps - 1);
+    for (int d = 0; d < kDepth; ++d) load_c(s + d * NW < p.steps ? s + d * NW : p.steps - 1, v[d]);
+  };
+  if (p.steps > 0) load(w < p.steps ? w : p.steps - 1);
+  if constexpr (kPlain) {
+    const int work = static_cast<int>(p.rows) * p.steps;
+    for (int i = threadIdx.x / 16; i < work; i += NW * 4) {   // 16 lanes a block
+      const int r = i / p.steps, b = i - r * p.steps, at = b * kBlock + i16 * 8;
+      float x[8];
+      load_row<8>(reinterpret_cast<const X*>(p.r) + r * p.k + at, x, p.k - at);
+      uint32_t scale;
+      *reinterpret_cast<u32x2_t*>(plain + r * (p.pitch + 16) + at) = fp8_block_codes(x, scale);
+      if (i16 == 0) plain[p.rows * (p.pitch + 16) + i] = static_cast<unsigned char>(scale);
     }
+    __syncthreads();
+  }
+  for (int s = w; s < p.steps; s += NW * kDepth) {
+    if (s != w) load(s);
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) load_r(s + d * NW < p.steps ? s + d * NW : p.steps - 1, v[d]);
 #pragma unroll
     for (int d = 0; d < kDepth; ++d)
       if (s + d * NW < p.steps) multiply(v[d]);
@@ -670,7 +667,11 @@ Tiling pick(const Fp8ProductArgs& a) {
 
 }  // namespace
 
-bool fp8_product_takes_plain(const Fp8ProductArgs& a) { return pick(a).kind == kFew16; }
+// LDS that plain rows take in 8 bits, and how much of it leaves room for four workgroups on a CU
+int64_t plain_bytes(const Fp8ProductArgs& a) { return a.rows * (fp8_blocks(a.k) * (kBlock + 1) + 16); }
+constexpr int64_t kMostPlain = 24 << 10;
+
+bool fp8_product_takes_plain(const Fp8ProductArgs& a) { return pick(a).kind == kFew16 && plain_bytes(a) <= kMostPlain; }
 
 size_t fp8_product_workspace_bytes(const Fp8ProductArgs& a) {
   if (a.rows == 0 || a.cols == 0) return 0;
@@ -710,8 +711,8 @@ hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream) {
       case kFew32: few_product_kernel<2, 2, 8, E4m3, T><<<grid, 512, 0, stream>>>(p); break;
       case kFew16:
         if (a.r.scales != nullptr) few_product_kernel<1, 1, 8, E4m3, T><<<grid, 512, 0, stream>>>(p);
-        else if (a.r_io) few_product_kernel<1, 1, 8, uint16_t, T><<<grid, 512, 0, stream>>>(p);
-        else few_product_kernel<1, 1, 8, float, T><<<grid, 512, 0, stream>>>(p);
+        else if (a.r_io) few_product_kernel<1, 1, 8, uint16_t, T><<<grid, 512, plain_bytes(a), stream>>>(p);
+        else few_product_kernel<1, 1, 8, float, T><<<grid, 512, plain_bytes(a), stream>>>(p);
         break;
     }
   };
