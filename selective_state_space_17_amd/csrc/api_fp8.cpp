@@ -245,9 +245,11 @@ int mssm_fp8_linear_bwd(const mssm_fp8_linear_desc* desc, const void* x, const v
                       {workspace, static_cast<int64_t>(b.bytes)}};
   if (!disjoint(in, outs)) return MSSM_ERR_INVALID_ARG;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  mssm::Fp8Args q{};
+  mssm::Fp8Args q{}, t{};
   q.rows = d.tokens; q.cols = d.out_features; q.io = d.io_dtype; q.x = dout; q.m = b.dout; q.t = b.dout_t;
-  int e = done(mssm::fp8_quantize_launch(q, s));
+  t.rows = d.tokens; t.cols = d.in_features;
+  t.m = {const_cast<void*>(x), const_cast<void*>(x_scales)}; t.t = b.x_t;
+  int e = done(dweight != nullptr ? mssm::fp8_both_launch(q, t, s) : mssm::fp8_quantize_launch(q, s));
   if (e == MSSM_OK && dx != nullptr) {
     b.dx.r = b.dout;
     b.dx.c = {const_cast<void*>(weight_t), const_cast<void*>(weight_t_scales)};
@@ -255,11 +257,6 @@ int mssm_fp8_linear_bwd(const mssm_fp8_linear_desc* desc, const void* x, const v
     e = done(mssm::fp8_product_launch(b.dx, s));
   }
   if (e == MSSM_OK && dweight != nullptr) {
-    mssm::Fp8Args t{};
-    t.rows = d.tokens; t.cols = d.in_features;
-    t.m = {const_cast<void*>(x), const_cast<void*>(x_scales)}; t.t = b.x_t;
-    e = done(mssm::fp8_transpose_launch(t, s));
-    if (e != MSSM_OK) return e;
     b.dw.r = b.dout_t; b.dw.c = b.x_t; b.dw.out = dweight; b.dw.accumulate = accumulate != 0;
     e = done(mssm::fp8_product_launch(b.dw, s));
   }

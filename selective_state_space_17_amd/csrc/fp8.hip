@@ -32,16 +32,23 @@ constexpr int kTileThreads = 512;
 constexpr int kHigh = 4;   // rows of a thread
 struct E4m3 {};   // the type of inputs that are in 8 bits
 
-template <typename T, bool SQUARE> __global__ __launch_bounds__(kTileThreads, 4) void tile_kernel(TileParams p) {
+struct TileShared {
+  uint32_t tops[kTileThreads / kLanes][kBlock];
+  uint32_t turned[kBlock][kBlock / kHigh];   // [column][4 rows], the place xor-ed
+};
+
+// workgroup `group` of `groups`
+template <typename T, bool SQUARE>
+__device__ __forceinline__ void tiles(const TileParams& p, int64_t group, int64_t groups, TileShared& shared) {
   constexpr int kWaves = kTileThreads / kLanes;
-  __shared__ __attribute__((aligned(16))) uint32_t tops[kWaves][kBlock];
-  __shared__ __attribute__((aligned(16))) uint32_t turned[kBlock][kBlock / kHigh];   // [column][4 rows], the place xor-ed
+  auto& tops = shared.tops;
+  auto& turned = shared.turned;
   const int chunk = threadIdx.x % 16, rg = threadIdx.x / 16;
   const int wave = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
   const int64_t pitch = static_cast<int64_t>(p.tiles_c) * kBlock;            // of the codes
   const int64_t tiles_r = fp8_blocks(p.rows), pitch_t = tiles_r * kBlock;    // of the transposed ones
   const int64_t lines = fp8_lines(p.rows), lines_t = fp8_lines(p.cols);
-  for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+  for (int64_t tile = group; tile < p.tiles; tile += groups) {
     const int64_t tr = tile / p.tiles_c, r0 = tr * kBlock + rg * kHigh;
     const int tc = static_cast<int>(tile - tr * p.tiles_c), c0 = tc * kBlock + chunk * 8;
     float v[kHigh][8];
@@ -164,6 +171,19 @@ template <typename T, bool SQUARE> __global__ __launch_bounds__(kTileThreads, 4)
   }
 }
 
+template <typename T, bool SQUARE> __global__ __launch_bounds__(kTileThreads, 4) void tile_kernel(TileParams p) {
+  __shared__ __attribute__((aligned(16))) TileShared shared;
+  tiles<T, SQUARE>(p, blockIdx.x, gridDim.x, shared);
+}
+
+// a plain matrix and one in 8 bits side by side: the first `split` workgroups have the plain one
+template <typename T>
+__global__ __launch_bounds__(kTileThreads, 4) void two_kernel(TileParams plain, TileParams packed, unsigned split) {
+  __shared__ __attribute__((aligned(16))) TileShared shared;
+  if (blockIdx.x < split) tiles<T, false>(plain, blockIdx.x, split, shared);
+  else tiles<E4m3, false>(packed, blockIdx.x - split, gridDim.x - split, shared);
+}
+
 // values back from 8 bits, 8 a thread
 struct BackParams {
   int64_t rows, cols, chunks;    // chunks of 8 columns, rows x (cols / 8 rounded up)
@@ -205,11 +225,23 @@ TileParams tile_params(const Fp8Args& a) {
 
 }  // namespace
 
-hipError_t fp8_quantize_launch(const Fp8Args& a, hipStream_t stream) {
-  if (a.rows == 0) return hipSuccess;
+namespace {
+TileParams quantize_params(const Fp8Args& a) {
   TileParams p = tile_params(a);
   p.x = a.x;
   p.codes = static_cast<unsigned char*>(a.m.codes); p.scales = static_cast<unsigned char*>(a.m.scales);
+  return p;
+}
+TileParams transpose_params(const Fp8Args& a) {
+  TileParams p = tile_params(a);
+  p.x = a.m.codes; p.x_scales = static_cast<const unsigned char*>(a.m.scales);
+  return p;
+}
+}  // namespace
+
+hipError_t fp8_quantize_launch(const Fp8Args& a, hipStream_t stream) {
+  if (a.rows == 0) return hipSuccess;
+  const TileParams p = quantize_params(a);
   auto go = [&](auto kernel) { kernel<<<dim3(grid(p.tiles)), kTileThreads, 0, stream>>>(p); };
   if (a.io) go(a.square ? tile_kernel<uint16_t, true> : tile_kernel<uint16_t, false>);
   else go(a.square ? tile_kernel<float, true> : tile_kernel<float, false>);
@@ -218,9 +250,17 @@ hipError_t fp8_quantize_launch(const Fp8Args& a, hipStream_t stream) {
 
 hipError_t fp8_transpose_launch(const Fp8Args& a, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
-  TileParams p = tile_params(a);
-  p.x = a.m.codes; p.x_scales = static_cast<const unsigned char*>(a.m.scales);
+  const TileParams p = transpose_params(a);
   tile_kernel<E4m3, false><<<dim3(grid(p.tiles)), kTileThreads, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+hipError_t fp8_both_launch(const Fp8Args& plain, const Fp8Args& packed, hipStream_t stream) {
+  if (plain.rows == 0) return hipSuccess;
+  const TileParams a = quantize_params(plain), b = transpose_params(packed);
+  const unsigned split = grid(a.tiles), all = split + grid(b.tiles);
+  if (plain.io) two_kernel<uint16_t><<<dim3(all), kTileThreads, 0, stream>>>(a, b, split);
+  else two_kernel<float><<<dim3(all), kTileThreads, 0, stream>>>(a, b, split);
   return hipGetLastError();
 }
 

@@ -619,7 +619,7 @@ __global__ __launch_bounds__(NW * 64, CT * RT == 1 ? 4 : 2) void few_product_ker
 }
 
 // ---------------------------------------------------------------------------------------------- plan
-enum Kind { kLarge, kSmall, kFew64, kFew32, kFew16 };
+enum Kind { kLarge, kSmall, kFew64, kFew16 };
 
 struct Tiling {
   Kind kind;
@@ -627,42 +627,61 @@ struct Tiling {
   int grid;                // workgroups
   int64_t tiles;
   int whole, slices;
-  int64_t cost;
+  int64_t cost;            // nanoseconds, as the measurements below have it
 };
 
-// Slices of the last, partial round: the least time, in steps of a workgroup.  A slice costs some four steps more (its
-// start, its sums' way out) and the addition some eight.  At most two rounds of slices, which bounds the sums' memory.
-Tiling tiling(const Fp8ProductArgs& a, Kind kind, int bc, int br, int grid, int64_t weight) {
-  Tiling t{kind, bc, br, grid, 0, 0, 1, 0};
-  t.tiles = ((a.cols + bc - 1) / bc) * ((a.rows + br - 1) / br);
-  const int64_t steps = fp8_blocks(a.k), rest = t.tiles % grid;
-  int64_t best = rest > 0 ? steps : 0;
-  for (int64_t s = 2; rest > 0 && rest * s <= 2 * grid && steps / s >= 4; ++s) {
-    const int64_t time = (rest * s + grid - 1) / grid * ((steps + s - 1) / s + 4) + 8;
-    if (time < best) {
+constexpr int kCus = 256;
+constexpr int kMostSlices = 32;
+
+// Tiles on workgroups that stay.  one, two: nanoseconds of a step with one and with two workgroups on a CU; round: of a
+// tile's way out.  Slices of the last, partial round: those that take the least time, with 3 us for the second launch and
+// the sums' way through memory (measured, tiles of 128 x 128: some 0.7 us a MB, of 256 x 256 0.5).  At most two rounds of
+// slices, which bounds the sums' memory.
+Tiling tiling(const Fp8ProductArgs& a, Kind kind, int side, int grid, int64_t one, int64_t two, int64_t round, int64_t mb) {
+  Tiling t{kind, side, side, grid, 0, 0, 1, 0};
+  const int64_t tiles_r = (a.rows + side - 1) / side, steps = fp8_blocks(a.k);
+  t.tiles = (a.cols + side - 1) / side * tiles_r;
+  const int64_t rest = t.tiles % grid, whole = t.tiles / grid;
+  const int64_t sums = (a.rows + tiles_r - 1) / tiles_r * side * 4;     // bytes of a slice's sums
+  int64_t best = 0;
+  for (int64_t s = 1; rest > 0 && s <= kMostSlices && (s == 1 || (rest * s <= 2 * grid && steps / s >= 2)); ++s) {
+    const int64_t n = rest * s, each = (steps + s - 1) / s;
+    int64_t time = round + (n <= kCus ? each * one : (n + grid - 1) / grid * each * two);
+    if (s > 1) time += 3000 + (n * sums * mb >> 20);
+    if (s == 1 || time < best) {
       best = time;
       t.slices = static_cast<int>(s);
     }
   }
   t.whole = static_cast<int>(t.tiles - rest);
-  t.cost = weight * (t.tiles / grid * steps + best);
+  t.cost = 3000 + whole * (steps * two + round) + best;
   return t;
 }
 
-constexpr int kCus = 256;
+// A workgroup to a tile, its four waves a quarter of k each: 1.85 us a block (4.3 with fp32 results) for up to a
+// workgroup to a CU.
 Tiling few(const Fp8ProductArgs& a, Kind kind, int side) {
   Tiling t{kind, side, side, 0, 0, 0, 1, 0};
   t.tiles = ((a.cols + side - 1) / side) * ((a.rows + side - 1) / side);
-  t.grid = static_cast<int>(t.tiles);
+  const int64_t blocks = (fp8_blocks(a.k) + 3) / 4 * (a.out_io ? 1850 : 4300);
+  t.cost = 3000 + (t.tiles <= kCus ? blocks : blocks * t.tiles / kCus + blocks * 7 / 10);
+  t.grid = static_cast<int>(t.tiles < (1 << 20) ? t.tiles : 1 << 20);   // (more cost too much to be picked)
   return t;
 }
-// Tiles of 256 x 256, one workgroup to a CU, or of 128 x 128, two to a CU.
+
+// The least time by what the kernels took (a step of 256 x 256 1.5 us, of 128 x 128 0.6 with one and 1.13 with two
+// workgroups on a CU, with fp32 results 1.65 and 2.15): for instance with 5120 x 2560, bf16: 8 rows 7.8 us on the waves'
+// kernel (tiles of 128 x 128 11), 128 rows 15.8 on tiles of 128 x 128 in four slices (27.4 unsliced, 21 on 64 x 64), 1001
+// x 777 x 1000 6.9 on 64 x 64 (8.5 on 128 x 128), 16384 rows of 2560 x 10240 383 on 256 x 256 (530 on 128 x 128).
 Tiling pick(const Fp8ProductArgs& a) {
   if (a.rows <= 16) return few(a, kFew16, 16);
-  const Tiling small = tiling(a, kSmall, 128, 128, 2 * kCus, 5);
-  if (!a.out_io) return small;
-  const Tiling large = tiling(a, kLarge, 256, 256, kCus, 8);
-  return large.cost <= small.cost ? large : small;
+  const Tiling small = a.out_io ? tiling(a, kSmall, 128, 2 * kCus, 600, 1130, 2000, 700)
+                                : tiling(a, kSmall, 128, 2 * kCus, 1650, 2150, 2000, 700);
+  const Tiling low = few(a, kFew64, 64);
+  const Tiling best = low.cost < small.cost ? low : small;
+  if (!a.out_io) return best;
+  const Tiling large = tiling(a, kLarge, 256, kCus, 1500, 1600, 4000, 500);
+  return large.cost < best.cost ? large : best;
 }
 
 }  // namespace
@@ -708,7 +727,6 @@ hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream) {
         if (t.slices > 1) slices_kernel<128, 128, T><<<sum_grid, 256, 0, stream>>>(p);
         break;
       case kFew64: few_product_kernel<4, 4, 4, E4m3, T><<<grid, 256, 0, stream>>>(p); break;
-      case kFew32: few_product_kernel<2, 2, 8, E4m3, T><<<grid, 512, 0, stream>>>(p); break;
       case kFew16:
         if (a.r.scales != nullptr) few_product_kernel<1, 1, 8, E4m3, T><<<grid, 512, 0, stream>>>(p);
         else if (a.r_io) few_product_kernel<1, 1, 8, uint16_t, T><<<grid, 512, plain_bytes(a), stream>>>(p);

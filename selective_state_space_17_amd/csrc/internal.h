@@ -263,6 +263,8 @@ struct Fp8Args {
 hipError_t fp8_quantize_launch(const Fp8Args& a, hipStream_t stream);
 hipError_t fp8_transpose_launch(const Fp8Args& a, hipStream_t stream);
 hipError_t fp8_dequantize_launch(const Fp8Args& a, hipStream_t stream);
+// the first to 8 bits and the second, of as many rows, laid out the other way, side by side
+hipError_t fp8_both_launch(const Fp8Args& plain, const Fp8Args& packed, hipStream_t stream);
 
 // out[r, c] (+)= sum over k of R[r, k] C[c, k]
 struct Fp8ProductArgs {

@@ -115,7 +115,9 @@ def test_linear_arguments():
     assert fwd(d, out=AT[4] + 1) == MIS and fwd(d, out=AT[0]) == INV and fwd(d, out=AT[3]) == INV
     plain = lin(x_dtype=M.MSSM_BF16)
     assert fwd(plain) == INV, "a plain x has no scales"
-    need = M.fp8_linear_fwd_workspace_size(8, 200, 70, M.MSSM_BF16)
+    assert M.fp8_linear_fwd_workspace_size(8, 200, 70, M.MSSM_BF16) == 0, "a few plain rows are rounded in place"
+    plain = lin(tokens=100, x_dtype=M.MSSM_BF16)
+    need = M.fp8_linear_fwd_workspace_size(100, 200, 70, M.MSSM_BF16)
     assert need > 0
     for kw, want in ((dict(x=AT[0] + 1), MIS), (dict(nb=need - 1), WS), (dict(work=None), WS), (dict(work=AT[5] + 16), MIS),
                      (dict(work=AT[2]), INV), (dict(work=AT[4]), INV)):
