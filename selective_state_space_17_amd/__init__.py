@@ -988,7 +988,7 @@ def _norm_fwd(kind, x, weight, bias, residual, eps, return_residual, residual_dt
         if out is None:
             out = _fp8_empty(stream, rows, dim)
         else:
-            _fp8_expect("out", out, rows, dim, False, cur)
+            _fp8_rows("out", out, dim, False, cur, rows)
     elif out is None:
         out = _empty(stream, shape, xt, x)
     else:
@@ -1193,31 +1193,39 @@ def _fp8_shapes(rows, cols, square):
 def _fp8_empty(stream, rows, cols, square=False) -> Fp8Matrix:
     torch = _torch()
     codes, scales = _fp8_shapes(rows, cols, square)
+    if stream is None:
+        return Fp8Matrix(torch.empty(codes, dtype=torch.float8_e4m3fn, device="cuda"),
+                         torch.empty(scales, dtype=torch.float8_e8m0fnu, device="cuda"), cols, square)
     return Fp8Matrix(_empty(stream, codes, torch.float8_e4m3fn), _empty(stream, scales, torch.float8_e8m0fnu), cols,
                      square)
 
 
-def _fp8_expect(name, m, rows, cols, square, cur) -> None:
+def _fp8_rows(name, m, cols, square, cur, rows=None) -> int:
+    """Rows of an Fp8Matrix on the current GPU, whose columns, kind and rows are as given (None: its own)."""
     torch = _torch()
-    if not isinstance(m, Fp8Matrix):
-        raise TypeError(f"{name} must be an Fp8Matrix, got {type(m).__name__}")
-    if m.cols != cols:
-        raise ValueError(f"{name} must have {cols} columns, got {m.cols}")
-    if bool(m.square) != square:
-        raise ValueError(f"{name} must have a scale for each {'128 x 128' if square else '128 columns of a row'}")
-    codes, scales = _fp8_shapes(rows, cols, square)
-    _check_gpu(name + ".codes", m.codes, torch.float8_e4m3fn, codes, cur)
-    _check_gpu(name + ".scales", m.scales, torch.float8_e8m0fnu, scales, cur)
-
-
-def _fp8_check(name, m, cur) -> int:
-    """Rows of a matrix whose own sizes define the problem."""
+    if type(m) is Fp8Matrix:
+        codes, scales, own, kind = m
+        shape = codes.shape
+        # (a decode step's call is dominated by what happens here: all in one go, and what is wrong found out below)
+        if (len(shape) == 2 and 0 < own and (cols is None or own == cols) and (square is None or kind is square)
+                and (rows is None or rows == shape[0])):
+            want, lines = _fp8_shapes(shape[0], own, kind)
+            if (shape == want and scales.shape == lines and codes.dtype is torch.float8_e4m3fn
+                    and scales.dtype is torch.float8_e8m0fnu and codes.get_device() == cur
+                    and scales.get_device() == cur and codes.is_contiguous() and scales.is_contiguous()):
+                return shape[0]
     if not isinstance(m, Fp8Matrix):
         raise TypeError(f"{name} must be an Fp8Matrix, got {type(m).__name__}")
     if m.codes.dim() != 2 or m.cols <= 0:
         raise ValueError(f"{name} must have codes [rows, 128 * blocks] and at least one column")
-    rows = m.codes.shape[0]
-    _fp8_expect(name, m, rows, m.cols, bool(m.square), cur)
+    if cols is not None and m.cols != cols:
+        raise ValueError(f"{name} must have {cols} columns, got {m.cols}")
+    if square is not None and bool(m.square) != square:
+        raise ValueError(f"{name} must have a scale for each {'128 x 128' if square else '128 columns of a row'}")
+    rows = m.codes.shape[0] if rows is None else rows
+    want, lines = _fp8_shapes(rows, m.cols, bool(m.square))
+    _check_gpu(name + ".codes", m.codes, torch.float8_e4m3fn, want, cur)
+    _check_gpu(name + ".scales", m.scales, torch.float8_e8m0fnu, lines, cur)
     return rows
 
 
@@ -1245,14 +1253,14 @@ def fp8_quantize(x, square: bool = False, transposed: bool = False, both: bool =
         if m is None:
             m = _fp8_empty(stream, rows, cols, square)
         else:
-            _fp8_expect("out", m, rows, cols, square, cur)
+            _fp8_rows("out", m, cols, square, cur, rows)
     if both or transposed:
         if rows == 0:
             raise ValueError("the transpose of no rows has no columns")
         if t is None:
             t = _fp8_empty(stream, cols, rows, square)
         else:
-            _fp8_expect("out", t, cols, rows, square, cur)
+            _fp8_rows("out", t, rows, square, cur, cols)
     d = Fp8Desc(rows, cols, io, _fp8_kind(square), 0)
     st = lib.mssm_fp8_quantize(ctypes.byref(d), x.data_ptr(), _ptr(m and m.codes), _ptr(m and m.scales),
                                _ptr(t and t.codes), _ptr(t and t.scales), _stream_on(stream, cur))
@@ -1265,15 +1273,13 @@ def fp8_transpose(m, out=None, stream=None) -> Fp8Matrix:
     """The transpose of an Fp8Matrix with scales of rows, with scales of its own rows (mssm_fp8_transpose): the
     values that m stands for, but below 2^-6 of their new block's scale, where they are rounded to 2^-9 of it."""
     cur = _torch().cuda.current_device()
-    rows = _fp8_check("m", m, cur)
-    if m.square:
-        raise ValueError("m must have a scale for each 128 columns of a row")
+    rows = _fp8_rows("m", m, None, False, cur)
     if rows == 0:
         raise ValueError("the transpose of no rows has no columns")
     if out is None:
         out = _fp8_empty(stream, m.cols, rows)
     else:
-        _fp8_expect("out", out, m.cols, rows, False, cur)
+        _fp8_rows("out", out, rows, False, cur, m.cols)
     d = Fp8Desc(rows, m.cols, MSSM_F32, MSSM_FP8_ROWS, 0)
     st = lib.mssm_fp8_transpose(ctypes.byref(d), m.codes.data_ptr(), m.scales.data_ptr(), out.codes.data_ptr(),
                                 out.scales.data_ptr(), _stream_on(stream, cur))
@@ -1287,7 +1293,7 @@ def fp8_dequantize(m, dtype=None, out=None, stream=None):
     (mssm_fp8_dequantize)."""
     torch = _torch()
     cur = torch.cuda.current_device()
-    rows = _fp8_check("m", m, cur)
+    rows = _fp8_rows("m", m, None, None, cur)
     dtype = dtype or (torch.bfloat16 if out is None else out.dtype)
     io = _codes(dtype)
     if out is None:
@@ -1338,11 +1344,10 @@ def fp8_linear_fwd(x, weight, out_dtype=None, out=None, workspace=None, stream=N
     or float32, which also keeps more of the sums.  Returns [tokens, out], for a tensor x [..., out]."""
     torch = _torch()
     cur = torch.cuda.current_device()
-    n = _fp8_check("weight", weight, cur)
+    n = _fp8_rows("weight", weight, None, None, cur)
     k = weight.cols
     if isinstance(x, Fp8Matrix):
-        tokens = _fp8_check("x", x, cur)
-        _fp8_expect("x", x, tokens, k, False, cur)
+        tokens = _fp8_rows("x", x, k, False, cur)
         xd, xp, xs, shape = MSSM_E4M3, x.codes.data_ptr(), x.scales.data_ptr(), (tokens, n)
     else:
         if x.dim() < 1 or x.shape[-1] != k:
@@ -1387,13 +1392,11 @@ def fp8_linear_bwd(x, weight_t, dout, want_dx: bool = True, want_dweight: bool =
         raise ValueError("weight_t is required for dx")
     if want_dweight and x is None:
         raise ValueError("x is required for dweight")
-    k = _fp8_check("weight_t", weight_t, cur) if weight_t is not None else x.cols
+    k = None if weight_t is None else _fp8_rows("weight_t", weight_t, n, None, cur)
     square = weight_t is not None and bool(weight_t.square)
-    if weight_t is not None:
-        _fp8_expect("weight_t", weight_t, k, n, square, cur)
     if x is not None:
-        _fp8_check("x", x, cur)
-        _fp8_expect("x", x, tokens, k, False, cur)
+        _fp8_rows("x", x, k, False, cur, tokens)
+        k = x.cols
     if want_dx:
         dx = _empty(stream, (*dout.shape[:-1], k), dout.dtype) if dx is None else dx
         _check_gpu("dx", dx, dout.dtype, (*dout.shape[:-1], k), cur)

@@ -75,11 +75,14 @@ def same(got, want, what):
 
 
 def product(r, c, out_dtype, old=None, chunk=64, device="cpu"):
-    """sum_k r[., k] c[., k] of two matrices of values, and its bound.
+    """sum_k r[., k] c[., k] of two matrices in 8 bits, and its bound: see product_of_values."""
+    return product_of_values(values(r).to(device), values(c).to(device), out_dtype, old, chunk)
 
-    fp32: products of e4m3 numbers are exact in fp32 and are summed there; every addition inside the matrix cores may
+
+def product_of_values(rv, cv, out_dtype, old=None, chunk=64):
+    """fp32: products of e4m3 numbers are exact in fp32 and are summed there; every addition inside the matrix cores may
     lose a whole step, 2 u.  bf16: besides, of 8 neighbouring products each may lose 2^-13 of the largest."""
-    rv, cv = values(r).to(device), values(c).to(device)
+    device = rv.device
     k = rv.shape[1]
     ref, mag = rv @ cv.T, rv.abs() @ cv.abs().T
     bound = mag * 2 * (k + 64) * U
