@@ -505,7 +505,7 @@ __global__ __launch_bounds__(NW * 64, CT * RT == 1 ? 4 : 2) void few_product_ker
   constexpr bool kFine = std::is_same_v<T, float>, kPlain = !std::is_same_v<X, E4m3>;
   static_assert(!kPlain || RT == 1, "up to 16 plain rows");
   constexpr int kC = 16 * CT, kR = 16 * RT, kPad = kC + 4;   // a row in LDS: off the banks of the next
-  constexpr int kDepth = CT + RT <= 4 ? 4 : 2;    // blocks on their way at a time
+  constexpr int kDepth = CT + RT <= 4 ? 4 : kFine ? 1 : 2;   // blocks on their way at a time: what registers hold
   __shared__ __attribute__((aligned(16))) float sums[NW][kR][kPad];
   extern __shared__ __attribute__((aligned(16))) unsigned char plain[];   // [rows][pitch + 16], [rows][blocks] scales
   const int lane = threadIdx.x % kLanes, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
@@ -658,12 +658,16 @@ Tiling tiling(const Fp8ProductArgs& a, Kind kind, int side, int grid, int64_t on
   return t;
 }
 
-// A workgroup to a tile, its four waves a quarter of k each: 1.85 us a block (4.3 with fp32 results) for up to a
-// workgroup to a CU.
+// Waves of a tile of 64 x 64: with fp32 results widening the codes is most of the work, and more waves share it (64 x 5120
+// x 2560: 23 us with eight, 34 with four; bf16 22 and 21, and less LDS leaves room for two workgroups).
+template <typename T> constexpr int few_waves() { return std::is_same_v<T, float> ? 8 : 4; }
+
+// A workgroup to a tile whose waves share k: 1.85 us a block (4 with fp32 results) for up to a workgroup to a CU.
 Tiling few(const Fp8ProductArgs& a, Kind kind, int side) {
   Tiling t{kind, side, side, 0, 0, 0, 1, 0};
   t.tiles = ((a.cols + side - 1) / side) * ((a.rows + side - 1) / side);
-  const int64_t blocks = (fp8_blocks(a.k) + 3) / 4 * (a.out_io ? 1850 : 4300);
+  const int64_t waves = a.out_io ? few_waves<uint16_t>() : few_waves<float>();
+  const int64_t blocks = (fp8_blocks(a.k) + waves - 1) / waves * (a.out_io ? 1850 : 4000);
   t.cost = 3000 + (t.tiles <= kCus ? blocks : blocks * t.tiles / kCus + blocks * 7 / 10);
   t.grid = static_cast<int>(t.tiles < (1 << 20) ? t.tiles : 1 << 20);   // (more cost too much to be picked)
   return t;
@@ -726,7 +730,7 @@ hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream) {
         else tile_product_kernel<128, 128, 2, 2, false, T><<<grid, 256, 0, stream>>>(p);
         if (t.slices > 1) slices_kernel<128, 128, T><<<sum_grid, 256, 0, stream>>>(p);
         break;
-      case kFew64: few_product_kernel<4, 4, 4, E4m3, T><<<grid, 256, 0, stream>>>(p); break;
+      case kFew64: few_product_kernel<4, 4, few_waves<T>(), E4m3, T><<<grid, few_waves<T>() * kLanes, 0, stream>>>(p); break;
       case kFew16:
         if (a.r.scales != nullptr) few_product_kernel<1, 1, 8, E4m3, T><<<grid, 512, 0, stream>>>(p);
         else if (a.r_io) few_product_kernel<1, 1, 8, uint16_t, T><<<grid, 512, plain_bytes(a), stream>>>(p);
