@@ -249,18 +249,14 @@ int mssm_fp8_linear_bwd(const mssm_fp8_linear_desc* desc, const void* x, const v
   q.rows = d.tokens; q.cols = d.out_features; q.io = d.io_dtype; q.x = dout; q.m = b.dout; q.t = b.dout_t;
   t.rows = d.tokens; t.cols = d.in_features;
   t.m = {const_cast<void*>(x), const_cast<void*>(x_scales)}; t.t = b.x_t;
-  int e = done(dweight != nullptr ? mssm::fp8_both_launch(q, t, s) : mssm::fp8_quantize_launch(q, s));
-  if (e == MSSM_OK && dx != nullptr) {
-    b.dx.r = b.dout;
-    b.dx.c = {const_cast<void*>(weight_t), const_cast<void*>(weight_t_scales)};
-    b.dx.out = dx;
-    e = done(mssm::fp8_product_launch(b.dx, s));
-  }
-  if (e == MSSM_OK && dweight != nullptr) {
-    b.dw.r = b.dout_t; b.dw.c = b.x_t; b.dw.out = dweight; b.dw.accumulate = accumulate != 0;
-    e = done(mssm::fp8_product_launch(b.dw, s));
-  }
-  return e;
+  const int e = done(dweight != nullptr ? mssm::fp8_both_launch(q, t, s) : mssm::fp8_quantize_launch(q, s));
+  if (e != MSSM_OK) return e;
+  b.dx.r = b.dout;
+  b.dx.c = {const_cast<void*>(weight_t), const_cast<void*>(weight_t_scales)};
+  b.dx.out = dx;
+  b.dw.r = b.dout_t; b.dw.c = b.x_t; b.dw.out = dweight; b.dw.accumulate = accumulate != 0;
+  if (dx != nullptr && dweight != nullptr) return done(mssm::fp8_two_products_launch(b.dx, b.dw, s));
+  return done(mssm::fp8_product_launch(dx != nullptr ? b.dx : b.dw, s));
 }
 
 }  // extern "C"

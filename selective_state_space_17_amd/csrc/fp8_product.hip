@@ -500,17 +500,22 @@ __device__ __forceinline__ i32x8_t codes_at(const unsigned char* p) {
                  static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]), static_cast<int>(b[3])};
 }
 
+template <int CT, int RT, int NW> struct FewShared {
+  float sums[NW][16 * RT][16 * CT + 4];   // a row off the banks of the next
+};
+
+// workgroup `group`
 template <int CT, int RT, int NW, typename X, typename T>
-__global__ __launch_bounds__(NW * 64, CT * RT == 1 ? 4 : 2) void few_product_kernel(Fp8Params p) {
+__device__ __forceinline__ void few_product(const Fp8Params& p, unsigned group, FewShared<CT, RT, NW>& shared) {
   constexpr bool kFine = std::is_same_v<T, float>, kPlain = !std::is_same_v<X, E4m3>;
   static_assert(!kPlain || RT == 1, "up to 16 plain rows");
-  constexpr int kC = 16 * CT, kR = 16 * RT, kPad = kC + 4;   // a row in LDS: off the banks of the next
+  constexpr int kC = 16 * CT, kR = 16 * RT;
   constexpr int kDepth = CT + RT <= 4 ? 4 : kFine ? 1 : 2;   // blocks on their way at a time: what registers hold
-  __shared__ __attribute__((aligned(16))) float sums[NW][kR][kPad];
+  auto& sums = shared.sums;
   extern __shared__ __attribute__((aligned(16))) unsigned char plain[];   // [rows][pitch + 16], [rows][blocks] scales
   const int lane = threadIdx.x % kLanes, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
   const int i16 = lane % 16, part = lane / 16;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x % p.tiles_c) * kC, r0 = static_cast<int64_t>(blockIdx.x / p.tiles_c) * kR;
+  const int64_t c0 = static_cast<int64_t>(group % p.tiles_c) * kC, r0 = static_cast<int64_t>(group / p.tiles_c) * kR;
   const unsigned char *ca[CT], *ra[RT];
 #pragma unroll
   for (int t = 0; t < CT; ++t) {
@@ -618,6 +623,19 @@ __global__ __launch_bounds__(NW * 64, CT * RT == 1 ? 4 : 2) void few_product_ker
   }
 }
 
+template <int CT, int RT, int NW, typename X, typename T>
+__global__ __launch_bounds__(NW * 64, CT * RT == 1 ? 4 : 2) void few_product_kernel(Fp8Params p) {
+  __shared__ __attribute__((aligned(16))) FewShared<CT, RT, NW> shared;
+  few_product<CT, RT, NW, X, T>(p, blockIdx.x, shared);
+}
+// two products side by side: the first `split` workgroups have the first
+template <int CT, int RT, int NW, typename X, typename T>
+__global__ __launch_bounds__(NW * 64, CT * RT == 1 ? 4 : 2) void two_products_kernel(Fp8Params p, Fp8Params q, unsigned split) {
+  __shared__ __attribute__((aligned(16))) FewShared<CT, RT, NW> shared;
+  const bool first = blockIdx.x < split;
+  few_product<CT, RT, NW, X, T>(first ? p : q, first ? blockIdx.x : blockIdx.x - split, shared);
+}
+
 // ---------------------------------------------------------------------------------------------- plan
 enum Kind { kLarge, kSmall, kFew64, kFew16 };
 
@@ -702,8 +720,8 @@ size_t fp8_product_workspace_bytes(const Fp8ProductArgs& a) {
   return t.slices > 1 ? static_cast<size_t>(t.tiles - t.whole) * t.slices * t.bc * t.br * 4 : 0;
 }
 
-hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream) {
-  if (a.rows == 0 || a.cols == 0) return hipSuccess;
+namespace {
+Fp8Params params(const Fp8ProductArgs& a, const Tiling& t) {
   Fp8Params p{};
   p.r = static_cast<const unsigned char*>(a.r.codes); p.rs = static_cast<const unsigned char*>(a.r.scales);
   p.c = static_cast<const unsigned char*>(a.c.codes); p.cs = static_cast<const unsigned char*>(a.c.scales);
@@ -711,9 +729,35 @@ hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream) {
   p.steps = static_cast<int>(fp8_blocks(a.k)); p.pitch = fp8_blocks(a.k) * kBlock;
   p.r_lines = fp8_lines(a.rows); p.c_lines = a.square ? fp8_blocks(a.cols) : fp8_lines(a.cols);
   p.out = a.out; p.accumulate = a.accumulate;
-  const Tiling t = pick(a);
   p.tiles_c = static_cast<int>((a.cols + t.bc - 1) / t.bc); p.tiles_r = static_cast<int>((a.rows + t.br - 1) / t.br);
   p.whole = t.whole; p.slices = t.slices; p.sums = static_cast<float*>(a.workspace);
+  return p;
+}
+}  // namespace
+
+hipError_t fp8_two_products_launch(const Fp8ProductArgs& a, const Fp8ProductArgs& b, hipStream_t stream) {
+  if (a.rows > 0 && a.cols > 0 && b.rows > 0 && b.cols > 0 && a.out_io == b.out_io) {
+    const Tiling t = pick(a), u = pick(b);
+    if (t.kind == kFew64 && u.kind == kFew64) {
+      const Fp8Params p = params(a, t), q = params(b, u);
+      auto go = [&](auto out) {
+        using T = decltype(out);
+        two_products_kernel<4, 4, few_waves<T>(), E4m3, T>
+            <<<dim3(static_cast<unsigned>(t.grid + u.grid)), few_waves<T>() * kLanes, 0, stream>>>(p, q, t.grid);
+      };
+      if (a.out_io) go(uint16_t{});
+      else go(float{});
+      return hipGetLastError();
+    }
+  }
+  const hipError_t e = fp8_product_launch(a, stream);
+  return e == hipSuccess ? fp8_product_launch(b, stream) : e;
+}
+
+hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream) {
+  if (a.rows == 0 || a.cols == 0) return hipSuccess;
+  const Tiling t = pick(a);
+  const Fp8Params p = params(a, t);
   const dim3 grid(static_cast<unsigned>(t.grid)), sum_grid(static_cast<unsigned>((t.tiles - t.whole) * kShares));
   auto go = [&](auto out) {
     using T = decltype(out);

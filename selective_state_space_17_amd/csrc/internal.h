@@ -283,5 +283,7 @@ struct Fp8ProductArgs {
 bool fp8_product_takes_plain(const Fp8ProductArgs& a);
 size_t fp8_product_workspace_bytes(const Fp8ProductArgs& a);
 hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream);
+// one after the other (they may share a workspace), or side by side in one launch where either is small
+hipError_t fp8_two_products_launch(const Fp8ProductArgs& a, const Fp8ProductArgs& b, hipStream_t stream);
 
 }  // namespace mssm
