@@ -47,13 +47,6 @@ __device__ __forceinline__ uint32_t fp8_codes(float a, float b, float c, float d
   v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v, c, d, s, true);
   return __builtin_bit_cast(uint32_t, v);
 }
-// the same of two pairs of bf16
-__device__ __forceinline__ uint32_t fp8_codes(uint32_t ab, uint32_t cd, uint32_t scale) {
-  const float s = __uint_as_float(scale << 23);
-  i16x2_t v = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(i16x2_t{0, 0}, __builtin_bit_cast(bf16x2_t, ab), s, false);
-  v = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(v, __builtin_bit_cast(bf16x2_t, cd), s, true);
-  return __builtin_bit_cast(uint32_t, v);
-}
 __device__ __forceinline__ void fp8_values(uint32_t codes, float (&v)[4]) {
   const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(codes), false);
   const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(codes), true);

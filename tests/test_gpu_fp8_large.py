@@ -98,3 +98,16 @@ def test_most_tokens(M):
     bound = mag * 2 * (tokens + 64) * 2.0 ** -24
     err = (got.double() - ref).abs()
     assert bool((err <= bound).all())
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_no_tokens_many_tiles(M, accumulate):
+    """A gradient of more tiles of 64 x 64 than a launch takes, of no tokens: zeros everywhere, or what was there."""
+    n, k = 65600, 65600
+    say("fp8 weight gradient of no tokens", n, k, accumulate)
+    x = M.fp8_quantize(torch.empty(0, k, device="cuda"))
+    dw = torch.full((n, k), 1.5, device="cuda", dtype=BF16)
+    M.fp8_linear_bwd(x, None, torch.empty(0, n, device="cuda", dtype=BF16), want_dx=False, dweight=dw,
+                     accumulate=accumulate)
+    want = 1.5 if accumulate else 0.0
+    assert dw.min().item() == want and dw.max().item() == want
