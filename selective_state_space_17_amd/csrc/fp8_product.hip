@@ -99,19 +99,17 @@ template <int BC, int BR> __device__ __forceinline__ Place place_of(const Fp8Par
           __builtin_amdgcn_readfirstlane((band * kBand + in_band % wide) * BR)};
 }
 
-// 8 neighbouring elements of a row of the output, the first `left` of which exist, to where they belong
-template <typename T> __device__ __forceinline__ void put(T* to, float (&v)[8], int64_t left, int accumulate) {
+// V neighbouring elements of a row of the output, the first `left` of which exist, to where they belong
+template <int V, typename T> __device__ __forceinline__ void put(T* to, float (&v)[V], int64_t left, int accumulate) {
   if (accumulate) {
-    float o[8];
-    load_row<8>(to, o, left);
+    float o[V];
+    load_row<V>(to, o, left);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += o[e];
+    for (int e = 0; e < V; ++e) v[e] += o[e];
   }
-  store_row<8>(to, v, left);
+  store_row<V>(to, v, left);
 }
 
-// C's rows are the matrix instructions' rows: a lane's accumulators are neighbours in the output.
-//
 // A workgroup stays on a CU (two of the small tile) and takes tile after tile, each 128 k (a block) a step, in halves of
 // 64 k.  Four halves are in LDS or on their way there.  While a half is multiplied from registers the next one's
 // fragments are read, and the place that it was read from before takes the loads of the half four ahead; one barrier
@@ -119,9 +117,12 @@ template <typename T> __device__ __forceinline__ void put(T* to, float (&v)[8], 
 // halves of multiplications to arrive in, and crosses the borders of tiles (with two whole steps in LDS and a barrier a
 // step it had two: 497 us at 8192^3, where this takes 448; a ring of eight halves was no faster).
 //
-// A wave holds TC x TR tiles of 32 x 32.  Row i of tile t is row TC i + t of its share: a lane's scales for its tiles
-// are then TC neighbouring bytes of memory, one word, from which the instruction picks a byte; and what a lane holds of
-// an output row are runs of 4 TC neighbouring elements.
+// A wave holds TC x TR tiles of 32 x 32.  Of R, row i of tile t is row TR i + t of its share, of C row 2 TC (i % 16) +
+// TC (i / 16) + t: a lane's scales for its tiles are then neighbouring bytes of memory, one word, from which the
+// instruction picks a byte.  R's rows are the matrix instructions' rows, so that a lane's accumulators are TC neighbours of
+// many output rows.  After lanes 16 apart have exchanged every other row they are 2 TC neighbours, and those of 16 lanes
+// are one stretch of a row, 128 bytes or more, which leaves in one store (in pieces of 64 bytes of 16 rows: 712 us for
+// 32768 x 2560 x 10240, as here 677; with rows that begin off a line, 10001 columns: 947 and 747).
 template <int BC, int BR, int WC, int WR, bool SQUARE, typename T>
 __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params p) {
   constexpr bool kFine = std::is_same_v<T, float>;
@@ -131,9 +132,10 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
   constexpr int kLoads = (LC + LR + TC - 1) / TC;          // loads between two rows of multiplications
   constexpr int kReads = (TC + TR + TC - 1) / TC;          // fragments read there
   constexpr int kAhead = 2 * (LC + LR) + 2;                // loads of two neighbouring halves, scales among them
-  constexpr int kStores = TC * TR * static_cast<int>(sizeof(T));   // a whole tile's stores of a wave, 16 bytes a lane
+  constexpr int kStores = TR * 8;                          // a whole tile's stores of a wave
   static_assert(LC * 16 * kW == BC && LR * 16 * kW == BR, "loads split evenly over the waves");
   static_assert(TC == 2 || TC == 4, "a lane's scales of C are a word or half of one");
+  static_assert(!kFine || TC == 2, "a lane's run of fp32 is one store");
   static_assert(TR == 2, "and those of R half of one");
   static_assert(kAhead + kStores < 64, "what the wait instruction can count");
   constexpr int kC = BC * kRow, kR = BR * kRow;            // bytes of a half
@@ -191,12 +193,13 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
   const unsigned char *lc = nullptr, *lr = nullptr, *lcs = nullptr, *lrs = nullptr;
   uint32_t oc[LC], orr[LR], ocs = 0, ors = 0;
   const uint32_t pitch = static_cast<uint32_t>(p.pitch);
-  auto offsets = [&](int64_t rows, int of, auto& off) {   // rows: of the matrix, from the tile's first on
+  auto offsets = [&](int64_t rows, int of, int turned, auto& off) {   // rows: of the matrix, from the tile's first on
     const int last = rows < 256 ? static_cast<int>(rows) - 1 : 255;
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(off) / sizeof(off[0])); ++i) {
       const int at = (i * kW + w) * 16 + lrow;
-      const int r = at / (32 * of) * (32 * of) + at % 32 * of + at / 32 % of;
+      const int row = at % 32, t = at / 32 % of;
+      const int r = at / (32 * of) * (32 * of) + (turned ? row % 16 * 2 + row / 16 : row) * of + t;
       off[i] = static_cast<uint32_t>(r < last ? r : last) * pitch + chunk;   // (pitch <= 2^22)
     }
   };
@@ -205,11 +208,11 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
       const Job j = job_at(ljob);
       if (j.steps > 0) {
         lleft = j.steps;
-        offsets(p.cols - j.c0, TC, oc);
-        offsets(p.rows - j.r0, TR, orr);
+        offsets(p.cols - j.c0, TC, 1, oc);
+        offsets(p.rows - j.r0, TR, 0, orr);
         lc = p.c + static_cast<int64_t>(j.c0) * p.pitch + j.begin * kBlock;
         lr = p.r + static_cast<int64_t>(j.r0) * p.pitch + j.begin * kBlock;
-        const int c = wc * (32 * TC) + lane % 32 * TC, r = wr * (32 * TR) + lane % 32 * TR;
+        const int c = wc * (32 * TC) + (lane % 16 * 2 + lane / 16 % 2) * TC, r = wr * (32 * TR) + lane % 32 * TR;
         const int64_t left_c = p.c_lines - j.c0 - TC, left_r = p.r_lines - j.r0 - TR;
         lcs = p.cs + j.begin * p.c_lines + (SQUARE ? j.c0 / kBlock : j.c0);
         lrs = p.rs + j.begin * p.r_lines + j.r0;
@@ -295,14 +298,14 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
         for (int c = 0; c < TC; ++c) {
           const bf16x8_t a = wide_codes(fc[h][c], q, sc[c]);
 #pragma unroll
-          for (int r = 0; r < TR; ++r) acc[c][r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b[r], acc[c][r], 0, 0, 0);
+          for (int r = 0; r < TR; ++r) acc[c][r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[r], a, acc[c][r], 0, 0, 0);
         }
       }
     } else {
       unrolled<TR>([&](auto j) {
         constexpr int J = decltype(j)::value;
-        acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fc[h][I], fr[h][J], acc[I][J], 0, 0, I,
-                                                                    static_cast<int>(s.c), J, static_cast<int>(s.r));
+        acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fr[h][J], fc[h][I], acc[I][J], 0, 0, J,
+                                                                    static_cast<int>(s.r), I, static_cast<int>(s.c));
         // stays here: the compiler knows of no reason not to move a multiplication to where its result is used
         asm volatile("" : "+v"(acc[I][J]));
       });
@@ -380,71 +383,75 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
       loaded();
     }
 
-    // accumulator e = 4 q + f of tile (i, j): C's row TC (8 q + 4 (lane / 32) + f) + i and R's row TR (lane % 32) + j of
-    // the wave's shares
-    const int wave_c = wc * TC * 32 + lane / 32 * 4 * TC, wave_r = wr * TR * 32 + lane % 32 * TR;
-    auto each = [&](auto&& to) {   // every run of 8 neighbouring elements: (row of the tile, column of it, values)
+    // accumulator e = 4 q + f of tile (i, j): R's row TR (8 q + 4 (lane / 32) + f) + j of the wave's share, and row i of
+    // C's that are the lane's.  Lanes 16 apart exchange f and f + 1.
+    constexpr int kRun = 2 * TC;
+    int wave_r = wr * TR * 32 + (lane / 32 * 4 + lane / 16 % 2) * TR;
+    asm volatile("" : "+v"(wave_r));   // (known before the loop over jobs, all the rows' places would be registers in it)
+    const int c = wc * TC * 32 + lane % 16 * kRun;
+    auto each = [&](auto&& to) {   // every pair of f: (row of the tile after wave_r, tile j, first accumulator)
+      unrolled<TR * 8>([&](auto i) {
+        constexpr int I = decltype(i)::value, J = I / 8, E = I % 8 * 2;
+        to(std::integral_constant<int, (E / 4 * 8 + E % 4) * TR + J>{}, std::integral_constant<int, J>{},
+           std::integral_constant<int, E>{});
+      });
+    };
+    // (way: which of the three below, so that the compiler does not take what two have in common before the branch, where
+    // a second set of accumulators finds no registers)
+    auto exchanged = [&](auto way, auto j, auto e, float (&v)[kRun]) {
+      constexpr int J = decltype(j)::value, E = decltype(e)::value;
 #pragma unroll
-      for (int j = 0; j < TR; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int h = 0; h < TC / 2; ++h) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = acc[e % TC][j][4 * q + (8 * h + e) / TC];
-            to(wave_r + j, wave_c + 8 * TC * q + 8 * h, v);
-          }
+      for (int t = 0; t < TC; ++t) {
+        float a = acc[t][J][E];
+        asm volatile("" : "+v"(a) : "n"(decltype(way)::value));
+        const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(acc[t][J][E + 1]), false, false);
+        v[t] = __uint_as_float(x[0]);
+        v[TC + t] = __uint_as_float(x[1]);
+      }
     };
     if (cur.sum >= 0) {
-      float* const to = p.sums + static_cast<int64_t>(cur.sum) * BR * BC;
-      const int64_t rows = p.rows - cur.r0;
-      each([&](int r, int c, float (&v)[8]) {
-        if (r < rows) store_row<8>(to + r * BC + c, v);
+      float* const to = p.sums + static_cast<int64_t>(cur.sum) * BR * BC + wave_r * BC + c;
+      const int64_t rows = p.rows - cur.r0 - wave_r;
+      each([&](auto r, auto j, auto e) {
+        float v[kRun];
+        exchanged(std::integral_constant<int, 0>{}, j, e, v);
+        if (r < rows) store_row<kRun>(to + r * BC, v);
       });
     } else {
-      T* const to = static_cast<T*>(p.out) + cur.r0 * p.cols + cur.c0;
+      T* const tile = static_cast<T*>(p.out) + cur.r0 * p.cols + cur.c0;
+      const uint32_t at = static_cast<uint32_t>(wave_r * static_cast<int>(p.cols) + c) * sizeof(T);   // (cols <= 2^20)
+      auto to = [&](auto r) { return reinterpret_cast<T*>(reinterpret_cast<unsigned char*>(tile + r * p.cols) + at); };
       const int64_t rows = p.rows - cur.r0, cols = p.cols - cur.c0;
       if (rows >= BR && cols >= BC && !p.accumulate) {
-        if constexpr (kFine) {
-          each([&](int r, int c, float (&v)[8]) { store_row<8>(to + r * p.cols + c, v); });
-        } else {
-          // A run of a row is 16 (TC 2) or 32 bytes of lane l and as many after it of lane l + 32.  Pieces of 16 bytes change
-          // places between lanes 16 apart, so that a store writes 64 bytes of each of 16 rows, past the cache: kept there,
-          // the output pushed the operands out of it (32768 x 2560 x 10240, which writes 671 MB: 817 us, as here 767; past
-          // the cache but in pieces of 32 bytes 955).
-          constexpr bool kTwo = TC == 4;             // a run is two pieces: they change places, else runs q and q + 1
-          const int row16 = lane / 16 % 2;
+        // past the cache: kept there, the output pushes the operands out of it (32768 x 2560 x 10240, which writes 671 MB:
+        // 677 us, kept 730)
+        each([&](auto r, auto j, auto e) {
+          if constexpr (kFine) {
+            float v[kRun];
+            exchanged(std::integral_constant<int, 1>{}, j, e, v);
+            __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4_u*>(to(r)));
+          } else {
+            constexpr int J = decltype(j)::value, E = decltype(e)::value;
+            typedef uint32_t Run __attribute__((ext_vector_type(TC)));
+            typedef Run Run_u __attribute__((aligned(2)));
+            Run v;
 #pragma unroll
-          for (int j = 0; j < TR; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; q += kTwo ? 1 : 2) {
-              u32x4_t piece[2];
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int at = (kTwo ? 8 * h : 0) + 2 * e, run = 4 * (kTwo ? q : q + h);
-                  piece[h][e] = pack_bf16(acc[at % TC][j][run + at / TC], acc[(at + 1) % TC][j][run + (at + 1) / TC]);
-                }
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const auto t = __builtin_amdgcn_permlane16_swap(piece[0][e], piece[1][e], false, false);
-                piece[0][e] = t[0];
-                piece[1][e] = t[1];
-              }
-              const int c = wave_c + 8 * TC * q + row16 * (kTwo ? 8 : 8 * TC);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int r = wr * TR * 32 + (lane % 16 + 16 * h) * TR + j;
-                __builtin_nontemporal_store(piece[h], reinterpret_cast<u32x4_u*>(to + r * p.cols + c));
-              }
+            for (int h = 0; h < TC / 2; ++h) {
+              const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16(acc[2 * h][J][E], acc[2 * h + 1][J][E]),
+                                                              pack_bf16(acc[2 * h][J][E + 1], acc[2 * h + 1][J][E + 1]),
+                                                              false, false);
+              v[h] = x[0];
+              v[TC / 2 + h] = x[1];
             }
-        }
+            __builtin_nontemporal_store(v, reinterpret_cast<Run_u*>(to(r)));
+          }
+        });
         stored = 2;
       } else {
-        each([&](int r, int c, float (&v)[8]) {
-          if (r < rows) put(to + r * p.cols + c, v, cols - c, p.accumulate);
+        each([&](auto r, auto j, auto e) {
+          float v[kRun];
+          exchanged(std::integral_constant<int, 2>{}, j, e, v);
+          if (r + wave_r < rows) put(to(r), v, cols - c, p.accumulate);
         });
       }
     }

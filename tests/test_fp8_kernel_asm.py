@@ -10,7 +10,7 @@ import pytest
 
 from test_kernel_asm import _device_asm
 
-# (tile, waves, TC, TR): stores of a wave and whole tile 16 bytes a lane, loads of a half
+# tile and waves: (TC, TR, loads of a half); a wave stores 2 TC elements a lane, two of TR x 16 rows at a time
 TILES = {"ILi256ELi256ELi2ELi4E": (4, 2, 4), "ILi128ELi128ELi2ELi2E": (2, 2, 4)}
 
 
@@ -51,7 +51,8 @@ def test_loads_and_stores_are_those_that_the_waits_count(bodies):
         assert not [ln for ln in loop if "accvgpr" in ln], name
         waits = {int(v) for ln in body for v in re.findall(r"vmcnt\((\d+)\) lgkmcnt\(0\)", ln)}
         ahead = 2 * loads + 2
-        stores = tc * tr * (4 if fine else 2)
+        stores = tr * 16 // 2
         assert {ahead, ahead + stores} <= waits, (name, waits)
-        if not fine:
-            assert sum("global_store_dwordx4" in ln and " nt" in ln for ln in body) == stores, name
+        words = 2 * tc if fine else tc
+        assert sum(bool(re.search(r"global_store_.* nt$", ln)) for ln in body) == stores, name
+        assert sum(f"global_store_dwordx{words}" in ln and " nt" in ln for ln in body) == stores, name
