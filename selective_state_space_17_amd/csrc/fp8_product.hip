@@ -487,13 +487,15 @@ template <int BC, int BR, typename T> __global__ __launch_bounds__(256) void sli
 
 // ------------------------------------------------------------------------------------------- few rows
 // For up to some hundred rows the time goes into C's bytes and into latency, not into multiplications.  A workgroup owns
-// a tile of 16 CT x 16 RT; its waves take k's blocks in turn, the operands straight from global memory (C's bytes serve
+// a tile of 16 CT x 16 RT; its 8 waves take k's blocks in turn, the operands straight from global memory (C's bytes serve
 // once, R's come from the L2), and their sums are added in LDS in the waves' order, a thread 8 neighbouring elements.  No
-// barrier and no wait for another wave before that.
+// barrier and no wait for another wave before that.  What hides a load's latency are the other waves: a wave that had
+// several blocks on their way at a time was no faster or slower (8 x 2560 x 20480: 13.5 us, with four blocks, of which the
+// last ones are often past the end, 22; 64 x 2560 x 5120: 12.3, two blocks 12.9).
 // As above, row i of tile t is row CT i + t of C's 16 CT and RT i + t of R's.
 // X: R's type, E4m3 or a plain one for up to 16 rows that fit into LDS in 8 bits: each workgroup rounds them again while
-// its first loads of C are on their way, which saves a launch (1 x 2560 x 10240:
-// 9.1 us, 21.5 with each lane rounding its own operands).
+// its first loads of C are on their way, which saves a launch (1 x 2560 x 10240: 7.3 us of the GPU, 26 MB; with each lane
+// rounding its own operands 20).
 struct E4m3 {};
 
 template <int N> __device__ __forceinline__ uint32_t scales_at(const unsigned char* at) {
@@ -519,7 +521,6 @@ __device__ __forceinline__ void few_product(const Fp8Params& p, unsigned group, 
   constexpr bool kFine = std::is_same_v<T, float>, kPlain = !std::is_same_v<X, E4m3>;
   static_assert(!kPlain || RT == 1, "up to 16 plain rows");
   constexpr int kC = 16 * CT, kR = 16 * RT;
-  constexpr int kDepth = CT + RT <= 4 ? 4 : kFine ? 1 : 2;   // blocks on their way at a time: what registers hold
   auto& sums = shared.sums;
   extern __shared__ __attribute__((aligned(16))) unsigned char plain[];   // [rows][pitch + 16], [rows][blocks] scales
   const int lane = threadIdx.x % kLanes, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
@@ -578,13 +579,8 @@ __device__ __forceinline__ void few_product(const Fp8Params& p, unsigned group, 
       });
     }
   };
-  // kDepth blocks are loaded together (past the last one: the last again) and then multiplied
-  Step v[kDepth];
-  auto load = [&](int s) {
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) load_c(s + d * NW < p.steps ? s + d * NW : p.steps - 1, v[d]);
-  };
-  if (p.steps > 0) load(w < p.steps ? w : p.steps - 1);
+  Step v;
+  if (w < p.steps) load_c(w, v);
   if constexpr (kPlain) {
     const int work = static_cast<int>(p.rows) * p.steps;
     for (int i = threadIdx.x / 16; i < work; i += NW * 4) {   // 16 lanes a block
@@ -597,13 +593,10 @@ __device__ __forceinline__ void few_product(const Fp8Params& p, unsigned group, 
     }
     __syncthreads();
   }
-  for (int s = w; s < p.steps; s += NW * kDepth) {
-    if (s != w) load(s);
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) load_r(s + d * NW < p.steps ? s + d * NW : p.steps - 1, v[d]);
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d)
-      if (s + d * NW < p.steps) multiply(v[d]);
+  for (int s = w; s < p.steps; s += NW) {
+    if (s != w) load_c(s, v);
+    load_r(s, v);
+    multiply(v);
   }
   // accumulator e of tile (i, j): C's row CT (4 part + e) + i and R's row RT i16 + j
 #pragma unroll
@@ -646,7 +639,7 @@ __global__ __launch_bounds__(NW * 64, CT * RT == 1 ? 4 : 2) void two_products_ke
 }
 
 // ---------------------------------------------------------------------------------------------- plan
-enum Kind { kLarge, kSmall, kFew64, kFew16 };
+enum Kind { kLarge, kSmall, kFew64, kFew64x32, kFew32, kFew16 };   // (few: columns x rows of a tile)
 
 struct Tiling {
   Kind kind;
@@ -685,36 +678,59 @@ Tiling tiling(const Fp8ProductArgs& a, Kind kind, int side, int grid, int64_t on
   return t;
 }
 
-// Waves of a tile of 64 x 64: with fp32 results widening the codes is most of the work, and more waves share it (64 x 5120
-// x 2560: 23 us with eight, 34 with four; bf16 22 and 21, and less LDS leaves room for two workgroups).
-template <typename T> constexpr int few_waves() { return std::is_same_v<T, float> ? 8 : 4; }
+// Waves of the kernel for few rows: with fp32 results widening the codes is most of the work, and more waves share it
+// (64 x 2560 x 5120: 14.5 us with eight, 19.6 with four; bf16 12.3 and 12.7).
+constexpr int kFewWaves = 8;
+constexpr int kFewRows = 16;   // up to here one row of tiles of 16 x 16, and rows may be plain
 
-// A workgroup to a tile whose waves share k: 1.85 us a block (4 with fp32 results) for up to a workgroup to a CU.
-Tiling few(const Fp8ProductArgs& a, Kind kind, int side) {
-  Tiling t{kind, side, side, 0, 0, 0, 1, 0};
-  t.tiles = ((a.cols + side - 1) / side) * ((a.rows + side - 1) / side);
-  const int64_t waves = a.out_io ? few_waves<uint16_t>() : few_waves<float>();
-  const int64_t blocks = (fp8_blocks(a.k) + waves - 1) / waves * (a.out_io ? 1850 : 4000);
-  t.cost = 3000 + (t.tiles <= kCus ? blocks : blocks * t.tiles / kCus + blocks * 7 / 10);
+// A workgroup to a tile whose waves share k.  A workgroup on every CU takes one block of each wave in the time that stands
+// with each tile: the smaller tiles fill the chip where there are few, the larger ones read less (bf16: 32 x 2560 x 5120
+// 9.3, 7.1, 9.3 and 10.9 us on tiles of 16 x 16, 32 x 32, 64 x 32 and 64 x 64; 64 x 2560 x 5120 13.9, 11.5, 9.4 and 12.6; 300
+// x 2560 x 2560 29.5, 19.3, 16.1 and 12.8).
+Tiling few(const Fp8ProductArgs& a, Kind kind) {
+  struct Few {
+    int bc, br;
+    int64_t bf16, fp32;   // nanoseconds
+  };
+  constexpr Few kFews[] = {{64, 64, 3500, 4200}, {64, 32, 2400, 3100}, {32, 32, 1600, 1800}, {16, 16, 800, 850}};
+  const Few& f = kFews[kind - kFew64];
+  Tiling t{kind, f.bc, f.br, 0, 0, 0, 1, 0};
+  t.tiles = ((a.cols + f.bc - 1) / f.bc) * ((a.rows + f.br - 1) / f.br);
+  const int64_t blocks = (fp8_blocks(a.k) + kFewWaves - 1) / kFewWaves;
+  t.cost = 2200 + blocks * ((t.tiles + kCus - 1) / kCus) * (a.out_io ? f.bf16 : f.fp32);
   constexpr int kMostGrid = 1 << 20;   // (more are also slower, but where k is empty: those go to workgroups that stay)
   if (t.tiles > kMostGrid) t.cost = std::numeric_limits<int64_t>::max();
   t.grid = static_cast<int>(t.tiles < kMostGrid ? t.tiles : kMostGrid);
   return t;
 }
+// go(CT, RT) of a kind's kernel
+template <typename F> void with_few(Kind kind, F&& go) {
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
+  using Four = std::integral_constant<int, 4>;
+  if (kind == kFew64) go(Four{}, Four{});
+  else if (kind == kFew64x32) go(Four{}, Two{});
+  else if (kind == kFew32) go(Two{}, Two{});
+  else go(One{}, One{});
+}
 
 // The least time by what the kernels took (a step of 256 x 256 1.5 us, of 128 x 128 0.6 with one and 1.13 with two
-// workgroups on a CU, with fp32 results 1.65 and 2.15): for instance with 5120 x 2560, bf16: 8 rows 7.8 us on the waves'
+// workgroups on a CU, with fp32 results 1.65 and 2.15): for instance with 5120 x 2560, bf16: 8 rows 6.4 us on the waves'
 // kernel (tiles of 128 x 128 11), 128 rows 15.8 on tiles of 128 x 128 in four slices (27.4 unsliced, 21 on 64 x 64), 1001
 // x 777 x 1000 6.9 on 64 x 64 (8.5 on 128 x 128), 16384 rows of 2560 x 10240 383 on 256 x 256 (530 on 128 x 128).
 Tiling pick(const Fp8ProductArgs& a) {
-  if (a.rows <= 16) return few(a, kFew16, 16);
-  const Tiling small = a.out_io ? tiling(a, kSmall, 128, 2 * kCus, 600, 1130, 2000, 700)
-                                : tiling(a, kSmall, 128, 2 * kCus, 1650, 2150, 2000, 700);
-  const Tiling low = few(a, kFew64, 64);
-  const Tiling best = low.cost < small.cost ? low : small;
-  if (!a.out_io) return best;
-  const Tiling large = tiling(a, kLarge, 256, kCus, 1500, 1600, 4000, 500);
-  return large.cost < best.cost ? large : best;
+  Tiling best = few(a, kFew16);
+  if (a.rows <= kFewRows) return best;
+  auto or_this = [&](const Tiling& t) {
+    if (t.cost < best.cost) best = t;
+  };
+  or_this(few(a, kFew32));
+  or_this(few(a, kFew64x32));
+  or_this(few(a, kFew64));
+  or_this(a.out_io ? tiling(a, kSmall, 128, 2 * kCus, 600, 1130, 2000, 700)
+                   : tiling(a, kSmall, 128, 2 * kCus, 1650, 2150, 2000, 700));
+  if (a.out_io) or_this(tiling(a, kLarge, 256, kCus, 1500, 1600, 4000, 500));
+  return best;
 }
 
 }  // namespace
@@ -723,7 +739,7 @@ Tiling pick(const Fp8ProductArgs& a) {
 int64_t plain_bytes(const Fp8ProductArgs& a) { return a.rows * (fp8_blocks(a.k) * (kBlock + 1) + 16); }
 constexpr int64_t kMostPlain = 24 << 10;
 
-bool fp8_product_takes_plain(const Fp8ProductArgs& a) { return pick(a).kind == kFew16 && plain_bytes(a) <= kMostPlain; }
+bool fp8_product_takes_plain(const Fp8ProductArgs& a) { return a.rows <= kFewRows && plain_bytes(a) <= kMostPlain; }
 
 size_t fp8_product_workspace_bytes(const Fp8ProductArgs& a) {
   if (a.rows == 0 || a.cols == 0) return 0;
@@ -749,12 +765,14 @@ Fp8Params params(const Fp8ProductArgs& a, const Tiling& t) {
 hipError_t fp8_two_products_launch(const Fp8ProductArgs& a, const Fp8ProductArgs& b, hipStream_t stream) {
   if (a.rows > 0 && a.cols > 0 && b.rows > 0 && b.cols > 0 && a.out_io == b.out_io) {
     const Tiling t = pick(a), u = pick(b);
-    if (t.kind == kFew64 && u.kind == kFew64) {
+    if (t.kind == u.kind && t.kind >= kFew64) {
       const Fp8Params p = params(a, t), q = params(b, u);
       auto go = [&](auto out) {
         using T = decltype(out);
-        two_products_kernel<4, 4, few_waves<T>(), E4m3, T>
-            <<<dim3(static_cast<unsigned>(t.grid + u.grid)), few_waves<T>() * kLanes, 0, stream>>>(p, q, t.grid);
+        with_few(t.kind, [&](auto ct, auto rt) {
+          two_products_kernel<ct, rt, kFewWaves, E4m3, T>
+              <<<dim3(static_cast<unsigned>(t.grid + u.grid)), kFewWaves * kLanes, 0, stream>>>(p, q, t.grid);
+        });
       };
       if (a.out_io) go(uint16_t{});
       else go(float{});
@@ -785,11 +803,15 @@ hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream) {
         else tile_product_kernel<128, 128, 2, 2, false, T><<<grid, 256, 0, stream>>>(p);
         if (t.slices > 1) slices_kernel<128, 128, T><<<sum_grid, 256, 0, stream>>>(p);
         break;
-      case kFew64: few_product_kernel<4, 4, few_waves<T>(), E4m3, T><<<grid, few_waves<T>() * kLanes, 0, stream>>>(p); break;
-      case kFew16:
-        if (a.r.scales != nullptr) few_product_kernel<1, 1, 8, E4m3, T><<<grid, 512, 0, stream>>>(p);
-        else if (a.r_io) few_product_kernel<1, 1, 8, uint16_t, T><<<grid, 512, plain_bytes(a), stream>>>(p);
-        else few_product_kernel<1, 1, 8, float, T><<<grid, 512, plain_bytes(a), stream>>>(p);
+      default:
+        if (a.r.scales == nullptr) {
+          if (a.r_io) few_product_kernel<1, 1, kFewWaves, uint16_t, T><<<grid, kFewWaves * kLanes, plain_bytes(a), stream>>>(p);
+          else few_product_kernel<1, 1, kFewWaves, float, T><<<grid, kFewWaves * kLanes, plain_bytes(a), stream>>>(p);
+        } else {
+          with_few(t.kind, [&](auto ct, auto rt) {
+            few_product_kernel<ct, rt, kFewWaves, E4m3, T><<<grid, kFewWaves * kLanes, 0, stream>>>(p);
+          });
+        }
         break;
     }
   };

@@ -111,3 +111,37 @@ def test_no_tokens_many_tiles(M, accumulate):
                      accumulate=accumulate)
     want = 1.5 if accumulate else 0.0
     assert dw.min().item() == want and dw.max().item() == want
+
+
+# one for each tile of the kernel for few rows: 16 x 16, 32 x 32, 64 x 32, 64 x 64
+@pytest.mark.parametrize("square", [False, True], ids=["rows", "square"])
+@pytest.mark.parametrize("shape", [(33, 1000, 777), (29, 2500, 5003), (61, 2561, 5090), (301, 1000, 2561)], ids=str)
+def test_few_rows(M, shape, square):
+    tokens, k, n = shape
+    say("few rows of fp8 linear", shape, square)
+    g = gen(tokens)
+    x = M.fp8_quantize(rnd(g, tokens, k) * torch.exp(rnd(g, k)))
+    w = M.fp8_quantize(rnd(g, n, k) * torch.exp(rnd(g, n, 1)), square=square)
+    xv, wv = vals(M, x), vals(M, w)
+    for dt in (BF16, F32):
+        R.check(M.fp8_linear_fwd(x, w, out_dtype=dt), Q.product_of_values(xv, wv, dt, chunk=64), f"out {dt}")
+
+
+@pytest.mark.parametrize("io", [BF16, F32], ids=str)
+@pytest.mark.parametrize("shape", [(70, 130, 90), (300, 700, 600), (500, 1000, 1500), (40, 2560, 2000)], ids=str)
+def test_gradients_of_few_rows(M, shape, io):
+    """Both products small: side by side in one launch where their tiles are the same, else one after the other."""
+    tokens, k, n = shape
+    say("small gradients of fp8 linear", shape, io)
+    g = gen(tokens + n)
+    x = M.fp8_quantize(rnd(g, tokens, k))
+    wt = M.fp8_quantize(rnd(g, k, n) * k ** -0.5, square=True)
+    dout = (rnd(g, tokens, n) * 1e-3).to(io)
+    old = rnd(g, n, k).to(io)
+    d, dt = M.fp8_quantize(dout, both=True)
+    dw_rows, x_rows = vals(M, dt), vals(M, M.fp8_transpose(x))
+    for accumulate in (False, True):
+        dw = old.clone()
+        got = M.fp8_linear_bwd(x, wt, dout, dweight=dw, accumulate=accumulate)
+        R.check(got["dx"], Q.product_of_values(vals(M, d), vals(M, wt), io), "dx")
+        R.check(dw, Q.product_of_values(dw_rows, x_rows, io, old if accumulate else None), "dweight")
