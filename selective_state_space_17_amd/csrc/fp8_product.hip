@@ -8,6 +8,10 @@
 // largest product (measured: 1.2e-5 of the result's 2-norm for normally distributed values, 1 / 300 of bf16's own
 // rounding).  fp32 results are to be better than that: the codes are widened to bf16, which holds them and their
 // scales exactly, and the bf16 instructions' sums keep fp32's bits, at half the rate.
+//
+// Large products are bound by the matrix cores under the power limit (32768 x 2560 x 10240: 677 us, 2.5 PFLOP/s, matrix
+// cores busy 0.70 of the cycles at some 1.8 GHz; 8192^3: 415 us, 2.65), with fp32 results by the widening (1097 us: 16
+// cycles of a SIMD for two codes), few rows by latency and the weight's bytes (1 x 2560 x 10240: 7.1 us, 26 MB).
 #include <limits>
 #include <type_traits>
 #include <utility>
@@ -115,7 +119,7 @@ template <int V, typename T> __device__ __forceinline__ void put(T* to, float (&
 // fragments are read, and the place that it was read from before takes the loads of the half four ahead; one barrier
 // after each half, before which a wave waits for its loads of the half after the next, by count.  So a load has three
 // halves of multiplications to arrive in, and crosses the borders of tiles (with two whole steps in LDS and a barrier a
-// step it had two: 497 us at 8192^3, where this takes 448; a ring of eight halves was no faster).
+// step it had two: 497 us at 8192^3, where the ring took 448; a ring of eight halves was no faster).
 //
 // A wave holds TC x TR tiles of 32 x 32.  Of R, row i of tile t is row TR i + t of its share, of C row 2 TC (i % 16) +
 // TC (i / 16) + t: a lane's scales for its tiles are then neighbouring bytes of memory, one word, from which the

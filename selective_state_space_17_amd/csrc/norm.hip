@@ -79,6 +79,7 @@ template <typename T, typename R> __device__ __forceinline__ float norm_at(const
 
 // 8 neighbouring values of a row's output to 8 bits, 16 lanes together: a thread owns 8 columns an access and a row
 // starts with a wave's first thread, so a block of 128 columns is one row of 16 lanes.  y is 0 past the row's end.
+// Bound by memory as the norm itself is (32768 x 2560, bf16 with an fp32 stream: 175 us, 923 MB, 5.3 TB/s).
 __device__ __forceinline__ void put_fp8(const NormParams& p, int64_t row, int col, const float (&y)[8]) {
   const int blocks = static_cast<int>(fp8_blocks(p.dim));
   uint32_t scale;
