@@ -10,8 +10,8 @@
 // scales exactly, and the bf16 instructions' sums keep fp32's bits, at half the rate.
 //
 // Large products are bound by the matrix cores under the power limit (32768 x 2560 x 10240: 677 us, 2.5 PFLOP/s, matrix
-// cores busy 0.70 of the cycles at some 1.8 GHz; 8192^3: 415 us, 2.65), with fp32 results by the widening (1097 us: 16
-// cycles of a SIMD for two codes), few rows by latency and the weight's bytes (1 x 2560 x 10240: 7.1 us, 26 MB).
+// cores busy 0.70 of the cycles at some 1.8 GHz; 8192^3: 415 us, 2.65; with fp32 results 809 us, 1.36,
+// where the library's bf16 product takes 699), few rows by latency and the weight's bytes (1 x 2560 x 10240: 7.1 us, 26 MB).
 #include <limits>
 #include <type_traits>
 #include <utility>
@@ -40,16 +40,13 @@ struct Fp8Params {
   float* sums;                   // [slice][BR][BC]
 };
 
-// 8 codes (words 2 q and 2 q + 1) times s, as bf16: exact
-__device__ __forceinline__ bf16x8_t wide_codes(const i32x8_t& v, int q, float s) {
-  bf16x8_t o;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * q + h], s, false);
-    const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * q + h], s, true);
-    o[4 * h] = a[0]; o[4 * h + 1] = a[1]; o[4 * h + 2] = b[0]; o[4 * h + 3] = b[1];
-  }
-  return o;
+// 8 codes times s, as bf16: exact
+__device__ __forceinline__ bf16x8_t wide_codes(uint32_t lo, uint32_t hi, float s) {
+  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(static_cast<int>(lo), s, false);
+  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(static_cast<int>(lo), s, true);
+  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(static_cast<int>(hi), s, false);
+  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(static_cast<int>(hi), s, true);
+  return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
 // -------------------------------------------------------------------------------------------------- tiles
@@ -103,68 +100,28 @@ template <int BC, int BR> __device__ __forceinline__ Place place_of(const Fp8Par
           __builtin_amdgcn_readfirstlane((band * kBand + in_band % wide) * BR)};
 }
 
-// V neighbouring elements of a row of the output, the first `left` of which exist, to where they belong
-template <int V, typename T> __device__ __forceinline__ void put(T* to, float (&v)[V], int64_t left, int accumulate) {
-  if (accumulate) {
-    float o[V];
-    load_row<V>(to, o, left);
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] += o[e];
+// Jobs of a workgroup that stays.  Whole tiles as long as every workgroup gets one; the tiles of the last, partial round
+// are cut along k where that fills the chip, each slice with sums of its own that are added afterwards.  Workgroups b,
+// b + 8, ... share an XCD and its L2: each XCD takes a contiguous range of an order that walks bands of 4 tiles of R, C
+// outer.
+struct Job {
+  int c0, r0, sum, begin, steps;   // sum: which sums, or -1
+};
+template <int BC, int BR> struct Jobs {
+  const Fp8Params& p;
+  int rest, xcd, whole8, cut8, first, end, stride;
+  __device__ __forceinline__ explicit Jobs(const Fp8Params& q) : p(q) {
+    rest = p.tiles_c * p.tiles_r - p.whole;
+    const int cut = rest * p.slices;
+    xcd = blockIdx.x % 8;
+    stride = gridDim.x / 8;
+    whole8 = p.whole / 8;   // of an XCD
+    cut8 = (cut + 7) / 8;
+    const int mine = cut - xcd * cut8 < cut8 ? cut - xcd * cut8 : cut8;
+    first = blockIdx.x / 8;
+    end = whole8 + (mine > 0 ? mine : 0);
   }
-  store_row<V>(to, v, left);
-}
-
-// A workgroup stays on a CU (two of the small tile) and takes tile after tile, each 128 k (a block) a step, in halves of
-// 64 k.  Four halves are in LDS or on their way there.  While a half is multiplied from registers the next one's
-// fragments are read, and the place that it was read from before takes the loads of the half four ahead; one barrier
-// after each half, before which a wave waits for its loads of the half after the next, by count.  So a load has three
-// halves of multiplications to arrive in, and crosses the borders of tiles (with two whole steps in LDS and a barrier a
-// step it had two: 497 us at 8192^3, where the ring took 448; a ring of eight halves was no faster).
-//
-// A wave holds TC x TR tiles of 32 x 32.  Of R, row i of tile t is row TR i + t of its share, of C row 2 TC (i % 16) +
-// TC (i / 16) + t: a lane's scales for its tiles are then neighbouring bytes of memory, one word, from which the
-// instruction picks a byte.  R's rows are the matrix instructions' rows, so that a lane's accumulators are TC neighbours of
-// many output rows.  After lanes 16 apart have exchanged every other row they are 2 TC neighbours, and those of 16 lanes
-// are one stretch of a row, 128 bytes or more, which leaves in one store (in pieces of 64 bytes of 16 rows: 712 us for
-// 32768 x 2560 x 10240, as here 677; with rows that begin off a line, 10001 columns: 947 and 747).
-template <int BC, int BR, int WC, int WR, bool SQUARE, typename T>
-__global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params p) {
-  constexpr bool kFine = std::is_same_v<T, float>;
-  constexpr int kW = WC * WR;
-  constexpr int TC = BC / WC / 32, TR = BR / WR / 32;      // 32 x 32 tiles of a wave
-  constexpr int LC = BC / 16 / kW, LR = BR / 16 / kW;      // 1 KB loads of a wave per half
-  constexpr int kLoads = (LC + LR + TC - 1) / TC;          // loads between two rows of multiplications
-  constexpr int kReads = (TC + TR + TC - 1) / TC;          // fragments read there
-  constexpr int kAhead = 2 * (LC + LR) + 2;                // loads of two neighbouring halves, scales among them
-  constexpr int kStores = TR * 8;                          // a whole tile's stores of a wave
-  static_assert(LC * 16 * kW == BC && LR * 16 * kW == BR, "loads split evenly over the waves");
-  static_assert(TC == 2 || TC == 4, "a lane's scales of C are a word or half of one");
-  static_assert(!kFine || TC == 2, "a lane's run of fp32 is one store");
-  static_assert(TR == 2, "and those of R half of one");
-  static_assert(kAhead + kStores < 64, "what the wait instruction can count");
-  constexpr int kC = BC * kRow, kR = BR * kRow;            // bytes of a half
-  // LDS: four halves of C, four of R, the scales of two steps, each wave's own (C's, R's).  The ring's two steps lie a power
-  // of two apart, so that an exclusive or takes an address from one to the other.
-  constexpr int kS = kW * 2 * kLanes * 4;
-  __shared__ __attribute__((aligned(4 * kC))) unsigned char lds[4 * kC + 4 * kR + 2 * kS];
-  static_assert((kC & (kC - 1)) == 0 && kC == kR && (kS & (kS - 1)) == 0, "powers of two");
-  const int lane = threadIdx.x % kLanes;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
-  const int wc = w / WR, wr = w % WR;
-
-  // Jobs.  Whole tiles as long as every workgroup gets one; the tiles of the last, partial round are cut along k where
-  // that fills the chip, each slice with sums of its own that are added afterwards.  Workgroups b, b + 8, ... share an
-  // XCD and its L2: each XCD takes a contiguous range of an order that walks bands of 4 tiles of R, C outer.
-  const int tiles = p.tiles_c * p.tiles_r;
-  const int rest = tiles - p.whole, cut = rest * p.slices;
-  const int xcd = blockIdx.x % 8, stride = gridDim.x / 8;
-  const int whole8 = p.whole / 8, cut8 = (cut + 7) / 8;    // of an XCD
-  const int mine = cut - xcd * cut8 < cut8 ? cut - xcd * cut8 : cut8;
-  const int job_first = blockIdx.x / 8, job_end = whole8 + (mine > 0 ? mine : 0);
-  struct Job {
-    int c0, r0, sum, begin, steps;   // sum: which sums, or -1
-  };
-  auto job_at = [&](int i) {
+  __device__ __forceinline__ Job at(int i) const {
     Job j;
     int tile;
     if (i < whole8) {
@@ -185,15 +142,145 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
     j.c0 = at.c0;
     j.r0 = at.r0;
     return j;
-  };
+  }
+};
 
+// V neighbouring elements of a row of the output, the first `left` of which exist, to where they belong
+template <int V, typename T> __device__ __forceinline__ void put(T* to, float (&v)[V], int64_t left, int accumulate) {
+  if (accumulate) {
+    float o[V];
+    load_row<V>(to, o, left);
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] += o[e];
+  }
+  store_row<V>(to, v, left);
+}
+
+// A tile's, or a slice's, accumulators to where they belong; true where that is the whole tile's kStores stores of a wave.
+template <int BC, int BR, int WC, int WR, typename T>
+__device__ __forceinline__ bool way_out(const Fp8Params& p, const Job& cur, int lane, int wc, int wr,
+                                        f32x16_t (&acc)[BC / WC / 32][BR / WR / 32]) {
+  constexpr bool kFine = std::is_same_v<T, float>;
+  constexpr int TC = BC / WC / 32, TR = BR / WR / 32;
+      // accumulator e = 4 q + f of tile (i, j): R's row TR (8 q + 4 (lane / 32) + f) + j of the wave's share, and row i of
+      // C's that are the lane's.  Lanes 16 apart exchange f and f + 1.
+      constexpr int kRun = 2 * TC;
+      int wave_r = wr * TR * 32 + (lane / 32 * 4 + lane / 16 % 2) * TR;
+      asm volatile("" : "+v"(wave_r));   // (known before the loop over jobs, all the rows' places would be registers in it)
+      const int c = wc * TC * 32 + lane % 16 * kRun;
+      auto each = [&](auto&& to) {   // every pair of f: (row of the tile after wave_r, tile j, first accumulator)
+        unrolled<TR * 8>([&](auto i) {
+          constexpr int I = decltype(i)::value, J = I / 8, E = I % 8 * 2;
+          to(std::integral_constant<int, (E / 4 * 8 + E % 4) * TR + J>{}, std::integral_constant<int, J>{},
+             std::integral_constant<int, E>{});
+        });
+      };
+      // (way: which of the three below, so that the compiler does not take what two have in common before the branch, where
+      // a second set of accumulators finds no registers)
+      auto exchanged = [&](auto way, auto j, auto e, float (&v)[kRun]) {
+        constexpr int J = decltype(j)::value, E = decltype(e)::value;
+  #pragma unroll
+        for (int t = 0; t < TC; ++t) {
+          float a = acc[t][J][E];
+          asm volatile("" : "+v"(a) : "n"(decltype(way)::value));
+          const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(acc[t][J][E + 1]), false, false);
+          v[t] = __uint_as_float(x[0]);
+          v[TC + t] = __uint_as_float(x[1]);
+        }
+      };
+      if (cur.sum >= 0) {
+        float* const to = p.sums + static_cast<int64_t>(cur.sum) * BR * BC + wave_r * BC + c;
+        const int64_t rows = p.rows - cur.r0 - wave_r;
+        each([&](auto r, auto j, auto e) {
+          float v[kRun];
+          exchanged(std::integral_constant<int, 0>{}, j, e, v);
+          if (r < rows) store_row<kRun>(to + r * BC, v);
+        });
+      } else {
+        T* const tile = static_cast<T*>(p.out) + cur.r0 * p.cols + cur.c0;
+        const uint32_t at = static_cast<uint32_t>(wave_r * static_cast<int>(p.cols) + c) * sizeof(T);   // (cols <= 2^20)
+        auto to = [&](auto r) { return reinterpret_cast<T*>(reinterpret_cast<unsigned char*>(tile + r * p.cols) + at); };
+        const int64_t rows = p.rows - cur.r0, cols = p.cols - cur.c0;
+        if (rows >= BR && cols >= BC && !p.accumulate) {
+          // past the cache: kept there, the output pushes the operands out of it (32768 x 2560 x 10240, which writes 671 MB:
+          // 677 us, kept 730)
+          each([&](auto r, auto j, auto e) {
+            if constexpr (kFine) {
+              float v[kRun];
+              exchanged(std::integral_constant<int, 1>{}, j, e, v);
+              __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4_u*>(to(r)));
+            } else {
+              constexpr int J = decltype(j)::value, E = decltype(e)::value;
+              typedef uint32_t Run __attribute__((ext_vector_type(TC)));
+              typedef Run Run_u __attribute__((aligned(2)));
+              Run v;
+  #pragma unroll
+              for (int h = 0; h < TC / 2; ++h) {
+                const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16(acc[2 * h][J][E], acc[2 * h + 1][J][E]),
+                                                                pack_bf16(acc[2 * h][J][E + 1], acc[2 * h + 1][J][E + 1]),
+                                                                false, false);
+                v[h] = x[0];
+                v[TC / 2 + h] = x[1];
+              }
+              __builtin_nontemporal_store(v, reinterpret_cast<Run_u*>(to(r)));
+            }
+          });
+          return true;
+        } else {
+          each([&](auto r, auto j, auto e) {
+            float v[kRun];
+            exchanged(std::integral_constant<int, 2>{}, j, e, v);
+            if (r + wave_r < rows) put(to(r), v, cols - c, p.accumulate);
+          });
+        }
+      }
+  return false;
+}
+
+// A workgroup stays on a CU (two of the small tile) and takes tile after tile, each 128 k (a block) a step, in halves of
+// 64 k.  Four halves are in LDS or on their way there.  While a half is multiplied from registers the next one's
+// fragments are read, and the place that it was read from before takes the loads of the half four ahead; one barrier
+// after each half, before which a wave waits for its loads of the half after the next, by count.  So a load has three
+// halves of multiplications to arrive in, and crosses the borders of tiles (with two whole steps in LDS and a barrier a
+// step it had two: 497 us at 8192^3, where the ring took 448; a ring of eight halves was no faster).
+//
+// A wave holds TC x TR tiles of 32 x 32.  Of R, row i of tile t is row TR i + t of its share, of C row 2 TC (i % 16) +
+// TC (i / 16) + t: a lane's scales for its tiles are then neighbouring bytes of memory, one word, from which the
+// instruction picks a byte.  R's rows are the matrix instructions' rows, so that a lane's accumulators are TC neighbours of
+// many output rows.  After lanes 16 apart have exchanged every other row they are 2 TC neighbours, and those of 16 lanes
+// are one stretch of a row, 128 bytes or more, which leaves in one store (in pieces of 64 bytes of 16 rows: 712 us for
+// 32768 x 2560 x 10240, as here 677; with rows that begin off a line, 10001 columns: 947 and 747).
+template <int BC, int BR, int WC, int WR, bool SQUARE>
+__global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params p) {
+  constexpr int kW = WC * WR;
+  constexpr int TC = BC / WC / 32, TR = BR / WR / 32;      // 32 x 32 tiles of a wave
+  constexpr int LC = BC / 16 / kW, LR = BR / 16 / kW;      // 1 KB loads of a wave per half
+  constexpr int kLoads = (LC + LR + TC - 1) / TC;          // loads between two rows of multiplications
+  constexpr int kReads = (TC + TR + TC - 1) / TC;          // fragments read there
+  constexpr int kAhead = 2 * (LC + LR) + 2;                // loads of two neighbouring halves, scales among them
+  constexpr int kStores = TR * 8;                          // a whole tile's stores of a wave
+  static_assert(LC * 16 * kW == BC && LR * 16 * kW == BR, "loads split evenly over the waves");
+  static_assert(TC == 2 || TC == 4, "a lane's scales of C are a word or half of one");
+  static_assert(TR == 2, "and those of R half of one");
+  static_assert(kAhead + kStores < 64, "what the wait instruction can count");
+  constexpr int kC = BC * kRow, kR = BR * kRow;            // bytes of a half
+  // LDS: four halves of C, four of R, the scales of two steps, each wave's own (C's, R's).  The ring's two steps lie a power
+  // of two apart, so that an exclusive or takes an address from one to the other.
+  constexpr int kS = kW * 2 * kLanes * 4;
+  __shared__ __attribute__((aligned(4 * kC))) unsigned char lds[4 * kC + 4 * kR + 2 * kS];
+  static_assert((kC & (kC - 1)) == 0 && kC == kR && (kS & (kS - 1)) == 0, "powers of two");
+  const int lane = threadIdx.x % kLanes;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
+  const int wc = w / WR, wr = w % WR;
+
+  const Jobs<BC, BR> jobs(p);
   // ---- loads.  A load is 16 rows x 64 bytes, a lane's part row lane / 4 and the 16-byte chunk lane % 4 as stored.  The
   // chunk it holds is xor-ed with bits 2 and 3 of the row: the reads below, where 32 lanes read one chunk of 32 rows, are
   // served 16 lanes, 256 bytes, at a time, four rows of 64 bytes side by side.  LDS row 32 t + i of a wave's share holds
   // row TC i + t of it.  Rows past the matrix are its last row again.
   const int lrow = lane / 4;
   const uint32_t chunk = static_cast<uint32_t>(((lane % 4) ^ (lane / 16)) * 16);
-  int ljob = job_first, lleft = 0;           // job of the next loads, and its steps that they have not come to
+  int ljob = jobs.first, lleft = 0;           // job of the next loads, and its steps that they have not come to
   const unsigned char *lc = nullptr, *lr = nullptr, *lcs = nullptr, *lrs = nullptr;
   uint32_t oc[LC], orr[LR], ocs = 0, ors = 0;
   const uint32_t pitch = static_cast<uint32_t>(p.pitch);
@@ -208,8 +295,8 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
     }
   };
   auto start_load = [&]() {   // the next job with steps, if there is one; else the last loads are repeated
-    while (ljob < job_end) {
-      const Job j = job_at(ljob);
+    while (ljob < jobs.end) {
+      const Job j = jobs.at(ljob);
       if (j.steps > 0) {
         lleft = j.steps;
         offsets(p.cols - j.c0, TC, 1, oc);
@@ -225,7 +312,7 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
         ors = r < left_r ? r : static_cast<int>(left_r);
         return;
       }
-      ljob += stride;
+      ljob += jobs.stride;
     }
   };
   const uint32_t c_lds = lds_addr(lds), r_lds = c_lds + 4 * kC, s_lds = r_lds + 4 * kR + w * (2 * kLanes * 4);
@@ -251,8 +338,8 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
       lr += kBlock;
       lcs += p.c_lines;
       lrs += p.r_lines;
-    } else if (ljob < job_end) {
-      ljob += stride;
+    } else if (ljob < jobs.end) {
+      ljob += jobs.stride;
       start_load();
     }
   };
@@ -286,34 +373,13 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
   };
   auto multiply_row = [&](auto i, int h, const Scales& s) {
     constexpr int I = decltype(i)::value;
-    if constexpr (kFine) {
-      // 16 k at a time, every fragment widened once
-      float sc[TC], sr[TR];
-#pragma unroll
-      for (int c = 0; c < TC; ++c) sc[c] = fp8_power((s.c >> (8 * c)) & 255u);
-#pragma unroll
-      for (int r = 0; r < TR; ++r) sr[r] = fp8_power((s.r >> (8 * r)) & 255u);
-#pragma unroll
-      for (int q = I * 4 / TC; q < (I + 1) * 4 / TC; ++q) {
-        bf16x8_t b[TR];
-#pragma unroll
-        for (int r = 0; r < TR; ++r) b[r] = wide_codes(fr[h][r], q, sr[r]);
-#pragma unroll
-        for (int c = 0; c < TC; ++c) {
-          const bf16x8_t a = wide_codes(fc[h][c], q, sc[c]);
-#pragma unroll
-          for (int r = 0; r < TR; ++r) acc[c][r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[r], a, acc[c][r], 0, 0, 0);
-        }
-      }
-    } else {
-      unrolled<TR>([&](auto j) {
-        constexpr int J = decltype(j)::value;
-        acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fr[h][J], fc[h][I], acc[I][J], 0, 0, J,
-                                                                    static_cast<int>(s.r), I, static_cast<int>(s.c));
-        // stays here: the compiler knows of no reason not to move a multiplication to where its result is used
-        asm volatile("" : "+v"(acc[I][J]));
-      });
-    }
+    unrolled<TR>([&](auto j) {
+      constexpr int J = decltype(j)::value;
+      acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fr[h][J], fc[h][I], acc[I][J], 0, 0, J,
+                                                                  static_cast<int>(s.r), I, static_cast<int>(s.c));
+      // stays here: the compiler knows of no reason not to move a multiplication to where its result is used
+      asm volatile("" : "+v"(acc[I][J]));
+    });
   };
 
   int stored = 0;   // halves whose wait may leave the last tile's stores outstanding too
@@ -344,8 +410,8 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
     now = read_scales();
     turn_over();
   }
-  for (int job = job_first; job < job_end; job += stride) {
-    const Job cur = job_at(job);
+  for (int job = jobs.first; job < jobs.end; job += jobs.stride) {
+    const Job cur = jobs.at(job);
 #pragma unroll
     for (int i = 0; i < TC; ++i)
 #pragma unroll
@@ -387,81 +453,155 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
       loaded();
     }
 
-    // accumulator e = 4 q + f of tile (i, j): R's row TR (8 q + 4 (lane / 32) + f) + j of the wave's share, and row i of
-    // C's that are the lane's.  Lanes 16 apart exchange f and f + 1.
-    constexpr int kRun = 2 * TC;
-    int wave_r = wr * TR * 32 + (lane / 32 * 4 + lane / 16 % 2) * TR;
-    asm volatile("" : "+v"(wave_r));   // (known before the loop over jobs, all the rows' places would be registers in it)
-    const int c = wc * TC * 32 + lane % 16 * kRun;
-    auto each = [&](auto&& to) {   // every pair of f: (row of the tile after wave_r, tile j, first accumulator)
-      unrolled<TR * 8>([&](auto i) {
-        constexpr int I = decltype(i)::value, J = I / 8, E = I % 8 * 2;
-        to(std::integral_constant<int, (E / 4 * 8 + E % 4) * TR + J>{}, std::integral_constant<int, J>{},
-           std::integral_constant<int, E>{});
-      });
-    };
-    // (way: which of the three below, so that the compiler does not take what two have in common before the branch, where
-    // a second set of accumulators finds no registers)
-    auto exchanged = [&](auto way, auto j, auto e, float (&v)[kRun]) {
-      constexpr int J = decltype(j)::value, E = decltype(e)::value;
-#pragma unroll
-      for (int t = 0; t < TC; ++t) {
-        float a = acc[t][J][E];
-        asm volatile("" : "+v"(a) : "n"(decltype(way)::value));
-        const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(acc[t][J][E + 1]), false, false);
-        v[t] = __uint_as_float(x[0]);
-        v[TC + t] = __uint_as_float(x[1]);
-      }
-    };
-    if (cur.sum >= 0) {
-      float* const to = p.sums + static_cast<int64_t>(cur.sum) * BR * BC + wave_r * BC + c;
-      const int64_t rows = p.rows - cur.r0 - wave_r;
-      each([&](auto r, auto j, auto e) {
-        float v[kRun];
-        exchanged(std::integral_constant<int, 0>{}, j, e, v);
-        if (r < rows) store_row<kRun>(to + r * BC, v);
-      });
-    } else {
-      T* const tile = static_cast<T*>(p.out) + cur.r0 * p.cols + cur.c0;
-      const uint32_t at = static_cast<uint32_t>(wave_r * static_cast<int>(p.cols) + c) * sizeof(T);   // (cols <= 2^20)
-      auto to = [&](auto r) { return reinterpret_cast<T*>(reinterpret_cast<unsigned char*>(tile + r * p.cols) + at); };
-      const int64_t rows = p.rows - cur.r0, cols = p.cols - cur.c0;
-      if (rows >= BR && cols >= BC && !p.accumulate) {
-        // past the cache: kept there, the output pushes the operands out of it (32768 x 2560 x 10240, which writes 671 MB:
-        // 677 us, kept 730)
-        each([&](auto r, auto j, auto e) {
-          if constexpr (kFine) {
-            float v[kRun];
-            exchanged(std::integral_constant<int, 1>{}, j, e, v);
-            __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4_u*>(to(r)));
-          } else {
-            constexpr int J = decltype(j)::value, E = decltype(e)::value;
-            typedef uint32_t Run __attribute__((ext_vector_type(TC)));
-            typedef Run Run_u __attribute__((aligned(2)));
-            Run v;
-#pragma unroll
-            for (int h = 0; h < TC / 2; ++h) {
-              const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16(acc[2 * h][J][E], acc[2 * h + 1][J][E]),
-                                                              pack_bf16(acc[2 * h][J][E + 1], acc[2 * h + 1][J][E + 1]),
-                                                              false, false);
-              v[h] = x[0];
-              v[TC / 2 + h] = x[1];
-            }
-            __builtin_nontemporal_store(v, reinterpret_cast<Run_u*>(to(r)));
-          }
-        });
-        stored = 2;
-      } else {
-        each([&](auto r, auto j, auto e) {
-          float v[kRun];
-          exchanged(std::integral_constant<int, 2>{}, j, e, v);
-          if (r + wave_r < rows) put(to(r), v, cols - c, p.accumulate);
-        });
-      }
-    }
+    if (way_out<BC, BR, WC, WR, uint16_t>(p, cur, lane, wc, wr, acc)) stored = 2;
   }
   // the last loads may still be on their way into this workgroup's LDS
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// fp32 results.  Converting two codes takes a SIMD 16 cycles, half of what a matrix instruction of 32 x 32 x 16 does, so a
+// code is widened once a workgroup, on its way into LDS: from memory into registers, a half of 64 k ahead, and from there,
+// times its scale, into the bf16 half that is multiplied next.  Two halves in LDS and a barrier a half.  (Widened by every
+// wave that multiplies it: 1103 us at 8192^3, as here 809, 1.36 PFLOP/s; with tiles of 128 x 128, whose fragments are read
+// more often, 1031 to 1057.)
+// A thread has 16 codes of two of C's rows and of two of R's; rows lie in LDS as above, 128 bytes each, their chunks of
+// 16 bytes xor-ed with bits 1 to 3 of the row, which keeps writes and reads off each other's banks.
+template <int B, int WC, int WR, bool SQUARE>
+__global__ __launch_bounds__(WC * WR * 64, 2) void fine_product_kernel(Fp8Params p) {
+  constexpr int TC = B / WC / 32, TR = B / WR / 32;
+  constexpr int kRows = WC * WR * kLanes / 4;          // that threads have of either matrix at a time
+  static_assert(B == 2 * kRows, "two rows of either a thread");
+  constexpr int kLine = kBlock;                        // bytes of a row of half a step in bf16
+  constexpr int kMatrix = B * kLine, kBuffer = 2 * kMatrix;
+  __shared__ __attribute__((aligned(16))) unsigned char lds[2 * kBuffer];
+  const int lane = threadIdx.x % kLanes;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
+  const int wc = w / WR, wr = w % WR;
+  const Jobs<B, B> jobs(p);
+
+  const int lrow = threadIdx.x / 4, part = threadIdx.x % 4;   // rows lrow and lrow + kRows of either, codes 16 part on
+  int ljob = jobs.first, lleft = 0;
+  const unsigned char *lc = nullptr, *lr = nullptr, *lcs = nullptr, *lrs = nullptr;
+  uint32_t off[4], soff[4];   // C's rows, R's
+  auto start_load = [&]() {   // the next job with steps, if there is one; else the last loads are repeated
+    while (ljob < jobs.end) {
+      const Job j = jobs.at(ljob);
+      if (j.steps > 0) {
+        lleft = j.steps;
+        const int64_t left_c = p.cols - j.c0 - 1, left_r = p.rows - j.r0 - 1;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int at = h * kRows + lrow, i = at % 32;
+          const int c = at / (32 * TC) * (32 * TC) + (i % 16 * 2 + i / 16) * TC + at / 32 % TC;
+          const int r = at / (32 * TR) * (32 * TR) + i * TR + at / 32 % TR;
+          const int cc = c < left_c ? c : static_cast<int>(left_c), rr = r < left_r ? r : static_cast<int>(left_r);
+          off[h] = static_cast<uint32_t>(cc) * static_cast<uint32_t>(p.pitch) + part * 16;       // (pitch <= 2^22)
+          off[2 + h] = static_cast<uint32_t>(rr) * static_cast<uint32_t>(p.pitch) + part * 16;
+          soff[h] = SQUARE ? cc / kBlock : cc;
+          soff[2 + h] = rr;
+          asm volatile("" : "+v"(soff[h]));   // (a load known to be the same for all lanes would be waited for at once)
+        }
+        lc = p.c + static_cast<int64_t>(j.c0) * p.pitch + j.begin * kBlock;
+        lr = p.r + static_cast<int64_t>(j.r0) * p.pitch + j.begin * kBlock;
+        lcs = p.cs + j.begin * p.c_lines + (SQUARE ? j.c0 / kBlock : j.c0);
+        lrs = p.rs + j.begin * p.r_lines + j.r0;
+        return;
+      }
+      ljob += jobs.stride;
+    }
+  };
+  u32x4_t codes[4];
+  uint32_t scales[4];
+  auto load_one = [&](int m, int h) {
+    const unsigned char* const from = m < 2 ? lc : lr;
+    codes[m] = *reinterpret_cast<const u32x4_t*>(from + off[m] + h * (kBlock / 2));
+  };
+  auto load_scale = [&](int m) { scales[m] = (m < 2 ? lcs : lrs)[soff[m]]; };
+  auto loaded = [&]() {   // after a step's last load
+    if (lleft > 1) {
+      --lleft;
+      lc += kBlock;
+      lr += kBlock;
+      lcs += p.c_lines;
+      lrs += p.r_lines;
+    } else if (ljob < jobs.end) {
+      ljob += jobs.stride;
+      start_load();
+    }
+  };
+  unsigned char* const put_at = lds + lrow * kLine + (((part * 2) ^ (lrow / 2 % 8)) << 4);
+  const int put_next = (((part * 2 + 1) ^ (lrow / 2 % 8)) << 4) - (((part * 2) ^ (lrow / 2 % 8)) << 4);
+  auto widen_one = [&](int m, int h) {   // codes[m] to half h
+    const float s = fp8_power(scales[m]);
+    unsigned char* const to = put_at + h * kBuffer + m / 2 * kMatrix + m % 2 * kRows * kLine;
+    *reinterpret_cast<bf16x8_t*>(to) = wide_codes(codes[m][0], codes[m][1], s);
+    *reinterpret_cast<bf16x8_t*>(to + put_next) = wide_codes(codes[m][2], codes[m][3], s);
+  };
+  const unsigned char *fc_at[4], *fr_at[4];   // fragments of 16 k
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int at = lane % 32 * kLine + (((2 * q + lane / 32) ^ (lane / 2 % 8)) << 4);
+    fc_at[q] = lds + wc * (32 * TC * kLine) + at;
+    fr_at[q] = lds + kMatrix + wr * (32 * TR * kLine) + at;
+  }
+  f32x16_t acc[TC][TR];
+  bf16x8_t fc[2][TC], fr[2][TR];
+  auto read = [&](int q, int h) {
+#pragma unroll
+    for (int t = 0; t < TR; ++t) fr[q % 2][t] = *reinterpret_cast<const bf16x8_t*>(fr_at[q] + h * kBuffer + t * 32 * kLine);
+#pragma unroll
+    for (int t = 0; t < TC; ++t) fc[q % 2][t] = *reinterpret_cast<const bf16x8_t*>(fc_at[q] + h * kBuffer + t * 32 * kLine);
+  };
+  auto meet = [&]() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  start_load();
+  if (lleft > 0) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      load_one(m, 0);
+      load_scale(m);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      widen_one(m, 0);
+      load_one(m, 1);
+    }
+    meet();
+  }
+  for (int job = jobs.first; job < jobs.end; job += jobs.stride) {
+    const Job cur = jobs.at(job);
+#pragma unroll
+    for (int i = 0; i < TC; ++i)
+#pragma unroll
+      for (int j = 0; j < TR; ++j) acc[i][j] = f32x16_t{};
+    for (int s = 0; s < cur.steps; ++s) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // in registers: step s's second half while its first is multiplied, the next step's first half then
+        if (h == 0) loaded();
+        read(0, h);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (q < 3) read(q + 1, h);
+          widen_one(q, h ^ 1);
+          load_one(q, h);
+          if (h == 0) load_scale(q);
+#pragma unroll
+          for (int c = 0; c < TC; ++c)
+#pragma unroll
+            for (int r = 0; r < TR; ++r)
+              acc[c][r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[q % 2][r], fc[q % 2][c], acc[c][r], 0, 0, 0);
+          fence_schedule();
+        }
+        meet();
+      }
+    }
+    way_out<B, B, WC, WR, float>(p, cur, lane, wc, wr, acc);
+  }
 }
 
 // Adds the slices of the tiles of the last round, in order: workgroup (tile, share of its rows).
@@ -565,10 +705,10 @@ __device__ __forceinline__ void few_product(const Fp8Params& p, unsigned group, 
       for (int q = 0; q < 4; ++q) {
         bf16x8_t b[RT];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) b[r] = wide_codes(v.r[r], q, fp8_power((v.sr >> (8 * r)) & 255u));
+        for (int r = 0; r < RT; ++r) b[r] = wide_codes(v.r[r][2 * q], v.r[r][2 * q + 1], fp8_power((v.sr >> (8 * r)) & 255u));
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
-          const bf16x8_t a = wide_codes(v.c[c], q, fp8_power((v.sc >> (8 * c)) & 255u));
+          const bf16x8_t a = wide_codes(v.c[c][2 * q], v.c[c][2 * q + 1], fp8_power((v.sc >> (8 * c)) & 255u));
 #pragma unroll
           for (int r = 0; r < RT; ++r) acc[c][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[r], acc[c][r], 0, 0, 0);
         }
@@ -719,9 +859,10 @@ template <typename F> void with_few(Kind kind, F&& go) {
 }
 
 // The least time by what the kernels took (a step of 256 x 256 1.5 us, of 128 x 128 0.6 with one and 1.13 with two
-// workgroups on a CU, with fp32 results 1.65 and 2.15): for instance with 5120 x 2560, bf16: 8 rows 6.4 us on the waves'
-// kernel (tiles of 128 x 128 11), 128 rows 15.8 on tiles of 128 x 128 in four slices (27.4 unsliced, 21 on 64 x 64), 1001
-// x 777 x 1000 6.9 on 64 x 64 (8.5 on 128 x 128), 16384 rows of 2560 x 10240 383 on 256 x 256 (530 on 128 x 128).
+// workgroups on a CU; with fp32 results 3.1, 1.3 and 2.0): for instance, bf16: 8 x 5120 x 2560 5.9 us on tiles of 16 x 16
+// (11 on 128 x 128), 1001 x 1000 x 777 7.3 on 64 x 64 (8.5), 128 x 5120 x 2560 15.8 on 128 x 128 in four slices (27.4
+// unsliced, 21 on 64 x 64), 16384 x 10240 x 2560 383 on 256 x 256 (530 on 128 x 128); fp32: 4096 x 1536 x 768 17.8 on 128 x
+// 128, 34.5 on 256 x 256, and 4096^3 138 and 108.
 Tiling pick(const Fp8ProductArgs& a) {
   Tiling best = few(a, kFew16);
   if (a.rows <= kFewRows) return best;
@@ -732,8 +873,8 @@ Tiling pick(const Fp8ProductArgs& a) {
   or_this(few(a, kFew64x32));
   or_this(few(a, kFew64));
   or_this(a.out_io ? tiling(a, kSmall, 128, 2 * kCus, 600, 1130, 2000, 700)
-                   : tiling(a, kSmall, 128, 2 * kCus, 1650, 2150, 2000, 700));
-  if (a.out_io) or_this(tiling(a, kLarge, 256, kCus, 1500, 1600, 4000, 500));
+                   : tiling(a, kSmall, 128, 2 * kCus, 1300, 2000, 2000, 700));
+  or_this(a.out_io ? tiling(a, kLarge, 256, kCus, 1500, 1600, 4000, 500) : tiling(a, kLarge, 256, kCus, 3000, 3200, 6000, 500));
   return best;
 }
 
@@ -797,14 +938,22 @@ hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream) {
     switch (t.kind) {
       case kLarge:
         if constexpr (std::is_same_v<T, uint16_t>) {
-          if (p.square) tile_product_kernel<256, 256, 2, 4, true, T><<<grid, 512, 0, stream>>>(p);
-          else tile_product_kernel<256, 256, 2, 4, false, T><<<grid, 512, 0, stream>>>(p);
-          if (t.slices > 1) slices_kernel<256, 256, T><<<sum_grid, 256, 0, stream>>>(p);
+          if (p.square) tile_product_kernel<256, 256, 2, 4, true><<<grid, 512, 0, stream>>>(p);
+          else tile_product_kernel<256, 256, 2, 4, false><<<grid, 512, 0, stream>>>(p);
+        } else {
+          if (p.square) fine_product_kernel<256, 4, 2, true><<<grid, 512, 0, stream>>>(p);
+          else fine_product_kernel<256, 4, 2, false><<<grid, 512, 0, stream>>>(p);
         }
+        if (t.slices > 1) slices_kernel<256, 256, T><<<sum_grid, 256, 0, stream>>>(p);
         break;
       case kSmall:
-        if (p.square) tile_product_kernel<128, 128, 2, 2, true, T><<<grid, 256, 0, stream>>>(p);
-        else tile_product_kernel<128, 128, 2, 2, false, T><<<grid, 256, 0, stream>>>(p);
+        if constexpr (std::is_same_v<T, uint16_t>) {
+          if (p.square) tile_product_kernel<128, 128, 2, 2, true><<<grid, 256, 0, stream>>>(p);
+          else tile_product_kernel<128, 128, 2, 2, false><<<grid, 256, 0, stream>>>(p);
+        } else {
+          if (p.square) fine_product_kernel<128, 2, 2, true><<<grid, 256, 0, stream>>>(p);
+          else fine_product_kernel<128, 2, 2, false><<<grid, 256, 0, stream>>>(p);
+        }
         if (t.slices > 1) slices_kernel<128, 128, T><<<sum_grid, 256, 0, stream>>>(p);
         break;
       default:

