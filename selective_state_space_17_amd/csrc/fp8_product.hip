@@ -317,7 +317,8 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
   };
   const uint32_t c_lds = lds_addr(lds), r_lds = c_lds + 4 * kC, s_lds = r_lds + 4 * kR + w * (2 * kLanes * 4);
   // where the ring's step that takes loads lies
-  uint32_t c_to = __builtin_amdgcn_readfirstlane(c_lds + w * 1024), r_to = c_to + 4 * kC, s_to = __builtin_amdgcn_readfirstlane(s_lds);
+  uint32_t c_to = __builtin_amdgcn_readfirstlane(c_lds + w * 1024), r_to = c_to + 4 * kC;
+  uint32_t s_to = __builtin_amdgcn_readfirstlane(s_lds);
   // load i of half h of a step
   auto load_one = [&](auto i, auto h) {
     constexpr int I = decltype(i)::value, H = decltype(h)::value;
@@ -799,8 +800,8 @@ constexpr int kMostSlices = 32;
 
 // Tiles on workgroups that stay.  one, two: nanoseconds of a step with one and with two workgroups on a CU; round: of a
 // tile's way out.  Slices of the last, partial round: those that take the least time, with 3 us for the second launch and
-// the sums' way through memory (measured, tiles of 128 x 128: some 0.7 us a MB, of 256 x 256 0.5).  At most two rounds of
-// slices, which bounds the sums' memory.
+// the sums' way through memory (measured: 0.45 to 0.5 us a MB; 256 x 5120 x 2560 18.8 us in four slices, 21.2 on 64 x
+// 64).  At most two rounds of slices, which bounds the sums' memory.
 Tiling tiling(const Fp8ProductArgs& a, Kind kind, int side, int grid, int64_t one, int64_t two, int64_t round, int64_t mb) {
   Tiling t{kind, side, side, grid, 0, 0, 1, 0};
   const int64_t tiles_r = (a.rows + side - 1) / side, steps = fp8_blocks(a.k);
@@ -822,26 +823,26 @@ Tiling tiling(const Fp8ProductArgs& a, Kind kind, int side, int grid, int64_t on
   return t;
 }
 
-// Waves of the kernel for few rows: with fp32 results widening the codes is most of the work, and more waves share it
-// (64 x 2560 x 5120: 14.5 us with eight, 19.6 with four; bf16 12.3 and 12.7).
+// Waves of the kernel for few rows (64 x 2560 x 5120 on tiles of 64 x 64: fp32, where widening the codes is most of the
+// work, 14.5 us with eight and 19.6 with four; bf16 12.3 and 12.7).
 constexpr int kFewWaves = 8;
 constexpr int kFewRows = 16;   // up to here one row of tiles of 16 x 16, and rows may be plain
 
 // A workgroup to a tile whose waves share k.  A workgroup on every CU takes one block of each wave in the time that stands
 // with each tile: the smaller tiles fill the chip where there are few, the larger ones read less (bf16: 32 x 2560 x 5120
-// 9.3, 7.1, 9.3 and 10.9 us on tiles of 16 x 16, 32 x 32, 64 x 32 and 64 x 64; 64 x 2560 x 5120 13.9, 11.5, 9.4 and 12.6; 300
-// x 2560 x 2560 29.5, 19.3, 16.1 and 12.8).
+// 9.3, 7.1, 9.3 and 10.9 us on tiles of 16 x 16, 32 x 32, 64 x 32 and 64 x 64; 64 x 2560 x 5120 13.9, 11.5, 9.4 and 12.6;
+// 300 x 2560 x 2560 29.5, 19.3, 16.1 and 12.8; fp32 within a twentieth of that).
 Tiling few(const Fp8ProductArgs& a, Kind kind) {
   struct Few {
     int bc, br;
-    int64_t bf16, fp32;   // nanoseconds
+    int64_t block;   // nanoseconds
   };
-  constexpr Few kFews[] = {{64, 64, 3500, 4200}, {64, 32, 2400, 3100}, {32, 32, 1600, 1800}, {16, 16, 800, 850}};
+  constexpr Few kFews[] = {{64, 64, 3500}, {64, 32, 2400}, {32, 32, 1600}, {16, 16, 800}};
   const Few& f = kFews[kind - kFew64];
   Tiling t{kind, f.bc, f.br, 0, 0, 0, 1, 0};
   t.tiles = ((a.cols + f.bc - 1) / f.bc) * ((a.rows + f.br - 1) / f.br);
   const int64_t blocks = (fp8_blocks(a.k) + kFewWaves - 1) / kFewWaves;
-  t.cost = 2200 + blocks * ((t.tiles + kCus - 1) / kCus) * (a.out_io ? f.bf16 : f.fp32);
+  t.cost = 2200 + blocks * ((t.tiles + kCus - 1) / kCus) * f.block;
   constexpr int kMostGrid = 1 << 20;   // (more are also slower, but where k is empty: those go to workgroups that stay)
   if (t.tiles > kMostGrid) t.cost = std::numeric_limits<int64_t>::max();
   t.grid = static_cast<int>(t.tiles < kMostGrid ? t.tiles : kMostGrid);
@@ -859,7 +860,7 @@ template <typename F> void with_few(Kind kind, F&& go) {
 }
 
 // The least time by what the kernels took (a step of 256 x 256 1.5 us, of 128 x 128 0.6 with one and 1.13 with two
-// workgroups on a CU; with fp32 results 3.1, 1.3 and 2.0): for instance, bf16: 8 x 5120 x 2560 5.9 us on tiles of 16 x 16
+// workgroups on a CU; with fp32 results 3.1, 1.1 and 2.0): for instance, bf16: 8 x 5120 x 2560 5.9 us on tiles of 16 x 16
 // (11 on 128 x 128), 1001 x 1000 x 777 7.3 on 64 x 64 (8.5), 128 x 5120 x 2560 15.8 on 128 x 128 in four slices (27.4
 // unsliced, 21 on 64 x 64), 16384 x 10240 x 2560 383 on 256 x 256 (530 on 128 x 128); fp32: 4096 x 1536 x 768 17.8 on 128 x
 // 128, 34.5 on 256 x 256, and 4096^3 138 and 108.
@@ -872,9 +873,10 @@ Tiling pick(const Fp8ProductArgs& a) {
   or_this(few(a, kFew32));
   or_this(few(a, kFew64x32));
   or_this(few(a, kFew64));
-  or_this(a.out_io ? tiling(a, kSmall, 128, 2 * kCus, 600, 1130, 2000, 700)
-                   : tiling(a, kSmall, 128, 2 * kCus, 1300, 2000, 2000, 700));
-  or_this(a.out_io ? tiling(a, kLarge, 256, kCus, 1500, 1600, 4000, 500) : tiling(a, kLarge, 256, kCus, 3000, 3200, 6000, 500));
+  or_this(a.out_io ? tiling(a, kSmall, 128, 2 * kCus, 600, 1130, 2000, 450)
+                   : tiling(a, kSmall, 128, 2 * kCus, 1100, 2000, 2000, 450));
+  or_this(a.out_io ? tiling(a, kLarge, 256, kCus, 1500, 1600, 4000, 500)
+                   : tiling(a, kLarge, 256, kCus, 3000, 3200, 6000, 500));
   return best;
 }
 
