@@ -18,7 +18,7 @@ def M():
     return m
 
 
-# rows that go to the kernel of few rows, to tiles of 64 x 64, of 128 x 128 and of 256 x 256
+# sizes for the kernel for few rows and, the larger two, for the kernels with tiles of 128 x 128 and 256 x 256
 SHAPES = [(9, 300, 70), (60, 300, 200), (700, 300, 4000), (9000, 129, 3001)]
 
 
