@@ -91,3 +91,30 @@ def test_two_streams_at_once(M):
     for i, (out, grads) in enumerate(got):
         _, _, _, _, want, wanted = sets[i % 2]
         assert torch.equal(out, want) and all(torch.equal(grads[k], wanted[k]) for k in wanted)
+
+
+@pytest.mark.parametrize("shape", [(4096, 768, 640), (300, 700, 600)], ids=["slices", "pair"])
+def test_gradients_replayed(M, shape):
+    """Gradients captured once, with sums of slices in the workspace or both products in one launch, and replayed with new
+    inputs and other work on the GPU between: every replay is the eager call's result."""
+    tokens, k, n = shape
+    say("fp8 gradients in a graph", shape)
+    g = torch.Generator(device="cuda").manual_seed(k)
+
+    def rnd(*s):
+        return torch.randn(*s, generator=g, device="cuda")
+
+    x, wt = M.fp8_quantize(rnd(tokens, k)), M.fp8_quantize(rnd(k, n), square=True)
+    dout = rnd(tokens, n).to(BF16)
+    M.fp8_linear_bwd(x, wt, dout, dweight_dtype=F32)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = M.fp8_linear_bwd(x, wt, dout, dweight_dtype=F32)
+    for _ in range(4):
+        dout.copy_(rnd(tokens, n))
+        M.fp8_quantize(rnd(tokens, k), out=x)
+        want = M.fp8_linear_bwd(x, wt, dout, dweight_dtype=F32)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got["dx"], want["dx"]) and torch.equal(got["dweight"], want["dweight"])
