@@ -75,7 +75,8 @@ Fwd plan_fwd(const mssm_fp8_linear_desc& d, void* workspace) {
   Pieces w{static_cast<unsigned char*>(workspace)};
   f.product.rows = d.tokens; f.product.cols = d.out_features; f.product.k = d.in_features;
   f.product.square = d.weight_kind == MSSM_FP8_SQUARE; f.product.out_io = d.io_dtype; f.product.r_io = d.x_dtype;
-  f.rounds = d.x_dtype != MSSM_E4M3 && !mssm::fp8_product_takes_plain(f.product);
+  f.product.plain = d.x_dtype != MSSM_E4M3 && mssm::fp8_product_takes_plain(f.product);
+  f.rounds = d.x_dtype != MSSM_E4M3 && !f.product.plain;
   if (f.rounds) f.x = w.matrix(d.tokens, d.in_features);
   f.product.workspace = w.take(mssm::fp8_product_workspace_bytes(f.product));
   f.bytes = w.used;

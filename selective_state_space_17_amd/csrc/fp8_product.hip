@@ -843,7 +843,7 @@ Tiling few(const Fp8ProductArgs& a, Kind kind) {
   t.tiles = ((a.cols + f.bc - 1) / f.bc) * ((a.rows + f.br - 1) / f.br);
   const int64_t blocks = (fp8_blocks(a.k) + kFewWaves - 1) / kFewWaves;
   t.cost = 2200 + blocks * ((t.tiles + kCus - 1) / kCus) * f.block;
-  constexpr int kMostGrid = 1 << 20;   // (more are also slower, but where k is empty: those go to workgroups that stay)
+  constexpr int kMostGrid = 1 << 20;   // (more are also slower than on workgroups that stay)
   if (t.tiles > kMostGrid) t.cost = std::numeric_limits<int64_t>::max();
   t.grid = static_cast<int>(t.tiles < kMostGrid ? t.tiles : kMostGrid);
   return t;
@@ -864,7 +864,9 @@ template <typename F> void with_few(Kind kind, F&& go) {
 // (11 on 128 x 128), 1001 x 1000 x 777 7.3 on 64 x 64 (8.5), 128 x 5120 x 2560 15.8 on 128 x 128 in four slices (27.4
 // unsliced, 21 on 64 x 64), 16384 x 10240 x 2560 383 on 256 x 256 (530 on 128 x 128); fp32: 4096 x 1536 x 768 17.8 on 128 x
 // 128, 34.5 on 256 x 256, and 4096^3 138 and 108.
+// No k: zeros, which the workgroups that stay write without a load.
 Tiling pick(const Fp8ProductArgs& a) {
+  if (a.k == 0) return tiling(a, kSmall, 128, 2 * kCus, 0, 0, 2000, 0);
   Tiling best = few(a, kFew16);
   if (a.rows <= kFewRows) return best;
   auto or_this = [&](const Tiling& t) {
@@ -931,8 +933,9 @@ hipError_t fp8_two_products_launch(const Fp8ProductArgs& a, const Fp8ProductArgs
 }
 
 hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream) {
-  if (a.rows == 0 || a.cols == 0) return hipSuccess;
+  if (a.rows == 0 || a.cols == 0 || (a.k == 0 && a.accumulate)) return hipSuccess;
   const Tiling t = pick(a);
+  if (a.plain && (!fp8_product_takes_plain(a) || t.kind != kFew16)) return hipErrorInvalidValue;
   const Fp8Params p = params(a, t);
   const dim3 grid(static_cast<unsigned>(t.grid)), sum_grid(static_cast<unsigned>((t.tiles - t.whole) * kShares));
   auto go = [&](auto out) {
@@ -959,7 +962,7 @@ hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream) {
         if (t.slices > 1) slices_kernel<128, 128, T><<<sum_grid, 256, 0, stream>>>(p);
         break;
       default:
-        if (a.r.scales == nullptr) {
+        if (a.plain) {
           if (a.r_io) few_product_kernel<1, 1, kFewWaves, uint16_t, T><<<grid, kFewWaves * kLanes, plain_bytes(a), stream>>>(p);
           else few_product_kernel<1, 1, kFewWaves, float, T><<<grid, kFewWaves * kLanes, plain_bytes(a), stream>>>(p);
         } else {

@@ -244,7 +244,7 @@ hipError_t xent_bwd_launch(const XentArgs& a, hipStream_t stream);
 // ---------------------------------------------------------------------------
 // 8-bit linear layer
 // ---------------------------------------------------------------------------
-// a matrix in 8 bits (layout: fp8_util.h), or a plain one where scales is null
+// a matrix in 8 bits (layout: fp8_util.h)
 struct Fp8View {
   void* codes = nullptr;
   void* scales = nullptr;
@@ -269,7 +269,8 @@ hipError_t fp8_both_launch(const Fp8Args& plain, const Fp8Args& packed, hipStrea
 // out[r, c] (+)= sum over k of R[r, k] C[c, k]
 struct Fp8ProductArgs {
   int64_t rows, cols, k;
-  Fp8View r;             // row scales; a plain matrix (r_io: 0 fp32, 1 bf16) without scales where that is taken
+  Fp8View r;             // row scales
+  int plain;             // r.codes is a plain matrix (r_io: 0 fp32, 1 bf16) instead: only where fp8_product_takes_plain()
   int r_io;
   Fp8View c;
   int square;            // C's scales
@@ -279,9 +280,10 @@ struct Fp8ProductArgs {
   void* workspace;
 };
 
-// whether R may be a plain matrix, which is then rounded on the way (the sizes and out_io decide)
+// whether R may be a plain matrix, which is then rounded on the way (the sizes decide)
 bool fp8_product_takes_plain(const Fp8ProductArgs& a);
 size_t fp8_product_workspace_bytes(const Fp8ProductArgs& a);
+// (of no k: zeros, or with accumulate nothing; operands may then be null)
 hipError_t fp8_product_launch(const Fp8ProductArgs& a, hipStream_t stream);
 // one after the other (they may share a workspace), or side by side in one launch where either is small
 hipError_t fp8_two_products_launch(const Fp8ProductArgs& a, const Fp8ProductArgs& b, hipStream_t stream);
