@@ -698,9 +698,11 @@ int mssm_norm_fp8_fwd(const mssm_norm_desc* desc, const void* x, const void* res
  * bf16 come from the 8-bit matrix instructions, which drop what lies some 14
  * bits below the largest of 8 neighbouring products (2^-13 of it at most each:
  * some 1e-5 of the result in the mean square); results in fp32 from products
- * that are kept whole, at up to twice the time, of the values as fp32 numbers
- * (codes * scales beyond 2^128 are infinite there).  A NaN, among codes or
- * scales, reaches the outputs that its row or column enters.
+ * that are kept whole, at up to twice the time, of the values as bf16 numbers:
+ * all of them exactly under scales from 2^-124 on; under smaller ones those
+ * below 2^-126 to the nearest multiple of 2^-133, halves to even; codes *
+ * scales beyond 2^128 are infinite there.  A NaN, among codes or scales,
+ * reaches the outputs that its row or column enters.
  * tokens may be 0 (dweight is then zeroed, or left as it is with accumulate),
  * up to 2^22; features up to 2^20 (MSSM_ERR_UNSUPPORTED above).  codes are
  * 16-byte, scales 4-byte, others element-aligned.  workspace: at least the

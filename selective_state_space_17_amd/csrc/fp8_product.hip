@@ -6,8 +6,10 @@
 // bf16 results: the 8-bit matrix instructions with a scale, 128 k at a time, which is one block: they multiply by the
 // two e8m0 scales themselves and sum in fp32.  Within 8 neighbouring k they drop what lies some 14 bits below the
 // largest product (measured: 1.2e-5 of the result's 2-norm for normally distributed values, 1 / 300 of bf16's own
-// rounding).  fp32 results are to be better than that: the codes are widened to bf16, which holds them and their
-// scales exactly, and the bf16 instructions' sums keep fp32's bits, at half the rate.
+// rounding).  fp32 results are to be better than that: the codes are widened to bf16, and the bf16 instructions' sums keep
+// fp32's bits, at half the rate.  bf16 holds a code times its scale exactly from 2^-124 on (e4m3 ends at 2^-9 of it, bf16 at
+// 2^-133); under the scales 2^-127 to 2^-125 the smallest 24, 16 and 8 magnitudes become multiples of 2^-133, halves to
+// even.  (A factor that lifts one operand's smallest values would take as much from its largest.)
 //
 // Large products are bound by the matrix cores under the power limit (32768 x 2560 x 10240: 677 us, 2.5 PFLOP/s, matrix
 // cores busy 0.70 of the cycles at some 1.8 GHz; 8192^3: 415 us, 2.65; with fp32 results 809 us, 1.36,
@@ -40,7 +42,7 @@ struct Fp8Params {
   float* sums;                   // [slice][BR][BC]
 };
 
-// 8 codes times s, as bf16: exact
+// 8 codes times s, as bf16: exact from s = 2^-124 on (above)
 __device__ __forceinline__ bf16x8_t wide_codes(uint32_t lo, uint32_t hi, float s) {
   const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(static_cast<int>(lo), s, false);
   const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(static_cast<int>(lo), s, true);
