@@ -650,6 +650,10 @@ size_t mssm_linear_cross_entropy_bwd_workspace_size(const mssm_cross_entropy_des
  *                         its code's bits but below 2^-6 of its new block's scale.
  *   mssm_fp8_dequantize : values back (io_dtype, rounded once; exact in fp32, and
  *                         in bf16 from 2^-126 on)
+ * Values beyond fp32's range, 2^128 and more (mssm_fp8_quantize rounds what is
+ * 248 x 2^120 or more to 2^128; larger ones come from elsewhere), become
+ * infinities in mssm_fp8_dequantize, and NaN in mssm_fp8_transpose and in the
+ * dweight that they enter; no other value changes.
  * (mssm_fp8_transpose takes no notice of io_dtype.)
  * rows may be 0; rows and cols up to 2^22 (MSSM_ERR_UNSUPPORTED above).  codes
  * are 16-byte, scales 4-byte, others element-aligned.  Other rules as

@@ -45,3 +45,31 @@ def test_smallest_values(M, shape, byte, turned):
     for dtype, want in ((BF16, v), (F32, near)):
         got = M.fp8_linear_fwd(w, x, out_dtype=dtype).T if turned else M.fp8_linear_fwd(x, w, out_dtype=dtype)
         assert torch.equal(got.cpu().to(F64), (want * 2.0 ** 100)[:, None].expand(rows, n)), dtype
+
+
+def test_values_beyond_fp32(M):
+    """2^128 and more, which no fp32 number is: infinite as fp32 or bf16, NaN laid out the other way, and nothing else in
+    their rows and columns changes; the smallest such values are what fp8_quantize makes of fp32's largest."""
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(9, 300, generator=g)
+    border = 248 * 2.0 ** 120                            # between 240 and 256 under the scale 2^120: to the even one, 256
+    below = float(torch.nextafter(torch.tensor(border), torch.tensor(0.0)))
+    x[2, 5], x[2, 6], x[2, 7], x[2, 8] = torch.finfo(F32).max, border, -border, below
+    m = M.fp8_quantize(x.cuda())
+    assert int(m.scales.view(torch.uint8)[0, 2]) == 247
+    assert m.codes[2, 5:9].cpu().tolist() == [256.0, 256.0, -256.0, 240.0]
+    inf = float("inf")
+    for dtype in (F32, BF16):
+        assert M.fp8_dequantize(m, dtype)[2, 5:9].cpu().tolist() == [inf, inf, -inf, 240 * 2.0 ** 120]
+    x[2, 5:8] = 0
+    clean = M.fp8_quantize(x.cuda())
+    got, want = M.fp8_transpose(m), M.fp8_transpose(clean)
+    assert bool(got.codes.float()[5:8, 2].isnan().all())
+    a, b = M.fp8_dequantize(got, F32), M.fp8_dequantize(want, F32)
+    b[5:8, 2] = a[5:8, 2]
+    assert torch.equal(a.view(torch.int32), b.view(torch.int32))
+    dout = torch.randn(9, 40, generator=g).cuda()
+    dw = M.fp8_linear_bwd(m, None, dout, want_dx=False)["dweight"]
+    same = M.fp8_linear_bwd(clean, None, dout, want_dx=False)["dweight"]
+    keep = [i for i in range(300) if i not in (5, 6, 7)]
+    assert bool(dw[:, 5:8].isnan().all()) and torch.equal(dw[:, keep], same[:, keep])
