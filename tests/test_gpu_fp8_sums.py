@@ -53,6 +53,23 @@ def test_whole_numbers(M, shape, square):
         assert torch.equal(M.fp8_linear_fwd(x8, w8, out_dtype=dtype), want.to(dtype)), dtype
 
 
+@pytest.mark.parametrize("square", [False, True], ids=["rows", "square"])
+@pytest.mark.parametrize("shape", KERNELS, ids=str)
+def test_small_products_beside_large_ones(M, shape, square):
+    """In every block of 128 one product of 256 and 8 neighbours of 1.5 x 2^-8, which the 8-bit instructions drop beside it.
+    A sum of b blocks is 256 b + 3 b 2^-6, all of its parts multiples of 2^-9 below 2^15: exact in fp32 in any order."""
+    tokens, k, n = shape
+    say("small products beside large ones", shape, square)
+    blocks = (k - 9) // 128 + 1                              # those that hold all nine
+    assert 256 * blocks + 1 < 1 << 15
+    x, w = torch.zeros(tokens, k), torch.zeros(n, k)
+    for b in range(blocks):
+        x[:, 128 * b], w[:, 128 * b] = 16.0, 16.0
+        x[:, 128 * b + 1:128 * b + 9], w[:, 128 * b + 1:128 * b + 9] = 2.0 ** -4, 1.5 * 2.0 ** -4
+    got = M.fp8_linear_fwd(M.fp8_quantize(x.cuda()), M.fp8_quantize(w.cuda(), square=square), out_dtype=F32)
+    assert bool((got == blocks * (256 + 3 * 2.0 ** -6)).all())
+
+
 # tokens, in_features, out_features of gradients in fp32: both products small and side by side; dweight in slices of 128 x
 # 128; both on 256 x 256
 @pytest.mark.parametrize("shape", [(300, 384, 200), (1000, 900, 700), (8000, 700, 600), (4100, 4000, 4200)], ids=str)
