@@ -1,0 +1,47 @@
+"""Gradients of the 8-bit layer from a transposed weight whose scales are those of its rows."""
+import pytest
+import torch
+
+import fp8_ops as Q
+import model_ops as R
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def M():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import selective_state_space_17_amd as m
+    return m
+
+
+# tokens, in_features, out_features; dx on tiles of 16 x 16 (two), 64 x 32, 64 x 64 (with dweight in one launch), 32 x 32, 128
+# x 128 and 256 x 256
+@pytest.mark.parametrize("io", [BF16, F32], ids=str)
+@pytest.mark.parametrize("shape", [(1, 130, 7), (16, 700, 333), (300, 1000, 777), (1000, 900, 700), (60, 2500, 1000), (2030, 1500, 130),
+                                   (4000, 4000, 1000)], ids=str)
+def test_linear_bwd(M, shape, io):
+    tokens, k, n = shape
+    say("fp8 linear gradients, weight with scales of rows", shape, io)
+    g = torch.Generator(device="cuda").manual_seed(tokens + k)
+
+    def rnd(*s):
+        return torch.randn(*s, generator=g, device="cuda")
+
+    x = M.fp8_quantize(rnd(tokens, k))
+    # rows and columns of sizes far apart: a scale of 128 x 128 would leave little of the small ones
+    weight = rnd(n, k) * torch.exp(2 * rnd(n, 1)) * torch.exp(2 * rnd(k))
+    wt = M.fp8_quantize(weight, transposed=True)
+    dout = (rnd(tokens, n) * 1e-3).to(io)
+    got = M.fp8_linear_bwd(x, wt, dout)
+    d8 = M.fp8_quantize(dout)
+    dv, wv = (M.fp8_dequantize(m, F32).double() for m in (d8, wt))
+    R.check(got["dx"], Q.product_of_values(dv, wv, io, chunk=128), "dx")
+    assert torch.equal(got["dx"], M.fp8_linear_bwd(None, wt, dout, want_dweight=False)["dx"])
+    assert torch.equal(got["dx"], M.fp8_linear_fwd(d8, wt, out_dtype=io)), "dx is the product of the rounded gradient"
+    assert torch.equal(got["dweight"], M.fp8_linear_bwd(x, None, dout, want_dx=False)["dweight"])
+    square = M.fp8_linear_bwd(x, M.fp8_quantize(weight, square=True, transposed=True), dout)
+    assert torch.equal(got["dweight"], square["dweight"]) and not torch.equal(got["dx"], square["dx"])
