@@ -468,7 +468,10 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
 // wave that multiplies it: 1103 us at 8192^3, as here 809, 1.36 PFLOP/s; with tiles of 128 x 128, whose fragments are read
 // more often, 1031 to 1057.)
 // A thread has 16 codes of two of C's rows and of two of R's; rows lie in LDS as above, 128 bytes each, their chunks of
-// 16 bytes xor-ed with bits 1 to 3 of the row, which keeps writes and reads off each other's banks.
+// 16 bytes xor-ed with a key of the row: bits 1 to 3, so that 16 lanes that read one chunk of 16 rows find them on other
+// banks, and bit 0 once more, so that 8 lanes that write every other chunk of two rows do (counter: no conflicts; without
+// bit 0 8 cycles for every write, 1 to 4 % of the kernel: dweight of 8192 x 1536 x 768 33.5 us, as here 32.5).
+__device__ __forceinline__ int fine_key(int row) { return (row / 2 % 8) ^ (row % 2); }
 template <int B, int WC, int WR, bool SQUARE>
 __global__ __launch_bounds__(WC * WR * 64, 2) void fine_product_kernel(Fp8Params p) {
   constexpr int TC = B / WC / 32, TR = B / WR / 32;
@@ -532,8 +535,8 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void fine_product_kernel(Fp8Params
       start_load();
     }
   };
-  unsigned char* const put_at = lds + lrow * kLine + (((part * 2) ^ (lrow / 2 % 8)) << 4);
-  const int put_next = (((part * 2 + 1) ^ (lrow / 2 % 8)) << 4) - (((part * 2) ^ (lrow / 2 % 8)) << 4);
+  unsigned char* const put_at = lds + lrow * kLine + (((part * 2) ^ fine_key(lrow)) << 4);
+  const int put_next = (((part * 2 + 1) ^ fine_key(lrow)) << 4) - (((part * 2) ^ fine_key(lrow)) << 4);
   auto widen_one = [&](int m, int h) {   // codes[m] to half h
     const float s = fp8_power(scales[m]);
     unsigned char* const to = put_at + h * kBuffer + m / 2 * kMatrix + m % 2 * kRows * kLine;
@@ -543,7 +546,7 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void fine_product_kernel(Fp8Params
   const unsigned char *fc_at[4], *fr_at[4];   // fragments of 16 k
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const int at = lane % 32 * kLine + (((2 * q + lane / 32) ^ (lane / 2 % 8)) << 4);
+    const int at = lane % 32 * kLine + (((2 * q + lane / 32) ^ fine_key(lane)) << 4);
     fc_at[q] = lds + wc * (32 * TC * kLine) + at;
     fr_at[q] = lds + kMatrix + wr * (32 * TR * kLine) + at;
   }
