@@ -32,7 +32,6 @@ struct TileParams {
 constexpr int kThreads = 256;
 constexpr int kTileThreads = 512;
 constexpr int kHigh = 4;   // rows of a thread
-struct E4m3 {};   // the type of inputs that are in 8 bits
 
 struct TileShared {
   uint32_t tops[kTileThreads / kLanes][kBlock];

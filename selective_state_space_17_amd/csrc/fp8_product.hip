@@ -164,78 +164,78 @@ __device__ __forceinline__ bool way_out(const Fp8Params& p, const Job& cur, int 
                                         f32x16_t (&acc)[BC / WC / 32][BR / WR / 32]) {
   constexpr bool kFine = std::is_same_v<T, float>;
   constexpr int TC = BC / WC / 32, TR = BR / WR / 32;
-      // accumulator e = 4 q + f of tile (i, j): R's row TR (8 q + 4 (lane / 32) + f) + j of the wave's share, and row i of
-      // C's that are the lane's.  Lanes 16 apart exchange f and f + 1.
-      constexpr int kRun = 2 * TC;
-      int wave_r = wr * TR * 32 + (lane / 32 * 4 + lane / 16 % 2) * TR;
-      asm volatile("" : "+v"(wave_r));   // (known before the loop over jobs, all the rows' places would be registers in it)
-      const int c = wc * TC * 32 + lane % 16 * kRun;
-      auto each = [&](auto&& to) {   // every pair of f: (row of the tile after wave_r, tile j, first accumulator)
-        unrolled<TR * 8>([&](auto i) {
-          constexpr int I = decltype(i)::value, J = I / 8, E = I % 8 * 2;
-          to(std::integral_constant<int, (E / 4 * 8 + E % 4) * TR + J>{}, std::integral_constant<int, J>{},
-             std::integral_constant<int, E>{});
-        });
-      };
-      // (way: which of the three below, so that the compiler does not take what two have in common before the branch, where
-      // a second set of accumulators finds no registers)
-      auto exchanged = [&](auto way, auto j, auto e, float (&v)[kRun]) {
-        constexpr int J = decltype(j)::value, E = decltype(e)::value;
-  #pragma unroll
-        for (int t = 0; t < TC; ++t) {
-          float a = acc[t][J][E];
-          asm volatile("" : "+v"(a) : "n"(decltype(way)::value));
-          const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(acc[t][J][E + 1]), false, false);
-          v[t] = __uint_as_float(x[0]);
-          v[TC + t] = __uint_as_float(x[1]);
-        }
-      };
-      if (cur.sum >= 0) {
-        float* const to = p.sums + static_cast<int64_t>(cur.sum) * BR * BC + wave_r * BC + c;
-        const int64_t rows = p.rows - cur.r0 - wave_r;
-        each([&](auto r, auto j, auto e) {
+  // accumulator e = 4 q + f of tile (i, j): R's row TR (8 q + 4 (lane / 32) + f) + j of the wave's share, and row i of
+  // C's that are the lane's.  Lanes 16 apart exchange f and f + 1.
+  constexpr int kRun = 2 * TC;
+  int wave_r = wr * TR * 32 + (lane / 32 * 4 + lane / 16 % 2) * TR;
+  asm volatile("" : "+v"(wave_r));   // (known before the loop over jobs, all the rows' places would be registers in it)
+  const int c = wc * TC * 32 + lane % 16 * kRun;
+  auto each = [&](auto&& to) {   // every pair of f: (row of the tile after wave_r, tile j, first accumulator)
+    unrolled<TR * 8>([&](auto i) {
+      constexpr int I = decltype(i)::value, J = I / 8, E = I % 8 * 2;
+      to(std::integral_constant<int, (E / 4 * 8 + E % 4) * TR + J>{}, std::integral_constant<int, J>{},
+         std::integral_constant<int, E>{});
+    });
+  };
+  // (way: which of the three below, so that the compiler does not take what two have in common before the branch, where
+  // a second set of accumulators finds no registers)
+  auto exchanged = [&](auto way, auto j, auto e, float (&v)[kRun]) {
+    constexpr int J = decltype(j)::value, E = decltype(e)::value;
+#pragma unroll
+    for (int t = 0; t < TC; ++t) {
+      float a = acc[t][J][E];
+      asm volatile("" : "+v"(a) : "n"(decltype(way)::value));
+      const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(acc[t][J][E + 1]), false, false);
+      v[t] = __uint_as_float(x[0]);
+      v[TC + t] = __uint_as_float(x[1]);
+    }
+  };
+  if (cur.sum >= 0) {
+    float* const to = p.sums + static_cast<int64_t>(cur.sum) * BR * BC + wave_r * BC + c;
+    const int64_t rows = p.rows - cur.r0 - wave_r;
+    each([&](auto r, auto j, auto e) {
+      float v[kRun];
+      exchanged(std::integral_constant<int, 0>{}, j, e, v);
+      if (r < rows) store_row<kRun>(to + r * BC, v);
+    });
+  } else {
+    T* const tile = static_cast<T*>(p.out) + cur.r0 * p.cols + cur.c0;
+    const uint32_t at = static_cast<uint32_t>(wave_r * static_cast<int>(p.cols) + c) * sizeof(T);   // (cols <= 2^20)
+    auto to = [&](auto r) { return reinterpret_cast<T*>(reinterpret_cast<unsigned char*>(tile + r * p.cols) + at); };
+    const int64_t rows = p.rows - cur.r0, cols = p.cols - cur.c0;
+    if (rows >= BR && cols >= BC && !p.accumulate) {
+      // past the cache: kept there, the output pushes the operands out of it (32768 x 2560 x 10240, which writes 671 MB:
+      // 677 us, kept 730)
+      each([&](auto r, auto j, auto e) {
+        if constexpr (kFine) {
           float v[kRun];
-          exchanged(std::integral_constant<int, 0>{}, j, e, v);
-          if (r < rows) store_row<kRun>(to + r * BC, v);
-        });
-      } else {
-        T* const tile = static_cast<T*>(p.out) + cur.r0 * p.cols + cur.c0;
-        const uint32_t at = static_cast<uint32_t>(wave_r * static_cast<int>(p.cols) + c) * sizeof(T);   // (cols <= 2^20)
-        auto to = [&](auto r) { return reinterpret_cast<T*>(reinterpret_cast<unsigned char*>(tile + r * p.cols) + at); };
-        const int64_t rows = p.rows - cur.r0, cols = p.cols - cur.c0;
-        if (rows >= BR && cols >= BC && !p.accumulate) {
-          // past the cache: kept there, the output pushes the operands out of it (32768 x 2560 x 10240, which writes 671 MB:
-          // 677 us, kept 730)
-          each([&](auto r, auto j, auto e) {
-            if constexpr (kFine) {
-              float v[kRun];
-              exchanged(std::integral_constant<int, 1>{}, j, e, v);
-              __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4_u*>(to(r)));
-            } else {
-              constexpr int J = decltype(j)::value, E = decltype(e)::value;
-              typedef uint32_t Run __attribute__((ext_vector_type(TC)));
-              typedef Run Run_u __attribute__((aligned(2)));
-              Run v;
-  #pragma unroll
-              for (int h = 0; h < TC / 2; ++h) {
-                const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16(acc[2 * h][J][E], acc[2 * h + 1][J][E]),
-                                                                pack_bf16(acc[2 * h][J][E + 1], acc[2 * h + 1][J][E + 1]),
-                                                                false, false);
-                v[h] = x[0];
-                v[TC / 2 + h] = x[1];
-              }
-              __builtin_nontemporal_store(v, reinterpret_cast<Run_u*>(to(r)));
-            }
-          });
-          return true;
+          exchanged(std::integral_constant<int, 1>{}, j, e, v);
+          __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4_u*>(to(r)));
         } else {
-          each([&](auto r, auto j, auto e) {
-            float v[kRun];
-            exchanged(std::integral_constant<int, 2>{}, j, e, v);
-            if (r + wave_r < rows) put(to(r), v, cols - c, p.accumulate);
-          });
+          constexpr int J = decltype(j)::value, E = decltype(e)::value;
+          typedef uint32_t Run __attribute__((ext_vector_type(TC)));
+          typedef Run Run_u __attribute__((aligned(2)));
+          Run v;
+#pragma unroll
+          for (int h = 0; h < TC / 2; ++h) {
+            const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16(acc[2 * h][J][E], acc[2 * h + 1][J][E]),
+                                                            pack_bf16(acc[2 * h][J][E + 1], acc[2 * h + 1][J][E + 1]),
+                                                            false, false);
+            v[h] = x[0];
+            v[TC / 2 + h] = x[1];
+          }
+          __builtin_nontemporal_store(v, reinterpret_cast<Run_u*>(to(r)));
         }
-      }
+      });
+      return true;
+    } else {
+      each([&](auto r, auto j, auto e) {
+        float v[kRun];
+        exchanged(std::integral_constant<int, 2>{}, j, e, v);
+        if (r + wave_r < rows) put(to(r), v, cols - c, p.accumulate);
+      });
+    }
+  }
   return false;
 }
 
@@ -646,8 +646,6 @@ template <int BC, int BR, typename T> __global__ __launch_bounds__(256) void sli
 // X: R's type, E4m3 or a plain one for up to 16 rows that fit into LDS in 8 bits: each workgroup rounds them again while
 // its first loads of C are on their way, which saves a launch (1 x 2560 x 10240: 7.3 us of the GPU, 26 MB; with each lane
 // rounding its own operands 20).
-struct E4m3 {};
-
 template <int N> __device__ __forceinline__ uint32_t scales_at(const unsigned char* at) {
   if constexpr (N == 4) return *reinterpret_cast<const uint32_t*>(at);
   else if constexpr (N == 2) return *reinterpret_cast<const uint16_t*>(at);
@@ -889,7 +887,10 @@ Tiling pick(const Fp8ProductArgs& a) {
 
 }  // namespace
 
-// LDS that plain rows take in 8 bits, and how much of it leaves room for four workgroups on a CU
+// LDS that plain rows take in 8 bits, and how much of it leaves room for four workgroups on a CU: each rounds all the rows
+// again, where a launch of its own rounds them once (bf16, rounded on the way and before: 8 x 2560 x 10240, 21 KB, 10.8 and
+// 12.7 us; 16 x 1280 x 10240, 21 KB, 9.4 and 9.8; 16 x 1536 x 10240, 25 KB, 10.8 and 10.7; 16 x 2560 x 10240, 42 KB, 15.5 and
+// 13.4; 2560 columns 5.9 and 7.8, 5.0 and 6.5, 5.6 and 6.8, 8.1 and 7.9; fp32 alike)
 int64_t plain_bytes(const Fp8ProductArgs& a) { return a.rows * (fp8_blocks(a.k) * (kBlock + 1) + 16); }
 constexpr int64_t kMostPlain = 24 << 10;
 

@@ -16,6 +16,7 @@ namespace mssm {
 
 constexpr int kBlock = 128;      // values that share a scale, along a row
 constexpr int kOne = 127;        // the byte of 2^0
+struct E4m3 {};                  // the type of a kernel's inputs that are in 8 bits
 
 inline __host__ __device__ int64_t fp8_blocks(int64_t cols) { return (cols + kBlock - 1) / kBlock; }
 inline __host__ __device__ int64_t fp8_lines(int64_t rows) { return (rows + 3) / 4 * 4; }
