@@ -18,11 +18,11 @@ def M():
     return m
 
 
-# tokens, in_features, out_features; dx on tiles of 16 x 16 (two), 64 x 32, 64 x 64 (with dweight in one launch), 32 x 32, 128
-# x 128 and 256 x 256
+# tokens, in_features, out_features; dx on tiles of 16 x 16 (two), 64 x 32, 64 x 64 (with dweight in one launch), 32 x 32,
+# 128 x 128 and 256 x 256
 @pytest.mark.parametrize("io", [BF16, F32], ids=str)
-@pytest.mark.parametrize("shape", [(1, 130, 7), (16, 700, 333), (300, 1000, 777), (1000, 900, 700), (60, 2500, 1000), (2030, 1500, 130),
-                                   (4000, 4000, 1000)], ids=str)
+@pytest.mark.parametrize("shape", [(1, 130, 7), (16, 700, 333), (300, 1000, 777), (1000, 900, 700),
+                                   (60, 2500, 1000), (2030, 1500, 130), (4000, 4000, 1000)], ids=str)
 def test_linear_bwd(M, shape, io):
     tokens, k, n = shape
     say("fp8 linear gradients, weight with scales of rows", shape, io)
