@@ -1382,7 +1382,8 @@ def fp8_linear_bwd(x, weight_t, dout, want_dx: bool = True, want_dweight: bool =
     [in, out], square or not (None without dx); dout: [tokens, out] (or any leading sizes), float32 or bfloat16,
     which is rounded to 8 bits along the sums that it enters.  dweight: [out, in] in dout's type or float32
     (allocated in dweight_dtype, else dout's, when None), overwritten, or added to when accumulate.
-    Returns a dict of dx [tokens, in] in dout's type and dweight (None for one that is not wanted)."""
+    Returns a dict of dx [tokens, in] (or dout's leading sizes) in dout's type and dweight (None for one that is not
+    wanted)."""
     torch = _torch()
     cur = torch.cuda.current_device()
     if not want_dx and not want_dweight:

@@ -4,9 +4,11 @@
 // A workgroup takes tiles of 128 x 128, so that a tile is one block along either axis: a thread holds 4 rows x 8
 // columns in registers, finds the largest magnitudes of its rows (over 16 lanes) and of its columns (over the
 // workgroup), and rounds with either; the transposed codes change places in LDS.  Bound by memory: each input is read
-// once and each output written once (both orders of 16384 x 10240 in bf16: 143 us, 671 MB, 4.7 TB/s; of 16384 x 1536: 24
-// us, 4.2 TB/s; 16384 x 2560 laid out the other way from 8 bits: 27 us; 16384 x 1536 back to bf16: 14 us, 5.4 TB/s).  With
-// 8 x 8 values a thread registers spilled (the first: 218 us).
+// once and each output written once (both orders of 16384 x 10240 in bf16: 143 us, 671 MB, 4.7 TB/s, in blocks of 128 x 128
+// 150; of 16384 x 1536: 24 us, 4.2 TB/s; 16384 x 1536 back to bf16: 14 us, 5.4 TB/s).  With 8 x 8 values a thread registers
+// spilled (the first: 218 us).  Laid out the other way from 8 bits less of the rate is reached (16384 x 2560: 27 us, 84 MB,
+// 3.2 TB/s; 16384 x 10240: 91, 3.7): half the bytes for the same work on each value, transposed codes leave as 128 bytes a
+// column, and the words that change places in LDS meet on banks for a seventh of a CU's cycles.
 // A matrix in 8 bits laid out the other way loses little: with powers of two its values are e4m3 numbers whatever the
 // scale, so under another block's scale they stay what they are, except below 2^-6 of it, where e4m3's steps stop
 // shrinking.

@@ -11,9 +11,12 @@
 // 2^-133); under the scales 2^-127 to 2^-125 the smallest 24, 16 and 8 magnitudes become multiples of 2^-133, halves to
 // even.  (A factor that lifts one operand's smallest values would take as much from its largest.)
 //
-// Large products are bound by the matrix cores under the power limit (32768 x 2560 x 10240: 677 us, 2.5 PFLOP/s, matrix
-// cores busy 0.70 of the cycles at some 1.8 GHz; 8192^3: 415 us, 2.65; with fp32 results 809 us, 1.36,
-// where the library's bf16 product takes 699), few rows by latency and the weight's bytes (1 x 2560 x 10240: 7.1 us, 26 MB).
+// Large products are bound by the matrix cores under the power limit, and their time goes with the clock.  32768 x 2560 x
+// 10240: 710 us (2.4 PFLOP/s) in a second of nothing else, 740 to 1010 in the first dozen calls after a pause, while the
+// clock settles, 677 at best (2.5; matrix cores busy 0.70 of the cycles at some 1.8 GHz).  8192^3: 438, at best 415; with
+// fp32 results 848 and 786, where the library's bf16 product of the same values takes 715 and 699.  Few rows are bound by
+// latency and the weight's bytes (1 x 2560 x 10240: 7.1 us, 26 MB).  Times below are the best of calls back to back, each
+// pair on one GPU.
 #include <limits>
 #include <type_traits>
 #include <utility>
@@ -465,8 +468,8 @@ __global__ __launch_bounds__(WC * WR * 64, 2) void tile_product_kernel(Fp8Params
 // fp32 results.  Converting two codes takes a SIMD 16 cycles, half of what a matrix instruction of 32 x 32 x 16 does, so a
 // code is widened once a workgroup, on its way into LDS: from memory into registers, a half of 64 k ahead, and from there,
 // times its scale, into the bf16 half that is multiplied next.  Two halves in LDS and a barrier a half.  (Widened by every
-// wave that multiplies it: 1103 us at 8192^3, as here 809, 1.36 PFLOP/s; with tiles of 128 x 128, whose fragments are read
-// more often, 1031 to 1057.)
+// wave that multiplies it: 1103 us at 8192^3, as here 809, 1.4 PFLOP/s; with tiles of 128 x 128, whose fragments
+// are read more often, 1031 to 1057.)
 // A thread has 16 codes of two of C's rows and of two of R's; rows lie in LDS as above, 128 bytes each, their chunks of
 // 16 bytes xor-ed with a key of the row: bits 1 to 3, so that 16 lanes that read one chunk of 16 rows find them on other
 // banks, and bit 0 once more, so that 8 lanes that write every other chunk of two rows do (counter: no conflicts; without
@@ -644,7 +647,7 @@ template <int BC, int BR, typename T> __global__ __launch_bounds__(256) void sli
 // last ones are often past the end, 22; 64 x 2560 x 5120: 12.3, two blocks 12.9).
 // As above, row i of tile t is row CT i + t of C's 16 CT and RT i + t of R's.
 // X: R's type, E4m3 or a plain one for up to 16 rows that fit into LDS in 8 bits: each workgroup rounds them again while
-// its first loads of C are on their way, which saves a launch (1 x 2560 x 10240: 7.3 us of the GPU, 26 MB; with each lane
+// its first loads of C are on their way, which saves a launch (1 x 2560 x 10240: 7.1 us of the GPU, 26 MB; with each lane
 // rounding its own operands 20).
 template <int N> __device__ __forceinline__ uint32_t scales_at(const unsigned char* at) {
   if constexpr (N == 4) return *reinterpret_cast<const uint32_t*>(at);
